@@ -11,8 +11,12 @@ from ._binding import (EXPORTED_SYMBOLS, FAULT_NONE, FAULT_STREAM_STAGE, FAULT_T
                        FLAG_CTA_PAIRS, FLAG_DETERMINISTIC, FLAG_FORCE_TC, FLAG_PERSISTENT, Dims, MoeFp4Error, check, forward, forward_gated, forward_host, forward_mx,
                        forward_noalloc, host_workspace_bytes, mx_workspace_bytes, lib_path, load_library, mxfp8_quantize, noalloc_check, route, router,
                        set_fault_injection, status_string, workspace_bytes)
+from ._ops import (block_residual, mxfp4_dequantize, mxfp4_linear, mxfp4_linear_workspace_bytes, mxfp4_matmul,
+                   mxfp4_quantize, mxfp4_tile_scales, mxfp4_tiled_scale_bytes, ops_check, rms_norm)
 
 __all__ = ["EXPORTED_SYMBOLS", "FAULT_NONE", "FAULT_STREAM_STAGE", "FAULT_TC_TOKEN_TILE", "FLAG_FORCE_GEMV",
            "FLAG_CTA_PAIRS", "FLAG_DETERMINISTIC", "FLAG_FORCE_TC", "FLAG_PERSISTENT", "Dims", "MoeFp4Error", "check", "forward", "forward_gated", "forward_host", "forward_mx",
            "forward_noalloc", "host_workspace_bytes", "mx_workspace_bytes", "lib_path", "load_library", "mxfp8_quantize", "noalloc_check", "route", "router",
-           "set_fault_injection", "status_string", "workspace_bytes"]
+           "set_fault_injection", "status_string", "workspace_bytes",
+           "block_residual", "mxfp4_dequantize", "mxfp4_linear", "mxfp4_linear_workspace_bytes", "mxfp4_matmul",
+           "mxfp4_quantize", "mxfp4_tile_scales", "mxfp4_tiled_scale_bytes", "ops_check", "rms_norm"]

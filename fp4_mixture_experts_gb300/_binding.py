@@ -39,6 +39,15 @@ EXPORTED_SYMBOLS = (
     "moe_fp4_forward_mx",
     "moe_fp4_check",
     "moe_fp4_status_string",
+    "moe_fp4_mxfp4_quantize",
+    "moe_fp4_mxfp4_dequantize",
+    "moe_fp4_mxfp4_tiled_scale_bytes",
+    "moe_fp4_mxfp4_tile_scales",
+    "moe_fp4_mxfp4_matmul",
+    "moe_fp4_mxfp4_linear_workspace_bytes",
+    "moe_fp4_mxfp4_linear",
+    "moe_fp4_block_norm",
+    "moe_fp4_ops_check",
 )
 
 
@@ -102,6 +111,19 @@ def load_library():
     lib.moe_fp4_forward_mx.argtypes = [pd, P, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P,
                                        ctypes.POINTER(ctypes.c_void_p)]
     lib.moe_fp4_forward_mx.restype = ctypes.c_int
+    i32, i64, size = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    for name, args, res in (  # the operators around the layer (_ops.py)
+            ("mxfp4_quantize", [P, i32, i64, i64, i32, P, i32, i64, P, i32, P, P, i32, P], i32),
+            ("mxfp4_dequantize", [P, P, i64, i32, i32, P, P], i32),
+            ("mxfp4_tiled_scale_bytes", [i64, i32, i32], size),
+            ("mxfp4_tile_scales", [P, i32, i32, i32, i32, P, P], i32),
+            ("mxfp4_matmul", [P, P, P, P, P, P, P, P], i32),
+            ("mxfp4_linear_workspace_bytes", [P], size),
+            ("mxfp4_linear", [P, P, i32, i64, i64, P, i32, P, P, P, P, P, size, P], i32),
+            ("block_norm", [P, P], i32),
+            ("ops_check", [P], i32)):
+        fn = getattr(lib, "moe_fp4_" + name)
+        fn.argtypes, fn.restype = args, res
     lib.moe_fp4_check.argtypes = [P, P]
     lib.moe_fp4_check.restype = ctypes.c_int
     lib.moe_fp4_status_string.argtypes = [ctypes.c_int]

@@ -86,6 +86,9 @@ bool layout_workspace(const moe_fp4_dims& d, void* base, bool with_staging, Work
 // elements); false if the driver rejects it.
 bool make_map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                  uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);
+// The same for 4 dimensions, innermost first; strides (bytes) of the outer three.
+bool make_map_4d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[4],
+                 const uint64_t (&strides)[3], const uint32_t (&box)[4], CUtensorMapSwizzle sw);
 // SM count of the current device (cached per device).
 int num_sms();
 // Raises the kernel's dynamic shared memory limit to `bytes` on the current

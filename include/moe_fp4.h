@@ -316,6 +316,141 @@ int moe_fp4_forward_mx(const moe_fp4_dims* dims, const void* x_bf16, const float
                        uint8_t* x_scales, void* workspace, size_t workspace_bytes, void* cuda_stream,
                        void* const* stage_events);
 
+/* ---- Operators around the layer -------------------------------------------
+ * MXFP4 quantisation, products of MXFP4 matrices (dense, and grouped by
+ * expert) and the end of a block (norm, gate, residual, next norm).  As for
+ * the layer: device buffers owned by the caller, work enqueued on the given
+ * stream, nothing allocated, nothing synchronised, arguments checked on the
+ * host before anything is enqueued.  They keep no state between calls but an
+ * error word (moe_fp4_ops_check). */
+
+/* Element types of the operators' unquantised operands and results. */
+#define MOE_FP4_TYPE_BF16 0
+#define MOE_FP4_TYPE_F32 1
+
+/* MXFP4 form of rows: for each 32 consecutive elements of a row, with amax
+ * their largest magnitude (OCP Microscaling v1.0 conversion, E2M1 element),
+ *   scale byte  s = floor(log2(amax)) - 2 + 127, at least 0; 0 for an
+ *               all-zero block (the scale is 2^(s-127));
+ *   codes       E2M1 of x / 2^(s-127), rounded to nearest (ties to the even
+ *               code), saturated at +-6; two codes a byte, the LOW nibble the
+ *               even element; a negative zero keeps its sign.
+ * A block holding an infinity or a NaN gets the scale byte 0xFF (NaN).
+ *
+ *   x          bf16 or fp32, x_rows rows of K elements, row r at element
+ *              r * x_stride (x_stride >= K; any alignment of whole elements,
+ *              faster when rows start on 16 bytes)
+ *   row_index  NULL: output row r is row r of x; else int32 [rows], output row
+ *              r is row row_index[r] / index_div of x (the layer's sorted_slot
+ *              with index_div = k gathers the tokens of the expert sort).  An
+ *              index outside x gives a zero row and sets error bit 1.
+ *   codes      uint8 [rows, K/2], 16-byte aligned
+ *   scales     row-major (tiled = 0): uint8 [rows, K/32].
+ *              tiled = 1, the layout of the products' scales: tiles of 128 rows
+ *              by 4 scales, uint8 [row tiles][ceil(K/128)][512], the byte of
+ *              row r and scale b of a tile at 16 (r % 32) + 4 (r / 32) + b;
+ *              scales past K/32 are written as 0, those of rows past the end
+ *              are left as they were.  Without groups row r is in tile r / 128.
+ *              With group_offsets (int32 [groups + 1] on the device, groups <=
+ *              1024, not decreasing, rows of group e in [off[e], off[e+1]))
+ *              every group starts a tile: row r of group e is row r - off[e] of
+ *              the tiles from off[e] / 128 + e on.  rows / 128 + groups tiles
+ *              in all (moe_fp4_mxfp4_tiled_scale_bytes, 16-byte aligned).
+ *              Rows in no group get codes and no scales.
+ * K a positive multiple of 32, at most 32768; rows K < 2^36; rows = 0
+ * enqueues nothing. */
+int moe_fp4_mxfp4_quantize(const void* x, int x_type, int64_t x_rows, int64_t x_stride, int32_t K,
+                           const int32_t* row_index, int32_t index_div, int64_t rows, const int32_t* group_offsets,
+                           int32_t groups, uint8_t* codes, uint8_t* scales, int tiled, void* cuda_stream);
+
+/* The values that codes [rows, K/2] with row-major scales [rows, K/32] stand
+ * for: out [rows, K], bf16 or fp32 (both hold every value but those beyond
+ * their range, which become infinities).  codes and out 16-byte aligned. */
+int moe_fp4_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t K, int out_type,
+                             void* out, void* cuda_stream);
+
+/* Bytes of the tiled scales of `rows` rows of K elements in `groups` groups
+ * (1 when there are none): (rows / 128 + groups) ceil(K / 128) 512; 0 for
+ * sizes moe_fp4_mxfp4_quantize rejects. */
+size_t moe_fp4_mxfp4_tiled_scale_bytes(int64_t rows, int32_t groups, int32_t K);
+
+/* Row-major scales [E, N, K/32] (the layer's w13_scale and w2_scale) in the
+ * weights' layout of the products, once when weights are loaded: uint8
+ * [E][ceil(N/128)][ceil(K/128)][512], tiles as above, zeros past the ends.
+ * swiglu = 1: for a product with SwiGLU (N = 2I, gate rows then up rows), the
+ * rows of a tile are gate and up rows in turn.  tiled 16-byte aligned. */
+int moe_fp4_mxfp4_tile_scales(const uint8_t* scales, int32_t E, int32_t N, int32_t K, int swiglu, uint8_t* tiled,
+                              void* cuda_stream);
+
+/* Sizes and form of a product: a has M rows, w is E matrices of N rows. */
+typedef struct moe_fp4_mm_dims {
+  int32_t M, N, K, E;   /* M >= 0, N >= 1, K a multiple of 32 up to 32768, 1 <= E <= 1024 */
+  int32_t swiglu;       /* 0: y [M, N]; 1: N = 2I even, y [M, I] = silu(first I features) * last I */
+  int32_t y_type;       /* MOE_FP4_TYPE_BF16 or MOE_FP4_TYPE_F32 */
+} moe_fp4_mm_dims;
+
+/* y[m, n] = sum_K a[m, K] w_e[n, K] of MXFP4 matrices on block-scaled tensor
+ * cores (tcgen05.mma kind::mxf4: products of codes and scales exact, fp32
+ * sums, one rounding to y_type).
+ *   a, a_scales  codes [M, K/2] and tiled scales of moe_fp4_mxfp4_quantize
+ *   offsets      NULL (E = 1): all rows use the one matrix; else int32 [E + 1]
+ *                on the device, not decreasing: rows [off[e], off[e+1]) use
+ *                matrix e; empty groups are fine, rows in no group are not
+ *                written.  a_scales are then in the grouped tiled layout.
+ *   w, w_scales  codes [E, N, K/2], scales of moe_fp4_mxfp4_tile_scales
+ * a, w, a_scales, w_scales 16-byte aligned, y aligned to its element.  A NaN
+ * scale byte makes the results that it touches NaN.  The sums' order depends
+ * on the sizes alone: the same call gives the same bits. */
+int moe_fp4_mxfp4_matmul(const moe_fp4_mm_dims* dims, const uint8_t* a, const uint8_t* a_scales,
+                         const int32_t* offsets, const uint8_t* w, const uint8_t* w_scales, void* y,
+                         void* cuda_stream);
+
+/* Device workspace of moe_fp4_mxfp4_linear (the codes and scales of the
+ * quantised rows; 256-byte aligned base); 0 for unsupported sizes. */
+size_t moe_fp4_mxfp4_linear_workspace_bytes(const moe_fp4_mm_dims* dims);
+
+/* The product from unquantised rows: moe_fp4_mxfp4_quantize of x (bf16 or
+ * fp32, x_rows rows, stride x_stride; row_index / index_div as there, M output
+ * rows), then moe_fp4_mxfp4_matmul.  The same bits as the two calls. */
+int moe_fp4_mxfp4_linear(const moe_fp4_mm_dims* dims, const void* x, int x_type, int64_t x_rows, int64_t x_stride,
+                         const int32_t* row_index, int32_t index_div, const int32_t* offsets, const uint8_t* w,
+                         const uint8_t* w_scales, void* y, void* workspace, size_t workspace_bytes,
+                         void* cuda_stream);
+
+/* The end of a block in one pass over its rows.  With b = y (+ y2):
+ *   post_norm:  b = b * rsqrt(mean(b^2) + eps)
+ *   b = b * post_weight                      (NULL: 1)
+ *   b = b * gate, or * sigmoid(gate)         (gate_shape: none, [T], [d], [T, d])
+ *   out = residual + scale * b               (residual_type)
+ *   normed = out * rsqrt(mean(out^2) + eps) * next_weight   (bf16; NULL weight: 1)
+ * in fp32, each result rounded once (normed is of the unrounded sum).  y NULL:
+ * normed = the norm of residual alone (the norm before a block); out, if
+ * given, is then a copy of residual.  out may be residual itself; otherwise
+ * outputs overlap no input.  normed NULL: no next norm.  Rows are T of d
+ * elements, row t of an operand at element t * its stride (>= d); out and
+ * normed are contiguous unless out is residual itself with its stride. */
+#define MOE_FP4_GATE_NONE 0
+#define MOE_FP4_GATE_TOKEN 1    /* [T] */
+#define MOE_FP4_GATE_CHANNEL 2  /* [d] */
+#define MOE_FP4_GATE_ELEMENT 3  /* [T, d], gate_stride */
+typedef struct moe_fp4_block_norm_args {
+  int64_t T;                    /* >= 0; 0 enqueues nothing */
+  int32_t d;                    /* 1 .. 16384 */
+  int32_t post_norm, gate_shape, gate_sigmoid;
+  int32_t residual_type, y_type, y2_type, gate_type, post_weight_type, next_weight_type;
+  int64_t residual_stride, y_stride, y2_stride, gate_stride, out_stride;
+  float scale, eps;             /* eps >= 0 */
+  const void *residual, *y, *y2, *gate, *post_weight, *next_weight;
+  void *out, *normed;
+} moe_fp4_block_norm_args;
+int moe_fp4_block_norm(const moe_fp4_block_norm_args* args, void* cuda_stream);
+
+/* Synchronises the stream and reads the error word of the operators above on
+ * the current device: 1 = a row index out of range, 2 = a pipeline wait gave
+ * up after 2 s (results incomplete).  Returns MOE_FP4_OK, MOE_FP4_ERR_DEVICE
+ * or MOE_FP4_ERR_CUDA, and clears the word.  Not during a stream capture. */
+int moe_fp4_ops_check(void* cuda_stream);
+
 /* Fault injection, for tests of the failure path only (the layer's own
  * failure handling: every pipeline wait in the kernels is bounded, and a wait
  * that runs out sets bit 2 of the device error word, releases the kernel's
