@@ -9,6 +9,8 @@ status of the library becomes a MoeFp4Error.  `out`, `codes`, `scales` and
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 
 import torch
 
@@ -16,6 +18,10 @@ from . import _binding
 from ._binding import MoeFp4Error, load_library
 
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}
+_BF16, _U8, _I32 = torch.bfloat16, torch.uint8, torch.int32
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# struct moe_fp4_block_norm_args of include/moe_fp4.h: T; 10 int32; 5 strides; scale, eps; 8 pointers
+_BLOCK_NORM = struct.Struct("q10i5q2f8Q")
 
 
 class MmDims(ctypes.Structure):
@@ -38,8 +44,14 @@ def _lib():
     return _binding._lib or load_library()
 
 
-def _raw_stream(stream):
-    return (stream or torch.cuda.current_stream()).cuda_stream
+# The checks below run on every call: plain `if`s, messages built only when they are raised.
+
+def _raw_stream(stream, t):
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is not None:  # the handle alone, without the Stream object around it
+        return _current_raw_stream(t.get_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _type(t, what):
@@ -49,35 +61,35 @@ def _type(t, what):
     return code
 
 
-def _need(cond, what):
-    if not cond:
-        raise ValueError(what)
-
-
-def _rows2d(t, what):
-    """A GPU tensor of rows: 2-D, its last dimension contiguous (rows may be strided); its row stride"""
-    _need(t.is_cuda and t.dim() == 2, f"{what} must be a 2-D GPU tensor")
-    T, K = t.shape
-    if T <= 1:
-        _need(K <= 1 or t.stride(1) == 1, f"{what} must be contiguous along its rows")
-        return K
-    _need((K <= 1 or t.stride(1) == 1) and t.stride(0) >= K, f"{what} must have contiguous, separate rows")
-    return t.stride(0)
+def _rows(t, what):
+    """(rows, K, row stride) of a GPU tensor of rows: 2-D, contiguous along its rows, rows may be strided"""
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{what} must be a 2-D GPU tensor")
+    R, K = t.shape
+    s0, s1 = t.stride()
+    if (s1 != 1 and K > 1) or (s0 < K and R > 1):
+        raise ValueError(f"{what} must have contiguous, separate rows")
+    return R, K, s0 if R > 1 else K
 
 
 def _bytes(t, what, numel):
-    _need(t.is_cuda and t.dtype == torch.uint8 and t.is_contiguous() and t.numel() >= numel,
-          f"{what} must be a contiguous uint8 GPU tensor of at least {numel} elements")
+    if t.dtype is not _U8 or not t.is_cuda or not t.is_contiguous() or t.numel() < numel:
+        raise ValueError(f"{what} must be a contiguous uint8 GPU tensor of at least {numel} elements")
 
 
-def _indices(row_index, index_div, offsets):
-    if row_index is not None:
-        _need(row_index.is_cuda and row_index.dtype == torch.int32 and row_index.is_contiguous() and
-              row_index.dim() == 1, "row_index must be a contiguous 1-D int32 GPU tensor")
-        _need(index_div >= 1, "index_div must be at least 1")
-    if offsets is not None:
-        _need(offsets.is_cuda and offsets.dtype == torch.int32 and offsets.is_contiguous() and offsets.dim() == 1 and
-              offsets.numel() >= 2, "offsets must be a contiguous 1-D int32 GPU tensor of E + 1 elements")
+def _index_ptr(t, what):
+    if t is None:
+        return None
+    if t.dtype is not _I32 or not t.is_cuda or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous 1-D int32 GPU tensor")
+    return t.data_ptr()
+
+
+def _groups(offsets):
+    E = offsets.numel() - 1
+    if E < 1:
+        raise ValueError("offsets must have E + 1 elements")
+    return E
 
 
 def mxfp4_tiled_scale_bytes(rows: int, K: int, groups: int = 1) -> int:
@@ -92,27 +104,27 @@ def mxfp4_quantize(x, row_index=None, index_div: int = 1, offsets=None, tiled: b
     ([row tiles, ceil(K/128), 512]; by group with offsets, int32 [E + 1]).  row_index (int32 [S]) gathers: row r
     is row row_index[r] // index_div of x (sorted_slot and k of the layer's routing); without it S = R."""
     xt = _type(x, "x")
-    stride = _rows2d(x, "x")
-    _indices(row_index, index_div, offsets)
-    _need(offsets is None or tiled, "offsets need tiled scales")
-    R, K = x.shape
-    _need(K > 0 and K % 32 == 0, "K must be a multiple of 32")
+    R, K, stride = _rows(x, "x")
+    if K % 32 or K == 0:
+        raise ValueError("K must be a multiple of 32")
     S = R if row_index is None else row_index.numel()
-    E = 1 if offsets is None else offsets.numel() - 1
+    E = 1
+    if offsets is not None:
+        if not tiled:
+            raise ValueError("offsets need tiled scales")
+        E = _groups(offsets)
+    index, off = _index_ptr(row_index, "row_index"), _index_ptr(offsets, "offsets")
     if codes is None:
-        codes = torch.empty(S, K // 2, dtype=torch.uint8, device=x.device)
+        codes = torch.empty((S, K // 2), dtype=_U8, device=x.device)
     else:
         _bytes(codes, "codes", S * (K // 2))
-    kt = -(-K // 128)
+    shape = (S // 128 + E, -(-K // 128), 512) if tiled else (S, K // 32)
     if scales is None:
-        shape = (S // 128 + E, kt, 512) if tiled else (S, K // 32)
-        scales = torch.empty(shape, dtype=torch.uint8, device=x.device)
+        scales = torch.empty(shape, dtype=_U8, device=x.device)
     else:
-        _bytes(scales, "scales", (S // 128 + E) * kt * 512 if tiled else S * (K // 32))
-    rc = _lib().moe_fp4_mxfp4_quantize(
-        x.data_ptr(), xt, R, stride, K, None if row_index is None else row_index.data_ptr(), index_div, S,
-        None if offsets is None else offsets.data_ptr(), E, codes.data_ptr(), scales.data_ptr(), int(tiled),
-        _raw_stream(stream))
+        _bytes(scales, "scales", shape[0] * shape[1] * (512 if tiled else 1))
+    rc = _lib().moe_fp4_mxfp4_quantize(x.data_ptr(), xt, R, stride, K, index, index_div, S, off, E, codes.data_ptr(),
+                                       scales.data_ptr(), 1 if tiled else 0, _raw_stream(stream, x))
     if rc != 0:
         raise MoeFp4Error(rc, "moe_fp4_mxfp4_quantize")
     return codes, scales
@@ -120,19 +132,23 @@ def mxfp4_quantize(x, row_index=None, index_div: int = 1, offsets=None, tiled: b
 
 def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
     """The values (bf16 or fp32 [.., K]) of MXFP4 codes uint8 [.., K/2] with row-major scales uint8 [.., K/32]."""
-    _need(dtype in _TYPES, "dtype must be bf16 or fp32")
-    K = 2 * codes.shape[-1]
-    _need(K > 0 and K % 32 == 0, "K must be a multiple of 32")
-    rows = codes.numel() // (K // 2)
-    _bytes(codes, "codes", codes.numel())
+    ot = _TYPES.get(dtype)
+    if ot is None:
+        raise ValueError("dtype must be bf16 or fp32")
+    *lead, half = codes.shape
+    K = 2 * half
+    if K % 32 or K == 0:
+        raise ValueError("K must be a multiple of 32")
+    n = codes.numel()
+    rows = n // half
+    _bytes(codes, "codes", n)
     _bytes(scales, "scales", rows * (K // 32))
     if out is None:
-        out = torch.empty(*codes.shape[:-1], K, dtype=dtype, device=codes.device)
-    else:
-        _need(out.is_cuda and out.dtype == dtype and out.is_contiguous() and out.numel() == rows * K,
-              "out must be a contiguous GPU tensor of dtype with a value for each code")
-    rc = _lib().moe_fp4_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, K, _TYPES[dtype], out.data_ptr(),
-                                         _raw_stream(stream))
+        out = torch.empty((*lead, K), dtype=dtype, device=codes.device)
+    elif not out.is_cuda or out.dtype is not dtype or not out.is_contiguous() or out.numel() != 2 * n:
+        raise ValueError("out must be a contiguous GPU tensor of dtype with a value for each code")
+    rc = _lib().moe_fp4_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, K, ot, out.data_ptr(),
+                                         _raw_stream(stream, codes))
     if rc != 0:
         raise MoeFp4Error(rc, "moe_fp4_mxfp4_dequantize")
     return out
@@ -141,42 +157,61 @@ def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, out=None, stream=None)
 def mxfp4_tile_scales(scales, swiglu: bool = False, out=None, stream=None):
     """Row-major weight scales uint8 [E, N, K/32] or [N, K/32] in the layout of the products, uint8
     [E, ceil(N/128), ceil(K/128), 512]: once, when weights are loaded.  swiglu: for products with SwiGLU."""
-    _need(scales.dim() in (2, 3), "scales must be [E, N, K/32] or [N, K/32]")
+    if scales.dim() not in (2, 3):
+        raise ValueError("scales must be [E, N, K/32] or [N, K/32]")
     E = scales.shape[0] if scales.dim() == 3 else 1
     N, nb = scales.shape[-2:]
     _bytes(scales, "scales", E * N * nb)
     shape = (E, -(-N // 128), -(-nb // 4), 512)
     if out is None:
-        out = torch.empty(shape, dtype=torch.uint8, device=scales.device)
+        out = torch.empty(shape, dtype=_U8, device=scales.device)
     else:
         _bytes(out, "out", shape[0] * shape[1] * shape[2] * 512)
     rc = _lib().moe_fp4_mxfp4_tile_scales(scales.data_ptr(), E, N, 32 * nb, int(swiglu), out.data_ptr(),
-                                          _raw_stream(stream))
+                                          _raw_stream(stream, scales))
     if rc != 0:
         raise MoeFp4Error(rc, "moe_fp4_mxfp4_tile_scales")
     return out
 
 
-def _mm_dims(M, K, w, w_scale, offsets, swiglu, dtype):
-    _need(w.dim() in (2, 3) and w.shape[-1] * 2 == K, "w must be uint8 [E, N, K/2] or [N, K/2]")
-    E = w.shape[0] if w.dim() == 3 else 1
-    N = w.shape[-2]
-    _bytes(w, "w", w.numel())
-    _bytes(w_scale, "w_scale (tiled: mxfp4_tile_scales)", E * -(-N // 128) * -(-K // 128) * 512)
-    _need(dtype in _TYPES, "dtype must be bf16 or fp32")
-    _need(not swiglu or N % 2 == 0, "swiglu needs an even number of features")
-    if offsets is None:
-        _need(E == 1, "several matrices need offsets")
+@functools.lru_cache(maxsize=1024)
+def _mm_plan(M, N, K, E, swiglu, dtype):
+    """What a product's sizes alone give: its dims (kept alive beside their address), features of y, scale bytes of
+    both operands, workspace bytes of the linear form"""
+    yt = _TYPES.get(dtype)
+    if yt is None:
+        raise ValueError("dtype must be bf16 or fp32")
+    if swiglu and N % 2:
+        raise ValueError("swiglu needs an even number of features")
+    dims = MmDims(M, N, K, E, int(swiglu), yt)
+    kt = -(-K // 128)
+    return (ctypes.addressof(dims), N // 2 if swiglu else N, E * -(-N // 128) * kt * 512, (M // 128 + E) * kt * 512,
+            _lib().moe_fp4_mxfp4_linear_workspace_bytes(ctypes.byref(dims)), dims)
+
+
+def _plan_of(M, K, w, w_scale, offsets, swiglu, dtype):
+    shape = w.shape
+    if len(shape) == 3:
+        E, N, half = shape
+    elif len(shape) == 2:
+        E, (N, half) = 1, shape
     else:
-        _need(offsets.numel() == E + 1, "offsets must have E + 1 elements")
-    return MmDims(M, N, K, E, int(swiglu), _TYPES[dtype])
+        raise ValueError("w must be uint8 [E, N, K/2] or [N, K/2]")
+    if 2 * half != K:
+        raise ValueError(f"w must be uint8 [E, N, K/2] or [N, K/2] with K = {K}")
+    if (offsets.numel() != E + 1) if offsets is not None else E != 1:
+        raise ValueError("several matrices need offsets, of E + 1 elements")
+    plan = _mm_plan(M, N, K, E, swiglu, dtype)
+    _bytes(w, "w", 0)
+    _bytes(w_scale, "w_scale (tiled, by mxfp4_tile_scales)", plan[2])
+    return plan
 
 
-def _mm_out(out, M, n, dtype, device):
+def _result(out, M, n, dtype, device):
     if out is None:
-        return torch.empty(M, n, dtype=dtype, device=device)
-    _need(out.is_cuda and out.dtype == dtype and out.is_contiguous() and tuple(out.shape) == (M, n),
-          f"out must be a contiguous {dtype} GPU tensor [{M}, {n}]")
+        return torch.empty((M, n), dtype=dtype, device=device)
+    if not out.is_cuda or out.dtype is not dtype or not out.is_contiguous() or out.shape != (M, n):
+        raise ValueError(f"out must be a contiguous {dtype} GPU tensor [{M}, {n}]")
     return out
 
 
@@ -185,16 +220,16 @@ def mxfp4_matmul(a, a_scale, w, w_scale, offsets=None, swiglu: bool = False, dty
     """y = a w^T of MXFP4 matrices: a uint8 [M, K/2] with tiled scales (mxfp4_quantize), w uint8 [E, N, K/2] with
     tiled scales (mxfp4_tile_scales).  offsets (int32 [E + 1]): rows [off[e], off[e+1]) use w[e], and a_scale is in
     the grouped layout of the same offsets.  Returns [M, N], or with swiglu silu(first half) * second half [M, N/2]."""
-    _need(a.dim() == 2, "a must be uint8 [M, K/2]")
-    _indices(None, 1, offsets)
+    if a.dim() != 2:
+        raise ValueError("a must be uint8 [M, K/2]")
     M, K = a.shape[0], 2 * a.shape[1]
-    _bytes(a, "a", a.numel())
-    dims = _mm_dims(M, K, w, w_scale, offsets, swiglu, dtype)
-    _bytes(a_scale, "a_scale", (M // 128 + dims.E) * -(-K // 128) * 512)
-    out = _mm_out(out, M, dims.N // 2 if swiglu else dims.N, dtype, a.device)
-    rc = _lib().moe_fp4_mxfp4_matmul(ctypes.byref(dims), a.data_ptr(), a_scale.data_ptr(),
-                                     None if offsets is None else offsets.data_ptr(), w.data_ptr(),
-                                     w_scale.data_ptr(), out.data_ptr(), _raw_stream(stream))
+    off = _index_ptr(offsets, "offsets")
+    dims, n, _, a_bytes, _, _ = _plan_of(M, K, w, w_scale, offsets, swiglu, dtype)
+    _bytes(a, "a", 0)
+    _bytes(a_scale, "a_scale (tiled)", a_bytes)
+    out = _result(out, M, n, dtype, a.device)
+    rc = _lib().moe_fp4_mxfp4_matmul(dims, a.data_ptr(), a_scale.data_ptr(), off, w.data_ptr(), w_scale.data_ptr(),
+                                     out.data_ptr(), _raw_stream(stream, a))
     if rc != 0:
         raise MoeFp4Error(rc, "moe_fp4_mxfp4_matmul")
     return out
@@ -209,53 +244,45 @@ def mxfp4_linear(x, w, w_scale, offsets=None, row_index=None, index_div: int = 1
     """The product from unquantised rows x [R, K] (bf16 or fp32): mxfp4_quantize (with row_index / index_div, and
     offsets) and mxfp4_matmul in one call, the same bits."""
     xt = _type(x, "x")
-    stride = _rows2d(x, "x")
-    _indices(row_index, index_div, offsets)
-    R, K = x.shape
-    _need(K > 0 and K % 32 == 0, "K must be a multiple of 32")
+    R, K, stride = _rows(x, "x")
     M = R if row_index is None else row_index.numel()
-    dims = _mm_dims(M, K, w, w_scale, offsets, swiglu, dtype)
-    lib = _lib()
-    nbytes = lib.moe_fp4_mxfp4_linear_workspace_bytes(ctypes.byref(dims))
+    index, off = _index_ptr(row_index, "row_index"), _index_ptr(offsets, "offsets")
+    dims, n, _, _, nbytes, _ = _plan_of(M, K, w, w_scale, offsets, swiglu, dtype)
     if nbytes == 0:
         raise MoeFp4Error(-2, "moe_fp4_mxfp4_linear")
-    ws = _binding._workspace(nbytes, x.device, workspace)
-    out = _mm_out(out, M, dims.N // 2 if swiglu else dims.N, dtype, x.device)
-    rc = lib.moe_fp4_mxfp4_linear(ctypes.byref(dims), x.data_ptr(), xt, R, stride,
-                                  None if row_index is None else row_index.data_ptr(), index_div,
-                                  None if offsets is None else offsets.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
-                                  out.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(stream))
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=_U8, device=x.device)
+    else:
+        _bytes(workspace, "workspace", nbytes)
+    out = _result(out, M, n, dtype, x.device)
+    rc = _lib().moe_fp4_mxfp4_linear(dims, x.data_ptr(), xt, R, stride, index, index_div, off, w.data_ptr(),
+                                     w_scale.data_ptr(), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                     _raw_stream(stream, x))
     if rc != 0:
         raise MoeFp4Error(rc, "moe_fp4_mxfp4_linear")
     return out
 
 
-def _block_norm(a, stream):
-    rc = _lib().moe_fp4_block_norm(ctypes.byref(a), _raw_stream(stream))
-    if rc != 0:
-        raise MoeFp4Error(rc, "moe_fp4_block_norm")
-
-
-def _weight(a, name, w, d):
+def _weight(w, what, d):
+    """(pointer, type) of a weight [d], (0, 0) for none"""
     if w is None:
-        return
-    _need(w.is_cuda and w.is_contiguous() and tuple(w.shape) == (d,), f"{name} must be a contiguous GPU tensor [{d}]")
-    setattr(a, name + "_type", _type(w, name))
-    setattr(a, name, w.data_ptr())
+        return 0, 0
+    if not w.is_cuda or not w.is_contiguous() or w.shape != (d,):
+        raise ValueError(f"{what} must be a contiguous GPU tensor [{d}]")
+    return w.data_ptr(), _type(w, what)
 
 
 def rms_norm(x, weight=None, eps: float = 1e-6, out=None, stream=None):
     """The norm before a block: bf16 [T, d] = x rsqrt(mean(x^2) + eps) * weight.  x bf16 or fp32 [T, d] (rows may
     be strided), weight bf16 or fp32 [d]."""
-    a = BlockNormArgs()
-    a.residual_stride = _rows2d(x, "x")
-    T, d = x.shape
-    a.T, a.d, a.eps, a.scale = T, d, eps, 1.0
-    a.residual, a.residual_type = x.data_ptr(), _type(x, "x")
-    _weight(a, "next_weight", weight, d)
-    out = _mm_out(out, T, d, torch.bfloat16, x.device)
-    a.normed = out.data_ptr()
-    _block_norm(a, stream)
+    T, d, stride = _rows(x, "x")
+    wp, wt = _weight(weight, "weight", d)
+    out = _result(out, T, d, _BF16, x.device)
+    rc = _lib().moe_fp4_block_norm(
+        _BLOCK_NORM.pack(T, d, 0, 0, 0, _type(x, "x"), 0, 0, 0, 0, wt, stride, 0, 0, 0, 0, 1.0, eps, x.data_ptr(), 0, 0, 0,
+                         0, wp, 0, out.data_ptr()), _raw_stream(stream, x))
+    if rc != 0:
+        raise MoeFp4Error(rc, "moe_fp4_block_norm")
     return out
 
 
@@ -270,51 +297,53 @@ def block_residual(residual, y, y2=None, post_norm: bool = True, post_weight=Non
     residual, y, y2: bf16 or fp32 [T, d], rows may be strided.  gate: [T], [d] or [T, d] (T = d: give [T, 1],
     [1, d] or [T, d]).  Returns (out, normed): out of residual's type (out=residual adds in place), normed bf16,
     or None with next_norm=False."""
-    a = BlockNormArgs()
-    a.residual_stride = _rows2d(residual, "residual")
-    T, d = residual.shape
-    a.T, a.d, a.eps, a.scale, a.post_norm = T, d, eps, scale, int(post_norm)
-    a.residual, a.residual_type = residual.data_ptr(), _type(residual, "residual")
-    _need(tuple(y.shape) == (T, d), f"y must be [{T}, {d}]")
-    a.y, a.y_type, a.y_stride = y.data_ptr(), _type(y, "y"), _rows2d(y, "y")
+    T, d, r_stride = _rows(residual, "residual")
+    rt = _type(residual, "residual")
+    shape = residual.shape
+    if y.shape != shape:
+        raise ValueError(f"y must be [{T}, {d}]")
+    y_stride, yt = _rows(y, "y")[2], _type(y, "y")
+    y2p = y2t = y2_stride = gp = gt = g_shape = g_stride = 0
     if y2 is not None:
-        _need(tuple(y2.shape) == (T, d), f"y2 must be [{T}, {d}]")
-        a.y2, a.y2_type, a.y2_stride = y2.data_ptr(), _type(y2, "y2"), _rows2d(y2, "y2")
-    _weight(a, "post_weight", post_weight, d)
+        if y2.shape != shape:
+            raise ValueError(f"y2 must be [{T}, {d}]")
+        y2p, y2t, y2_stride = y2.data_ptr(), _type(y2, "y2"), _rows(y2, "y2")[2]
+    pp, pt = _weight(post_weight, "post_weight", d)
     if gate is not None:
-        _need(gate.is_cuda, "gate must be a GPU tensor")
-        shape = tuple(gate.shape)
-        _need(not (len(shape) == 1 and T == d), "gate is ambiguous for T = d: give [T, 1] or [1, d]")
-        if shape == (T, d) and not (T > 1 and d == 1):
-            a.gate_shape, a.gate_stride = 3, _rows2d(gate, "gate")
-        elif shape in ((T,), (T, 1)):
-            _need(gate.is_contiguous(), "gate must be contiguous")
-            a.gate_shape, a.gate_stride = 1, d
-        elif shape in ((d,), (1, d)):
-            _need(gate.is_contiguous(), "gate must be contiguous")
-            a.gate_shape, a.gate_stride = 2, d
+        g = gate.shape
+        if g == shape and not (T > 1 and d == 1):
+            g_shape, g_stride = 3, _rows(gate, "gate")[2]
         else:
-            raise ValueError(f"gate must be [T], [d] or [T, d], not {list(shape)}")
-        a.gate, a.gate_type, a.gate_sigmoid = gate.data_ptr(), _type(gate, "gate"), int(gate_sigmoid)
+            if len(g) == 1 and T == d:
+                raise ValueError("gate is ambiguous for T = d: give [T, 1] or [1, d]")
+            g_shape, g_stride = (1 if g == (T,) or g == (T, 1) else 2 if g == (d,) or g == (1, d) else 0), d
+            if g_shape == 0 or not gate.is_cuda or not gate.is_contiguous():
+                raise ValueError(f"gate must be a GPU tensor [T], [d] or [T, d], not {list(g)}")
+        gp, gt = gate.data_ptr(), _type(gate, "gate")
     if out is residual:
-        a.out_stride = a.residual_stride
+        o_stride = r_stride
     else:
-        out = _mm_out(out, T, d, residual.dtype, residual.device)
-        a.out_stride = d
-    a.out = out.data_ptr()
+        out = _result(out, T, d, residual.dtype, residual.device)
+        o_stride = d
+    npt = nwp = nwt = 0
     if next_norm:
-        _weight(a, "next_weight", next_weight, d)
-        normed = _mm_out(normed, T, d, torch.bfloat16, residual.device)
-        a.normed = normed.data_ptr()
-    else:
-        _need(next_weight is None and normed is None, "next_norm=False takes no next_weight and no normed")
-    _block_norm(a, stream)
+        nwp, nwt = _weight(next_weight, "next_weight", d)
+        normed = _result(normed, T, d, _BF16, residual.device)
+        npt = normed.data_ptr()
+    elif next_weight is not None or normed is not None:
+        raise ValueError("next_norm=False takes no next_weight and no normed")
+    rc = _lib().moe_fp4_block_norm(
+        _BLOCK_NORM.pack(T, d, 1 if post_norm else 0, g_shape, 1 if gate_sigmoid else 0, rt, yt, y2t, gt, pt, nwt,
+                         r_stride, y_stride, y2_stride, g_stride, o_stride, scale, eps, residual.data_ptr(),
+                         y.data_ptr(), y2p, gp, pp, nwp, out.data_ptr(), npt), _raw_stream(stream, residual))
+    if rc != 0:
+        raise MoeFp4Error(rc, "moe_fp4_block_norm")
     return out, normed
 
 
 def ops_check(stream=None) -> None:
     """Synchronise and raise if a kernel of an earlier operator call on this device reported an error (a row index
     out of range, or a pipeline wait that ran out); the error word is cleared."""
-    rc = _lib().moe_fp4_ops_check(_raw_stream(stream))
+    rc = _lib().moe_fp4_ops_check((stream or torch.cuda.current_stream()).cuda_stream)
     if rc != 0:
         raise MoeFp4Error(rc, "moe_fp4_ops_check")
