@@ -25,6 +25,7 @@ cudaError_t launch_mxfp4_quantize(const MxRows& R, uint8_t* codes, uint8_t* scal
 // the error words of the operators' kernels (one in each translation unit): read, or cleared
 cudaError_t ops_quant_error(int32_t* word, bool clear, cudaStream_t st);
 cudaError_t ops_mm_error(int32_t* word, bool clear, cudaStream_t st);
+cudaError_t ops_mm2_error(int32_t* word, bool clear, cudaStream_t st);
 
 #ifdef __CUDACC__
 

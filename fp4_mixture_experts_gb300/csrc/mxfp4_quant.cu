@@ -296,14 +296,17 @@ int moe_fp4_mxfp4_tile_scales(const uint8_t* scales, int32_t E, int32_t N, int32
 
 int moe_fp4_ops_check(void* cuda_stream) {
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  int32_t q = 0, m = 0;
-  if (ops_quant_error(&q, false, st) != cudaSuccess || ops_mm_error(&m, false, st) != cudaSuccess ||
-      cudaStreamSynchronize(st) != cudaSuccess)
-    return MOE_FP4_ERR_CUDA;
-  if ((q | m) == 0) return MOE_FP4_OK;
-  if (ops_quant_error(nullptr, true, st) != cudaSuccess || ops_mm_error(nullptr, true, st) != cudaSuccess ||
-      cudaStreamSynchronize(st) != cudaSuccess)
-    return MOE_FP4_ERR_CUDA;
+  cudaError_t (*const words[])(int32_t*, bool, cudaStream_t) = {ops_quant_error, ops_mm_error, ops_mm2_error};
+  int32_t bits = 0;
+  for (auto word : words) {
+    int32_t w = 0;
+    if (word(&w, false, st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess) return MOE_FP4_ERR_CUDA;
+    bits |= w;
+  }
+  if (bits == 0) return MOE_FP4_OK;
+  for (auto word : words)
+    if (word(nullptr, true, st) != cudaSuccess) return MOE_FP4_ERR_CUDA;
+  if (cudaStreamSynchronize(st) != cudaSuccess) return MOE_FP4_ERR_CUDA;
   return MOE_FP4_ERR_DEVICE;
 }
 
