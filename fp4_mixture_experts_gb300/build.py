@@ -1,7 +1,9 @@
 """Builds the CUDA library libmoe_fp4.so in the package directory (in-tree).
 
 Every .cu file under csrc/ is compiled for sm_103a in parallel and linked
-into one shared library with a plain C ABI (include/moe_fp4.h).
+into one shared library with a plain C ABI (include/moe_fp4.h).  The operators'
+Python binding (csrc/ops_binding.cpp, against PyTorch's headers) becomes
+_ops_native.so beside it.
 """
 from __future__ import annotations
 
@@ -16,6 +18,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_fp4.so")
+NATIVE = os.path.join(PKG, "_ops_native.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -38,16 +41,41 @@ def _compile(src: str, extra: list[str], bdir: str) -> str:
     return obj
 
 
+def build_binding(out: str = NATIVE) -> str:
+    """Compile the operators' Python binding for the running interpreter and its PyTorch."""
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = out + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           os.path.join(CSRC, "ops_binding.cpp"), "-o", tmp, "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(t, "include"), "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-L", os.path.join(t, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           "-Wl,-rpath," + os.path.join(t, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the operators' binding failed to build:\n{r.stderr}")
+    os.replace(tmp, out)
+    return out
+
+
 def build(verbose: bool = False, extra_flags: list[str] | None = None, out: str | None = None,
           build_dir: str | None = None) -> str:
-    """Compile csrc/*.cu and link libmoe_fp4.so (or `out`); returns the library path."""
+    """Compile csrc/*.cu and link libmoe_fp4.so (or `out`); returns the library path.  The operators' binding is
+    built with the package's own library."""
     lib_out = out or LIB
     bdir = build_dir or BUILD
     os.makedirs(bdir, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     extra = list(extra_flags or [])
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
+        binding = ex.submit(build_binding) if out is None else None
         objs = list(ex.map(lambda s: _compile(s, extra, bdir), srcs))
+    if binding is not None:
+        binding.result()
     tmp = lib_out + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
