@@ -26,6 +26,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "mxfp4_mm.cuh"
 
@@ -110,33 +111,53 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     Item t{};
     Ring<kStages> ring;
     int g = 0;
-    bool ok = true;
+    bool ok = true, waited = false;
     for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
       item_at<NT>(t, it, P.mblocks, off, pre);
       const int sf_rows = t.n > 128 ? 2 : 1;
       const uint8_t* ws = P.w_scales + ((size_t)t.g * P.mblocks + t.mb) * P.kt * kSfTile;
       const uint8_t* as = P.a_scales + ((size_t)((uniform(off[t.g]) >> 7) + t.g + (t.local >> 7))) * P.kt * kSfTile;
       const int wrow = t.mb * (SW ? 64 : 128);
-      for (int ks = 0; ks < nks; ++ks, ++g, ring.next()) {
-        uint64_t* bar = &full[ring.s];
+      auto load_w = [&](int ks, int s) {  // and announce the stage's bytes
+        if (elect_one()) {
+          uint8_t* st = smem + s * C::kStage;
+          const uint32_t sf_bytes = min(2, P.kt - 2 * ks) * kSfTile;
+          mbar_expect_tx(&full[s], C::kATile + C::kBTile + sf_bytes * (1 + sf_rows));
+          tma_load_4d(st, &map_w, ks * 128, 0, wrow, t.g, &full[s]);
+          bulk_load(st + C::kATile + C::kBTile, ws + ks * 2 * kSfTile, sf_bytes, &full[s]);
+        }
+        __syncwarp();
+      };
+      auto load_a = [&](int ks, int s) {
+        if (elect_one()) {
+          uint8_t* st = smem + s * C::kStage;
+          const uint32_t sf_bytes = min(2, P.kt - 2 * ks) * kSfTile;
+          tma_load_2d(st + C::kATile, &map_a, ks * 128, t.row0, &full[s]);
+          uint8_t* sf = st + C::kATile + C::kBTile;
+          for (int j = 0; j < sf_rows; ++j)
+            bulk_load(sf + (1 + j) * 2 * kSfTile, as + (j * P.kt + ks * 2) * kSfTile, sf_bytes, &full[s]);
+        }
+        __syncwarp();
+      };
+      int ks = 0;
+      if (!waited) {
+        // the first stages' weights do not depend on the kernel that quantises the rows
+        const int early = min(kStages, nks);
+        for (int i = 0; i < early; ++i) load_w(i, i);
+        griddep_wait();
+        waited = true;
+        for (; ks < early; ++ks, ++g, ring.next()) load_a(ks, ks);
+      }
+      for (; ks < nks; ++ks, ++g, ring.next()) {
         if (!warp_wait(&empty[ring.s], ring.phase ^ 1, abort_flag, P)) {
           ok = false;
           break;
         }
-        if (elect_one()) {
-          uint8_t* st = smem + ring.s * C::kStage;
-          const uint32_t sf_bytes = min(2, P.kt - 2 * ks) * kSfTile;
-          mbar_expect_tx(bar, C::kATile + C::kBTile + sf_bytes * (1 + sf_rows));
-          tma_load_4d(st, &map_w, ks * 128, 0, wrow, t.g, bar);
-          tma_load_2d(st + C::kATile, &map_a, ks * 128, t.row0, bar);
-          uint8_t* sf = st + C::kATile + C::kBTile;
-          bulk_load(sf, ws + ks * 2 * kSfTile, sf_bytes, bar);
-          for (int j = 0; j < sf_rows; ++j)
-            bulk_load(sf + (1 + j) * 2 * kSfTile, as + (j * P.kt + ks * 2) * kSfTile, sf_bytes, bar);
-        }
-        __syncwarp();
+        load_w(ks, ring.s);
+        load_a(ks, ring.s);
       }
     }
+    if (!waited) griddep_wait();  // no CTA ends before the kernel ahead: what follows this launch may rely on both
     // every issued copy has landed before shared memory is given back
     __syncwarp();
     for (int q = g > kStages ? g - kStages : 0; q < g; ++q)
@@ -201,13 +222,13 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     for (int it = blockIdx.x; it < items; it += gridDim.x, ++li) {
       item_at<NT>(t, it, P.mblocks, off, pre);
       const int b = li % C::kAccs, use = li / C::kAccs;
-      const bool ok = warp_wait(&acc_full[b], use & 1, abort_flag, P);
-      if (!all_of_epilogue(ok)) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const int f0 = t.mb * E::kFeatures, nf = min(E::kFeatures, P.n_out - f0);
-      e.item(P.y, tmem + b * NT, t.row0, t.n, f0, nf, 0, [&](bool, bool last) {
-        if (last && lane == 0) mbar_arrive(&acc_empty[b]);
-      });
+      const bool ok = warp_wait(&acc_full[b], use & 1, abort_flag, P);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      if (!e.item(P.y, tmem + b * NT, t.row0, t.n, f0, nf, 0, ok, [&](bool, bool last) {
+            if (last && lane == 0) mbar_arrive(&acc_empty[b]);
+          }))
+        break;
     }
   }
   __syncwarp();
@@ -238,6 +259,7 @@ cudaError_t launch_as(const CUtensorMap& map_w, const CUtensorMap& map_a, const 
                       cudaStream_t st) {
   const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(mm_kernel<NT, F32, SW>), Cfg<NT>::kSmem);
   if (e != cudaSuccess) return e;
+  if (P.early) return launch_early(mm_kernel<NT, F32, SW>, dim3(grid), dim3(kThreads), Cfg<NT>::kSmem, st, map_w, map_a, P);
   mm_kernel<NT, F32, SW><<<grid, kThreads, Cfg<NT>::kSmem, st>>>(map_w, map_a, P);
   return cudaGetLastError();
 }
@@ -288,8 +310,7 @@ int check_mm_pointers(const moe_fp4_mm_dims& d, const void* w, const void* ws, c
   return MOE_FP4_OK;
 }
 
-cudaError_t launch_mm(const moe_fp4_mm_dims& d, const uint8_t* a, const uint8_t* as, const int32_t* offsets,
-                      const uint8_t* w, const uint8_t* ws, void* y, cudaStream_t st) {
+MmParams params(const moe_fp4_mm_dims& d, const uint8_t* as, const int32_t* offsets, const uint8_t* ws, void* y) {
   MmParams P{};
   P.a_scales = as;
   P.w_scales = ws;
@@ -304,11 +325,58 @@ cudaError_t launch_mm(const moe_fp4_mm_dims& d, const uint8_t* a, const uint8_t*
   P.vec = ((size_t)P.n_out * (P.f32 ? 4 : 2)) % 16 == 0 && ((uintptr_t)y & 15) == 0;
   P.split = 1;
   P.wait_ns = wait_limit_ns();
-  // token rows per tile by the rows that a group has on average
-  const int64_t mean = (d.M + d.E - 1) / d.E;
-  if (mean <= 64) return launch_nt<64>(d, a, w, P, st);
-  if (mean <= 128) return launch_nt<128>(d, a, w, P, st);
-  return launch_pairs(d, a, w, P, st);
+  return P;
+}
+
+// few rows of one matrix have a kernel of their own, which quantises them itself
+bool few_rows(const moe_fp4_mm_dims& d, const int32_t* offsets) { return !offsets && d.M <= kFewRows; }
+
+cudaError_t launch_few(const moe_fp4_mm_dims& d, const MmParams& P, const MxRows* x, const uint8_t* codes,
+                       const uint8_t* w, cudaStream_t st) {
+  CUtensorMap map_w;
+  if (!make_w_map(d, w, &map_w)) return cudaErrorInvalidValue;
+  return launch_mm_few(map_w, P, x, codes, st);
+}
+
+// The kernel and tile of a product with more than a few rows: the one whose
+// time, rounds over the SMs x (stages x time of a stage + fixed time of an
+// item), is least.  Measured in us, over N = 1024 .. 16384, K = 1024 and 4096,
+// M = 16 .. 2048 and ragged groups of 1 .. 1024 rows: a stage takes 0.23, 0.24
+// and 0.29, an item 0.9, 1.2 and 3.2 beside them, with tiles of 128 weight rows
+// x 64 and 128 token rows on an SM and of 256 x 256 on a pair, whose launch
+// costs 1 more.  (M = 256, N = K = 4096: 9.4, 10.1 and 13.6 us; M = 2048: 36,
+// 26 and 24 us.)  The tiles of a group are estimated from the mean of the
+// groups' rows, half a standard deviation of a uniform routing taken off.
+int choose_tile(const moe_fp4_mm_dims& d) {
+  const int nks = (d.K + kStageK - 1) / kStageK, sms = num_sms();
+  const double mean = (double)d.M / d.E;
+  double best = 0;
+  int tile = 0;
+  const struct {
+    int rows, wrows, sms;
+    double stage, item, launch;
+  } kernels[] = {{64, 128, 1, 0.23, 0.9, 0}, {128, 128, 1, 0.24, 1.2, 0}, {256, 256, 2, 0.29, 3.2, 1}};
+  for (const auto& k : kernels) {
+    const double rows = d.E == 1 ? mean : std::max(mean - 0.5 * std::sqrt(mean), 1.0);
+    const double tiles = std::min(std::ceil(rows / k.rows) * d.E, (double)d.M);
+    const double items = tiles * ((d.N + k.wrows - 1) / k.wrows);
+    const double t = k.launch + std::ceil(items * k.sms / sms) * (nks * k.stage + k.item);
+    if (tile == 0 || t < best) best = t, tile = k.rows;
+  }
+  return tile;
+}
+
+// early: the launch may start before the kernel ahead of it, which writes a and as, has ended
+cudaError_t launch_mm(const moe_fp4_mm_dims& d, const uint8_t* a, const uint8_t* as, const int32_t* offsets,
+                      const uint8_t* w, const uint8_t* ws, void* y, bool early, cudaStream_t st) {
+  MmParams P = params(d, as, offsets, ws, y);
+  P.early = early;
+  if (few_rows(d, offsets)) return launch_few(d, P, nullptr, a, w, st);
+  switch (choose_tile(d)) {
+    case 64: return launch_nt<64>(d, a, w, P, st);
+    case 128: return launch_nt<128>(d, a, w, P, st);
+    default: return launch_pairs(d, a, w, P, st);
+  }
 }
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -339,7 +407,7 @@ int moe_fp4_mxfp4_matmul(const moe_fp4_mm_dims* dims, const uint8_t* a, const ui
   rc = check_mm_pointers(d, w, w_scales, y, offsets);
   if (rc != MOE_FP4_OK) return rc;
   if (!a || !a_scales || ((uintptr_t)a & 15) || ((uintptr_t)a_scales & 15)) return MOE_FP4_ERR_INVALID_ARG;
-  return launch_mm(d, a, a_scales, offsets, w, w_scales, y, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
+  return launch_mm(d, a, a_scales, offsets, w, w_scales, y, false, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
              ? MOE_FP4_OK
              : MOE_FP4_ERR_CUDA;
 }
@@ -366,10 +434,13 @@ int moe_fp4_mxfp4_linear(const moe_fp4_mm_dims* dims, const void* x, int x_type,
   if (!workspace || ((uintptr_t)workspace & 255)) return MOE_FP4_ERR_INVALID_ARG;
   if (workspace_bytes < moe_fp4_mxfp4_linear_workspace_bytes(dims)) return MOE_FP4_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (few_rows(d, offsets))
+    return launch_few(d, params(d, nullptr, nullptr, w_scales, y), &R, nullptr, w, st) == cudaSuccess ? MOE_FP4_OK
+                                                                                                     : MOE_FP4_ERR_CUDA;
   uint8_t* codes = static_cast<uint8_t*>(workspace);
   uint8_t* scales = codes + align256((size_t)d.M * (d.K / 2));
   if (launch_mxfp4_quantize(R, codes, scales, true, st) != cudaSuccess) return MOE_FP4_ERR_CUDA;
-  return launch_mm(d, codes, scales, offsets, w, w_scales, y, st) == cudaSuccess ? MOE_FP4_OK : MOE_FP4_ERR_CUDA;
+  return launch_mm(d, codes, scales, offsets, w, w_scales, y, true, st) == cudaSuccess ? MOE_FP4_OK : MOE_FP4_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -32,6 +32,7 @@ struct MmParams {
   int f32, swiglu;
   int vec;                   // rows of y start on 16 bytes
   int split;                 // CTAs of a cluster that share an item's K (1: none)
+  int early;                 // launched before the kernel that writes the rows has ended
   uint64_t wait_ns;
 };
 
@@ -115,6 +116,20 @@ __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t lo) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
   else
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+// this thread's TMEM lane, 32 columns
+__device__ __forceinline__ void tmem_ld32(uint32_t ta, uint32_t (&a)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
+        "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]),
+        "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]), "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]),
+        "=r"(a[24]), "=r"(a[25]), "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31])
+      : "r"(ta)
+      : "memory");
 }
 
 // four 8 x 8 matrices of 16-bit elements, transposed: lane l gives the address
@@ -346,14 +361,33 @@ struct Epilogue {
 #pragma unroll
       for (int k = 0; k < kTokens / kRowStep; ++k)
         if (in && r + k * kRowStep < rows) *reinterpret_cast<uint4*>(dst + k * kRowStep * ldy) = v[k];
+    } else if (F32) {
+      write_elements(reinterpret_cast<const float*>(b), reinterpret_cast<float*>(y), rows, nf);
     } else {
-      for (int i = q; i < rows; i += 4)
-        for (int f = lane; f < nf; f += 32) {
-          if (F32)
-            reinterpret_cast<float*>(y + i * ldy)[f] = reinterpret_cast<const float*>(b + i * kPitch)[f];
-          else
-            reinterpret_cast<uint16_t*>(y + i * ldy)[f] = reinterpret_cast<const uint16_t*>(b + i * kPitch)[f];
-        }
+      write_elements(reinterpret_cast<const uint16_t*>(b), reinterpret_cast<uint16_t*>(y), rows, nf);
+    }
+  }
+
+  // rows by warps, a row's features by lanes
+  template <typename T>
+  __device__ __forceinline__ void write_elements(const T* b, T* y, int rows, int nf) {
+    constexpr int kR = 4;  // rows in flight
+#pragma unroll
+    for (int i0 = 0; i0 < kTokens; i0 += 4 * kR) {
+      T v[kR][kFeatures / 32];
+#pragma unroll
+      for (int k = 0; k < kR; ++k)
+#pragma unroll
+        for (int u = 0; u < kFeatures / 32; ++u) v[k][u] = b[(i0 + 4 * k + q) * (kPitch / kEs) + 32 * u + lane];
+#pragma unroll
+      for (int k = 0; k < kR; ++k) {
+        const int i = i0 + 4 * k + q;
+        T* row = y + (size_t)i * n_out + lane;
+        if (i < rows)
+#pragma unroll
+          for (int u = 0; u < kFeatures / 32; ++u)
+            if (32 * u + lane < nf) row[32 * u] = v[k][u];
+      }
     }
   }
 
@@ -361,8 +395,10 @@ struct Epilogue {
   // (nf of them in y).  Chunks are taken from `first` on, cyclically.
   // after_reads(last): this group has read its chunks of the first round
   // (chunks first .. first + 127 / kTokens of the item), or, last, all of them.
+  // False, with nothing written, if some epilogue warp's wait for the
+  // accumulator ran out (not ok).
   template <typename F>
-  __device__ __forceinline__ void item(void* y, uint32_t taddr, int row0, int n, int f0, int nf, int first,
+  __device__ __forceinline__ bool item(void* y, uint32_t taddr, int row0, int n, int f0, int nf, int first, bool ok,
                                        F&& after_reads) {
     const int chunks = (n + kTokens - 1) / kTokens;
     uint8_t* const y0 = static_cast<uint8_t*>(y) + ((size_t)row0 * n_out + f0) * kEs;
@@ -379,6 +415,7 @@ struct Epilogue {
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       after_reads(i == h, i + 2 * kLoads >= chunks);
+      if (i == h && !all_of_epilogue(ok)) return false;
 #pragma unroll
       for (int k = 0; k < kLoads; ++k) {
         if (i + 2 * k >= chunks) break;
@@ -392,11 +429,17 @@ struct Epilogue {
       }
       i += 2 * kLoads;
     } while (i < chunks);
+    return true;
   }
 };
 
 }  // namespace mm
 
+// the kernel for few rows of one matrix, M <= kFewRows (mxfp4_mm1.cu): rows x
+// to quantise, or (x null) their codes with P.a_scales
+constexpr int kFewRows = 16;
+cudaError_t launch_mm_few(const CUtensorMap& map_w, const mm::MmParams& P, const MxRows* x, const uint8_t* codes,
+                          cudaStream_t st);
 // the pair kernel (mxfp4_mm2.cu); the boxes of map_a have 32 rows, those of
 // map_a128 128; map_ws and map_as: scale tiles as rows of 512 bytes, boxes of 2
 cudaError_t launch_mm_pairs(const CUtensorMap& map_w, const CUtensorMap& map_a, const CUtensorMap& map_a128,

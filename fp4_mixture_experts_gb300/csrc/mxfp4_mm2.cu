@@ -21,13 +21,13 @@
 // weight rows, its half of the token rows), warp 2 that of the scales (issuing
 // a copy takes ~80 cycles: one warp for both is slower than the MMAs), warp 1 of
 // the leader (rank 0) the MMA issuer, warps 4..11 the epilogue of the CTA's own
-// accumulator lanes.  The follower's copies complete on a barrier of the
-// leader (`peer_full`; its producers announce their bytes there), so that the
-// issuer waits for both halves itself.  (A warp of the follower that waits and
+// accumulator lanes.  The follower's copies complete on the leader's barrier
+// (its producers announce their bytes there), so that the issuer waits for
+// both halves at once.  (A warp of the follower that waits and
 // arrives on the leader's barrier instead needs ~1,300 cycles a stage for the
 // cluster-wide release, more than twice the stage's MMAs: measured.)
 //
-// All waits are bounded; the follower leaves the number of its issued stages
+// All waits are bounded; the producers leave the number of their issued stages
 // in the leader, which waits for them and for the MMAs before either CTA gives
 // memory back.
 #include <cuda.h>
@@ -150,16 +150,15 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* epi = smem + kStages * kStage;
   uint8_t* tail = epi + kEpiBytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(tail);    // [stage] leader: its own bytes landed
-  uint64_t* peer_full = full + kStages;                  // [stage] leader: the follower's bytes landed
-  uint64_t* empty = peer_full + kStages;                 // [stage] both: the stage's MMAs completed
+  uint64_t* full = reinterpret_cast<uint64_t*>(tail);    // [stage] leader: both CTAs' bytes landed
+  uint64_t* empty = full + kStages;                      // [stage] both: the stage's MMAs completed
   uint64_t* acc_full = empty + kStages;                  // [2] both
   uint64_t* acc_empty = acc_full + 2;                    // [2] leader: both epilogues read all of the accumulator
   uint64_t* part_free = acc_empty + 2;                   // [2] leader: ... its columns that the other one shares
   uint64_t* mma_done = part_free + 2;                    // both
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* peer_issued = abort_flag + 1;            // [2] leader: stages issued by the follower's producers
+  volatile int* issued = abort_flag + 1;                 // [4] leader: stages issued by each producer
   int* off = reinterpret_cast<int*>(tail + 512);
   int* pre = off + kMaxGroups + 1;
   const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -167,8 +166,7 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 2);  // one expect_tx of each producer
-      mbar_init(&peer_full[s], 2);
+      mbar_init(&full[s], 4);  // one expect_tx of each producer, of both CTAs
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -202,7 +200,7 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
     Ring<kStages> ring;
     int g = 0;
     bool ok = true;
-    uint64_t* const bars = rank == 0 ? full : peer_full;
+    griddep_wait();  // the kernel ahead writes the rows' codes and scales
     for (int it = first; it < items && ok; it += step) {
       item_at<kNT>(t, it, mblocks2, off, pre);
       const int mb = 2 * t.mb + rank;           // may be one past the last block: its rows read as 0,
@@ -220,7 +218,7 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
           break;
         }
         uint8_t* st = smem + ring.s * kStage;
-        const uint32_t bar = in_leader(&bars[ring.s]);
+        const uint32_t bar = in_leader(&full[ring.s]);
         if (warp == 0) {
           if (elect_one()) {
             expect_tx_cl(bar, kATile + b_bytes);
@@ -242,14 +240,10 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
         __syncwarp();
       }
     }
-    if (rank == 0) {
-      for (int q = g > kStages ? g - kStages : 0; q < g; ++q)
-        mbar_wait_drain(&full[q % kStages], (q / kStages) & 1, P.err, kErrWaitTimeout, P.wait_ns);
-    } else if (lane == 0) {
-      asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(in_leader(const_cast<int*>(&peer_issued[warp == 0 ? 0 : 1]))),
+    if (lane == 0)
+      asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(in_leader(const_cast<int*>(&issued[rank * 2 + (warp >> 1)]))),
                    "r"(g)
                    : "memory");
-    }
   } else if (warp == 1) {
     // the follower's warp goes on to the cluster barrier below, where the
     // leader arrives once its MMAs, which read both CTAs' memory, are done
@@ -263,17 +257,16 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
         item_at<kNT>(t, it, mblocks2, off, pre);
         const int b = li & 1, use = li >> 1;
         const int n_mma = (t.n + 31) & ~31;
-        if (!warp_wait_cl(&acc_empty[b], (use & 1) ^ 1, abort_flag, P)) break;
         // the other accumulator's columns that this one shares, where its item has values in them
-        const bool shared = b ? prev_n > (int)kAcc1 : n_mma > (int)kAcc1;
-        if (li > 0 && shared && !warp_wait_cl(&part_free[b ^ 1], ((li - 1) >> 1) & 1, abort_flag, P)) break;
+        const bool shared = li > 0 && (b ? prev_n > (int)kAcc1 : n_mma > (int)kAcc1);
         prev_n = n_mma;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (!warp_wait_cl(&acc_empty[b], (use & 1) ^ 1, abort_flag, P) ||
+            (shared && !warp_wait_cl(&part_free[b ^ 1], ((li - 1) >> 1) & 1, abort_flag, P)))
+          break;
         const uint32_t d_tmem = tmem + b * kAcc1;
         const uint32_t id0 = idesc_mxf4(2 * kBM, n_mma, 0), id1 = idesc_mxf4(2 * kBM, n_mma, 1);
         for (int ks = 0; ks < nks; ++ks, ++g, ring.next()) {
-          if (!warp_wait(&full[ring.s], ring.phase, abort_flag, P) ||
-              !warp_wait_cl(&peer_full[ring.s], ring.phase, abort_flag, P)) {
+          if (!warp_wait(&full[ring.s], ring.phase, abort_flag, P)) {
             ok = false;
             break;
           }
@@ -323,18 +316,19 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
     for (int it = first; it < items; it += step, ++li) {
       item_at<kNT>(t, it, mblocks2, off, pre);
       const int b = li & 1, use = li >> 1;
-      const bool ok = warp_wait(&acc_full[b], use & 1, abort_flag, P);
-      if (!all_of_epilogue(ok)) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const int f0 = (2 * t.mb + rank) * E::kFeatures, nf = max(0, min(E::kFeatures, P.n_out - f0));
+      const bool ok = warp_wait(&acc_full[b], use & 1, abort_flag, P);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       // the columns shared with the other accumulator are read in the first round: accumulator 0's from kAcc1 on,
       // so its chunks are taken from there; accumulator 1's first 256 - kAcc1
       const int chunks = (t.n + E::kTokens - 1) / E::kTokens, from = kAcc1 / E::kTokens;
-      e.item(P.y, tmem + b * kAcc1, t.row0, t.n, f0, nf, b == 0 && chunks > from ? from : 0, [&](bool round0, bool last) {
-        if (lane != 0) return;
-        if (round0) arrive_leader(&part_free[b]);
-        if (last) arrive_leader(&acc_empty[b]);
-      });
+      const int start = b == 0 && chunks > from ? from : 0;
+      if (!e.item(P.y, tmem + b * kAcc1, t.row0, t.n, f0, nf, start, ok, [&](bool round0, bool last) {
+            if (lane != 0) return;
+            if (round0) arrive_leader(&part_free[b]);
+            if (last) arrive_leader(&acc_empty[b]);
+          }))
+        break;
     }
   }
   __syncwarp();
@@ -342,10 +336,11 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
   __syncthreads();
   cluster_sync();  // every role has ended, in both CTAs
   if (rank == 0 && warp == 0) {
-    // the follower's copies: all have landed if every item was done
-    const int g = max(peer_issued[0], peer_issued[1]);
+    // all copies of both CTAs have landed, if every item was done; if a wait ran out, what was issued is given
+    // the time of a bounded wait
+    const int g = max(max(issued[0], issued[1]), max(issued[2], issued[3]));
     for (int q = g > kStages ? g - kStages : 0; q < g; ++q)
-      mbar_wait_drain(&peer_full[q % kStages], (q / kStages) & 1, P.err, kErrWaitTimeout, P.wait_ns);
+      mbar_wait_drain(&full[q % kStages], (q / kStages) & 1, P.err, kErrWaitTimeout, P.wait_ns);
   }
   cluster_sync();  // no CTA leaves while its peer may still reach into it
   if (warp == 1) {
@@ -364,6 +359,9 @@ cudaError_t launch_as(const CUtensorMap& map_w, const CUtensorMap& map_a, const 
                       cudaStream_t st) {
   const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(mm2_kernel<F32, SW>), kSmem2);
   if (e != cudaSuccess) return e;
+  if (P.early)
+    return launch_early(mm2_kernel<F32, SW>, dim3(2 * pairs), dim3(kThreads), kSmem2, st, map_w, map_a, map_a128, map_ws,
+                        map_as, P);
   mm2_kernel<F32, SW><<<2 * pairs, kThreads, kSmem2, st>>>(map_w, map_a, map_a128, map_ws, map_as, P);
   return cudaGetLastError();
 }

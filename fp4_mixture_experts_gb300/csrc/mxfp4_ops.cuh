@@ -25,9 +25,70 @@ cudaError_t launch_mxfp4_quantize(const MxRows& R, uint8_t* codes, uint8_t* scal
 // the error words of the operators' kernels (one in each translation unit): read, or cleared
 cudaError_t ops_quant_error(int32_t* word, bool clear, cudaStream_t st);
 cudaError_t ops_mm_error(int32_t* word, bool clear, cudaStream_t st);
+cudaError_t ops_mm1_error(int32_t* word, bool clear, cudaStream_t st);
 cudaError_t ops_mm2_error(int32_t* word, bool clear, cudaStream_t st);
 
 #ifdef __CUDACC__
+
+// eight fp32 values -> eight E2M1 codes, element 0 in the low nibble
+__device__ __forceinline__ uint32_t e2m1x8(const float* v) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+// 16 consecutive elements as they are: 16 words of fp32, or 8 words of bf16
+// pairs (VEC: they start on 16 bytes)
+template <bool F32, bool VEC>
+__device__ __forceinline__ void load16_raw(const void* x, int64_t at, uint32_t (&w)[16]) {
+  if (VEC) {
+    const uint4* p = F32 ? reinterpret_cast<const uint4*>(static_cast<const float*>(x) + at)
+                         : reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
+#pragma unroll
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) {
+      const uint4 q = __ldg(p + i);
+      w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+    }
+  } else if (F32) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = __ldg(static_cast<const uint32_t*>(x) + at + i);
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(x) + at;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = (uint32_t)__ldg(p + 2 * i) | ((uint32_t)__ldg(p + 2 * i + 1) << 16);
+  }
+}
+
+template <bool F32>
+__device__ __forceinline__ void unpack16(const uint32_t (&w)[16], float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    v[i] = __uint_as_float(F32 ? w[i] : (i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+}
+
+// The codes of half a block, 16 elements, by a pair of lanes (l, l ^ 1) that
+// hold a block together (whole warp; every lane takes part), and the block's
+// scale byte; v is used up.
+__device__ __forceinline__ uint2 quantize16(float (&v)[16], uint32_t& scale) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+  const uint32_t ef = amax >> 23;
+  scale = ef == 255u ? 255u : (ef > 2u ? ef - 2u : 0u);
+  if (scale == 255u) return make_uint2(0x77777777u, 0x77777777u);
+  const float inv = __uint_as_float((254u - scale) << 23);  // 2^(127 - scale), normal for scale in [0, 253]
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] *= inv;
+  return make_uint2(e2m1x8(v), e2m1x8(v + 8));
+}
 
 // The group that holds row r: the last e with off[e] <= r, if r < off[e + 1];
 // -1 if none does.  Offsets are taken as they are; a row is given a group only

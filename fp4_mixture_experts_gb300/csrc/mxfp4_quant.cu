@@ -16,22 +16,8 @@ namespace {
 
 __device__ int32_t g_quant_err[4];
 
-constexpr int kPer = 16;       // elements per thread
+constexpr int kPer = 16;  // elements per thread
 constexpr int kThreads = 256;
-
-// eight fp32 values -> eight E2M1 codes, element 0 in the low nibble
-__device__ __forceinline__ uint32_t e2m1x8(const float* v) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
-      "mov.b32 %0, {b0, b1, b2, b3};\n}"
-      : "=r"(r)
-      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
-  return r;
-}
 
 struct QuantParams {
   const void* x;
@@ -44,43 +30,9 @@ struct QuantParams {
   int K, div, groups;
 };
 
-// 16 consecutive elements as fp32
-template <bool F32, bool VEC>
-__device__ __forceinline__ void load16(const void* x, int64_t at, float (&v)[kPer]) {
-  if (F32) {
-    const float* p = static_cast<const float*>(x) + at;
-    if (VEC) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(p) + i);
-        v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = __ldg(p + i);
-    }
-  } else {
-    const uint16_t* p = static_cast<const uint16_t*>(x) + at;
-    if (VEC) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-          v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = bf16_to_f32(__ldg(p + i));
-    }
-  }
-}
-
 template <bool F32, bool VEC, bool TILED>
 __global__ void __launch_bounds__(kThreads) mxfp4_quantize_kernel(const QuantParams P) {
+  griddep_launch_dependents();  // a product that waits for these rows may be set up meanwhile
   const int per_row = P.K / kPer, nb = P.K / 32, kt = (P.K + 127) / 128;
   const int64_t total = P.rows * per_row;
   // whole warps leave the loop together (the shuffle below needs both lanes of a block)
@@ -90,35 +42,24 @@ __global__ void __launch_bounds__(kThreads) mxfp4_quantize_kernel(const QuantPar
     const bool in = i < total;
     const int64_t r = in ? i / per_row : 0;
     const int c = in ? (int)(i - r * per_row) : 0;
-    float v[kPer];
+    uint32_t w[kPer];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) v[j] = 0.f;
+    for (int j = 0; j < kPer; ++j) w[j] = 0;
     int64_t src = r;
     if (P.row_index) {
       src = P.row_index[r];
       src = src < 0 ? -1 : src / P.div;
     }
     if (src >= 0 && src < P.x_rows) {
-      if (in) load16<F32, VEC>(P.x, src * P.x_stride + (int64_t)c * kPer, v);
+      if (in) load16_raw<F32, VEC>(P.x, src * P.x_stride + (int64_t)c * kPer, w);
     } else if (c == 0) {
       atomicOr(&g_quant_err[0], kErrBadExpertId);
     }
-    uint32_t amax = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+    float v[kPer];
+    unpack16<F32>(w, v);
+    uint32_t sb;
+    const uint2 q = quantize16(v, sb);
     if (!in) continue;
-    const uint32_t ef = amax >> 23;
-    const uint32_t sb = ef == 255u ? 255u : (ef > 2u ? ef - 2u : 0u);
-    uint2 q;
-    if (sb == 255u) {
-      q = make_uint2(0x77777777u, 0x77777777u);
-    } else {
-      const float inv = __uint_as_float((254u - sb) << 23);  // 2^(127 - sb), normal for sb in [0, 253]
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) v[j] *= inv;
-      q = make_uint2(e2m1x8(v), e2m1x8(v + 8));
-    }
     *reinterpret_cast<uint2*>(P.codes + r * (P.K / 2) + (int64_t)c * (kPer / 2)) = q;
     if (c & 1) continue;
     const int b = c >> 1;
@@ -296,7 +237,8 @@ int moe_fp4_mxfp4_tile_scales(const uint8_t* scales, int32_t E, int32_t N, int32
 
 int moe_fp4_ops_check(void* cuda_stream) {
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  cudaError_t (*const words[])(int32_t*, bool, cudaStream_t) = {ops_quant_error, ops_mm_error, ops_mm2_error};
+  cudaError_t (*const words[])(int32_t*, bool, cudaStream_t) = {ops_quant_error, ops_mm_error, ops_mm1_error,
+                                                              ops_mm2_error};
   int32_t bits = 0;
   for (auto word : words) {
     int32_t w = 0;
