@@ -49,7 +49,7 @@ struct Cfg {
   static constexpr int kSfCols = 2 * 4 * (1 + kSfB);         // tensor-memory columns of a stage's scales
   static constexpr int kAccs = NT <= 128 ? 2 : 1;            // accumulators (double buffered where they fit)
   static constexpr int kGroupBytes = 2 * (kMaxGroups + 1) * 4;
-  static constexpr int kFixed = 1024 + 512 + kGroupBytes + kEpiBytes + 16;
+  static constexpr int kFixed = 1024 + 512 + kGroupBytes;
   static constexpr int kByMem = (kSmemMax - kFixed) / kStage;
   static constexpr int kByTmem = ((int)kTmemCols - kAccs * NT) / kSfCols;
   static constexpr int kStages = kByMem < kByTmem ? kByMem : kByTmem;
@@ -66,8 +66,7 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
   constexpr int kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* epi = smem + kStages * C::kStage;
-  uint8_t* tail = epi + kEpiBytes;
+  uint8_t* tail = smem + kStages * C::kStage;
   uint64_t* full = reinterpret_cast<uint64_t*>(tail);    // [stage]: bytes landed
   uint64_t* empty = full + kStages;                      // [stage]: its MMAs completed
   uint64_t* acc_full = empty + kStages;                  // [2]
@@ -216,7 +215,7 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     mbar_wait_drain(mma_done, 0, P.err, kErrWaitTimeout, P.wait_ns);
   } else if (warp >= 4) {
     using E = Epilogue<F32, SW>;
-    E e(P, epi, warp, lane);
+    E e(P, warp, lane);
     Item t{};
     int li = 0;
     for (int it = blockIdx.x; it < items; it += gridDim.x, ++li) {
@@ -322,7 +321,7 @@ MmParams params(const moe_fp4_mm_dims& d, const uint8_t* as, const int32_t* offs
   P.kt = (d.K + 127) / 128;
   P.f32 = d.y_type == MOE_FP4_TYPE_F32;
   P.swiglu = d.swiglu;
-  P.vec = ((size_t)P.n_out * (P.f32 ? 4 : 2)) % 16 == 0 && ((uintptr_t)y & 15) == 0;
+  P.vec = P.n_out % 2 == 0 && ((uintptr_t)y & 3) == 0;
   P.split = 1;
   P.wait_ns = wait_limit_ns();
   return P;

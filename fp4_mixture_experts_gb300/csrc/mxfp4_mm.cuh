@@ -30,7 +30,7 @@ struct MmParams {
   int mblocks;               // ceil(N / 128)
   int kt;                    // scale tiles along K
   int f32, swiglu;
-  int vec;                   // rows of y start on 16 bytes
+  int vec;                   // rows of y start on 4 bytes and have an even number of features
   int split;                 // CTAs of a cluster that share an item's K (1: none)
   int early;                 // launched before the kernel that writes the rows has ended
   uint64_t wait_ns;
@@ -118,12 +118,11 @@ __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t lo) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 
-// this thread's TMEM lane, 32 columns
-__device__ __forceinline__ void tmem_ld32(uint32_t ta, uint32_t (&a)[32]) {
+// this thread's TMEM lane, 32 columns; valid after tcgen05.wait::ld
+__device__ __forceinline__ void tmem_ld32_async(uint32_t ta, uint32_t (&a)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
         "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]),
         "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]), "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]),
@@ -132,17 +131,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t ta, uint32_t (&a)[32]) {
       : "memory");
 }
 
-// four 8 x 8 matrices of 16-bit elements, transposed: lane l gives the address
-// of row l % 8 of matrix l / 8
-__device__ __forceinline__ void stmatrix4_trans(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(a), "r"(b),
-               "r"(c), "r"(d)
-               : "memory");
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(uint32_t lo, uint32_t hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
   return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// Lanes l and l ^ d hold two bf16 each, (a0, a1) and (b0, b1): the lower lane
+// gets (a0, b0), the upper (a1, b1); sel is 0x5410 in the lower, 0x3276 in the upper.
+__device__ __forceinline__ uint32_t swap_pair(uint32_t p, int d, uint32_t sel) {
+  return __byte_perm(p, __shfl_xor_sync(0xFFFFFFFFu, p, d), sel);
 }
 
 // One work item; every role walks the same sequence with its own cursor.
@@ -220,21 +217,18 @@ struct Ring {
 
 // ---- epilogue -----------------------------------------------------------------
 // The accumulator has features in lanes and tokens in columns; y wants a
-// token's features side by side.  A chunk of 32 tokens (16 of a plain fp32
-// product) goes to shared memory, [token][feature], and leaves from there 16
-// bytes a thread (or, where rows of y do not start on 16 bytes, by single
-// elements).  bf16: TMEM is read as 16 x 8 fragments, which stmatrix stores
-// transposed: 16 conversions and 4 stores for 32 x 32 values.  (One bulk copy a
-// row instead costs its issuing thread ~70 cycles each, 2,300 a chunk:
-// measured.)
+// token's features side by side.  Values go from registers to y: a lane pair
+// swaps one value of every two tokens, so that each lane stores two adjacent
+// features of one of them (fp32: a token's 32 features, 128 bytes, a store as
+// they are).  Nothing passes through shared memory: the MMAs of 256 x 256 tiles
+// take all of its bandwidth, and an epilogue that turned its tile there took
+// 7,000 cycles beside them, longer than the MMAs of K = 2048.
 //
 // Eight warps, in two groups of four (a lane quarter each): group h takes every
-// other chunk, in two buffers of its own, one barrier a chunk.  Chunks are
-// read in rounds of 64 columns a group, so that the accumulator is given back
-// after the reads alone.
+// other chunk of 32 tokens.  Chunks are read in rounds of two a group, so that
+// the accumulator is given back after the reads alone.
 constexpr int kEpiWarps = 8;
-constexpr int kEpiBuf = 32 * (kBM * 2 + 16);
-constexpr int kEpiBytes = 4 * kEpiBuf;
+constexpr int kTokens = 32;  // tokens of a chunk = its columns
 
 // whether `ok` holds in all epilogue warps: they go on, or leave, together
 __device__ __forceinline__ bool all_of_epilogue(bool ok) {
@@ -250,184 +244,112 @@ __device__ __forceinline__ bool all_of_epilogue(bool ok) {
 
 template <bool F32, bool SW>
 struct Epilogue {
-  static constexpr int kTokens = F32 && !SW ? 16 : 32;         // tokens of a chunk = its columns
-  static constexpr int kLoads = 64 / kTokens;                  // chunks of a round
-  static constexpr int kFeatures = SW ? kBM / 2 : kBM;         // features of a tile
-  static constexpr int kRowBytes = kFeatures * (F32 ? 4 : 2);
-  static constexpr int kPitch = kRowBytes + 16;
-  static constexpr int kPerRow = kRowBytes / 16;               // threads of a row
-  static constexpr int kRowStep = kEpiWarps * 16 / kPerRow;    // rows of a step of the group
+  static constexpr int kFeatures = SW ? kBM / 2 : kBM;  // features of a tile
   static constexpr int kEs = F32 ? 4 : 2;
-  static_assert(kTokens * kPitch <= kEpiBuf, "buffer");
 
-  uint8_t* buf;      // the group's two buffers
   int q, h, lane;    // lane quarter, group
-  int tid;           // thread of the group
-  int vec, n_out;
-  uint32_t count;    // chunks of this group so far
+  int vec;           // rows of y start on 4 bytes, and n_out is even: two bf16 a store
+  size_t ldy;        // bytes
 
-  __device__ __forceinline__ Epilogue(const MmParams& P, uint8_t* epi, int warp, int lane_)
-      : buf(epi + ((warp >> 2) & 1) * 2 * kEpiBuf), q(warp & 3), h((warp >> 2) & 1), lane(lane_),
-        tid((warp & 3) * 32 + lane_), vec(P.vec), n_out(P.n_out), count(0) {}
+  __device__ __forceinline__ Epilogue(const MmParams& P, int warp, int lane_)
+      : q(warp & 3), h((warp >> 2) & 1), lane(lane_), vec(P.vec), ldy((size_t)P.n_out * kEs) {}
 
-  __device__ __forceinline__ void sync() { asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory"); }
-
-  // kTokens columns from taddr (with the warp's lane base)
-  __device__ __forceinline__ void load(uint32_t ta, uint32_t* a) {
-    if (F32 && !SW)
-      asm volatile(
-          "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-          : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
-            "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15])
-          : "r"(ta)
-          : "memory");
-    else
-      // 16 x 8 fragments: a[16 k + 4 j + i] of thread t is lane 16 k + t / 4 + 8 (i / 2), column
-      // 8 j + 2 (t % 4) + i % 2
-      asm volatile(
-          "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
-          "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
-          "[%33];"
-          : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
-            "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]),
-            "=r"(a[16]), "=r"(a[17]), "=r"(a[18]), "=r"(a[19]), "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]),
-            "=r"(a[24]), "=r"(a[25]), "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31])
-          : "r"(ta), "r"(ta + (16u << 16))
-          : "memory");
-  }
-
-  // a chunk's values to shared memory
-  __device__ __forceinline__ void stage(uint32_t* v, uint8_t* b) {
-    if (F32 && !SW) {
-      float* o = reinterpret_cast<float*>(b) + q * 32 + lane;
+  // rows tokens of one chunk to y (at its first token, the tile's first
+  // feature), nf features.  ALL: 32 tokens and a whole tile.
+  template <bool ALL>
+  __device__ __forceinline__ void put(const uint32_t (&v)[kTokens], uint8_t* y, int rows, int nf) {
+    const bool odd = lane & 1;
+    if (!SW && F32) {
+      const int f = q * 32 + lane;
+      y += f * 4;
 #pragma unroll
-      for (int j = 0; j < kTokens; ++j) o[j * (kPitch / 4)] = __uint_as_float(v[j]);
-      return;
-    }
-    if (!SW) {
-      const uint32_t s = smem_u32(b) + (lane & 7) * kPitch + (q * 32 + (lane >> 3) * 8) * 2;
+      for (int j = 0; j < kTokens; ++j)
+        if (ALL || (j < rows && f < nf)) *reinterpret_cast<uint32_t*>(y + j * ldy) = v[j];
+    } else if (!SW && vec) {
+      const int f = q * 32 + (lane & ~1);
+      const uint32_t sel = odd ? 0x3276u : 0x5410u;
+      y += (odd ? ldy : 0) + f * 2;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        stmatrix4_trans(s + 8 * j * kPitch, pack_bf16(v[4 * j], v[4 * j + 1]), pack_bf16(v[4 * j + 2], v[4 * j + 3]),
-                        pack_bf16(v[16 + 4 * j], v[16 + 4 * j + 1]), pack_bf16(v[16 + 4 * j + 2], v[16 + 4 * j + 3]));
-      return;
-    }
-    // Gate and up rows alternate: of a fragment's rows r = t / 4 and r + 8,
-    // threads of even r compute feature r / 2 (rows r, r + 1), threads of odd r
-    // feature 4 + (r - 1) / 2 (rows r + 7, r + 8).
-    const bool odd = (lane >> 2) & 1;
-    const int r = lane >> 2;
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      const uint32_t x0 = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[i] : v[i + 2], 4);
-      const uint32_t x1 = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[i + 1] : v[i + 3], 4);
-      const float g0 = __uint_as_float(odd ? x0 : v[i]), u0 = __uint_as_float(odd ? v[i + 2] : x0);
-      const float g1 = __uint_as_float(odd ? x1 : v[i + 1]), u1 = __uint_as_float(odd ? v[i + 3] : x1);
-      v[i] = __float_as_uint(swiglu(g0, u0));
-      v[i + 1] = __float_as_uint(swiglu(g1, u1));
-    }
-    if (F32) {
-      float* o = reinterpret_cast<float*>(b) + q * 16 + (odd ? 4 + (r >> 1) : r >> 1) + 2 * (lane & 3) * (kPitch / 4);
-#pragma unroll
-      for (int i = 0; i < 32; i += 4) {
-        float* p = o + 8 * ((i & 15) >> 2) * (kPitch / 4) + 8 * (i >> 4);
-        p[0] = __uint_as_float(v[i]);
-        p[kPitch / 4] = __uint_as_float(v[i + 1]);
+      for (int j = 0; j < kTokens; j += 2) {
+        const uint32_t p = swap_pair(pack_bf16(v[j], v[j + 1]), 1, sel);
+        if (ALL || (j + (odd ? 1 : 0) < rows && f < nf)) *reinterpret_cast<uint32_t*>(y + j * ldy) = p;
       }
+    } else if (!SW) {
+      const int f = q * 32 + lane;
+      y += f * 2;
+#pragma unroll
+      for (int j = 0; j < kTokens; ++j)
+        if (j < rows && f < nf) *reinterpret_cast<uint16_t*>(y + j * ldy) = f32_to_bf16_rn(__uint_as_float(v[j]));
     } else {
-      // feature f back to the threads of matrix row f; h[j], h[4 + j]: lanes 0..15 and 16..31 of columns 8 j on
-      const int src = (r < 4 ? 2 * r : 2 * r - 7) * 4 + (lane & 3);
-      uint32_t hv[8];
+      // gate in even lanes, up in odd ones: of tokens j and j + 1 the even lane takes the first, the odd the second
+      float s[kTokens / 2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) hv[i] = __shfl_sync(0xFFFFFFFFu, pack_bf16(v[4 * i], v[4 * i + 1]), src);
-      const int m = lane >> 3;
-      const uint32_t s = smem_u32(b) + (8 * (m >> 1) + (lane & 7)) * kPitch + (q * 16 + (m & 1) * 8) * 2;
-      stmatrix4_trans(s, hv[0], hv[4], hv[1], hv[5]);
-      stmatrix4_trans(s + 16 * kPitch, hv[2], hv[6], hv[3], hv[7]);
-    }
-  }
-
-  // a staged chunk to y (at its first token and feature): `rows` tokens, nf features
-  __device__ __forceinline__ void write(const uint8_t* b, uint8_t* y, int rows, int nf) {
-    const size_t ldy = (size_t)n_out * kEs;
-    if (vec) {
-      const int r = tid / kPerRow, c = (tid % kPerRow) * 16;
-      const uint8_t* src = b + r * kPitch + c;
-      uint8_t* dst = y + r * ldy + c;
-      const bool in = c < nf * kEs;
-      uint4 v[kTokens / kRowStep];
+      for (int j = 0; j < kTokens; j += 2) {
+        const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j] : v[j + 1], 1);
+        s[j / 2] = swiglu(__uint_as_float(odd ? other : v[j]), __uint_as_float(odd ? v[j + 1] : other));
+      }
+      if (F32 || !vec) {
+        const int f = q * 16 + (lane >> 1);
+        y += (odd ? ldy : 0) + f * kEs;
 #pragma unroll
-      for (int k = 0; k < kTokens / kRowStep; ++k) v[k] = *reinterpret_cast<const uint4*>(src + k * kRowStep * kPitch);
+        for (int j = 0; j < kTokens; j += 2)
+          if (ALL || (j + (odd ? 1 : 0) < rows && f < nf)) {
+            if (F32)
+              *reinterpret_cast<float*>(y + j * ldy) = s[j / 2];
+            else
+              *reinterpret_cast<uint16_t*>(y + j * ldy) = f32_to_bf16_rn(s[j / 2]);
+          }
+      } else {
+        // the same swap between lanes 2 apart, which hold adjacent features: each stores two features of one token
+        const bool second = lane & 2;
+        const uint32_t sel = second ? 0x3276u : 0x5410u;
+        const int f = q * 16 + (lane >> 2) * 2, jj = (odd ? 1 : 0) + (second ? 2 : 0);
+        y += jj * ldy + f * 2;
 #pragma unroll
-      for (int k = 0; k < kTokens / kRowStep; ++k)
-        if (in && r + k * kRowStep < rows) *reinterpret_cast<uint4*>(dst + k * kRowStep * ldy) = v[k];
-    } else if (F32) {
-      write_elements(reinterpret_cast<const float*>(b), reinterpret_cast<float*>(y), rows, nf);
-    } else {
-      write_elements(reinterpret_cast<const uint16_t*>(b), reinterpret_cast<uint16_t*>(y), rows, nf);
-    }
-  }
-
-  // rows by warps, a row's features by lanes
-  template <typename T>
-  __device__ __forceinline__ void write_elements(const T* b, T* y, int rows, int nf) {
-    constexpr int kR = 4;  // rows in flight
-#pragma unroll
-    for (int i0 = 0; i0 < kTokens; i0 += 4 * kR) {
-      T v[kR][kFeatures / 32];
-#pragma unroll
-      for (int k = 0; k < kR; ++k)
-#pragma unroll
-        for (int u = 0; u < kFeatures / 32; ++u) v[k][u] = b[(i0 + 4 * k + q) * (kPitch / kEs) + 32 * u + lane];
-#pragma unroll
-      for (int k = 0; k < kR; ++k) {
-        const int i = i0 + 4 * k + q;
-        T* row = y + (size_t)i * n_out + lane;
-        if (i < rows)
-#pragma unroll
-          for (int u = 0; u < kFeatures / 32; ++u)
-            if (32 * u + lane < nf) row[32 * u] = v[k][u];
+        for (int j = 0; j < kTokens; j += 4) {
+          const uint32_t p =
+              swap_pair(pack_bf16(__float_as_uint(s[j / 2]), __float_as_uint(s[j / 2 + 1])), 2, sel);
+          if (ALL || (j + jj < rows && f < nf)) *reinterpret_cast<uint32_t*>(y + j * ldy) = p;
+        }
       }
     }
   }
 
   // One item: n tokens from row0, its accumulator at taddr, features from f0
   // (nf of them in y).  Chunks are taken from `first` on, cyclically.
-  // after_reads(last): this group has read its chunks of the first round
-  // (chunks first .. first + 127 / kTokens of the item), or, last, all of them.
+  // after_reads(round0, last): this group has read its chunks of the first
+  // round (the item's chunks first .. first + 3), or, last, all of them.
   // False, with nothing written, if some epilogue warp's wait for the
   // accumulator ran out (not ok).
   template <typename F>
   __device__ __forceinline__ bool item(void* y, uint32_t taddr, int row0, int n, int f0, int nf, int first, bool ok,
                                        F&& after_reads) {
     const int chunks = (n + kTokens - 1) / kTokens;
-    uint8_t* const y0 = static_cast<uint8_t*>(y) + ((size_t)row0 * n_out + f0) * kEs;
+    uint8_t* const y0 = static_cast<uint8_t*>(y) + (size_t)row0 * ldy + (size_t)f0 * kEs;
     taddr += (uint32_t)(q * 32) << 16;
     int i = h;
     do {
-      uint32_t v[kLoads][kTokens];
+      uint32_t v[2][kTokens];
 #pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
+      for (int k = 0; k < 2; ++k) {
         const int at = first + i + 2 * k;
-        if (i + 2 * k < chunks) load(taddr + (at < chunks ? at : at - chunks) * kTokens, v[k]);
+        if (i + 2 * k < chunks) tmem_ld32_async(taddr + (at < chunks ? at : at - chunks) * kTokens, v[k]);
       }
       asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      after_reads(i == h, i + 2 * kLoads >= chunks);
+      after_reads(i == h, i + 4 >= chunks);
       if (i == h && !all_of_epilogue(ok)) return false;
 #pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
+      for (int k = 0; k < 2; ++k) {
         if (i + 2 * k >= chunks) break;
         const int at = first + i + 2 * k, t0 = (at < chunks ? at : at - chunks) * kTokens;
-        // (a warp here has passed the barrier of the last chunk, and with it every warp of the group has read
-        // what the chunk before that left in this buffer)
-        uint8_t* b = buf + (count++ & 1) * kEpiBuf;
-        stage(v[k], b);
-        sync();
-        write(b, y0 + (size_t)t0 * n_out * kEs, min(kTokens, n - t0), nf);
+        if (n - t0 >= kTokens && nf == kFeatures)
+          put<true>(v[k], y0 + (size_t)t0 * ldy, kTokens, nf);
+        else
+          put<false>(v[k], y0 + (size_t)t0 * ldy, min(kTokens, n - t0), nf);
       }
-      i += 2 * kLoads;
+      i += 4;
     } while (i < chunks);
     return true;
   }

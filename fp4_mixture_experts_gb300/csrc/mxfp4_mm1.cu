@@ -250,7 +250,8 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       uint32_t v[32];
       const int q = warp & 3;
-      tmem_ld32(tmem + ((uint32_t)(q * 32) << 16), v);
+      tmem_ld32_async(tmem + ((uint32_t)(q * 32) << 16), v);
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
       for (int j = 0; j < kRows; ++j)
         if (j < P.M) part[j * kPartPitch + q * 32 + lane] = __uint_as_float(v[j]);

@@ -50,7 +50,7 @@ constexpr int kBoxRows = 32;                             // token rows per small
 constexpr int kATile = kBM * 128;
 constexpr int kBTile = kNT / 2 * 128;                    // this CTA's half
 constexpr int kStage = kATile + kBTile + 6 * kSfTile;    // scales: 2 weight tiles, 2 x 2 token tiles
-constexpr int kFixed = 1024 + 512 + 2 * (kMaxGroups + 1) * 4 + kEpiBytes + 16;
+constexpr int kFixed = 1024 + 512 + 2 * (kMaxGroups + 1) * 4;
 constexpr int kStages = (kSmemMax - kFixed) / kStage;
 constexpr int kSmem2 = kStages * kStage + kFixed;
 constexpr uint32_t kAcc1 = 184;                          // first column of accumulator 1
@@ -73,7 +73,7 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
-      "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n}" ::"r"(smem_u32(bar))
+      "mbarrier.arrive.shared::cluster.b64 _, [a];\n}" ::"r"(smem_u32(bar))
       : "memory");
 }
 // the address, in the cluster's shared memory, of p's place in the leader CTA
@@ -148,8 +148,7 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
   P.err = &g_mm2_err[0];
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* epi = smem + kStages * kStage;
-  uint8_t* tail = epi + kEpiBytes;
+  uint8_t* tail = smem + kStages * kStage;
   uint64_t* full = reinterpret_cast<uint64_t*>(tail);    // [stage] leader: both CTAs' bytes landed
   uint64_t* empty = full + kStages;                      // [stage] both: the stage's MMAs completed
   uint64_t* acc_full = empty + kStages;                  // [2] both
@@ -310,7 +309,7 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
     }
   } else if (warp >= 4) {
     using E = Epilogue<F32, SW>;
-    E e(P, epi, warp, lane);
+    E e(P, warp, lane);
     Item t{};
     int li = 0;
     for (int it = first; it < items; it += step, ++li) {
@@ -321,7 +320,7 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       // the columns shared with the other accumulator are read in the first round: accumulator 0's from kAcc1 on,
       // so its chunks are taken from there; accumulator 1's first 256 - kAcc1
-      const int chunks = (t.n + E::kTokens - 1) / E::kTokens, from = kAcc1 / E::kTokens;
+      const int chunks = (t.n + kTokens - 1) / kTokens, from = kAcc1 / kTokens;
       const int start = b == 0 && chunks > from ? from : 0;
       if (!e.item(P.y, tmem + b * kAcc1, t.row0, t.n, f0, nf, start, ok, [&](bool round0, bool last) {
             if (lane != 0) return;
