@@ -20,8 +20,10 @@
 // Roles, in both CTAs: warp 0 the TMA producer of the CTA's own codes (its 128
 // weight rows, its half of the token rows), warp 2 that of the scales (issuing
 // a copy takes ~80 cycles: one warp for both is slower than the MMAs), warp 1 of
-// the leader (rank 0) the MMA issuer, warps 4..11 the epilogue of the CTA's own
-// accumulator lanes.  The follower's copies complete on the leader's barrier
+// the leader (rank 0) the MMA issuer, warp 3 of the leader the issuer of the
+// scales' copies to tensor memory (in one warp with the MMAs they made it the
+// bound for tiles of fewer than 256 tokens), warps 4..11 the epilogue of the
+// CTA's own accumulator lanes.  The follower's copies complete on the leader's barrier
 // (its producers announce their bytes there), so that the issuer waits for
 // both halves at once.  (A warp of the follower that waits and
 // arrives on the leader's barrier instead needs ~1,300 cycles a stage for the
@@ -112,6 +114,12 @@ __device__ __forceinline__ void commit_both(uint64_t* bar) {
       : "memory");
 }
 
+// ... of its tensor-core operations to a barrier of this CTA
+__device__ __forceinline__ void commit_one(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+
 // a bounded wait of the whole warp on a barrier that the peer CTA arrives on
 __device__ __forceinline__ bool warp_wait_cl(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                              const MmParams& P) {
@@ -154,7 +162,9 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
   uint64_t* acc_full = empty + kStages;                  // [2] both
   uint64_t* acc_empty = acc_full + 2;                    // [2] leader: both epilogues read all of the accumulator
   uint64_t* part_free = acc_empty + 2;                   // [2] leader: ... its columns that the other one shares
-  uint64_t* mma_done = part_free + 2;                    // both
+  uint64_t* sf_full = part_free + 2;                     // [slot] leader: a stage's scales are in tensor memory
+  uint64_t* sf_done = sf_full + kSfSlots;                // leader
+  uint64_t* mma_done = sf_done + 1;                      // both
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* issued = abort_flag + 1;                 // [4] leader: stages issued by each producer
@@ -173,6 +183,8 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
       mbar_init(&acc_empty[b], 2 * kEpiWarps);
       mbar_init(&part_free[b], 2 * kEpiWarps);
     }
+    for (int i = 0; i < kSfSlots; ++i) mbar_init(&sf_full[i], 1);
+    mbar_init(sf_done, 1);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     mbar_fence_init();
@@ -248,8 +260,9 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
     // leader arrives once its MMAs, which read both CTAs' memory, are done
     if (rank == 0) {
       Item t{};
-      Ring<kStages> ring, behind;   // behind: the stage that last used this stage's scale slot
-      int li = 0, g = 0, slot = 0, prev_n = 0;
+      Ring<kStages> ring;
+      Ring<kSfSlots> slot;
+      int li = 0, prev_n = 0;
       bool ok = true;
       const uint32_t lo0 = desc_lo(smem_u32(smem));
       for (int it = first; it < items && ok; it += step, ++li) {
@@ -264,30 +277,16 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
           break;
         const uint32_t d_tmem = tmem + b * kAcc1;
         const uint32_t id0 = idesc_mxf4(2 * kBM, n_mma, 0), id1 = idesc_mxf4(2 * kBM, n_mma, 1);
-        for (int ks = 0; ks < nks; ++ks, ++g, ring.next()) {
-          if (!warp_wait(&full[ring.s], ring.phase, abort_flag, P)) {
+        for (int ks = 0; ks < nks; ++ks, ring.next(), slot.next()) {
+          if (!warp_wait(&sf_full[slot.s], slot.phase, abort_flag, P)) {
             ok = false;
             break;
-          }
-          if (g >= kSfSlots) {  // the MMAs that read this scale slot have completed
-            if (!warp_wait(&empty[behind.s], behind.phase, abort_flag, P)) {
-              ok = false;
-              break;
-            }
-            behind.next();
           }
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           if (elect_one()) {
             const uint32_t lo = lo0 + ring.s * (kStage >> 4);
             const uint32_t a_lo = lo | kDescLoSw128, b_lo = (lo + (kATile >> 4)) | kDescLoSw128;
-            const uint32_t sf_lo = lo + ((kATile + kBTile) >> 4);
-            const uint32_t sf_t = tmem + kSfBase + slot * kSfCols;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              tmem_cp_scales<2>(sf_t + 4 * c, sf_lo + c * (kSfTile >> 4));
-              tmem_cp_scales<2>(sf_t + 8 + 8 * c, sf_lo + (2 + c) * (kSfTile >> 4));
-              tmem_cp_scales<2>(sf_t + 12 + 8 * c, sf_lo + (4 + c) * (kSfTile >> 4));
-            }
+            const uint32_t sf_t = tmem + kSfBase + slot.s * kSfCols;
             const int steps = (P.K - ks * kStageK + 63) / 64;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
@@ -299,13 +298,53 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
             if (ks == nks - 1) commit_both(&acc_full[b]);
           }
           __syncwarp();
-          slot = slot == kSfSlots - 1 ? 0 : slot + 1;
         }
       }
       __syncwarp();
       if (elect_one()) commit_both(mma_done);
       __syncwarp();
       mbar_wait_drain(mma_done, 0, P.err, kErrWaitTimeout, P.wait_ns);
+    }
+  } else if (warp == 3) {
+    if (rank == 0) {
+      // scales of each landed stage to a slot of tensor memory
+      Ring<kStages> ring, behind;  // behind: the stage that last used this stage's slot
+      Ring<kSfSlots> slot;
+      const uint32_t lo0 = desc_lo(smem_u32(smem)) + ((kATile + kBTile) >> 4);
+      int g = 0;
+      bool ok = true;
+      for (int it = first; it < items && ok; it += step)
+        for (int ks = 0; ks < nks; ++ks, ++g, ring.next(), slot.next()) {
+          if (!warp_wait(&full[ring.s], ring.phase, abort_flag, P)) {
+            ok = false;
+            break;
+          }
+          if (g >= kSfSlots) {  // the MMAs that read this slot have completed
+            if (!warp_wait(&empty[behind.s], behind.phase, abort_flag, P)) {
+              ok = false;
+              break;
+            }
+            behind.next();
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (elect_one()) {
+            const uint32_t sf_lo = lo0 + ring.s * (kStage >> 4);
+            const uint32_t sf_t = tmem + kSfBase + slot.s * kSfCols;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              tmem_cp_scales<2>(sf_t + 4 * c, sf_lo + c * (kSfTile >> 4));
+              tmem_cp_scales<2>(sf_t + 8 + 8 * c, sf_lo + (2 + c) * (kSfTile >> 4));
+              tmem_cp_scales<2>(sf_t + 12 + 8 * c, sf_lo + (4 + c) * (kSfTile >> 4));
+            }
+            commit_one(&sf_full[slot.s]);
+          }
+          __syncwarp();
+        }
+      // every copy has completed before tensor memory is given back
+      __syncwarp();
+      if (elect_one()) commit_one(sf_done);
+      __syncwarp();
+      mbar_wait_drain(sf_done, 0, P.err, kErrWaitTimeout, P.wait_ns);
     }
   } else if (warp >= 4) {
     using E = Epilogue<F32, SW>;
