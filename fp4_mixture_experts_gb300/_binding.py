@@ -45,6 +45,7 @@ EXPORTED_SYMBOLS = (
     "moe_fp4_mxfp4_tile_scales",
     "moe_fp4_mxfp4_matmul",
     "moe_fp4_mxfp4_linear_workspace_bytes",
+    "moe_fp4_mxfp4_gathered_workspace_bytes",
     "moe_fp4_mxfp4_linear",
     "moe_fp4_block_norm",
     "moe_fp4_ops_check",
@@ -119,6 +120,7 @@ def load_library():
             ("mxfp4_tile_scales", [P, i32, i32, i32, i32, P, P], i32),
             ("mxfp4_matmul", [P, P, P, P, P, P, P, P], i32),
             ("mxfp4_linear_workspace_bytes", [P], size),
+            ("mxfp4_gathered_workspace_bytes", [P, i64], size),
             ("mxfp4_linear", [P, P, i32, i64, i64, P, i32, P, P, P, P, P, size, P], i32),
             ("block_norm", [P, P], i32),
             ("ops_check", [P], i32)):

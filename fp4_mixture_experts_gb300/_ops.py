@@ -52,7 +52,7 @@ class _Unloaded:
                                "fp4_mixture_experts_gb300.build` (there is no fallback implementation)") from e
         native.bind(tuple(ctypes.cast(getattr(lib, "moe_fp4_" + n), ctypes.c_void_p).value for n in (
             "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_tile_scales", "mxfp4_matmul", "mxfp4_linear",
-            "mxfp4_linear_workspace_bytes", "block_norm")), _raise)
+            "mxfp4_linear_workspace_bytes", "mxfp4_gathered_workspace_bytes", "block_norm")), _raise)
         _native, _BF16 = native, torch.bfloat16
         return getattr(native, name)
 
@@ -100,8 +100,13 @@ def mxfp4_matmul(a, a_scale, w, w_scale, offsets=None, swiglu: bool = False, dty
     return f(a, a_scale, w, w_scale, offsets, swiglu, dtype or _BF16, out, _handle(stream))
 
 
-def mxfp4_linear_workspace_bytes(M: int, N: int, K: int, E: int = 1) -> int:
-    return int(load_library().moe_fp4_mxfp4_linear_workspace_bytes(ctypes.byref(MmDims(M, N, K, E, 0, 0))))
+def mxfp4_linear_workspace_bytes(M: int, N: int, K: int, E: int = 1, x_rows: int | None = None) -> int:
+    """Bytes of mxfp4_linear's workspace; x_rows: of a call that gathers its M rows from that many, enough to quantise
+    rows that are used several times once (less, down to the size without x_rows, is fine too)."""
+    dims = ctypes.byref(MmDims(M, N, K, E, 0, 0))
+    if x_rows is None:
+        return int(load_library().moe_fp4_mxfp4_linear_workspace_bytes(dims))
+    return int(load_library().moe_fp4_mxfp4_gathered_workspace_bytes(dims, x_rows))
 
 
 def mxfp4_linear(x, w, w_scale, offsets=None, row_index=None, index_div: int = 1, swiglu: bool = False, dtype=None,

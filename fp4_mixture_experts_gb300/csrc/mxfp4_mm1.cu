@@ -224,9 +224,7 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
         q = make_uint2(cur[0], cur[1]);
         sb = cur[2];
       } else {
-        float v[16];
-        unpack16<SRC == 1>(cur, v);
-        q = quantize16(v, sb);
+        q = quantize16<SRC == 1>(cur, sb);
       }
       // the stages of this pass are free
       Ring<kStages> at = ring;

@@ -22,6 +22,11 @@ struct MxRows {
 
 int check_mx_rows(const MxRows& R);  // a moe_fp4_status
 cudaError_t launch_mxfp4_quantize(const MxRows& R, uint8_t* codes, uint8_t* scales, bool tiled, cudaStream_t st);
+// The same result (tiled) for rows that are used several times: every row of x
+// is quantised once (row_codes [x_rows, K/2], 16-byte aligned, row_scales
+// [x_rows, K/32]), then gathered.
+cudaError_t launch_mxfp4_quantize_once(const MxRows& R, uint8_t* row_codes, uint8_t* row_scales, uint8_t* codes,
+                                       uint8_t* scales, cudaStream_t st);
 // the error words of the operators' kernels (one in each translation unit): read, or cleared
 cudaError_t ops_quant_error(int32_t* word, bool clear, cudaStream_t st);
 cudaError_t ops_mm_error(int32_t* word, bool clear, cudaStream_t st);
@@ -66,27 +71,44 @@ __device__ __forceinline__ void load16_raw(const void* x, int64_t at, uint32_t (
   }
 }
 
+// The codes of half a block, 16 elements as load16_raw leaves them, by a pair of
+// lanes (l, l ^ 1) that hold a block together (whole warp; every lane takes
+// part), and the block's scale byte.  bf16 elements stay in pairs up to the
+// conversion: magnitudes compare as their bit patterns do, and x 2^-e is exact
+// in bf16 too (an underflow ends at the code 0 with its sign all the same).
 template <bool F32>
-__device__ __forceinline__ void unpack16(const uint32_t (&w)[16], float (&v)[16]) {
+__device__ __forceinline__ uint2 quantize16(const uint32_t (&w)[16], uint32_t& scale) {
+  uint32_t amax;  // bits of the largest magnitude as fp32
+  if (F32) {
+    amax = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    v[i] = __uint_as_float(F32 ? w[i] : (i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
-}
-
-// The codes of half a block, 16 elements, by a pair of lanes (l, l ^ 1) that
-// hold a block together (whole warp; every lane takes part), and the block's
-// scale byte; v is used up.
-__device__ __forceinline__ uint2 quantize16(float (&v)[16], uint32_t& scale) {
-  uint32_t amax = 0;
+    for (int j = 0; j < 16; ++j) amax = max(amax, w[j] & 0x7FFFFFFFu);
+    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+  } else {
+    uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+    for (int j = 0; j < 8; ++j) m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
+    m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    amax = max(m << 16, m & 0xFFFF0000u);
+  }
   const uint32_t ef = amax >> 23;
   scale = ef == 255u ? 255u : (ef > 2u ? ef - 2u : 0u);
   if (scale == 255u) return make_uint2(0x77777777u, 0x77777777u);
-  const float inv = __uint_as_float((254u - scale) << 23);  // 2^(127 - scale), normal for scale in [0, 253]
+  float v[16];
+  if (F32) {
+    const float inv = __uint_as_float((254u - scale) << 23);  // 2^(127 - scale), normal for scale in [0, 253]
 #pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] *= inv;
+    for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(w[j]) * inv;
+  } else {
+    const uint32_t inv = ((254u - scale) << 7) * 0x10001u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t p;
+      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p) : "r"(w[j]), "r"(inv));
+      v[2 * j] = __uint_as_float(p << 16);
+      v[2 * j + 1] = __uint_as_float(p & 0xFFFF0000u);
+    }
+  }
   return make_uint2(e2m1x8(v), e2m1x8(v + 8));
 }
 
@@ -104,6 +126,21 @@ __device__ __forceinline__ int find_group(const int32_t* off, int groups, int64_
   }
   const int64_t first = __ldg(off + lo), end = __ldg(off + lo + 1);
   return first >= 0 && first <= r && r < end && end <= rows ? lo : -1;
+}
+
+// The same by a whole warp, in one round of loads for each 32 groups; *first is
+// the group's first row.
+__device__ __forceinline__ int find_group_warp(const int32_t* off, int groups, int r, int rows, int* first) {
+  const int lane = threadIdx.x & 31;
+  int below = 0;  // groups that begin at or before r
+  for (int e0 = 0; e0 < groups; e0 += 32) {
+    const int e = e0 + lane;
+    below += __popc(__ballot_sync(0xFFFFFFFFu, e < groups && __ldg(off + min(e, groups)) <= r));
+  }
+  if (below == 0) return -1;
+  const int b = __ldg(off + below - 1), end = __ldg(off + below);
+  *first = b;
+  return b >= 0 && b <= r && r < end && end <= rows ? below - 1 : -1;
 }
 
 #endif

@@ -30,6 +30,7 @@ struct Entry {
   decltype(&moe_fp4_mxfp4_matmul) matmul;
   decltype(&moe_fp4_mxfp4_linear) linear;
   decltype(&moe_fp4_mxfp4_linear_workspace_bytes) linear_workspace_bytes;
+  decltype(&moe_fp4_mxfp4_gathered_workspace_bytes) gathered_workspace_bytes;
   decltype(&moe_fp4_block_norm) block_norm;
 } g_entry;
 PyObject* g_raise = nullptr;  // called with (status, entry point); raises
@@ -291,7 +292,7 @@ NATIVE_BEGIN(linear, 11)
   if (need == 0) return ok(MOE_FP4_ERR_UNSUPPORTED, "moe_fp4_mxfp4_linear"), nullptr;
   at::Tensor ws;
   if (none(a[9]))
-    ws = fresh({(int64_t)need}, at::kByte, x);
+    ws = fresh({(int64_t)(index ? g_entry.gathered_workspace_bytes(&W.dims, r.rows) : need)}, at::kByte, x);
   else
     ws = tensor(a[9], "workspace"), bytes_of(ws, "workspace", (int64_t)need);
   const at::Tensor out = result(a[8], M, W.n_out, t, x, "out");

@@ -357,7 +357,7 @@ int moe_fp4_forward_mx(const moe_fp4_dims* dims, const void* x_bf16, const float
  *              the tiles from off[e] / 128 + e on.  rows / 128 + groups tiles
  *              in all (moe_fp4_mxfp4_tiled_scale_bytes, 16-byte aligned).
  *              Rows in no group get codes and no scales.
- * K a positive multiple of 32, at most 32768; rows K < 2^36; rows = 0
+ * K a positive multiple of 32, at most 32768; rows K < 2^35; rows = 0
  * enqueues nothing. */
 int moe_fp4_mxfp4_quantize(const void* x, int x_type, int64_t x_rows, int64_t x_stride, int32_t K,
                            const int32_t* row_index, int32_t index_div, int64_t rows, const int32_t* group_offsets,
@@ -408,6 +408,12 @@ int moe_fp4_mxfp4_matmul(const moe_fp4_mm_dims* dims, const uint8_t* a, const ui
 /* Device workspace of moe_fp4_mxfp4_linear (the codes and scales of the
  * quantised rows; 256-byte aligned base); 0 for unsupported sizes. */
 size_t moe_fp4_mxfp4_linear_workspace_bytes(const moe_fp4_mm_dims* dims);
+
+/* The same for a call that gathers its rows (row_index) from x_rows rows: with
+ * this much, rows that are used several times are quantised once.  At least
+ * moe_fp4_mxfp4_linear_workspace_bytes, which is enough too; the results are
+ * the same. */
+size_t moe_fp4_mxfp4_gathered_workspace_bytes(const moe_fp4_mm_dims* dims, int64_t x_rows);
 
 /* The product from unquantised rows: moe_fp4_mxfp4_quantize of x (bf16 or
  * fp32, x_rows rows, stride x_stride; row_index / index_div as there, M output

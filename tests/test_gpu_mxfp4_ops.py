@@ -341,3 +341,37 @@ def test_no_rows():
     c, s = moe.mxfp4_quantize(x)
     assert c.shape == (0, 32) and s.shape == (0, 2)
     assert moe.mxfp4_dequantize(c, s).shape == (0, 64)
+
+
+def test_rows_used_several_times_are_quantised_once_with_the_same_bits():
+    """a workspace that lets the call quantise each source row once and gather its codes"""
+    rng = np.random.default_rng(21)
+    T, k, E, N, K = 1100, 8, 16, 96, 544
+    S = T * k
+    counts = rng.multinomial(S, np.ones(E) / E)
+    counts[3] += counts[4]
+    counts[4] = 0
+    off = gpu(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32))
+    slot = rng.permutation(S).astype(np.int32)
+    slot[5] = S + 3                                     # out of range: a zero row, and an error
+    slot = gpu(slot)
+    x = rows(rng, T, K)
+    w, ws = weights(rng, E, N, K)
+    wt, w = moe.mxfp4_tile_scales(gpu(ws)), gpu(w)
+    small = moe.mxfp4_linear_workspace_bytes(S, N, K, E)
+    large = moe.mxfp4_linear_workspace_bytes(S, N, K, E, x_rows=T)
+    assert large > small
+    got = []
+    for size in (small, large):
+        buf = torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV)
+        got.append(moe.mxfp4_linear(x, w, wt, offsets=off, row_index=slot, index_div=k, workspace=buf))
+        with pytest.raises(moe.MoeFp4Error):
+            moe.ops_check()
+    assert torch.equal(got[0], got[1])
+    assert not got[0][5].any()
+    a = O.values(*O.quantize(f64(x)))[np.minimum(slot.cpu().numpy(), S - 1) // k]
+    a[5] = 0
+    o = off.cpu().numpy()
+    for e in range(E):
+        if counts[e]:
+            check_product(got[1][o[e]:o[e + 1]], a[o[e]:o[e + 1]], O.values(w[e].cpu().numpy(), ws[e]), False, f"expert {e}")
