@@ -32,6 +32,7 @@ cudaError_t ops_quant_error(int32_t* word, bool clear, cudaStream_t st);
 cudaError_t ops_mm_error(int32_t* word, bool clear, cudaStream_t st);
 cudaError_t ops_mm1_error(int32_t* word, bool clear, cudaStream_t st);
 cudaError_t ops_mm2_error(int32_t* word, bool clear, cudaStream_t st);
+cudaError_t ops_norm_error(int32_t* word, bool clear, cudaStream_t st);
 
 #ifdef __CUDACC__
 

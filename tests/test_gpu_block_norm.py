@@ -152,3 +152,31 @@ def test_no_rows():
     e = torch.empty(0, 64, dtype=BF, device=DEV)
     out, normed = moe.block_residual(e, e)
     assert out.shape == normed.shape == (0, 64)
+
+
+@pytest.mark.parametrize("T,d", [(2600, 64), (5000, 8), (5001, 520), (1300, 1032), (1250, 4096), (620, 7168), (700, 8192),
+                                 (650, 8200), (4900, 250), (640, 16384)])
+@pytest.mark.parametrize("gate,sig,post", [("token", True, True), ("element", False, False), ("channel", True, True),
+                                           (None, False, True)])
+def test_many_rows(T, d, gate, sig, post):
+    """enough rows for the persistent form (and widths that it does not take)"""
+    run(T, d, rt=F32 if gate == "channel" else BF, yt=BF if gate == "element" else F32, two=gate != "channel", gate=gate, sig=sig,
+        post=post, seed=T)
+
+
+@pytest.mark.parametrize("d", [512, 4096])
+def test_many_rows_strided_in_place_without_norms_and_rms_norm(d):
+    rng = np.random.default_rng(d)
+    T = 20000 if d == 512 else 3000
+    buf = rand(rng, (T, d + 64), BF, 3.0)
+    r, keep = buf[:, :d], buf[:, d:].clone()
+    y = rand(rng, (T, d + 8), F32)[:, 8:]
+    w = rand(rng, (d,), BF)
+    n = f64(r) * rms(f64(r), 1e-6) * f64(w)
+    close(moe.rms_norm(r, w), n, 2.0 ** -17 * np.abs(n), "rms_norm")
+    ref, err, _, _ = reference(r, y, None, False, None, None, False, 2.0, None, 1e-6)
+    out, none = moe.block_residual(r, y, post_norm=False, scale=2.0, next_norm=False, out=r)
+    assert none is None
+    close(out, ref, err, "out")
+    assert torch.equal(buf[:, d:], keep)
+    moe.ops_check()
