@@ -116,6 +116,7 @@ __device__ __forceinline__ float cta_sum(float s, float* part) {
 
 template <int NC, bool VEC>
 __global__ void __launch_bounds__(512) block_norm_kernel(const NormParams P) {
+  griddep_begin();
   __shared__ float part[2][32];
   const moe_fp4_block_norm_args& a = P.a;
   const int64_t t = blockIdx.x;
@@ -244,6 +245,7 @@ __device__ __forceinline__ void weight8(const void* w, int type, int at, float t
 template <bool KEEP>
 __global__ void __launch_bounds__(KEEP ? kRingThreads : 2 * kRingThreads, 1)
 block_norm_ring_kernel(const RingParams R) {
+  griddep_begin();
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ float part[2][2][32];
   __shared__ uint64_t full[kRingMaxSlots];
@@ -420,8 +422,7 @@ cudaError_t launch_ring(const RingParams& R, int threads, int ctas, cudaStream_t
   auto* k = threads <= kRingThreads ? block_norm_ring_kernel<true> : block_norm_ring_kernel<false>;
   const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(k), kRingSmem);
   if (e != cudaSuccess) return e;
-  k<<<ctas, threads, R.slots * R.slot_bytes, st>>>(R);
-  return cudaGetLastError();
+  return launch_early(k, dim3(ctas), dim3(threads), R.slots * R.slot_bytes, st, R);
 }
 
 template <bool VEC>
@@ -434,13 +435,10 @@ cudaError_t launch_norm(const NormParams& P, cudaStream_t st) {
   const int nc = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : 4;
   const int threads = ((chunks + nc - 1) / nc + 31) / 32 * 32;
   const unsigned grid = (unsigned)P.a.T;
-  if (nc == 1)
-    block_norm_kernel<1, VEC><<<grid, threads, 0, st>>>(P);
-  else if (nc == 2)
-    block_norm_kernel<2, VEC><<<grid, threads, 0, st>>>(P);
-  else
-    block_norm_kernel<4, VEC><<<grid, threads, 0, st>>>(P);
-  return cudaGetLastError();
+  return launch_early(nc == 1   ? block_norm_kernel<1, VEC>
+                      : nc == 2 ? block_norm_kernel<2, VEC>
+                                : block_norm_kernel<4, VEC>,
+                      dim3(grid), dim3(threads), 0, st, P);
 }
 
 bool is_type(int t) { return t == MOE_FP4_TYPE_BF16 || t == MOE_FP4_TYPE_F32; }

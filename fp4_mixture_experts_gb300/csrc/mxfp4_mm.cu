@@ -97,6 +97,8 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                  "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  // behind the quantiser of its rows (rows_ahead) only the rows are waited for, by their producer
+  if (!P.rows_ahead) griddep_wait();
   if (warp == 2) group_tables<NT>(P, off, pre, lane);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
@@ -144,6 +146,7 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
         const int early = min(kStages, nks);
         for (int i = 0; i < early; ++i) load_w(i, i);
         griddep_wait();
+        griddep_launch_dependents();
         waited = true;
         for (; ks < early; ++ks, ++g, ring.next()) load_a(ks, ks);
       }
@@ -258,9 +261,7 @@ cudaError_t launch_as(const CUtensorMap& map_w, const CUtensorMap& map_a, const 
                       cudaStream_t st) {
   const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(mm_kernel<NT, F32, SW>), Cfg<NT>::kSmem);
   if (e != cudaSuccess) return e;
-  if (P.early) return launch_early(mm_kernel<NT, F32, SW>, dim3(grid), dim3(kThreads), Cfg<NT>::kSmem, st, map_w, map_a, P);
-  mm_kernel<NT, F32, SW><<<grid, kThreads, Cfg<NT>::kSmem, st>>>(map_w, map_a, P);
-  return cudaGetLastError();
+  return launch_early(mm_kernel<NT, F32, SW>, dim3(grid), dim3(kThreads), Cfg<NT>::kSmem, st, map_w, map_a, P);
 }
 
 template <int NT>
@@ -365,11 +366,11 @@ int choose_tile(const moe_fp4_mm_dims& d) {
   return tile;
 }
 
-// early: the launch may start before the kernel ahead of it, which writes a and as, has ended
+// rows_ahead: the kernel ahead of this one quantises the rows, to a and as
 cudaError_t launch_mm(const moe_fp4_mm_dims& d, const uint8_t* a, const uint8_t* as, const int32_t* offsets,
-                      const uint8_t* w, const uint8_t* ws, void* y, bool early, cudaStream_t st) {
+                      const uint8_t* w, const uint8_t* ws, void* y, bool rows_ahead, cudaStream_t st) {
   MmParams P = params(d, as, offsets, ws, y);
-  P.early = early;
+  P.rows_ahead = rows_ahead;
   if (few_rows(d, offsets)) return launch_few(d, P, nullptr, a, w, st);
   switch (choose_tile(d)) {
     case 64: return launch_nt<64>(d, a, w, P, st);

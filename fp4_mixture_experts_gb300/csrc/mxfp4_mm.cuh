@@ -32,7 +32,7 @@ struct MmParams {
   int f32, swiglu;
   int vec;                   // rows of y start on 4 bytes and have an even number of features
   int split;                 // CTAs of a cluster that share an item's K (1: none)
-  int early;                 // launched before the kernel that writes the rows has ended
+  int rows_ahead;            // the kernel ahead writes the rows (a and a_scales); all before it has ended
   uint64_t wait_ns;
 };
 

@@ -114,6 +114,7 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
       mbar_fence_init();
     }
     __syncwarp();
+    griddep_wait();
     for (int i = 0; i < min(kStages, k1 - k0); ++i) load_weights(k0 + i, i);
   }
   if (warp == 1) {
@@ -121,6 +122,7 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
                  "r"(kCols1));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  griddep_begin();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -292,17 +294,19 @@ cudaError_t launch_as(const CUtensorMap& map_w, const Mm1Params& Q, cudaStream_t
   auto* k = mm1_kernel<SRC, F32, SW>;
   const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(k), kSmem1);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = Q.m.split;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = Q.m.mblocks * Q.m.split;
   cfg.blockDim = kThreads;
   cfg.dynamicSmemBytes = kSmem1;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, k, map_w, Q);
 }
 

@@ -195,6 +195,8 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
                  "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
+  // behind the quantiser of its rows (rows_ahead) only the rows are waited for, by their producers
+  if (!P.rows_ahead) griddep_wait();
   if (warp == 4) group_tables<kNT>(P, off, pre, lane);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
@@ -211,7 +213,7 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
     Ring<kStages> ring;
     int g = 0;
     bool ok = true;
-    griddep_wait();  // the kernel ahead writes the rows' codes and scales
+    griddep_begin();  // the kernel ahead writes the rows' codes and scales
     for (int it = first; it < items && ok; it += step) {
       item_at<kNT>(t, it, mblocks2, off, pre);
       const int mb = 2 * t.mb + rank;           // may be one past the last block: its rows read as 0,
@@ -397,11 +399,8 @@ cudaError_t launch_as(const CUtensorMap& map_w, const CUtensorMap& map_a, const 
                       cudaStream_t st) {
   const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(mm2_kernel<F32, SW>), kSmem2);
   if (e != cudaSuccess) return e;
-  if (P.early)
-    return launch_early(mm2_kernel<F32, SW>, dim3(2 * pairs), dim3(kThreads), kSmem2, st, map_w, map_a, map_a128, map_ws,
-                        map_as, P);
-  mm2_kernel<F32, SW><<<2 * pairs, kThreads, kSmem2, st>>>(map_w, map_a, map_a128, map_ws, map_as, P);
-  return cudaGetLastError();
+  return launch_early(mm2_kernel<F32, SW>, dim3(2 * pairs), dim3(kThreads), kSmem2, st, map_w, map_a, map_a128, map_ws,
+                      map_as, P);
 }
 
 }  // namespace

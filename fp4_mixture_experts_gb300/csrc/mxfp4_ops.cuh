@@ -36,6 +36,16 @@ cudaError_t ops_norm_error(int32_t* word, bool clear, cudaStream_t st);
 
 #ifdef __CUDACC__
 
+// The operators' kernels are launched early, so that a chain of them pays for a
+// launch while the kernel before still runs, and begin with this (every
+// thread): wait until all work before has ended and is visible, then let the
+// next kernel be set up.  In this order: a kernel that starts early knows that
+// everything before the kernel ahead of it has ended.
+__device__ __forceinline__ void griddep_begin() {
+  griddep_wait();
+  griddep_launch_dependents();
+}
+
 // eight fp32 values -> eight E2M1 codes, element 0 in the low nibble
 __device__ __forceinline__ uint32_t e2m1x8(const float* v) {
   uint32_t r;

@@ -58,7 +58,7 @@ __device__ __forceinline__ int source_row(const QuantParams& P, int r) {
 // took 63 us.
 template <bool F32, bool VEC, bool TILED>
 __global__ void __launch_bounds__(kThreads) mxfp4_quantize_rows_kernel(const QuantParams P) {
-  griddep_launch_dependents();  // a product that waits for these rows may be set up meanwhile
+  griddep_begin();
   const int per_row = P.K / kPer, nb = P.K / 32, kt = (P.K + 127) / 128;
   const int lane = threadIdx.x & 31, warps = gridDim.x * (kThreads / 32);
   bool bad = false;
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) mxfp4_quantize_rows_kernel(const Qua
 // Few or short rows: flat over the chunks of 16 elements
 template <bool F32, bool VEC, bool TILED>
 __global__ void __launch_bounds__(kThreads) mxfp4_quantize_flat_kernel(const QuantParams P) {
-  griddep_launch_dependents();
+  griddep_begin();
   const int per_row = P.K / kPer, nb = P.K / 32, kt = (P.K + 127) / 128;
   const uint32_t total = (uint32_t)P.rows * per_row;  // rows K < 2^35
   // whole warps leave the loop together (the shuffle needs both lanes of a block)
@@ -162,7 +162,7 @@ mxfp4_gather_kernel(const QuantParams P, const uint8_t* __restrict__ codes, cons
       bad |= src[i] < 0;
       tile[i] = i < n ? tile_row(P, (int)r0 + i, kt) : nullptr;
     }
-    if (!waited) {  // the kernel ahead writes the source rows
+    if (!waited) {  // the kernel ahead writes the source rows (what was before that has ended: griddep_begin)
       griddep_wait();
       griddep_launch_dependents();
       waited = true;
@@ -208,6 +208,7 @@ template <bool F32>
 __global__ void __launch_bounds__(kThreads)
 mxfp4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t total,
                         void* __restrict__ out) {
+  griddep_begin();
   // one thread: 8 elements, 4 bytes of codes
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
     const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
@@ -238,6 +239,7 @@ mxfp4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __rest
 __global__ void __launch_bounds__(kThreads)
 tile_scales_kernel(const uint8_t* __restrict__ scales, int N, int nb, int rt, int kt, int swiglu, int64_t words,
                    uint32_t* __restrict__ tiled) {
+  griddep_begin();
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < words; i += (int64_t)gridDim.x * kThreads) {
     const int w = (int)(i & 127);                  // word of the tile: row (w % 4) * 32 + w / 4
     const int64_t t = i >> 7;
@@ -268,10 +270,10 @@ template <bool F32, bool VEC, bool TILED>
 cudaError_t launch_quant(const QuantParams& P, cudaStream_t st) {
   // a warp a row where that fills the SMs (8 rows each at least) and most lanes
   if (P.K >= 512 && P.rows >= 8 * num_sms())
-    mxfp4_quantize_rows_kernel<F32, VEC, TILED><<<grid_for(P.rows * 32, 8), kThreads, 0, st>>>(P);
-  else
-    mxfp4_quantize_flat_kernel<F32, VEC, TILED><<<grid_for(P.rows * (P.K / kPer), 8), kThreads, 0, st>>>(P);
-  return cudaGetLastError();
+    return launch_early(mxfp4_quantize_rows_kernel<F32, VEC, TILED>, dim3(grid_for(P.rows * 32, 8)), dim3(kThreads), 0,
+                        st, P);
+  return launch_early(mxfp4_quantize_flat_kernel<F32, VEC, TILED>, dim3(grid_for(P.rows * (P.K / kPer), 8)),
+                      dim3(kThreads), 0, st, P);
 }
 
 template <bool F32>
@@ -359,11 +361,10 @@ int moe_fp4_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const int64_t total = rows * (K / 8);
   const int grid = grid_for(total, 16);
-  if (out_type == MOE_FP4_TYPE_F32)
-    mxfp4_dequantize_kernel<true><<<grid, kThreads, 0, st>>>(codes, scales, total, out);
-  else
-    mxfp4_dequantize_kernel<false><<<grid, kThreads, 0, st>>>(codes, scales, total, out);
-  return cudaGetLastError() == cudaSuccess ? MOE_FP4_OK : MOE_FP4_ERR_CUDA;
+  return launch_early(out_type == MOE_FP4_TYPE_F32 ? mxfp4_dequantize_kernel<true> : mxfp4_dequantize_kernel<false>,
+                      dim3(grid), dim3(kThreads), 0, st, codes, scales, total, out) == cudaSuccess
+             ? MOE_FP4_OK
+             : MOE_FP4_ERR_CUDA;
 }
 
 int moe_fp4_mxfp4_tile_scales(const uint8_t* scales, int32_t E, int32_t N, int32_t K, int swiglu, uint8_t* tiled,
@@ -373,9 +374,11 @@ int moe_fp4_mxfp4_tile_scales(const uint8_t* scales, int32_t E, int32_t N, int32
     return MOE_FP4_ERR_INVALID_ARG;
   const int rt = (N + 127) / 128, kt = (K + 127) / 128;
   const int64_t words = (int64_t)E * rt * kt * 128;
-  tile_scales_kernel<<<grid_for(words, 16), kThreads, 0, static_cast<cudaStream_t>(cuda_stream)>>>(
-      scales, N, K / 32, rt, kt, swiglu, words, reinterpret_cast<uint32_t*>(tiled));
-  return cudaGetLastError() == cudaSuccess ? MOE_FP4_OK : MOE_FP4_ERR_CUDA;
+  return launch_early(tile_scales_kernel, dim3(grid_for(words, 16)), dim3(kThreads), 0,
+                      static_cast<cudaStream_t>(cuda_stream), scales, N, K / 32, rt, kt, swiglu, words,
+                      reinterpret_cast<uint32_t*>(tiled)) == cudaSuccess
+             ? MOE_FP4_OK
+             : MOE_FP4_ERR_CUDA;
 }
 
 int moe_fp4_ops_check(void* cuda_stream) {
