@@ -454,12 +454,12 @@ int moe_fp4_mxfp4_linear(const moe_fp4_mm_dims* dims, const void* x, int x_type,
   if (rc != MOE_FP4_OK || d.M == 0) return rc;
   rc = check_mm_pointers(d, w, w_scales, y, offsets);
   if (rc != MOE_FP4_OK) return rc;
-  if (!workspace || ((uintptr_t)workspace & 255)) return MOE_FP4_ERR_INVALID_ARG;
-  if (workspace_bytes < moe_fp4_mxfp4_linear_workspace_bytes(dims)) return MOE_FP4_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   if (few_rows(d, offsets))
     return launch_few(d, params(d, nullptr, nullptr, w_scales, y), &R, nullptr, w, st) == cudaSuccess ? MOE_FP4_OK
                                                                                                      : MOE_FP4_ERR_CUDA;
+  if (!workspace || ((uintptr_t)workspace & 255)) return MOE_FP4_ERR_INVALID_ARG;
+  if (workspace_bytes < moe_fp4_mxfp4_linear_workspace_bytes(dims)) return MOE_FP4_ERR_WORKSPACE;
   uint8_t* codes = static_cast<uint8_t*>(workspace);
   uint8_t* scales = codes + align256((size_t)d.M * (d.K / 2));
   const size_t base = moe_fp4_mxfp4_linear_workspace_bytes(dims), once = once_bytes(R);

@@ -351,7 +351,7 @@ struct Epilogue {
 
 // the kernel for few rows of one matrix, M <= kFewRows (mxfp4_mm1.cu): rows x
 // to quantise, or (x null) their codes with P.a_scales
-constexpr int kFewRows = 16;
+constexpr int kFewRows = MOE_FP4_MXFP4_FEW_ROWS;
 cudaError_t launch_mm_few(const CUtensorMap& map_w, const mm::MmParams& P, const MxRows* x, const uint8_t* codes,
                           cudaStream_t st);
 // the pair kernel (mxfp4_mm2.cu); the boxes of map_a have 32 rows, those of

@@ -406,7 +406,9 @@ int moe_fp4_mxfp4_matmul(const moe_fp4_mm_dims* dims, const uint8_t* a, const ui
                          void* cuda_stream);
 
 /* Device workspace of moe_fp4_mxfp4_linear (the codes and scales of the
- * quantised rows; 256-byte aligned base); 0 for unsupported sizes. */
+ * quantised rows; 256-byte aligned base); 0 for unsupported sizes.  Products of
+ * at most MOE_FP4_MXFP4_FEW_ROWS rows without offsets use none: it may be NULL. */
+#define MOE_FP4_MXFP4_FEW_ROWS 16
 size_t moe_fp4_mxfp4_linear_workspace_bytes(const moe_fp4_mm_dims* dims);
 
 /* The same for a call that gathers its rows (row_index) from x_rows rows: with

@@ -375,3 +375,23 @@ def test_rows_used_several_times_are_quantised_once_with_the_same_bits():
     for e in range(E):
         if counts[e]:
             check_product(got[1][o[e]:o[e + 1]], a[o[e]:o[e + 1]], O.values(w[e].cpu().numpy(), ws[e]), False, f"expert {e}")
+
+
+def test_a_given_stream_owns_what_a_call_allocates():
+    """results and workspaces of a call with stream= are not handed to the current stream's work while it runs"""
+    rng = np.random.default_rng(33)
+    M, N, K = 300, 512, 2048
+    x = rows(rng, M, K)
+    w, ws = weights(rng, 1, N, K)
+    w, wt = gpu(w), moe.mxfp4_tile_scales(gpu(ws))
+    want = moe.mxfp4_linear(x, w, wt)
+    size = moe.mxfp4_linear_workspace_bytes(M, N, K)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(50):
+        got = [moe.mxfp4_linear(x, w, wt, stream=s) for _ in range(4)]
+        junk = [torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV) for _ in range(4)]  # on the current stream
+        s.synchronize()
+        for y in got:
+            assert torch.equal(y, want)
+        del got, junk

@@ -58,7 +58,7 @@ def test_dequantize_and_scale_layout(lib):
 
 
 def test_products(lib):
-    dims = dict(M=4, N=8, K=64, E=1, swiglu=0, y_type=0)
+    dims = dict(M=40, N=8, K=64, E=1, swiglu=0, y_type=0)
 
     def matmul(a=FAKE, s=FAKE, off=None, w=FAKE, ws=FAKE, y=FAKE, null_dims=False, **kw):
         d = MmDims(*{**dims, **kw}.values())
@@ -72,18 +72,19 @@ def test_products(lib):
     assert matmul(M=0, a=None, w=None, y=None) == 0
     assert matmul(M=1 << 30, K=64, N=1 << 20) == -2
 
-    def linear(x=FAKE, xt=0, x_rows=4, stride=64, index=None, div=1, off=None, w=FAKE, ws=FAKE, y=FAKE, work=FAKE, size=1 << 30,
+    def linear(x=FAKE, xt=0, x_rows=40, stride=64, index=None, div=1, off=None, w=FAKE, ws=FAKE, y=FAKE, work=FAKE, size=1 << 30,
                **kw):
         d = MmDims(*{**dims, **kw}.values())
         return lib.moe_fp4_mxfp4_linear(ctypes.byref(d), x, xt, x_rows, stride, index, div, off, w, ws, y, work, size, None)
 
-    need = moe.mxfp4_linear_workspace_bytes(4, 8, 64)
-    assert need > 0 and moe.mxfp4_linear_workspace_bytes(4, 8, 65) == 0
-    for bad in (dict(x=None), dict(xt=3), dict(x_rows=3), dict(stride=32), dict(index=FAKE, div=0), dict(w=None), dict(y=None),
+    need = moe.mxfp4_linear_workspace_bytes(40, 8, 64)
+    assert need > 0 and moe.mxfp4_linear_workspace_bytes(40, 8, 65) == 0
+    for bad in (dict(x=None), dict(xt=3), dict(x_rows=39), dict(stride=32), dict(index=FAKE, div=0), dict(w=None), dict(y=None),
                 dict(work=None), dict(work=FAKE + 16), dict(E=2), dict(K=33)):
         assert linear(**bad) == -1, bad
     assert linear(size=need - 1) == -3
     assert linear(M=0, x=None, work=None) == 0
+    assert linear(M=16, x_rows=16, E=2, off=FAKE, work=None) == -1  # few rows need none, but not with offsets
 
 
 def test_block_norm(lib):
