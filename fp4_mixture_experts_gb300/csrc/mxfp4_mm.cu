@@ -148,7 +148,8 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
         griddep_wait();
         griddep_launch_dependents();
         waited = true;
-        for (; ks < early; ++ks, ++g, ring.next()) load_a(ks, ks);
+        for (; ks < early; ++ks, ++g, ring.next())
+          if (!(P.fault && blockIdx.x == 0 && ks == 0)) load_a(ks, ks);
       }
       for (; ks < nks; ++ks, ++g, ring.next()) {
         if (!warp_wait(&empty[ring.s], ring.phase ^ 1, abort_flag, P)) {
@@ -324,6 +325,7 @@ MmParams params(const moe_fp4_mm_dims& d, const uint8_t* as, const int32_t* offs
   P.swiglu = d.swiglu;
   P.vec = P.n_out % 2 == 0 && ((uintptr_t)y & 3) == 0;
   P.split = 1;
+  P.fault = fault_site() == MOE_FP4_FAULT_TC_TOKEN_TILE;
   P.wait_ns = wait_limit_ns();
   return P;
 }

@@ -33,6 +33,7 @@ struct MmParams {
   int vec;                   // rows of y start on 4 bytes and have an even number of features
   int split;                 // CTAs of a cluster that share an item's K (1: none)
   int rows_ahead;            // the kernel ahead writes the rows (a and a_scales); all before it has ended
+  int fault;                 // nonzero: the first CTA withholds its first stage (fault-injection test)
   uint64_t wait_ns;
 };
 

@@ -36,13 +36,18 @@ constexpr int kRows = kFewRows;
 constexpr int kATile = kBM * 128;
 constexpr int kBTile = kRows * 128;
 constexpr int kStage = kATile + kBTile + 4 * kSfTile;
-constexpr int kStages = 10;
 constexpr int kPartPitch = kBM + 4;  // floats of a token's partial sums
-constexpr int kOffPart = kStages * kStage;
-constexpr int kOffBar = kOffPart + kRows * kPartPitch * 4;
-constexpr int kSmem1 = kOffBar + 512 + 1024;
+// Ring stages: 5 where a CTA has no more (two CTAs then fit an SM, and the next
+// launch is set up while this one runs), else 10.
+template <int S>
+struct Cfg {
+  static constexpr int kOffPart = S * kStage;
+  static constexpr int kOffBar = kOffPart + kRows * kPartPitch * 4;
+  static constexpr int kSmem = kOffBar + 512 + 1024;
+  static_assert(kSmem <= (S <= 5 ? kSmemMax / 2 : kSmemMax) && kRows + 16 * S <= 256, "layout");
+};
 constexpr uint32_t kCols1 = 256;     // tensor memory: 16 accumulator columns, 16 of scales a stage
-static_assert(kStage % 1024 == 0 && kSmem1 <= kSmemMax && kRows + 16 * kStages <= (int)kCols1, "layout");
+static_assert(kStage % 1024 == 0, "stages stay 1 KB aligned for the 128-byte swizzle");
 
 struct Mm1Params {
   MmParams m;
@@ -71,15 +76,15 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
 }
 
 // SRC 0: bf16 rows, 1: fp32 rows, 2: codes with tiled scales
-template <int SRC, bool F32, bool SW>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int kStages, int SRC, bool F32, bool SW>
+__global__ void __launch_bounds__(kThreads, kStages <= 5 ? 2 : 1)
 mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
   MmParams& P = Q.m;
   P.err = &g_mm1_err[0];
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* part = reinterpret_cast<float*>(smem + kOffPart);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);  // [stage]: weights landed
+  float* part = reinterpret_cast<float*>(smem + Cfg<kStages>::kOffPart);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg<kStages>::kOffBar);  // [stage]: weights landed
   uint64_t* written = full + kStages;                            // [stage]: rows written
   uint64_t* empty = written + kStages;                           // [stage]: its MMAs completed
   uint64_t* acc_full = empty + kStages;
@@ -115,7 +120,8 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
     }
     __syncwarp();
     griddep_wait();
-    for (int i = 0; i < min(kStages, k1 - k0); ++i) load_weights(k0 + i, i);
+    for (int i = 0; i < min(kStages, k1 - k0); ++i)
+      if (!(P.fault && blockIdx.x == 0 && i == 0)) load_weights(k0 + i, i);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -176,7 +182,7 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
     // ---------------- writers: rows into the stages ----------------
     // A pass covers 256 chunks of 16 elements (8 bytes of codes): 16 a row and
     // stage, so that with few rows one pass covers several stages.  A pass's
-    // rows are loaded before the last one's are quantised.
+    // rows are loaded two passes before they are quantised.
     const int tid = threadIdx.x - 128;
     int per_log = 4;                                           // chunks of a stage: its rows, rounded up to a
     while ((16 << (per_log - 4)) < 16 * P.M) ++per_log;        // power of two, times 16
@@ -196,8 +202,8 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
       }
       if (src > 0) src *= Q.x_stride;
     }
-    uint32_t raw[16];
-    auto load = [&](int ks) {  // this thread's chunk of the pass from stage ks on
+    uint32_t next[2][16];
+    auto load = [&](int ks, uint32_t (&raw)[16]) {  // this thread's chunk of the pass from stage ks on
 #pragma unroll
       for (int j = 0; j < 16; ++j) raw[j] = 0;
       const int k = (ks + sub) * kStageK + c * 16;
@@ -212,15 +218,19 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
         load16_raw<SRC == 1, false>(Q.x, src + k, raw);
       }
     };
-    load(k0);
+    load(k0, next[0]);
+    load(k0 + group, next[1]);
     Ring<kStages> ring;
     bool ok = true;
     for (int ks = k0; ks < k1 && ok; ks += group) {
       const int here = min(group, k1 - ks);
       uint32_t cur[16], sb;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) cur[j] = raw[j];
-      if (ks + group < k1) load(ks + group);
+      for (int j = 0; j < 16; ++j) {
+        cur[j] = next[0][j];
+        next[0][j] = next[1][j];
+      }
+      load(ks + 2 * group, next[1]);
       uint2 q;
       if (SRC == 2) {
         q = make_uint2(cur[0], cur[1]);
@@ -234,8 +244,7 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
         if (ks - k0 + i >= kStages) ok = warp_wait(&empty[at.s], at.phase ^ 1, abort_flag, P);
       if (!ok) break;
       if (mine && sub < here) {
-        const int s = ring.s + sub < kStages ? ring.s + sub : ring.s + sub - kStages;
-        uint8_t* st = smem + s * kStage;
+        uint8_t* st = smem + (ring.s + sub < kStages ? ring.s + sub : ring.s + sub - kStages) * kStage;
         // 128-byte swizzle: the 16-byte chunk at (c / 2) ^ (row % 8); past the end of K codes and scales are 0
         *reinterpret_cast<uint2*>(st + kATile + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8) = q;
         if ((c & 1) == 0) st[kATile + kBTile + (2 + (c >> 3)) * kSfTile + 16 * row + ((c >> 1) & 3)] = (uint8_t)sb;
@@ -289,10 +298,10 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
   }
 }
 
-template <int SRC, bool F32, bool SW>
+template <int S, int SRC, bool F32, bool SW>
 cudaError_t launch_as(const CUtensorMap& map_w, const Mm1Params& Q, cudaStream_t st) {
-  auto* k = mm1_kernel<SRC, F32, SW>;
-  const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(k), kSmem1);
+  auto* k = mm1_kernel<S, SRC, F32, SW>;
+  const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(k), Cfg<S>::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -303,17 +312,25 @@ cudaError_t launch_as(const CUtensorMap& map_w, const Mm1Params& Q, cudaStream_t
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = Q.m.mblocks * Q.m.split;
   cfg.blockDim = kThreads;
-  cfg.dynamicSmemBytes = kSmem1;
+  cfg.dynamicSmemBytes = Cfg<S>::kSmem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, k, map_w, Q);
 }
 
+template <int SRC, bool F32, bool SW>
+cudaError_t launch_stages(const CUtensorMap& map_w, const Mm1Params& Q, cudaStream_t st) {
+  const int nks = (Q.m.K + kStageK - 1) / kStageK;
+  return (nks + Q.m.split - 1) / Q.m.split <= 5 ? launch_as<5, SRC, F32, SW>(map_w, Q, st)
+                                                : launch_as<10, SRC, F32, SW>(map_w, Q, st);
+}
+
 template <int SRC>
 cudaError_t launch_src(const CUtensorMap& map_w, const Mm1Params& Q, cudaStream_t st) {
-  if (Q.m.f32) return Q.m.swiglu ? launch_as<SRC, true, true>(map_w, Q, st) : launch_as<SRC, true, false>(map_w, Q, st);
-  return Q.m.swiglu ? launch_as<SRC, false, true>(map_w, Q, st) : launch_as<SRC, false, false>(map_w, Q, st);
+  if (Q.m.f32)
+    return Q.m.swiglu ? launch_stages<SRC, true, true>(map_w, Q, st) : launch_stages<SRC, true, false>(map_w, Q, st);
+  return Q.m.swiglu ? launch_stages<SRC, false, true>(map_w, Q, st) : launch_stages<SRC, false, false>(map_w, Q, st);
 }
 
 }  // namespace

@@ -230,6 +230,7 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
           ok = false;
           break;
         }
+        if (P.fault && blockIdx.x <= 1 && g == 0) continue;
         uint8_t* st = smem + ring.s * kStage;
         const uint32_t bar = in_leader(&full[ring.s]);
         if (warp == 0) {

@@ -180,3 +180,16 @@ def test_many_rows_strided_in_place_without_norms_and_rms_norm(d):
     close(out, ref, err, "out")
     assert torch.equal(buf[:, d:], keep)
     moe.ops_check()
+
+
+def test_offsets_beyond_32_bits():
+    rng = np.random.default_rng(4)
+    T, d = 140000, 16384
+    r = torch.zeros(T, d, dtype=BF, device=DEV)
+    y = torch.zeros(T, d, dtype=BF, device=DEV)
+    r[-3:], y[-3:] = rand(rng, (3, d), BF), rand(rng, (3, d), BF)
+    o, oe, n, ne = reference(r[-3:], y[-3:], None, True, None, None, False, 1.0, None, 1e-6)
+    out, normed = moe.block_residual(r, y)
+    close(out[-3:], o, oe, "out")
+    close(normed[-3:], n, ne, "normed")
+    assert not out[:16].any()

@@ -395,3 +395,74 @@ def test_a_given_stream_owns_what_a_call_allocates():
         for y in got:
             assert torch.equal(y, want)
         del got, junk
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("M", [1, 5, 16, 17, 90])
+@pytest.mark.parametrize("K,pad,shift", [(544, 24, 8), (1056, 3, 1)])
+def test_linear_strided_and_unaligned_rows(M, K, pad, shift, f32):
+    rng = np.random.default_rng(M + K)
+    buf = rows(rng, M, K + 32, f32)[:, :K + pad].contiguous()
+    x = buf[:, shift:shift + K - 32]
+    K -= 32
+    w, ws = weights(rng, 1, 130, K)
+    y = moe.mxfp4_linear(x, gpu(w), moe.mxfp4_tile_scales(gpu(ws)), dtype=torch.float32)
+    check_product(y, O.values(*O.quantize(f64(x))), O.values(w[0], ws[0]), False, "strided")
+
+
+@pytest.mark.parametrize("M", [3, 16, 40])
+def test_linear_gathers_without_groups(M):
+    rng = np.random.default_rng(M)
+    x = rows(rng, 9, 288)
+    index = rng.integers(0, 18, M).astype(np.int32)
+    index[1] = 18                                       # out of range: a zero row, and an error
+    w, ws = weights(rng, 1, 66, 288)
+    y = moe.mxfp4_linear(x, gpu(w), moe.mxfp4_tile_scales(gpu(ws)), row_index=gpu(index), index_div=2, dtype=torch.float32)
+    with pytest.raises(moe.MoeFp4Error):
+        moe.ops_check()
+    a = O.values(*O.quantize(f64(x)))[np.minimum(index, 17) // 2]
+    a[1] = 0
+    check_product(y, a, O.values(w[0], ws[0]), False, "gathered")
+    assert not y[1].any()
+
+
+@pytest.mark.parametrize("M", [4, 60, 120, 2000])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(M):
+    """host-planted: the first CTA never loads its first stage (no fault on the GPU); every waiting role gives up"""
+    rng = np.random.default_rng(M)
+    N, K = (256, 1024) if M < 2000 else (4096, 1024)
+    x = rows(rng, M, K)
+    w, ws = weights(rng, 1, N, K)
+    w, wt = gpu(w), moe.mxfp4_tile_scales(gpu(ws))
+    want = moe.mxfp4_linear(x, w, wt)
+    moe.ops_check()
+    moe.set_fault_injection(moe.FAULT_TC_TOKEN_TILE, 2000)
+    try:
+        moe.mxfp4_linear(x, w, wt)
+        torch.cuda.synchronize()
+    finally:
+        moe.set_fault_injection(moe.FAULT_NONE)
+    with pytest.raises(moe.MoeFp4Error):
+        moe.ops_check()
+    assert torch.equal(moe.mxfp4_linear(x, w, wt), want)
+    moe.ops_check()
+
+
+def test_offsets_beyond_32_bits():
+    """more than 2^31 elements of rows, codes and results: the last rows are right"""
+    rng = np.random.default_rng(5)
+    last = 5
+    x = torch.zeros(70016, 32768, dtype=torch.bfloat16, device=DEV)
+    x[-last:] = rows(rng, last, 32768)
+    codes, scales = moe.mxfp4_quantize(x)
+    want_c, want_s = O.quantize(f64(x[-last:]))
+    np.testing.assert_array_equal(codes[-last:].cpu().numpy(), want_c)
+    np.testing.assert_array_equal(scales[-last:].cpu().numpy(), want_s)
+    back = moe.mxfp4_dequantize(codes, scales)
+    np.testing.assert_array_equal(f64(back[-last:]), O.values(want_c, want_s))
+    del back, codes, scales
+    w, ws = weights(rng, 1, 32768, 64)
+    y = moe.mxfp4_linear(x[:, -64:], gpu(w), moe.mxfp4_tile_scales(gpu(ws)))
+    check_product(y[-last:], O.values(*O.quantize(f64(x[-last:, -64:]))), O.values(w[0], ws[0]), False, "last rows")
+    assert not y[:64].any()
+    moe.ops_check()
