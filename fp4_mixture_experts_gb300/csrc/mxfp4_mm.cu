@@ -19,10 +19,20 @@
 // extent 2 between K and the feature), so that a pair of lanes holds the gate
 // and the up value of one feature.
 //
+// This kernel, one SM a tile, serves groups of up to some 100 rows and dense
+// products that cannot fill the SM pairs of mxfp4_mm2.cu.  There reading the
+// weights bounds it: the experts' W13 of a 32-token batch (256 x 4096 x 4096, 1.5
+// GB touched) takes 210 us, 6.9 TB/s.  What it took beyond a simple ring: uniform
+// issue (elect_one), descriptors as sums, the epilogue in registers, and for few
+// rounds the start: the first stages' weights are loaded while the kernel ahead
+// still quantises the rows (333 x 1056 x 1000, fp32: 13.2 -> 5.9 us with the
+// smaller tiles that choose_tile picks).
+//
 // Warp roles: 0 the TMA producer, 1 the MMA issuer (and owner of tensor
-// memory), 2..5 the epilogue.  All waits are bounded; on a timeout every role
-// leaves its loop, and copies and MMAs in flight end before memory is given
-// back.
+// memory), 4..11 the epilogue.  Two accumulators, so that the epilogue of one
+// item runs beside the MMAs of the next.  All waits are bounded; on a timeout
+// every role leaves its loop, and copies and MMAs in flight end before memory
+// is given back.
 #include <cuda.h>
 
 #include <algorithm>
@@ -44,21 +54,23 @@ template <int NT>
 struct Cfg {
   static constexpr int kATile = kBM * 128;
   static constexpr int kBTile = NT * 128;
-  static constexpr int kSfB = (NT + 127) / 128;              // scale tiles of the token rows, per K = 128
-  static constexpr int kStage = kATile + kBTile + 2 * kSfTile * (1 + kSfB);
-  static constexpr int kSfCols = 2 * 4 * (1 + kSfB);         // tensor-memory columns of a stage's scales
-  static constexpr int kAccs = NT <= 128 ? 2 : 1;            // accumulators (double buffered where they fit)
+  static constexpr int kStage = kATile + kBTile + 4 * kSfTile;
+  static constexpr int kSfCols = 16;                         // tensor-memory columns of a stage's scales
   static constexpr int kGroupBytes = 2 * (kMaxGroups + 1) * 4;
   static constexpr int kFixed = 1024 + 512 + kGroupBytes;
   static constexpr int kByMem = (kSmemMax - kFixed) / kStage;
-  static constexpr int kByTmem = ((int)kTmemCols - kAccs * NT) / kSfCols;
+  static constexpr int kByTmem = ((int)kTmemCols - 2 * NT) / kSfCols;
   static constexpr int kStages = kByMem < kByTmem ? kByMem : kByTmem;
   static constexpr int kSmem = kStages * kStage + kFixed;
+  static_assert(NT <= 128, "a token tile's rows lie in one scale tile");
   static_assert(kStage % 1024 == 0, "stages stay 1 KB aligned for the 128-byte swizzle");
   static_assert(kStages >= 3, "ring too short");
 };
 
-template <int NT, bool F32, bool SW>
+// SPLIT: a dense product with too few tiles for the SMs.  The CTAs of a cluster
+// share one tile's K; their partial sums meet in rank order through distributed
+// shared memory, each CTA summing every split-th token.
+template <int NT, bool F32, bool SW, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, MmParams P) {
   P.err = &g_mm_err[0];
@@ -104,18 +116,21 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
-  const uint32_t sf_base = tmem + C::kAccs * NT;
+  const uint32_t sf_base = tmem + 2 * NT;
   const int items = uniform(pre[P.E]) * P.mblocks;
-  const int nks = (P.K + kStageK - 1) / kStageK;
+  // this CTA's items, and its stages of K
+  const int rank = SPLIT ? uniform((int)cluster_rank()) : 0;
+  const int first = SPLIT ? blockIdx.x / P.split : blockIdx.x, step = SPLIT ? items : gridDim.x;
+  const int all_ks = (P.K + kStageK - 1) / kStageK;
+  const int k0 = SPLIT ? all_ks * rank / P.split : 0, k1 = SPLIT ? all_ks * (rank + 1) / P.split : all_ks;
 
   if (warp == 0) {
     Item t{};
     Ring<kStages> ring;
     int g = 0;
     bool ok = true, waited = false;
-    for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+    for (int it = first; it < items && ok; it += step) {
       item_at<NT>(t, it, P.mblocks, off, pre);
-      const int sf_rows = t.n > 128 ? 2 : 1;
       const uint8_t* ws = P.w_scales + ((size_t)t.g * P.mblocks + t.mb) * P.kt * kSfTile;
       const uint8_t* as = P.a_scales + ((size_t)((uniform(off[t.g]) >> 7) + t.g + (t.local >> 7))) * P.kt * kSfTile;
       const int wrow = t.mb * (SW ? 64 : 128);
@@ -123,7 +138,7 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
         if (elect_one()) {
           uint8_t* st = smem + s * C::kStage;
           const uint32_t sf_bytes = min(2, P.kt - 2 * ks) * kSfTile;
-          mbar_expect_tx(&full[s], C::kATile + C::kBTile + sf_bytes * (1 + sf_rows));
+          mbar_expect_tx(&full[s], C::kATile + C::kBTile + 2 * sf_bytes);
           tma_load_4d(st, &map_w, ks * 128, 0, wrow, t.g, &full[s]);
           bulk_load(st + C::kATile + C::kBTile, ws + ks * 2 * kSfTile, sf_bytes, &full[s]);
         }
@@ -134,24 +149,22 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
           uint8_t* st = smem + s * C::kStage;
           const uint32_t sf_bytes = min(2, P.kt - 2 * ks) * kSfTile;
           tma_load_2d(st + C::kATile, &map_a, ks * 128, t.row0, &full[s]);
-          uint8_t* sf = st + C::kATile + C::kBTile;
-          for (int j = 0; j < sf_rows; ++j)
-            bulk_load(sf + (1 + j) * 2 * kSfTile, as + (j * P.kt + ks * 2) * kSfTile, sf_bytes, &full[s]);
+          bulk_load(st + C::kATile + C::kBTile + 2 * kSfTile, as + ks * 2 * kSfTile, sf_bytes, &full[s]);
         }
         __syncwarp();
       };
-      int ks = 0;
+      int ks = k0;
       if (!waited) {
         // the first stages' weights do not depend on the kernel that quantises the rows
-        const int early = min(kStages, nks);
-        for (int i = 0; i < early; ++i) load_w(i, i);
+        const int early = min(kStages, k1 - k0);
+        for (int i = 0; i < early; ++i) load_w(k0 + i, i);
         griddep_wait();
         griddep_launch_dependents();
         waited = true;
-        for (; ks < early; ++ks, ++g, ring.next())
-          if (!(P.fault && blockIdx.x == 0 && ks == 0)) load_a(ks, ks);
+        for (; g < early; ++ks, ++g, ring.next())
+          if (!(P.fault && blockIdx.x == 0 && g == 0)) load_a(ks, g);
       }
-      for (; ks < nks; ++ks, ++g, ring.next()) {
+      for (; ks < k1; ++ks, ++g, ring.next()) {
         if (!warp_wait(&empty[ring.s], ring.phase ^ 1, abort_flag, P)) {
           ok = false;
           break;
@@ -171,15 +184,15 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     int li = 0;
     bool ok = true;
     const uint32_t lo0 = desc_lo(smem_u32(smem));
-    for (int it = blockIdx.x; it < items && ok; it += gridDim.x, ++li) {
+    for (int it = first; it < items && ok; it += step, ++li) {
       item_at<NT>(t, it, P.mblocks, off, pre);
-      const int b = li % C::kAccs, use = li / C::kAccs;
+      const int b = li & 1, use = li >> 1;
       if (!warp_wait(&acc_empty[b], (use & 1) ^ 1, abort_flag, P)) break;
       const uint32_t d_tmem = tmem + b * NT;
       const int n_mma = (t.n + 15) & ~15;
       const uint32_t id0 = idesc_mxf4(kBM, n_mma, 0), id1 = idesc_mxf4(kBM, n_mma, 1);
       const uint32_t shift = (t.local & 127) >> 5;  // a 64-row tile may start in the middle of a scale tile
-      for (int ks = 0; ks < nks; ++ks, ring.next()) {
+      for (int ks = k0; ks < k1; ++ks, ring.next()) {
         if (!warp_wait(&full[ring.s], ring.phase, abort_flag, P)) {
           ok = false;
           break;
@@ -190,25 +203,19 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
           const uint32_t a_lo = lo | kDescLoSw128, b_lo = (lo + (C::kATile >> 4)) | kDescLoSw128;
           const uint32_t sf_lo = lo + ((C::kATile + C::kBTile) >> 4);
           const uint32_t sf_t = sf_base + ring.s * C::kSfCols;
-          // columns [4 c, 4 c + 4): weights of K chunk c (128 elements); 8 + 4 kSfB c on: the token rows' kSfB
-          // tiles.  Tiles past the end of K or of the rows copy what the stage holds; no MMA result that is kept
-          // depends on them.
+          // the weights' two K chunks (128 elements each), then the token rows'; a chunk past the end of K copies
+          // what the stage holds, and no MMA uses it
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            tmem_cp_scales<1>(sf_t + 4 * c, sf_lo + c * (kSfTile >> 4));
-#pragma unroll
-            for (int j = 0; j < C::kSfB; ++j)
-              tmem_cp_scales<1>(sf_t + 8 + 4 * (C::kSfB * c + j), sf_lo + ((1 + j) * 2 + c) * (kSfTile >> 4));
-          }
+          for (int i = 0; i < 4; ++i) tmem_cp_scales<1>(sf_t + 4 * i, sf_lo + i * (kSfTile >> 4));
           const int steps = (P.K - ks * kStageK + 63) / 64;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             if (kk < steps)
               umma_mxf4<1>(d_tmem, desc(a_lo + 2 * kk, kDescHiSw128), desc(b_lo + 2 * kk, kDescHiSw128),
-                           (kk & 1) ? id1 : id0, sf_t + 4 * (kk >> 1), sf_t + 8 + 4 * C::kSfB * (kk >> 1) + shift,
-                           kk > 0 ? 1u : (uint32_t)ks);
+                           (kk & 1) ? id1 : id0, sf_t + 4 * (kk >> 1), sf_t + 8 + 4 * (kk >> 1) + shift,
+                           kk > 0 ? 1u : (uint32_t)(ks - k0));
           umma_commit(&empty[ring.s]);
-          if (ks == nks - 1) umma_commit(&acc_full[b]);
+          if (ks == k1 - 1) umma_commit(&acc_full[b]);
         }
         __syncwarp();
       }
@@ -222,21 +229,41 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     E e(P, warp, lane);
     Item t{};
     int li = 0;
-    for (int it = blockIdx.x; it < items; it += gridDim.x, ++li) {
+    for (int it = first; it < items; it += step, ++li) {
       item_at<NT>(t, it, P.mblocks, off, pre);
-      const int b = li % C::kAccs, use = li / C::kAccs;
+      const int b = li & 1, use = li >> 1;
       const int f0 = t.mb * E::kFeatures, nf = min(E::kFeatures, P.n_out - f0);
       const bool ok = warp_wait(&acc_full[b], use & 1, abort_flag, P);
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      if (!e.item(P.y, tmem + b * NT, t.row0, t.n, f0, nf, 0, ok, [&](bool, bool last) {
-            if (last && lane == 0) mbar_arrive(&acc_empty[b]);
-          }))
+      if (SPLIT) {
+        // [token][weight row] to the stages' memory: all copies have landed and all MMAs that read it are done
+        float* const part = reinterpret_cast<float*>(smem);
+        for (int c0 = e.h * kTokens; ok && c0 < t.n; c0 += 2 * kTokens) {
+          uint32_t v[kTokens];
+          tmem_ld32_async(tmem + ((uint32_t)(e.q * 32) << 16) + c0, v);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+          for (int j = 0; j < kTokens; ++j) part[(c0 + j) * kPartPitch + e.q * 32 + lane] = __uint_as_float(v[j]);
+        }
+      } else if (!e.item(P.y, tmem + b * NT, t.row0, t.n, f0, nf, 0, ok, [&](bool, bool last) {
+                   if (last && lane == 0) mbar_arrive(&acc_empty[b]);
+                 })) {
         break;
+      }
     }
   }
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  if (SPLIT) {
+    cluster_sync();  // every CTA's partial sums are written
+    Item t{};
+    if (first < items) {
+      item_at<NT>(t, first, P.mblocks, off, pre);
+      sum_parts<F32, SW>(P, smem_u32(smem), rank, t.row0, t.n, t.mb, warp, lane);
+    }
+    cluster_sync();  // no CTA leaves while another may still read its sums
+  }
   if (warp == 1) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
@@ -258,11 +285,13 @@ bool make_a_map(const moe_fp4_mm_dims& d, const uint8_t* a, int rows, CUtensorMa
 }
 
 template <int NT, bool F32, bool SW>
-cudaError_t launch_as(const CUtensorMap& map_w, const CUtensorMap& map_a, const MmParams& P, int grid,
+cudaError_t launch_as(const CUtensorMap& map_w, const CUtensorMap& map_a, const MmParams& P, int items,
                       cudaStream_t st) {
-  const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(mm_kernel<NT, F32, SW>), Cfg<NT>::kSmem);
+  auto* k = P.split > 1 ? mm_kernel<NT, F32, SW, true> : mm_kernel<NT, F32, SW, false>;
+  const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(k), Cfg<NT>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_early(mm_kernel<NT, F32, SW>, dim3(grid), dim3(kThreads), Cfg<NT>::kSmem, st, map_w, map_a, P);
+  const int grid = P.split > 1 ? items * P.split : std::min(items, num_sms());
+  return launch_cluster_early(k, grid, P.split, kThreads, Cfg<NT>::kSmem, st, map_w, map_a, P);
 }
 
 template <int NT>
@@ -270,13 +299,14 @@ cudaError_t launch_nt(const moe_fp4_mm_dims& d, const uint8_t* a, const uint8_t*
                       cudaStream_t st) {
   CUtensorMap map_w, map_a;
   if (!make_w_map(d, w, &map_w) || !make_a_map(d, a, NT, &map_a)) return cudaErrorInvalidValue;
-  const int64_t most = ((int64_t)d.M / NT + std::min(d.E, d.M)) * P.mblocks;
-  const int grid = (int)std::min<int64_t>(most, num_sms());
+  // exactly, or for groups at most
+  const int64_t tiles = P.offsets ? (int64_t)d.M / NT + std::min(d.E, d.M) : ((int64_t)d.M + NT - 1) / NT;
+  const int items = (int)std::min<int64_t>(tiles * P.mblocks, INT32_MAX);
   if (P.f32)
-    return P.swiglu ? launch_as<NT, true, true>(map_w, map_a, P, grid, st)
-                    : launch_as<NT, true, false>(map_w, map_a, P, grid, st);
-  return P.swiglu ? launch_as<NT, false, true>(map_w, map_a, P, grid, st)
-                  : launch_as<NT, false, false>(map_w, map_a, P, grid, st);
+    return P.swiglu ? launch_as<NT, true, true>(map_w, map_a, P, items, st)
+                    : launch_as<NT, true, false>(map_w, map_a, P, items, st);
+  return P.swiglu ? launch_as<NT, false, true>(map_w, map_a, P, items, st)
+                  : launch_as<NT, false, false>(map_w, map_a, P, items, st);
 }
 
 cudaError_t launch_pairs(const moe_fp4_mm_dims& d, const uint8_t* a, const uint8_t* w, const MmParams& P,
@@ -348,24 +378,35 @@ cudaError_t launch_few(const moe_fp4_mm_dims& d, const MmParams& P, const MxRows
 // x 64 and 128 token rows on an SM and of 256 x 256 on a pair, whose launch
 // costs 1 more.  (M = 256, N = K = 4096: 9.4, 10.1 and 13.6 us; M = 2048: 36,
 // 26 and 24 us.)  The tiles of a group are estimated from the mean of the
-// groups' rows, half a standard deviation of a uniform routing taken off.
-int choose_tile(const moe_fp4_mm_dims& d) {
+// groups' rows, half a standard deviation of a uniform routing taken off.  A
+// dense product may split K over clusters of 2 or 4 CTAs (of 8, too few fit the
+// GPCs: 32 x 4096 x 2048 10 us), which costs 0.8 and 0.017 a token row.  (N = K =
+// 4096: M = 17 8.0 -> 6.3, 64 8.0 -> 7.1; K = 8192: M = 64 11.6 -> 8.7 us.)
+struct Choice {
+  int rows, split;
+};
+
+Choice choose_tile(const moe_fp4_mm_dims& d, bool grouped) {
   const int nks = (d.K + kStageK - 1) / kStageK, sms = num_sms();
   const double mean = (double)d.M / d.E;
   double best = 0;
-  int tile = 0;
+  Choice choice{0, 1};
   const struct {
     int rows, wrows, sms;
     double stage, item, launch;
   } kernels[] = {{64, 128, 1, 0.23, 0.9, 0}, {128, 128, 1, 0.24, 1.2, 0}, {256, 256, 2, 0.29, 3.2, 1}};
   for (const auto& k : kernels) {
-    const double rows = d.E == 1 ? mean : std::max(mean - 0.5 * std::sqrt(mean), 1.0);
+    const double rows = grouped ? std::max(mean - 0.5 * std::sqrt(mean), 1.0) : mean;
     const double tiles = std::min(std::ceil(rows / k.rows) * d.E, (double)d.M);
     const double items = tiles * ((d.N + k.wrows - 1) / k.wrows);
-    const double t = k.launch + std::ceil(items * k.sms / sms) * (nks * k.stage + k.item);
-    if (tile == 0 || t < best) best = t, tile = k.rows;
+    for (int split = 1; split <= 4; split *= 2) {
+      if (split > 1 && (grouped || k.sms > 1 || split * items > 0.85 * sms || nks < 2 * split)) break;
+      const double t = k.launch + (split > 1 ? 0.8 + 0.017 * std::min(d.M, k.rows) : 0) +
+                       std::ceil(items * k.sms / sms) * ((nks + split - 1) / split * k.stage + k.item);
+      if (choice.rows == 0 || t < best) best = t, choice = {k.rows, split};
+    }
   }
-  return tile;
+  return choice;
 }
 
 // rows_ahead: the kernel ahead of this one quantises the rows, to a and as
@@ -374,7 +415,9 @@ cudaError_t launch_mm(const moe_fp4_mm_dims& d, const uint8_t* a, const uint8_t*
   MmParams P = params(d, as, offsets, ws, y);
   P.rows_ahead = rows_ahead;
   if (few_rows(d, offsets)) return launch_few(d, P, nullptr, a, w, st);
-  switch (choose_tile(d)) {
+  const Choice c = choose_tile(d, offsets != nullptr);
+  P.split = c.split;
+  switch (c.rows) {
     case 64: return launch_nt<64>(d, a, w, P, st);
     case 128: return launch_nt<128>(d, a, w, P, st);
     default: return launch_pairs(d, a, w, P, st);

@@ -135,6 +135,63 @@ __device__ __forceinline__ uint32_t swap_pair(uint32_t p, int d, uint32_t sel) {
   return __byte_perm(p, __shfl_xor_sync(0xFFFFFFFFu, p, d), sel);
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// four floats of shared memory at this offset in CTA `rank` of the cluster
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+
+// K split over a cluster: the CTAs' partial sums [token][weight row] (floats,
+// kPartPitch apart, at the same offset `part` in each) summed in rank order; a
+// warp a token, four rows a lane, CTA `rank` the tokens rank, rank + split, ...
+constexpr int kPartPitch = kBM + 4;
+template <bool F32, bool SW>
+__device__ __forceinline__ void sum_parts(const MmParams& P, uint32_t part, int rank, int row0, int n, int mb, int warp,
+                                          int lane) {
+  constexpr int kF = SW ? kBM / 2 : kBM, kOwn = SW ? 2 : 4;  // features of a tile, of a lane
+  const int f = mb * kF + lane * kOwn, warps = blockDim.x >> 5;
+  for (int t = rank + warp * P.split; t < n; t += warps * P.split) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = 0; r < P.split; ++r) {
+      const float4 v = ld_cluster4(part + (t * kPartPitch + 4 * lane) * 4, r);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    float o[4] = {s.x, s.y, s.z, s.w};
+    if (SW) o[0] = swiglu(s.x, s.y), o[1] = swiglu(s.z, s.w);
+    const size_t at = (size_t)(row0 + t) * P.n_out + f;
+    if (!F32 && P.vec) {
+#pragma unroll
+      for (int j = 0; j < kOwn; j += 2)
+        if (f + j < P.n_out)
+          *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(P.y) + at + j) =
+              pack_bf16(__float_as_uint(o[j]), __float_as_uint(o[j + 1]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < kOwn; ++j)
+        if (f + j < P.n_out) {
+          if (F32)
+            static_cast<float*>(P.y)[at + j] = o[j];
+          else
+            static_cast<uint16_t*>(P.y)[at + j] = f32_to_bf16_rn(o[j]);
+        }
+    }
+  }
+}
+
 // One work item; every role walks the same sequence with its own cursor.
 struct Item {
   int g;        // group
@@ -349,6 +406,26 @@ struct Epilogue {
 };
 
 }  // namespace mm
+
+// launch_early with clusters of `cluster` CTAs
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster_early(void (*kernel)(KArgs...), int grid, int cluster, int threads, size_t smem,
+                                 cudaStream_t st, Args&&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = threads;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
+}
 
 // the kernel for few rows of one matrix, M <= kFewRows (mxfp4_mm1.cu): rows x
 // to quantise, or (x null) their codes with P.a_scales

@@ -36,7 +36,6 @@ constexpr int kRows = kFewRows;
 constexpr int kATile = kBM * 128;
 constexpr int kBTile = kRows * 128;
 constexpr int kStage = kATile + kBTile + 4 * kSfTile;
-constexpr int kPartPitch = kBM + 4;  // floats of a token's partial sums
 // Ring stages: 5 where a CTA has no more (two CTAs then fit an SM, and the next
 // launch is set up while this one runs), else 10.
 template <int S>
@@ -56,24 +55,6 @@ struct Mm1Params {
   const int32_t* row_index;
   int div, vec;              // vec: rows of x start on 16 bytes
 };
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
-  float v;
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n}"
-      : "=f"(v)
-      : "r"(addr), "r"(rank)
-      : "memory");
-  return v;
-}
 
 // SRC 0: bf16 rows, 1: fp32 rows, 2: codes with tiled scales
 template <int kStages, int SRC, bool F32, bool SW>
@@ -270,27 +251,7 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   cluster_sync();  // every CTA's partial sums are written
-  if (warp >= 4) {
-    // the sums over the cluster, in rank order, shared out among its CTAs
-    constexpr int kF = SW ? kBM / 2 : kBM;
-    const int f0 = mb * kF, nf = min(kF, P.n_out - f0);
-    for (int o = rank * kWriters * 32 + (threadIdx.x - 128); o < P.M * kF; o += P.split * kWriters * 32) {
-      const int t = o / kF, f = o % kF;
-      if (f >= nf) continue;
-      const uint32_t a = smem_u32(part + t * kPartPitch + (SW ? 2 * f : f));
-      float s = 0.f, u = 0.f;
-      for (int r = 0; r < P.split; ++r) {
-        s += ld_cluster(a, r);
-        if (SW) u += ld_cluster(a + 4, r);
-      }
-      if (SW) s = swiglu(s, u);
-      const size_t at = (size_t)t * P.n_out + f0 + f;
-      if (F32)
-        static_cast<float*>(P.y)[at] = s;
-      else
-        static_cast<uint16_t*>(P.y)[at] = f32_to_bf16_rn(s);
-    }
-  }
+  sum_parts<F32, SW>(P, smem_u32(part), rank, 0, P.M, mb, warp, lane);
   cluster_sync();  // no CTA leaves while another may still read its sums
   if (warp == 1) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -303,20 +264,7 @@ cudaError_t launch_as(const CUtensorMap& map_w, const Mm1Params& Q, cudaStream_t
   auto* k = mm1_kernel<S, SRC, F32, SW>;
   const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(k), Cfg<S>::kSmem);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = Q.m.split;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = Q.m.mblocks * Q.m.split;
-  cfg.blockDim = kThreads;
-  cfg.dynamicSmemBytes = Cfg<S>::kSmem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k, map_w, Q);
+  return launch_cluster_early(k, Q.m.mblocks * Q.m.split, Q.m.split, kThreads, Cfg<S>::kSmem, st, map_w, Q);
 }
 
 template <int SRC, bool F32, bool SW>

@@ -63,14 +63,6 @@ static_assert(kStage % 1024 == 0 && kStages >= 4, "ring");
 static_assert(kNT - kAcc1 <= 128 - 32 && kNT - kAcc1 / 32 * 32 <= 128, "the shared columns are in the first round's reads");
 static_assert(kSfBase >= kAcc1 + kNT && kSfBase + kSfSlots * kSfCols <= kTmemCols, "tensor memory columns");
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // arrive on the barrier at the same offset in the leader CTA
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
   asm volatile(
