@@ -424,16 +424,14 @@ cudaError_t launch_mm(const moe_fp4_mm_dims& d, const uint8_t* a, const uint8_t*
   }
 }
 
-// Bytes for the rows of x quantised once, before they are gathered; 0 where
-// that does not pay.  T = 4608 tokens, 8 rows each, K = 2048: 63 -> 15 us; below
-// 2^22 gathered elements the second launch costs more than it saves.
-size_t once_bytes(const MxRows& R);
-
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
+// Bytes of the lists with which rows of x that are used several times are
+// quantised once; 0 where that does not pay: three launches more, so from 2^22
+// gathered elements, and two uses of a row, on.
 size_t once_bytes(const MxRows& R) {
   if (!R.row_index || R.rows < 2 * R.x_rows || R.rows * R.K < (1LL << 22)) return 0;
-  return align256((size_t)R.x_rows * (R.K / 2)) + align256((size_t)R.x_rows * (R.K / 32));
+  return (size_t)(R.x_rows + 1 + R.rows) * sizeof(int32_t);
 }
 
 }  // namespace
@@ -507,11 +505,10 @@ int moe_fp4_mxfp4_linear(const moe_fp4_mm_dims* dims, const void* x, int x_type,
   if (workspace_bytes < moe_fp4_mxfp4_linear_workspace_bytes(dims)) return MOE_FP4_ERR_WORKSPACE;
   uint8_t* codes = static_cast<uint8_t*>(workspace);
   uint8_t* scales = codes + align256((size_t)d.M * (d.K / 2));
-  const size_t base = moe_fp4_mxfp4_linear_workspace_bytes(dims), once = once_bytes(R);
+  const size_t base = align256(moe_fp4_mxfp4_linear_workspace_bytes(dims)), once = once_bytes(R);
   const cudaError_t e =
-      once != 0 && workspace_bytes >= align256(base) + once
-          ? launch_mxfp4_quantize_once(R, codes + align256(base), codes + align256(base) + align256((size_t)x_rows * (d.K / 2)),
-                                       codes, scales, st)
+      once != 0 && workspace_bytes >= base + once
+          ? launch_mxfp4_quantize_once(R, reinterpret_cast<int32_t*>(codes + base), codes, scales, st)
           : launch_mxfp4_quantize(R, codes, scales, true, st);
   if (e != cudaSuccess) return MOE_FP4_ERR_CUDA;
   return launch_mm(d, codes, scales, offsets, w, w_scales, y, true, st) == cudaSuccess ? MOE_FP4_OK : MOE_FP4_ERR_CUDA;

@@ -23,10 +23,9 @@ struct MxRows {
 int check_mx_rows(const MxRows& R);  // a moe_fp4_status
 cudaError_t launch_mxfp4_quantize(const MxRows& R, uint8_t* codes, uint8_t* scales, bool tiled, cudaStream_t st);
 // The same result (tiled) for rows that are used several times: every row of x
-// is quantised once (row_codes [x_rows, K/2], 16-byte aligned, row_scales
-// [x_rows, K/32]), then gathered.
-cudaError_t launch_mxfp4_quantize_once(const MxRows& R, uint8_t* row_codes, uint8_t* row_scales, uint8_t* codes,
-                                       uint8_t* scales, cudaStream_t st);
+// is quantised once.  lists: x_rows + 1 + rows integers.
+cudaError_t launch_mxfp4_quantize_once(const MxRows& R, int32_t* lists, uint8_t* codes, uint8_t* scales,
+                                       cudaStream_t st);
 // the error words of the operators' kernels (one in each translation unit): read, or cleared
 cudaError_t ops_quant_error(int32_t* word, bool clear, cudaStream_t st);
 cudaError_t ops_mm_error(int32_t* word, bool clear, cudaStream_t st);

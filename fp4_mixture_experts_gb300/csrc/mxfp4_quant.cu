@@ -141,66 +141,87 @@ __global__ void __launch_bounds__(kThreads) mxfp4_quantize_flat_kernel(const Qua
   }
 }
 
-// Rows that are quantised already, gathered: a warp takes four rows together
-// (one at a time, the chain of index, loads and stores made 36,864 rows of 1 KB
-// take 22 us), 16 bytes of codes a lane and load; the scales (row-major, of the
-// source rows) go into their tiles.
-__global__ void __launch_bounds__(kThreads)
-mxfp4_gather_kernel(const QuantParams P, const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales) {
-  constexpr int kR = 4;
-  const int n16 = P.K / 32, kt = (P.K + 127) / 128, lane = threadIdx.x & 31;
-  const int warps = gridDim.x * (kThreads / 32);
-  bool bad = false, waited = false;
-  for (int64_t r0 = kR * (int64_t)(blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)); r0 < P.rows; r0 += kR * warps) {
-    const int n = (int)min((int64_t)kR, P.rows - r0);
-    int src[kR];
-    uint8_t* tile[kR];
-#pragma unroll
-    for (int i = 0; i < kR; ++i) {
-      src[i] = i < n ? source_row(P, (int)r0 + i) : 0;
-      bad |= src[i] < 0;
-      tile[i] = i < n ? tile_row(P, (int)r0 + i, kt) : nullptr;
-    }
-    if (!waited) {  // the kernel ahead writes the source rows (what was before that has ended: griddep_begin)
-      griddep_wait();
-      griddep_launch_dependents();
-      waited = true;
-    }
-    for (int c = lane; c - lane < n16; c += 64) {
-      uint4 v[kR][2];
-#pragma unroll
-      for (int i = 0; i < kR; ++i)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          v[i][u] = i < n && src[i] >= 0 && c + 32 * u < n16
-                        ? __ldcg(reinterpret_cast<const uint4*>(codes + (size_t)src[i] * (P.K / 2)) + c + 32 * u)
-                        : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < kR; ++i)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          if (i < n && c + 32 * u < n16)
-            reinterpret_cast<uint4*>(P.codes + (size_t)(r0 + i) * (P.K / 2))[c + 32 * u] = v[i][u];
-    }
-    // eight lanes a row: the words of four scales, byte by byte where rows of scales do not start on words
-    const int i = lane >> 3;
-    const int s_row = i == 0 ? src[0] : i == 1 ? src[1] : i == 2 ? src[2] : src[3];
-    uint8_t* const t = i == 0 ? tile[0] : i == 1 ? tile[1] : i == 2 ? tile[2] : tile[3];
-    const uint8_t* p = scales + (size_t)max(s_row, 0) * n16;
-    if (t != nullptr)
-      for (int k = lane & 7; k < kt; k += 8) {
-        uint32_t s = 0;
-        if (s_row >= 0) {
-          if (n16 % 4 == 0)
-            s = __ldcg(reinterpret_cast<const uint32_t*>(p) + k);
-          else
-            for (int j = 0; j < 4 && 4 * k + j < n16; ++j) s |= (uint32_t)__ldcg(p + 4 * k + j) << (8 * j);
-        }
-        *reinterpret_cast<uint32_t*>(t + k * 512) = s;
-      }
+// ---- rows used several times ----
+// The expert sort uses every token k times.  Quantising each output row does
+// the arithmetic k times, and that bounds it (27 us for 36,864 rows of 2048 from
+// 4608); so the places of a source row are linked into a list, and a warp a
+// source row quantises it once and writes it to all of them (16 us).
+// head[s], s < x_rows: first place of row s, -1 none; head[x_rows]: places whose
+// index is out of range, which get zeros.  next[r]: the place after r.  The
+// lists' order depends on the atomics' and does not change what is written.
+__global__ void __launch_bounds__(kThreads) list_init_kernel(int32_t* head, int n) {
+  griddep_begin();
+  const int i = blockIdx.x * kThreads + threadIdx.x;
+  if (i < n) head[i] = -1;
+}
+
+__global__ void __launch_bounds__(kThreads) list_link_kernel(const QuantParams P, int32_t* head, int32_t* next) {
+  griddep_begin();
+  const int r = blockIdx.x * kThreads + threadIdx.x;
+  if (r >= (int)P.rows) return;
+  int s = source_row(P, r);
+  if (s < 0) {
+    atomicOr(&g_quant_err[0], kErrBadExpertId);
+    s = (int)P.x_rows;
   }
-  if (!waited) griddep_wait();
-  if (bad && lane == 0) atomicOr(&g_quant_err[0], kErrBadExpertId);
+  next[r] = atomicExch(&head[s], r);
+}
+
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+mxfp4_quantize_places_kernel(const QuantParams P, const int32_t* __restrict__ head, const int32_t* __restrict__ next) {
+  griddep_begin();
+  const int per_row = P.K / kPer, kt = (P.K + 127) / 128;
+  const int lane = threadIdx.x & 31, s = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (s > (int)P.x_rows) return;
+  for (int r = __ldcg(head + s); r >= 0;) {
+    // up to 32 places, one a lane
+    int n = 0, mine = 0;
+    for (; n < 32 && r >= 0; ++n) {
+      if (lane == n) mine = r;
+      r = __ldcg(next + r);
+    }
+    int tile = mine >> 7, row = mine & 127;
+    bool in_group = true;
+    if (P.offsets) {
+      const int e = find_group(P.offsets, P.groups, mine, P.rows);
+      in_group = e >= 0;
+      const int first = in_group ? P.offsets[e] : 0;
+      tile = (first >> 7) + e + ((mine - first) >> 7);
+      row = (mine - first) & 127;
+    }
+    const int64_t at = in_group ? (int64_t)tile * kt * 512 + 16 * (row & 31) + 4 * (row >> 5) : -1;
+    for (int c0 = lane; c0 - lane < per_row; c0 += 64) {
+      uint32_t w[2][kPer];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) w[u][j] = 0;
+        if (s < (int)P.x_rows && c0 + 32 * u < per_row)
+          load16_raw<F32, VEC>(P.x, s * P.x_stride + (c0 + 32 * u) * kPer, w[u]);
+      }
+      uint2 q[2];
+      uint32_t sw[2];  // in every eighth lane, the word of four scales
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        q[u] = quantize16<F32>(w[u], sw[u]);
+        sw[u] <<= 8 * ((lane >> 1) & 3);
+        sw[u] |= __shfl_xor_sync(0xFFFFFFFFu, sw[u], 2);
+        sw[u] |= __shfl_xor_sync(0xFFFFFFFFu, sw[u], 4);
+      }
+      for (int i = 0; i < n; ++i) {
+        uint8_t* const codes = P.codes + (size_t)__shfl_sync(0xFFFFFFFFu, mine, i) * (P.K / 2);
+        const int64_t t = __shfl_sync(0xFFFFFFFFu, at, i);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int c = c0 + 32 * u;
+          if (c >= per_row) continue;
+          *reinterpret_cast<uint2*>(codes + c * (kPer / 2)) = q[u];
+          if (t >= 0 && (lane & 7) == 0) *reinterpret_cast<uint32_t*>(P.scales + t + (c >> 3) * 512) = sw[u];
+        }
+      }
+    }
+  }
 }
 
 template <bool F32>
@@ -299,23 +320,29 @@ cudaError_t launch_quant(const QuantParams& P, bool vec, bool tiled, cudaStream_
 
 }  // namespace
 
+static bool rows_vec(const MxRows& R) {
+  return ((uintptr_t)R.x & 15) == 0 && (R.x_stride * (R.f32 ? 4 : 2)) % 16 == 0;
+}
+
 cudaError_t launch_mxfp4_quantize(const MxRows& R, uint8_t* codes, uint8_t* scales, bool tiled, cudaStream_t st) {
   const QuantParams P{R.x, R.x_rows, R.x_stride, R.row_index, R.offsets, codes, scales, R.rows, R.K, R.div, R.groups};
-  const bool vec = ((uintptr_t)R.x & 15) == 0 && (R.x_stride * (R.f32 ? 4 : 2)) % 16 == 0;
+  const bool vec = rows_vec(R);
   return R.f32 ? launch_quant<true>(P, vec, tiled, st) : launch_quant<false>(P, vec, tiled, st);
 }
 
-cudaError_t launch_mxfp4_quantize_once(const MxRows& R, uint8_t* row_codes, uint8_t* row_scales, uint8_t* codes,
-                                       uint8_t* scales, cudaStream_t st) {
-  MxRows each = R;
-  each.row_index = nullptr;
-  each.offsets = nullptr;
-  each.rows = R.x_rows;
-  const cudaError_t e = launch_mxfp4_quantize(each, row_codes, row_scales, false, st);
-  if (e != cudaSuccess) return e;
+cudaError_t launch_mxfp4_quantize_once(const MxRows& R, int32_t* lists, uint8_t* codes, uint8_t* scales,
+                                       cudaStream_t st) {
   const QuantParams P{R.x, R.x_rows, R.x_stride, R.row_index, R.offsets, codes, scales, R.rows, R.K, R.div, R.groups};
-  return launch_early(mxfp4_gather_kernel, dim3(grid_for((R.rows + 3) / 4 * 32, 8)), dim3(kThreads), 0, st, P,
-                      (const uint8_t*)row_codes, (const uint8_t*)row_scales);
+  int32_t *const head = lists, *const next = lists + R.x_rows + 1;
+  const auto blocks = [](int64_t threads) { return dim3((unsigned)((threads + kThreads - 1) / kThreads)); };
+  cudaError_t e = launch_early(list_init_kernel, blocks(R.x_rows + 1), dim3(kThreads), 0, st, head, (int)R.x_rows + 1);
+  if (e == cudaSuccess) e = launch_early(list_link_kernel, blocks(R.rows), dim3(kThreads), 0, st, P, head, next);
+  if (e != cudaSuccess) return e;
+  const bool vec = rows_vec(R);
+  auto* k = R.f32 ? (vec ? mxfp4_quantize_places_kernel<true, true> : mxfp4_quantize_places_kernel<true, false>)
+                  : (vec ? mxfp4_quantize_places_kernel<false, true> : mxfp4_quantize_places_kernel<false, false>);
+  return launch_early(k, blocks((R.x_rows + 1) * 32), dim3(kThreads), 0, st, P, (const int32_t*)head,
+                      (const int32_t*)next);
 }
 
 cudaError_t ops_quant_error(int32_t* word, bool clear, cudaStream_t st) {
