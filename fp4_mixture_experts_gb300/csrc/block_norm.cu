@@ -115,7 +115,7 @@ __device__ __forceinline__ float cta_sum(float s, float* part) {
 }
 
 template <int NC, bool VEC>
-__global__ void __launch_bounds__(512) block_norm_kernel(const NormParams P) {
+__global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams P) {
   griddep_begin();
   __shared__ float part[2][32];
   const moe_fp4_block_norm_args& a = P.a;
@@ -276,7 +276,7 @@ block_norm_ring_kernel(const RingParams R) {
   if (tid == 0)
     for (int i = 0; i < R.slots && blockIdx.x + i * step < T; ++i) fill(blockIdx.x + i * step, i);
   // what multiplies the branch (its weight, a channel gate, the scale), and the next norm's weight
-  int at[2];
+  const int at[2] = {tid * 8, ((int)blockDim.x + tid) * 8};
   auto branch_weights = [&](int c, float (&w)[8]) {
     weight8(a.post_weight, a.post_weight_type, at[c], a.scale, w);
     if (a.gate_shape != MOE_FP4_GATE_CHANNEL) return;
@@ -287,14 +287,12 @@ block_norm_ring_kernel(const RingParams R) {
   };
   float bw[KEEP ? 2 : 1][8], nw[KEEP ? 2 : 1][8];
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    at[c] = (c * (int)blockDim.x + tid) * 8;
-    if (!KEEP) continue;
+  for (int c = 0; c < (KEEP ? 2 : 1); ++c) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) bw[KEEP ? c : 0][j] = nw[KEEP ? c : 0][j] = 0.f;
-    if (at[c] >= d) continue;
-    branch_weights(c, bw[KEEP ? c : 0]);
-    weight8(a.next_weight, a.next_weight_type, at[c], 1.f, nw[KEEP ? c : 0]);
+    for (int j = 0; j < 8; ++j) bw[c][j] = nw[c][j] = 0.f;
+    if (!KEEP || at[c] >= d) continue;
+    branch_weights(c, bw[c]);
+    weight8(a.next_weight, a.next_weight_type, at[c], 1.f, nw[c]);
   }
   __syncthreads();
   int s = 0, i = 0;
@@ -430,15 +428,11 @@ cudaError_t launch_norm(const NormParams& P, cudaStream_t st) {
   RingParams R;
   int ring_threads, ctas;
   if (VEC && ring_layout(P, &R, &ring_threads, &ctas)) return launch_ring(R, ring_threads, ctas, st);
-  const int chunks = (P.a.d + 7) / 8;
-  // chunks of 8 elements per thread: 1 up to 512 threads, then 2, 4
-  const int nc = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : 4;
+  // a CTA a row: one chunk of 8 elements a thread up to 1024 threads (few rows are bound by latency), else two
+  const int chunks = (P.a.d + 7) / 8, nc = chunks <= 1024 ? 1 : 2;
   const int threads = ((chunks + nc - 1) / nc + 31) / 32 * 32;
-  const unsigned grid = (unsigned)P.a.T;
-  return launch_early(nc == 1   ? block_norm_kernel<1, VEC>
-                      : nc == 2 ? block_norm_kernel<2, VEC>
-                                : block_norm_kernel<4, VEC>,
-                      dim3(grid), dim3(threads), 0, st, P);
+  return launch_spread(nc == 1 ? block_norm_kernel<1, VEC> : block_norm_kernel<2, VEC>, (unsigned)P.a.T,
+                       (unsigned)threads, st, P);
 }
 
 bool is_type(int t) { return t == MOE_FP4_TYPE_BF16 || t == MOE_FP4_TYPE_F32; }

@@ -130,7 +130,7 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     int g = 0;
     bool ok = true, waited = false;
     for (int it = first; it < items && ok; it += step) {
-      item_at<NT>(t, it, P.mblocks, off, pre);
+      item_at<NT>(t, it, P.mblocks, off, pre, P.E);
       const uint8_t* ws = P.w_scales + ((size_t)t.g * P.mblocks + t.mb) * P.kt * kSfTile;
       const uint8_t* as = P.a_scales + ((size_t)((uniform(off[t.g]) >> 7) + t.g + (t.local >> 7))) * P.kt * kSfTile;
       const int wrow = t.mb * (SW ? 64 : 128);
@@ -185,7 +185,7 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     bool ok = true;
     const uint32_t lo0 = desc_lo(smem_u32(smem));
     for (int it = first; it < items && ok; it += step, ++li) {
-      item_at<NT>(t, it, P.mblocks, off, pre);
+      item_at<NT>(t, it, P.mblocks, off, pre, P.E);
       const int b = li & 1, use = li >> 1;
       if (!warp_wait(&acc_empty[b], (use & 1) ^ 1, abort_flag, P)) break;
       const uint32_t d_tmem = tmem + b * NT;
@@ -230,7 +230,7 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     Item t{};
     int li = 0;
     for (int it = first; it < items; it += step, ++li) {
-      item_at<NT>(t, it, P.mblocks, off, pre);
+      item_at<NT>(t, it, P.mblocks, off, pre, P.E);
       const int b = li & 1, use = li >> 1;
       const int f0 = t.mb * E::kFeatures, nf = min(E::kFeatures, P.n_out - f0);
       const bool ok = warp_wait(&acc_full[b], use & 1, abort_flag, P);
@@ -259,7 +259,7 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     cluster_sync();  // every CTA's partial sums are written
     Item t{};
     if (first < items) {
-      item_at<NT>(t, first, P.mblocks, off, pre);
+      item_at<NT>(t, first, P.mblocks, off, pre, P.E);
       sum_parts<F32, SW>(P, smem_u32(smem), rank, t.row0, t.n, t.mb, warp, lane);
     }
     cluster_sync();  // no CTA leaves while another may still read its sums

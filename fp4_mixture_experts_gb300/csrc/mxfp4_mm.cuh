@@ -201,11 +201,18 @@ struct Item {
   int mb;       // block of weight rows
 };
 
+// The item of number `item` (of a tile below pre[E]) from a cursor that is not
+// past it; whole warp: 32 groups a step.
 template <int NT>
-__device__ __forceinline__ void item_at(Item& t, int item, int mblocks, const int* off, const int* pre) {
-  const int tile = item / mblocks;
+__device__ __forceinline__ void item_at(Item& t, int item, int mblocks, const int* off, const int* pre, int groups) {
+  const int tile = item / mblocks, lane = threadIdx.x & 31;
   t.mb = item - tile * mblocks;
-  while (tile >= uniform(pre[t.g + 1])) ++t.g;
+  int passed;
+  do {
+    const int e = t.g + 1 + lane;
+    passed = __popc(__ballot_sync(0xFFFFFFFFu, e < groups && pre[min(e, groups)] <= tile));
+    t.g += passed;
+  } while (passed == 32);
   t.local = (tile - uniform(pre[t.g])) * NT;
   t.row0 = uniform(off[t.g]) + t.local;
   t.n = min(NT, uniform(off[t.g + 1]) - t.row0);

@@ -207,7 +207,7 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
     bool ok = true;
     griddep_begin();  // the kernel ahead writes the rows' codes and scales
     for (int it = first; it < items && ok; it += step) {
-      item_at<kNT>(t, it, mblocks2, off, pre);
+      item_at<kNT>(t, it, mblocks2, off, pre, P.E);
       const int mb = 2 * t.mb + rank;           // may be one past the last block: its rows read as 0,
       const int mb_sf = min(mb, P.mblocks - 1);  // with any scales
       const int half = ((t.n + 31) & ~31) / 2;   // token rows of this CTA
@@ -261,7 +261,7 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
       bool ok = true;
       const uint32_t lo0 = desc_lo(smem_u32(smem));
       for (int it = first; it < items && ok; it += step, ++li) {
-        item_at<kNT>(t, it, mblocks2, off, pre);
+        item_at<kNT>(t, it, mblocks2, off, pre, P.E);
         const int b = li & 1, use = li >> 1;
         const int n_mma = (t.n + 31) & ~31;
         // the other accumulator's columns that this one shares, where its item has values in them
@@ -347,7 +347,7 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
     Item t{};
     int li = 0;
     for (int it = first; it < items; it += step, ++li) {
-      item_at<kNT>(t, it, mblocks2, off, pre);
+      item_at<kNT>(t, it, mblocks2, off, pre, P.E);
       const int b = li & 1, use = li >> 1;
       const int f0 = (2 * t.mb + rank) * E::kFeatures, nf = max(0, min(E::kFeatures, P.n_out - f0));
       const bool ok = warp_wait(&acc_full[b], use & 1, abort_flag, P);

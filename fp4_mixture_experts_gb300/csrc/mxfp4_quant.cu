@@ -306,10 +306,9 @@ template <bool F32, bool VEC, bool TILED>
 cudaError_t launch_quant(const QuantParams& P, cudaStream_t st) {
   // a warp a row where that fills the SMs (8 rows each at least) and most lanes
   if (P.K >= 512 && P.rows >= 8 * num_sms())
-    return launch_early(mxfp4_quantize_rows_kernel<F32, VEC, TILED>, dim3((unsigned)((P.rows + 7) / 8)), dim3(kThreads),
-                        0, st, P);
-  return launch_early(mxfp4_quantize_flat_kernel<F32, VEC, TILED>, dim3(grid_for(P.rows * (P.K / kPer), 8)),
-                      dim3(kThreads), 0, st, P);
+    return launch_spread(mxfp4_quantize_rows_kernel<F32, VEC, TILED>, (unsigned)((P.rows + 7) / 8), kThreads, st, P);
+  return launch_spread(mxfp4_quantize_flat_kernel<F32, VEC, TILED>, (unsigned)grid_for(P.rows * (P.K / kPer), 8),
+                       kThreads, st, P);
 }
 
 template <bool F32>
@@ -334,15 +333,14 @@ cudaError_t launch_mxfp4_quantize_once(const MxRows& R, int32_t* lists, uint8_t*
                                        cudaStream_t st) {
   const QuantParams P{R.x, R.x_rows, R.x_stride, R.row_index, R.offsets, codes, scales, R.rows, R.K, R.div, R.groups};
   int32_t *const head = lists, *const next = lists + R.x_rows + 1;
-  const auto blocks = [](int64_t threads) { return dim3((unsigned)((threads + kThreads - 1) / kThreads)); };
-  cudaError_t e = launch_early(list_init_kernel, blocks(R.x_rows + 1), dim3(kThreads), 0, st, head, (int)R.x_rows + 1);
-  if (e == cudaSuccess) e = launch_early(list_link_kernel, blocks(R.rows), dim3(kThreads), 0, st, P, head, next);
+  const auto blocks = [](int64_t threads) { return (unsigned)((threads + kThreads - 1) / kThreads); };
+  cudaError_t e = launch_spread(list_init_kernel, blocks(R.x_rows + 1), kThreads, st, head, (int)R.x_rows + 1);
+  if (e == cudaSuccess) e = launch_spread(list_link_kernel, blocks(R.rows), kThreads, st, P, head, next);
   if (e != cudaSuccess) return e;
   const bool vec = rows_vec(R);
   auto* k = R.f32 ? (vec ? mxfp4_quantize_places_kernel<true, true> : mxfp4_quantize_places_kernel<true, false>)
                   : (vec ? mxfp4_quantize_places_kernel<false, true> : mxfp4_quantize_places_kernel<false, false>);
-  return launch_early(k, blocks((R.x_rows + 1) * 32), dim3(kThreads), 0, st, P, (const int32_t*)head,
-                      (const int32_t*)next);
+  return launch_spread(k, blocks((R.x_rows + 1) * 32), kThreads, st, P, (const int32_t*)head, (const int32_t*)next);
 }
 
 cudaError_t ops_quant_error(int32_t* word, bool clear, cudaStream_t st) {
@@ -403,8 +401,8 @@ int moe_fp4_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const int64_t total = rows * (K / 8);
   const unsigned grid = (unsigned)((total + kDequantRuns * kThreads - 1) / (kDequantRuns * kThreads));
-  return launch_early(out_type == MOE_FP4_TYPE_F32 ? mxfp4_dequantize_kernel<true> : mxfp4_dequantize_kernel<false>,
-                      dim3(grid), dim3(kThreads), 0, st, codes, scales, total, out) == cudaSuccess
+  return launch_spread(out_type == MOE_FP4_TYPE_F32 ? mxfp4_dequantize_kernel<true> : mxfp4_dequantize_kernel<false>,
+                       grid, kThreads, st, codes, scales, total, out) == cudaSuccess
              ? MOE_FP4_OK
              : MOE_FP4_ERR_CUDA;
 }
@@ -416,9 +414,9 @@ int moe_fp4_mxfp4_tile_scales(const uint8_t* scales, int32_t E, int32_t N, int32
     return MOE_FP4_ERR_INVALID_ARG;
   const int rt = (N + 127) / 128, kt = (K + 127) / 128;
   const int64_t words = (int64_t)E * rt * kt * 128;
-  return launch_early(tile_scales_kernel, dim3(grid_for(words, 16)), dim3(kThreads), 0,
-                      static_cast<cudaStream_t>(cuda_stream), scales, N, K / 32, rt, kt, swiglu, words,
-                      reinterpret_cast<uint32_t*>(tiled)) == cudaSuccess
+  return launch_spread(tile_scales_kernel, (unsigned)grid_for(words, 16), kThreads,
+                       static_cast<cudaStream_t>(cuda_stream), scales, N, K / 32, rt, kt, swiglu, words,
+                       reinterpret_cast<uint32_t*>(tiled)) == cudaSuccess
              ? MOE_FP4_OK
              : MOE_FP4_ERR_CUDA;
 }
