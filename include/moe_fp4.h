@@ -322,7 +322,12 @@ int moe_fp4_forward_mx(const moe_fp4_dims* dims, const void* x_bf16, const float
  * the layer: device buffers owned by the caller, work enqueued on the given
  * stream, nothing allocated, nothing synchronised, arguments checked on the
  * host before anything is enqueued.  They keep no state between calls but an
- * error word (moe_fp4_ops_check). */
+ * error word (moe_fp4_ops_check).  Their kernels are launched with programmatic
+ * dependent launch: each is set up while the kernel before it on the stream
+ * still runs and waits on the device until all work before has ended and is
+ * visible, so that ordinary stream order holds; and each lets a kernel that the
+ * caller launches early be set up while it runs (such a kernel must wait on the
+ * device, griddepcontrol.wait, as any early-launched kernel must). */
 
 /* Element types of the operators' unquantised operands and results. */
 #define MOE_FP4_TYPE_BF16 0
@@ -476,6 +481,9 @@ int moe_fp4_ops_check(void* cuda_stream);
  *                                 loads its first weight stage.
  * Nothing faults, traps or hangs: the waiting threads give up, the outputs of
  * that call are incomplete, and moe_fp4_check reports MOE_FP4_ERR_DEVICE.
+ * The products (moe_fp4_mxfp4_matmul, moe_fp4_mxfp4_linear) take
+ * MOE_FP4_FAULT_TC_TOKEN_TILE too (the first CTA, or pair, never loads its first
+ * stage; moe_fp4_ops_check reports it), and the limit.
  * MOE_FP4_FAULT_NONE (wait_limit_us ignored) restores normal operation.
  * Returns MOE_FP4_ERR_INVALID_ARG for an unknown site or a zero limit. */
 #define MOE_FP4_FAULT_NONE 0
