@@ -3,7 +3,7 @@
 //
 // A single-token operator runs for a few microseconds; marshalling its
 // arguments in Python takes longer than that on the host (one-token block end:
-// 13 us a call through ctypes, 6 us so).  The module holds no state but
+// 13 us a call through ctypes, 3.7 us so).  The module holds no state but
 // the entry points' addresses and the exception to raise, both set by bind().
 #include <Python.h>
 
