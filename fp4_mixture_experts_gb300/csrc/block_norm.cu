@@ -28,12 +28,40 @@ struct NormParams {
   float k;  // d^-1/2: the squares of k v sum to the mean, which overflows only if the mean itself does
 };
 
-// where element j of a thread's chunk c is: chunks of 8 adjacent elements
-// (VEC: rows start on 16 bytes and d is a multiple of 8), else interleaved
+// where element j of a thread's chunk c is: 8 adjacent elements (VEC: rows
+// start on 16 bytes and d is a multiple of 8), else a warp's 256 in 8 turns of
+// 32, so that one address and one comparison serve the 8
 template <bool VEC>
 __device__ __forceinline__ int elem(int c, int j) {
-  return VEC ? (c * (int)blockDim.x + (int)threadIdx.x) * 8 + j
-             : (c * 8 + j) * (int)blockDim.x + (int)threadIdx.x;
+  const int i = c * (int)blockDim.x + (int)threadIdx.x;
+  return VEC ? i * 8 + j : (i & ~31) * 8 + (i & 31) + 32 * j;
+}
+
+template <typename T>
+__device__ __forceinline__ void load8_apart(const T* p, int left, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = 0.f;
+    if (32 * j < left) {
+      if constexpr (sizeof(T) == 4)
+        v[j] = p[32 * j];
+      else
+        v[j] = bf16_to_f32(p[32 * j]);
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8_apart(T* p, int left, const float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (32 * j < left) {
+      if constexpr (sizeof(T) == 4)
+        p[32 * j] = v[j];
+      else
+        p[32 * j] = f32_to_bf16_rn(v[j]);
+    }
+  }
 }
 
 template <bool VEC>
@@ -59,13 +87,11 @@ __device__ __forceinline__ void load8(const void* base, int type, int64_t row_at
       }
     }
   } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = elem<false>(c, j);
-      v[j] = e >= d ? 0.f
-             : type == MOE_FP4_TYPE_F32 ? static_cast<const float*>(base)[row_at + e]
-                                        : bf16_to_f32(static_cast<const uint16_t*>(base)[row_at + e]);
-    }
+    const int e = elem<false>(c, 0);
+    if (type == MOE_FP4_TYPE_F32)
+      load8_apart(static_cast<const float*>(base) + row_at + e, d - e, v);
+    else
+      load8_apart(static_cast<const uint16_t*>(base) + row_at + e, d - e, v);
   }
 }
 
@@ -88,15 +114,11 @@ __device__ __forceinline__ void store8(void* base, int type, int64_t row_at, int
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + row_at + e) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = elem<false>(c, j);
-      if (e >= d) continue;
-      if (type == MOE_FP4_TYPE_F32)
-        static_cast<float*>(base)[row_at + e] = v[j];
-      else
-        static_cast<uint16_t*>(base)[row_at + e] = f32_to_bf16_rn(v[j]);
-    }
+    const int e = elem<false>(c, 0);
+    if (type == MOE_FP4_TYPE_F32)
+      store8_apart(static_cast<float*>(base) + row_at + e, d - e, v);
+    else
+      store8_apart(static_cast<uint16_t*>(base) + row_at + e, d - e, v);
   }
 }
 
