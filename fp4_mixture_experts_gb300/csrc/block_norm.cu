@@ -218,21 +218,33 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams P) {
 }
 
 // ---- many rows ----
-// Chunk c of a thread: 8 adjacent elements at (c blockDim + thread) 8, two a
-// thread; rows start on 16 bytes and d is a multiple of 8.
+// Two chunks of 8 elements a thread, placed as above.  A bulk copy starts on 16
+// bytes and has a multiple of them: a row that does not is copied with its
+// neighbours' ends (up to 15 bytes on both sides) and read at its offset; the
+// first and the last row, beside which memory may be another's, are read where
+// they are.
 constexpr int kRingThreads = 512;      // with the weights in registers; 1024 read them again for every row
+constexpr int kRingSmThreads = 640;    // on an SM: 88 registers a thread are 5 warps of each of its quarters
 constexpr int kRingMaxSlots = 8;
 constexpr int kRingSmem = 200 * 1024;
 
 struct RingParams {
   NormParams n;
   int slots, slot_bytes;                    // rows in the ring
-  int y_bytes, y2_bytes, r_bytes, g_bytes;  // of a row; 0: not there
+  int y_bytes, y2_bytes, r_bytes, g_bytes;  // of a row in its slot; 0: not there
   uint64_t wait_ns;
 };
 
-// 8 values of shared or global memory
-__device__ __forceinline__ void unpack8(const void* p, bool f32, float (&v)[8]) {
+// a thread's 8 values of shared or global memory; `left`: elements from the first to the row's end
+template <bool VEC>
+__device__ __forceinline__ void unpack8(const void* p, bool f32, int left, float (&v)[8]) {
+  if (!VEC) {
+    if (f32)
+      load8_apart(static_cast<const float*>(p), left, v);
+    else
+      load8_apart(static_cast<const uint16_t*>(p), left, v);
+    return;
+  }
   const uint4* q = static_cast<const uint4*>(p);
   if (f32) {
     const uint4 x = q[0], y = q[1];
@@ -251,11 +263,12 @@ __device__ __forceinline__ void unpack8(const void* p, bool f32, float (&v)[8]) 
 
 __device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + __expf(-g)); }
 
-// The row weights of chunk `at`, or `to` where there are none.
-__device__ __forceinline__ void weight8(const void* w, int type, int at, float to, float (&v)[8]) {
+// The row weights from element `at` on, or `to` where there are none.
+template <bool VEC>
+__device__ __forceinline__ void weight8(const void* w, int type, int at, int d, float to, float (&v)[8]) {
   if (w) {
     const bool f = type == MOE_FP4_TYPE_F32;
-    unpack8(static_cast<const uint8_t*>(w) + (size_t)at * (f ? 4 : 2), f, v);
+    unpack8<VEC>(static_cast<const uint8_t*>(w) + (size_t)at * (f ? 4 : 2), f, d - at, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 1.f;
@@ -264,7 +277,7 @@ __device__ __forceinline__ void weight8(const void* w, int type, int at, float t
   for (int j = 0; j < 8; ++j) v[j] *= to;
 }
 
-template <bool KEEP>
+template <bool KEEP, bool VEC>
 __global__ void __launch_bounds__(KEEP ? kRingThreads : 2 * kRingThreads, 1)
 block_norm_ring_kernel(const RingParams R) {
   griddep_begin();
@@ -283,27 +296,49 @@ block_norm_ring_kernel(const RingParams R) {
     abort_word = 0;
     mbar_fence_init();
   }
+  // where row t of an operand is, and whether it is read there
+  auto row = [&](const void* base, bool f, int64_t stride, int64_t t) {
+    return static_cast<const uint8_t*>(base) + t * stride * (f ? 4 : 2);
+  };
+  auto edge = [&](int64_t t) { return !VEC && (t == 0 || t == T - 1); };
   // one thread: the operands of row t to slot s
   auto fill = [&](int64_t t, int s) {
+    if (edge(t)) {
+      mbar_arrive(&full[s]);
+      return;
+    }
     uint8_t* p = ring + (size_t)s * R.slot_bytes;
-    mbar_expect_tx(&full[s], R.y_bytes + R.y2_bytes + R.r_bytes + R.g_bytes);
-    bulk_load(p, static_cast<const uint8_t*>(a.residual) + t * a.residual_stride * (rf ? 4 : 2), R.r_bytes, &full[s]);
-    p += R.r_bytes;
-    if (R.y_bytes) bulk_load(p, static_cast<const uint8_t*>(a.y) + t * a.y_stride * (yf ? 4 : 2), R.y_bytes, &full[s]);
-    p += R.y_bytes;
-    if (R.y2_bytes) bulk_load(p, static_cast<const uint8_t*>(a.y2) + t * a.y2_stride * (y2f ? 4 : 2), R.y2_bytes, &full[s]);
-    p += R.y2_bytes;
-    if (R.g_bytes) bulk_load(p, static_cast<const uint8_t*>(a.gate) + t * a.gate_stride * (gf ? 4 : 2), R.g_bytes, &full[s]);
+    const uint8_t* from[4] = {row(a.residual, rf, a.residual_stride, t), row(a.y, yf, a.y_stride, t),
+                              row(a.y2, y2f, a.y2_stride, t), row(a.gate, gf, a.gate_stride, t)};
+    const int room[4] = {R.r_bytes, R.y_bytes, R.y2_bytes, R.g_bytes};
+    const bool wide[4] = {rf, yf, y2f, gf};
+    uint32_t bytes[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      bytes[i] = room[i];
+      if (!VEC && room[i]) {
+        const uint32_t skip = (uint32_t)(uintptr_t)from[i] & 15;
+        from[i] -= skip;
+        bytes[i] = (skip + d * (wide[i] ? 4 : 2) + 15) & ~15u;
+      }
+      sum += bytes[i];
+    }
+    mbar_expect_tx(&full[s], sum);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (room[i]) bulk_load(p, from[i], bytes[i], &full[s]);
+      p += room[i];
+    }
   };
   if (tid == 0)
     for (int i = 0; i < R.slots && blockIdx.x + i * step < T; ++i) fill(blockIdx.x + i * step, i);
   // what multiplies the branch (its weight, a channel gate, the scale), and the next norm's weight
-  const int at[2] = {tid * 8, ((int)blockDim.x + tid) * 8};
+  const int at[2] = {elem<VEC>(0, 0), elem<VEC>(1, 0)};
   auto branch_weights = [&](int c, float (&w)[8]) {
-    weight8(a.post_weight, a.post_weight_type, at[c], a.scale, w);
+    weight8<VEC>(a.post_weight, a.post_weight_type, at[c], d, a.scale, w);
     if (a.gate_shape != MOE_FP4_GATE_CHANNEL) return;
     float g[8];
-    unpack8(static_cast<const uint8_t*>(a.gate) + (size_t)at[c] * (gf ? 4 : 2), gf, g);
+    unpack8<VEC>(static_cast<const uint8_t*>(a.gate) + (size_t)at[c] * (gf ? 4 : 2), gf, d - at[c], g);
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] *= a.gate_sigmoid ? sigmoid(g[j]) : g[j];
   };
@@ -314,7 +349,7 @@ block_norm_ring_kernel(const RingParams R) {
     for (int j = 0; j < 8; ++j) bw[c][j] = nw[c][j] = 0.f;
     if (!KEEP || at[c] >= d) continue;
     branch_weights(c, bw[c]);
-    weight8(a.next_weight, a.next_weight_type, at[c], 1.f, nw[c]);
+    weight8<VEC>(a.next_weight, a.next_weight_type, at[c], d, 1.f, nw[c]);
   }
   __syncthreads();
   int s = 0, i = 0;
@@ -326,10 +361,17 @@ block_norm_ring_kernel(const RingParams R) {
       if (a.gate_sigmoid) m = sigmoid(m);
     }
     mbar_wait(&full[s], phase, abort_flag, &g_norm_err[0], kErrWaitTimeout, R.wait_ns);
-    const uint8_t* const pr = ring + (size_t)s * R.slot_bytes;
-    const uint8_t* const py = pr + R.r_bytes;
-    const uint8_t* const py2 = py + R.y_bytes;
-    const uint8_t* const pg = py2 + R.y2_bytes;
+    const uint8_t* pr = ring + (size_t)s * R.slot_bytes;
+    const uint8_t* py = pr + R.r_bytes;
+    const uint8_t* py2 = py + R.y_bytes;
+    const uint8_t* pg = py2 + R.y2_bytes;
+    if (!VEC) {
+      auto at_row = [&](const uint8_t*& p, const uint8_t* g) { p = edge(t) ? g : p + ((uintptr_t)g & 15); };
+      at_row(pr, row(a.residual, rf, a.residual_stride, t));
+      at_row(py, row(a.y, yf, a.y_stride, t));
+      at_row(py2, row(a.y2, y2f, a.y2_stride, t));
+      at_row(pg, row(a.gate, gf, a.gate_stride, t));
+    }
     float r[2][8];
     if (a.y) {
       float b[2][8];
@@ -340,10 +382,10 @@ block_norm_ring_kernel(const RingParams R) {
           for (int j = 0; j < 8; ++j) b[c][j] = 0.f;
           continue;
         }
-        unpack8(py + at[c] * (yf ? 4 : 2), yf, b[c]);
+        unpack8<VEC>(py + at[c] * (yf ? 4 : 2), yf, d - at[c], b[c]);
         if (R.y2_bytes) {
           float v[8];
-          unpack8(py2 + at[c] * (y2f ? 4 : 2), y2f, v);
+          unpack8<VEC>(py2 + at[c] * (y2f ? 4 : 2), y2f, d - at[c], v);
 #pragma unroll
           for (int j = 0; j < 8; ++j) b[c][j] += v[j];
         }
@@ -363,13 +405,13 @@ block_norm_ring_kernel(const RingParams R) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) b[c][j] *= m * bw[KEEP ? c : 0][j];
         if (R.g_bytes && at[c] < d) {
-          unpack8(pg + at[c] * (gf ? 4 : 2), gf, v);
+          unpack8<VEC>(pg + at[c] * (gf ? 4 : 2), gf, d - at[c], v);
 #pragma unroll
           for (int j = 0; j < 8; ++j) b[c][j] *= a.gate_sigmoid ? sigmoid(v[j]) : v[j];
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[c][j] = 0.f;
-        if (at[c] < d) unpack8(pr + at[c] * (rf ? 4 : 2), rf, r[c]);
+        if (at[c] < d) unpack8<VEC>(pr + at[c] * (rf ? 4 : 2), rf, d - at[c], r[c]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[c][j] += b[c][j];
       }
@@ -378,12 +420,12 @@ block_norm_ring_kernel(const RingParams R) {
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[c][j] = 0.f;
-        if (at[c] < d) unpack8(pr + at[c] * (rf ? 4 : 2), rf, r[c]);
+        if (at[c] < d) unpack8<VEC>(pr + at[c] * (rf ? 4 : 2), rf, d - at[c], r[c]);
       }
     }
     if (a.out) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) store8<true>(a.out, a.residual_type, t * a.out_stride, c, d, r[c]);
+      for (int c = 0; c < 2; ++c) store8<VEC>(a.out, a.residual_type, t * a.out_stride, c, d, r[c]);
     }
     float n = 0.f;
     if (a.normed) {
@@ -402,10 +444,10 @@ block_norm_ring_kernel(const RingParams R) {
     if (a.normed) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        if (!KEEP && at[c] < d) weight8(a.next_weight, a.next_weight_type, at[c], 1.f, nw[0]);
+        if (!KEEP && at[c] < d) weight8<VEC>(a.next_weight, a.next_weight_type, at[c], d, 1.f, nw[0]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[c][j] *= n * nw[KEEP ? c : 0][j];
-        store8<true>(a.normed, MOE_FP4_TYPE_BF16, t * d, c, d, r[c]);
+        store8<VEC>(a.normed, MOE_FP4_TYPE_BF16, t * d, c, d, r[c]);
       }
     }
     if (++s == R.slots) {
@@ -416,30 +458,43 @@ block_norm_ring_kernel(const RingParams R) {
   // (every row that was filled has been waited for)
 }
 
-// The ring's layout and grid; false where the plain kernel is used: few rows,
-// rows that do not start on 16 bytes, or too wide ones.
+// The ring's layout and grid; false where the plain kernel is used: few rows, or
+// too wide ones.
+template <bool VEC>
 bool ring_layout(const NormParams& P, RingParams* R, int* threads, int* ctas) {
   const moe_fp4_block_norm_args& a = P.a;
-  const int chunks = a.d / 8;
+  const int chunks = (a.d + 7) / 8;
   *threads = std::max(32, ((chunks + 1) / 2 + 31) / 32 * 32);
   if (*threads > 2 * kRingThreads) return false;
-  const int per_sm = std::max(1, std::min(16, kRingThreads / *threads));
-  *ctas = per_sm * num_sms();
-  if (a.T < 4 * (int64_t)*ctas) return false;
-  auto bytes = [&](const void* p, int type) { return p ? a.d * (type == MOE_FP4_TYPE_F32 ? 4 : 2) : 0; };
+  // rows read element by element: by instructions, and the ring's fewer threads an
+  // SM lose for narrow ones (bf16: 16384 x 501 25 us, plain 21; x 1501 61 and 63;
+  // 8192 x 4001 83 and 93; 4096 x 7167 86 and 130)
+  if (!VEC && a.d < 1536) return false;
+  auto bytes = [&](const void* p, int type) {
+    const int n = a.d * (type == MOE_FP4_TYPE_F32 ? 4 : 2);
+    return p ? VEC ? n : (n + 30) / 16 * 16 : 0;
+  };
   R->n = P;
   R->y_bytes = bytes(a.y, a.y_type);
   R->y2_bytes = bytes(a.y2, a.y2_type);
   R->r_bytes = bytes(a.residual, a.residual_type);
   R->g_bytes = a.gate_shape == MOE_FP4_GATE_ELEMENT ? bytes(a.gate, a.gate_type) : 0;
   R->slot_bytes = (R->y_bytes + R->y2_bytes + R->r_bytes + R->g_bytes + 127) / 128 * 128;
+  // as many CTAs an SM as run there (4096 x 5120, bf16: two of 320 threads 37 us,
+  // one 54) with 2 rows in the ring (two are enough, 8192 x 3584, fp32: two CTAs of
+  // 2 rows 95 us, one of 4 154)
+  int per_sm = std::max(1, kRingSmThreads / *threads);
+  while (per_sm > 1 && kRingSmem / per_sm / R->slot_bytes < 2) --per_sm;
+  *ctas = per_sm * num_sms();
+  if (a.T < 4 * (int64_t)*ctas) return false;
   R->slots = std::min(kRingMaxSlots, kRingSmem / per_sm / R->slot_bytes);
   R->wait_ns = wait_limit_ns();
   return R->slots >= 2;
 }
 
+template <bool VEC>
 cudaError_t launch_ring(const RingParams& R, int threads, int ctas, cudaStream_t st) {
-  auto* k = threads <= kRingThreads ? block_norm_ring_kernel<true> : block_norm_ring_kernel<false>;
+  auto* k = threads <= kRingThreads ? block_norm_ring_kernel<true, VEC> : block_norm_ring_kernel<false, VEC>;
   const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(k), kRingSmem);
   if (e != cudaSuccess) return e;
   return launch_early(k, dim3(ctas), dim3(threads), R.slots * R.slot_bytes, st, R);
@@ -449,7 +504,7 @@ template <bool VEC>
 cudaError_t launch_norm(const NormParams& P, cudaStream_t st) {
   RingParams R;
   int ring_threads, ctas;
-  if (VEC && ring_layout(P, &R, &ring_threads, &ctas)) return launch_ring(R, ring_threads, ctas, st);
+  if (ring_layout<VEC>(P, &R, &ring_threads, &ctas)) return launch_ring<VEC>(R, ring_threads, ctas, st);
   // a CTA a row: one chunk of 8 elements a thread up to 1024 threads (few rows are bound by latency), else two
   const int chunks = (P.a.d + 7) / 8, nc = chunks <= 1024 ? 1 : 2;
   const int threads = ((chunks + nc - 1) / nc + 31) / 32 * 32;

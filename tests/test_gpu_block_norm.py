@@ -182,6 +182,35 @@ def test_many_rows_strided_in_place_without_norms_and_rms_norm(d):
     moe.ops_check()
 
 
+@pytest.mark.parametrize("T,d", [(9800, 33), (9729, 1), (5003, 604), (4900, 1001), (620, 7167), (650, 12001), (610, 16383)])
+@pytest.mark.parametrize("gate,sig,post", [("token", True, True), ("element", False, False), ("channel", True, True)])
+def test_many_rows_that_do_not_start_on_16_bytes(T, d, gate, sig, post):
+    run(T, d, rt=F32 if gate == "channel" else BF, yt=BF if gate == "element" else F32, two=gate != "channel",
+        pw=None if d == 1 else BF, gate=gate, sig=sig, post=post, seed=T)
+
+
+@pytest.mark.parametrize("d,off", [(1001, 1), (4096, 3), (604, 0)])
+def test_many_rows_at_odd_addresses_in_place(d, off):
+    """rows packed tightly behind an odd start: a copy of whole 16 bytes would reach beside the first and the last row"""
+    rng = np.random.default_rng(d)
+    T = 5000
+
+    def packed(dtype):
+        flat = rand(rng, (off + T * d,), dtype, 2.0)
+        return flat, flat[off:].view(T, d)
+
+    (flat, r), (_, y), (_, g) = packed(BF), packed(F32), packed(BF)
+    head = flat[:off].clone()
+    o, oe, n, ne = reference(r, y, None, True, None, g, True, 0.5, None, 1e-6)
+    first = moe.block_residual(r.clone(), y, gate=g, gate_sigmoid=True, scale=0.5)
+    out, normed = moe.block_residual(r, y, gate=g, gate_sigmoid=True, scale=0.5, out=r)
+    close(out, o, oe, "out")
+    close(normed, n, ne, "normed")
+    assert torch.equal(flat[:off], head)
+    assert torch.equal(out, first[0]) and torch.equal(normed, first[1])
+    moe.ops_check()
+
+
 def test_offsets_beyond_32_bits():
     rng = np.random.default_rng(4)
     T, d = 140000, 16384
