@@ -274,12 +274,13 @@ struct Ring {
 
 // ---- epilogue -----------------------------------------------------------------
 // The accumulator has features in lanes and tokens in columns; y wants a
-// token's features side by side.  Values go from registers to y: a lane pair
-// swaps one value of every two tokens, so that each lane stores two adjacent
-// features of one of them (fp32: a token's 32 features, 128 bytes, a store as
-// they are).  Nothing passes through shared memory: the MMAs of 256 x 256 tiles
-// take all of its bandwidth, and an epilogue that turned its tile there took
-// 7,000 cycles beside them, longer than the MMAs of K = 2048.
+// token's features side by side.  Values go from registers to y as they are, a
+// token's 32 features of a warp a store: whole sectors.  (bf16, with lane pairs
+// that swap values and store two features: 8192 x 2048 x 4096 28.5 us against
+// 27.4.  With SwiGLU's 16 features a warp that swap pays: 13073 x 128 x 1522 19
+// us against 20.)  Nothing passes through shared memory: the MMAs of 256 x 256
+// tiles take all of its bandwidth, and an epilogue that turned its tile there
+// took 7,000 cycles beside them, longer than the MMAs of K = 2048.
 //
 // Eight warps, in two groups of four (a lane quarter each): group h takes every
 // other chunk of 32 tokens.  Chunks are read in rounds of two a group, so that
@@ -305,7 +306,7 @@ struct Epilogue {
   static constexpr int kEs = F32 ? 4 : 2;
 
   int q, h, lane;    // lane quarter, group
-  int vec;           // rows of y start on 4 bytes, and n_out is even: two bf16 a store
+  int vec;           // rows of y start on 4 bytes, and n_out is even
   size_t ldy;        // bytes
 
   __device__ __forceinline__ Epilogue(const MmParams& P, int warp, int lane_)
@@ -322,21 +323,12 @@ struct Epilogue {
 #pragma unroll
       for (int j = 0; j < kTokens; ++j)
         if (ALL || (j < rows && f < nf)) *reinterpret_cast<uint32_t*>(y + j * ldy) = v[j];
-    } else if (!SW && vec) {
-      const int f = q * 32 + (lane & ~1);
-      const uint32_t sel = odd ? 0x3276u : 0x5410u;
-      y += (odd ? ldy : 0) + f * 2;
-#pragma unroll
-      for (int j = 0; j < kTokens; j += 2) {
-        const uint32_t p = swap_pair(pack_bf16(v[j], v[j + 1]), 1, sel);
-        if (ALL || (j + (odd ? 1 : 0) < rows && f < nf)) *reinterpret_cast<uint32_t*>(y + j * ldy) = p;
-      }
     } else if (!SW) {
       const int f = q * 32 + lane;
       y += f * 2;
 #pragma unroll
       for (int j = 0; j < kTokens; ++j)
-        if (j < rows && f < nf) *reinterpret_cast<uint16_t*>(y + j * ldy) = f32_to_bf16_rn(__uint_as_float(v[j]));
+        if (ALL || (j < rows && f < nf)) *reinterpret_cast<uint16_t*>(y + j * ldy) = f32_to_bf16_rn(__uint_as_float(v[j]));
     } else {
       // gate in even lanes, up in odd ones: of tokens j and j + 1 the even lane takes the first, the odd the second
       float s[kTokens / 2];

@@ -16,10 +16,10 @@
 // epilogue reads the shared columns first and then releases them
 // (`part_free`), so that the MMAs of the next item start while it reads the
 // rest.  (Two whole accumulators of 192 columns instead: 8192 x 4096 x 8192 86 us
-// against 82.)  Measured: 8192 x 4096 x 8192 82 us, 6.7 PFLOP/s; 16384 x 8192 x
-// 8192 275 us, 8.0 PFLOP/s, what four times the measured bf16 rate comes to.  A
+// against 82.)  Measured: 8192 x 4096 x 8192 80 us, 6.8 PFLOP/s; 16384 x 8192 x
+// 8192 274 us, 8.0 PFLOP/s, what four times the measured bf16 rate comes to.  A
 // layer's W2 for 256 experts of 144 rows each, K = 2048, N = 4096, is bound by
-// HBM: 223 us, 6.5 TB/s.
+// HBM: 220 us, 6.6 TB/s.
 //
 // Roles, in both CTAs: warp 0 the TMA producer of the CTA's own codes (its 128
 // weight rows, its half of the token rows), warp 2 that of the scales (issuing
@@ -67,7 +67,9 @@ static_assert(kStage % 1024 == 0 && kStages >= 4, "ring");
 static_assert(kNT - kAcc1 <= 128 - 32 && kNT - kAcc1 / 32 * 32 <= 128, "the shared columns are in the first round's reads");
 static_assert(kSfBase >= kAcc1 + kNT && kSfBase + kSfSlots * kSfCols <= kTmemCols, "tensor memory columns");
 
-// arrive on the barrier at the same offset in the leader CTA
+// Arrive on the barrier at the same offset in the leader CTA: this warp's reads
+// of tensor memory have ended (tcgen05.wait::ld, the fence before it), and that
+// is all the leader's MMAs wait for.
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
@@ -114,34 +116,6 @@ __device__ __forceinline__ void commit_both(uint64_t* bar) {
 __device__ __forceinline__ void commit_one(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
-}
-
-// a bounded wait of the whole warp on a barrier that the peer CTA arrives on
-__device__ __forceinline__ bool warp_wait_cl(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                             const MmParams& P) {
-  auto test = [&] {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return __all_sync(0xFFFFFFFFu, ok != 0);
-  };
-  if (test()) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (true) {
-    if (test()) return true;
-    const bool late = global_timer_ns() - t0 > P.wait_ns;
-    if (__any_sync(0xFFFFFFFFu, late || *abort_flag)) break;
-  }
-  if ((threadIdx.x & 31) == 0 && !*abort_flag) {
-    *abort_flag = 1;
-    atomicOr(P.err, kErrWaitTimeout);
-  }
-  __syncwarp();
-  return false;
 }
 
 template <bool F32, bool SW>
@@ -271,8 +245,8 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
         // the other accumulator's columns that this one shares, where its item has values in them
         const bool shared = li > 0 && (b ? prev_n > (int)kAcc1 : n_mma > (int)kAcc1);
         prev_n = n_mma;
-        if (!warp_wait_cl(&acc_empty[b], (use & 1) ^ 1, abort_flag, P) ||
-            (shared && !warp_wait_cl(&part_free[b ^ 1], ((li - 1) >> 1) & 1, abort_flag, P)))
+        if (!warp_wait(&acc_empty[b], (use & 1) ^ 1, abort_flag, P) ||
+            (shared && !warp_wait(&part_free[b ^ 1], ((li - 1) >> 1) & 1, abort_flag, P)))
           break;
         const uint32_t d_tmem = tmem + b * kAcc1;
         const uint32_t id0 = idesc_mxf4(2 * kBM, n_mma, 0), id1 = idesc_mxf4(2 * kBM, n_mma, 1);
