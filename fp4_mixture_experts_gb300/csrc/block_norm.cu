@@ -28,99 +28,105 @@ struct NormParams {
   float k;  // d^-1/2: the squares of k v sum to the mean, which overflows only if the mean itself does
 };
 
-// where element j of a thread's chunk c is: 8 adjacent elements (VEC: rows
-// start on 16 bytes and d is a multiple of 8), else a warp's 256 in 8 turns of
-// 32, so that one address and one comparison serve the 8
-template <bool VEC>
+// Where element j of a thread's chunk c is.  V adjacent elements a load: 8 where
+// rows start on 16 bytes and d is a multiple of 8; else a warp's 256 elements in
+// turns of its 32 lanes, 2 (rows start on two elements, d is even) or 1 a lane, so
+// that one address and one comparison serve the 8.
+template <int V>
 __device__ __forceinline__ int elem(int c, int j) {
   const int i = c * (int)blockDim.x + (int)threadIdx.x;
-  return VEC ? i * 8 + j : (i & ~31) * 8 + (i & 31) + 32 * j;
+  return V == 8 ? i * 8 + j : (i & ~31) * 8 + (i & 31) * V + j / V * 32 * V + j % V;
 }
 
-template <typename T>
-__device__ __forceinline__ void load8_apart(const T* p, int left, float (&v)[8]) {
+// 8 values from p = the first on; `left` elements are there to the row's end
+template <int V>
+__device__ __forceinline__ void load8(const void* p, bool f32, int left, float (&v)[8]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    v[j] = 0.f;
-    if (32 * j < left) {
-      if constexpr (sizeof(T) == 4)
-        v[j] = p[32 * j];
-      else
-        v[j] = bf16_to_f32(p[32 * j]);
+  for (int j = 0; j < 8; j += V) {
+    const int at = V == 8 ? 0 : j * 32;
+    const float* const pf = static_cast<const float*>(p) + at;
+    const uint16_t* const ph = static_cast<const uint16_t*>(p) + at;
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[j + i] = 0.f;
+    if (at >= left) continue;
+    if constexpr (V == 8) {
+      if (f32) {
+        const float4 x = reinterpret_cast<const float4*>(pf)[0], y = reinterpret_cast<const float4*>(pf)[1];
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+      } else {
+        const uint4 x = *reinterpret_cast<const uint4*>(ph);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[2 * i] = __uint_as_float(w[i] << 16);
+          v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+      }
+    } else if constexpr (V == 2) {
+      if (f32) {
+        const float2 x = *reinterpret_cast<const float2*>(pf);
+        v[j] = x.x, v[j + 1] = x.y;
+      } else {
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(ph);
+        v[j] = __uint_as_float(x << 16);
+        v[j + 1] = __uint_as_float(x & 0xFFFF0000u);
+      }
+    } else {
+      v[j] = f32 ? *pf : bf16_to_f32(*ph);
     }
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void store8_apart(T* p, int left, const float (&v)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if (32 * j < left) {
-      if constexpr (sizeof(T) == 4)
-        p[32 * j] = v[j];
-      else
-        p[32 * j] = f32_to_bf16_rn(v[j]);
-    }
-  }
-}
-
-template <bool VEC>
+// chunk c of the row that starts at element row_at
+template <int V>
 __device__ __forceinline__ void load8(const void* base, int type, int64_t row_at, int c, int d, float (&v)[8]) {
-  if (VEC) {
-    const int e = elem<true>(c, 0);
-    if (e >= d) {
+  const int e = elem<V>(c, 0);
+  if (type == MOE_FP4_TYPE_F32)
+    load8<V>(static_cast<const float*>(base) + row_at + e, true, d - e, v);
+  else
+    load8<V>(static_cast<const uint16_t*>(base) + row_at + e, false, d - e, v);
+}
+
+template <int V>
+__device__ __forceinline__ void store8(void* base, int type, int64_t row_at, int c, int d, const float (&v)[8]) {
+  const int e = elem<V>(c, 0), left = d - e;
+  auto bf2 = [](float a, float b) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  };
+  if (type == MOE_FP4_TYPE_F32) {
+    float* const p = static_cast<float*>(base) + row_at + e;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.f;
-      return;
-    }
-    if (type == MOE_FP4_TYPE_F32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + row_at + e);
-      const float4 x = p[0], y = p[1];
-      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-    } else {
-      const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + row_at + e);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    for (int j = 0; j < 8; j += V) {
+      if ((V == 8 ? 0 : j * 32) >= left) continue;
+      if constexpr (V == 8) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+      } else if constexpr (V == 2) {
+        *reinterpret_cast<float2*>(p + j * 32) = make_float2(v[j], v[j + 1]);
+      } else {
+        p[j * 32] = v[j];
       }
     }
   } else {
-    const int e = elem<false>(c, 0);
-    if (type == MOE_FP4_TYPE_F32)
-      load8_apart(static_cast<const float*>(base) + row_at + e, d - e, v);
-    else
-      load8_apart(static_cast<const uint16_t*>(base) + row_at + e, d - e, v);
+    uint16_t* const p = static_cast<uint16_t*>(base) + row_at + e;
+#pragma unroll
+    for (int j = 0; j < 8; j += V) {
+      if ((V == 8 ? 0 : j * 32) >= left) continue;
+      if constexpr (V == 8)
+        *reinterpret_cast<uint4*>(p) =
+            make_uint4(bf2(v[0], v[1]), bf2(v[2], v[3]), bf2(v[4], v[5]), bf2(v[6], v[7]));
+      else if constexpr (V == 2)
+        *reinterpret_cast<uint32_t*>(p + j * 32) = bf2(v[j], v[j + 1]);
+      else
+        p[j * 32] = f32_to_bf16_rn(v[j]);
+    }
   }
 }
 
-template <bool VEC>
-__device__ __forceinline__ void store8(void* base, int type, int64_t row_at, int c, int d, const float (&v)[8]) {
-  if (VEC) {
-    const int e = elem<true>(c, 0);
-    if (e >= d) return;
-    if (type == MOE_FP4_TYPE_F32) {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + row_at + e);
-      p[0] = make_float4(v[0], v[1], v[2], v[3]);
-      p[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-        w[j] = *reinterpret_cast<const uint32_t*>(&p);
-      }
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + row_at + e) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  } else {
-    const int e = elem<false>(c, 0);
-    if (type == MOE_FP4_TYPE_F32)
-      store8_apart(static_cast<float*>(base) + row_at + e, d - e, v);
-    else
-      store8_apart(static_cast<uint16_t*>(base) + row_at + e, d - e, v);
-  }
-}
+// A few ulp, far below the bf16 rounding of what follows.  (With the rounded
+// division: a gate of every element, 16384 x 7168 in bf16, 338 us against 265.)
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
 
 // sum over the CTA, the same in every thread; `part` holds 32 floats
 __device__ __forceinline__ float cta_sum(float s, float* part) {
@@ -136,7 +142,7 @@ __device__ __forceinline__ float cta_sum(float s, float* part) {
   return t;
 }
 
-template <int NC, bool VEC>
+template <int NC, int V>
 __global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams P) {
   griddep_begin();
   __shared__ float part[2][32];
@@ -145,16 +151,16 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams P) {
   const int d = a.d;
   float r[NC][8];
 #pragma unroll
-  for (int c = 0; c < NC; ++c) load8<VEC>(a.residual, a.residual_type, t * a.residual_stride, c, d, r[c]);
+  for (int c = 0; c < NC; ++c) load8<V>(a.residual, a.residual_type, t * a.residual_stride, c, d, r[c]);
   if (a.y) {
     float b[NC][8];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) load8<VEC>(a.y, a.y_type, t * a.y_stride, c, d, b[c]);
+    for (int c = 0; c < NC; ++c) load8<V>(a.y, a.y_type, t * a.y_stride, c, d, b[c]);
     if (a.y2) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         float v[8];
-        load8<VEC>(a.y2, a.y2_type, t * a.y2_stride, c, d, v);
+        load8<V>(a.y2, a.y2_type, t * a.y2_stride, c, d, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) b[c][j] += v[j];
       }
@@ -163,7 +169,7 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams P) {
     if (a.gate_shape == MOE_FP4_GATE_TOKEN) {
       const float g = a.gate_type == MOE_FP4_TYPE_F32 ? static_cast<const float*>(a.gate)[t]
                                                       : bf16_to_f32(static_cast<const uint16_t*>(a.gate)[t]);
-      m *= a.gate_sigmoid ? 1.f / (1.f + __expf(-g)) : g;
+      m *= a.gate_sigmoid ? sigmoid(g) : g;
     }
     if (a.post_norm) {
       float s = 0.f;
@@ -179,14 +185,14 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams P) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) b[c][j] *= m;
       if (a.post_weight) {
-        load8<VEC>(a.post_weight, a.post_weight_type, 0, c, d, v);
+        load8<V>(a.post_weight, a.post_weight_type, 0, c, d, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) b[c][j] *= v[j];
       }
       if (a.gate_shape >= MOE_FP4_GATE_CHANNEL) {
-        load8<VEC>(a.gate, a.gate_type, a.gate_shape == MOE_FP4_GATE_ELEMENT ? t * a.gate_stride : 0, c, d, v);
+        load8<V>(a.gate, a.gate_type, a.gate_shape == MOE_FP4_GATE_ELEMENT ? t * a.gate_stride : 0, c, d, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) b[c][j] *= a.gate_sigmoid ? 1.f / (1.f + __expf(-v[j])) : v[j];
+        for (int j = 0; j < 8; ++j) b[c][j] *= a.gate_sigmoid ? sigmoid(v[j]) : v[j];
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) r[c][j] += b[c][j];
@@ -194,7 +200,7 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams P) {
   }
   if (a.out) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) store8<VEC>(a.out, a.residual_type, t * a.out_stride, c, d, r[c]);
+    for (int c = 0; c < NC; ++c) store8<V>(a.out, a.residual_type, t * a.out_stride, c, d, r[c]);
   }
   if (!a.normed) return;
   float s = 0.f;
@@ -209,11 +215,11 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams P) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) r[c][j] *= n;
     if (a.next_weight) {
-      load8<VEC>(a.next_weight, a.next_weight_type, 0, c, d, v);
+      load8<V>(a.next_weight, a.next_weight_type, 0, c, d, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) r[c][j] *= v[j];
     }
-    store8<VEC>(a.normed, MOE_FP4_TYPE_BF16, t * d, c, d, r[c]);
+    store8<V>(a.normed, MOE_FP4_TYPE_BF16, t * d, c, d, r[c]);
   }
 }
 
@@ -235,40 +241,12 @@ struct RingParams {
   uint64_t wait_ns;
 };
 
-// a thread's 8 values of shared or global memory; `left`: elements from the first to the row's end
-template <bool VEC>
-__device__ __forceinline__ void unpack8(const void* p, bool f32, int left, float (&v)[8]) {
-  if (!VEC) {
-    if (f32)
-      load8_apart(static_cast<const float*>(p), left, v);
-    else
-      load8_apart(static_cast<const uint16_t*>(p), left, v);
-    return;
-  }
-  const uint4* q = static_cast<const uint4*>(p);
-  if (f32) {
-    const uint4 x = q[0], y = q[1];
-    v[0] = __uint_as_float(x.x), v[1] = __uint_as_float(x.y), v[2] = __uint_as_float(x.z), v[3] = __uint_as_float(x.w);
-    v[4] = __uint_as_float(y.x), v[5] = __uint_as_float(y.y), v[6] = __uint_as_float(y.z), v[7] = __uint_as_float(y.w);
-  } else {
-    const uint4 x = q[0];
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
-  }
-}
-
-__device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + __expf(-g)); }
-
 // The row weights from element `at` on, or `to` where there are none.
-template <bool VEC>
+template <int V>
 __device__ __forceinline__ void weight8(const void* w, int type, int at, int d, float to, float (&v)[8]) {
   if (w) {
     const bool f = type == MOE_FP4_TYPE_F32;
-    unpack8<VEC>(static_cast<const uint8_t*>(w) + (size_t)at * (f ? 4 : 2), f, d - at, v);
+    load8<V>(static_cast<const uint8_t*>(w) + (size_t)at * (f ? 4 : 2), f, d - at, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 1.f;
@@ -277,7 +255,7 @@ __device__ __forceinline__ void weight8(const void* w, int type, int at, int d, 
   for (int j = 0; j < 8; ++j) v[j] *= to;
 }
 
-template <bool KEEP, bool VEC>
+template <bool KEEP, int V>
 __global__ void __launch_bounds__(KEEP ? kRingThreads : 2 * kRingThreads, 1)
 block_norm_ring_kernel(const RingParams R) {
   griddep_begin();
@@ -300,7 +278,7 @@ block_norm_ring_kernel(const RingParams R) {
   auto row = [&](const void* base, bool f, int64_t stride, int64_t t) {
     return static_cast<const uint8_t*>(base) + t * stride * (f ? 4 : 2);
   };
-  auto edge = [&](int64_t t) { return !VEC && (t == 0 || t == T - 1); };
+  auto edge = [&](int64_t t) { return V != 8 && (t == 0 || t == T - 1); };
   // one thread: the operands of row t to slot s
   auto fill = [&](int64_t t, int s) {
     if (edge(t)) {
@@ -316,7 +294,7 @@ block_norm_ring_kernel(const RingParams R) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       bytes[i] = room[i];
-      if (!VEC && room[i]) {
+      if (V != 8 && room[i]) {
         const uint32_t skip = (uint32_t)(uintptr_t)from[i] & 15;
         from[i] -= skip;
         bytes[i] = (skip + d * (wide[i] ? 4 : 2) + 15) & ~15u;
@@ -333,12 +311,12 @@ block_norm_ring_kernel(const RingParams R) {
   if (tid == 0)
     for (int i = 0; i < R.slots && blockIdx.x + i * step < T; ++i) fill(blockIdx.x + i * step, i);
   // what multiplies the branch (its weight, a channel gate, the scale), and the next norm's weight
-  const int at[2] = {elem<VEC>(0, 0), elem<VEC>(1, 0)};
+  const int at[2] = {elem<V>(0, 0), elem<V>(1, 0)};
   auto branch_weights = [&](int c, float (&w)[8]) {
-    weight8<VEC>(a.post_weight, a.post_weight_type, at[c], d, a.scale, w);
+    weight8<V>(a.post_weight, a.post_weight_type, at[c], d, a.scale, w);
     if (a.gate_shape != MOE_FP4_GATE_CHANNEL) return;
     float g[8];
-    unpack8<VEC>(static_cast<const uint8_t*>(a.gate) + (size_t)at[c] * (gf ? 4 : 2), gf, d - at[c], g);
+    load8<V>(static_cast<const uint8_t*>(a.gate) + (size_t)at[c] * (gf ? 4 : 2), gf, d - at[c], g);
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] *= a.gate_sigmoid ? sigmoid(g[j]) : g[j];
   };
@@ -349,7 +327,7 @@ block_norm_ring_kernel(const RingParams R) {
     for (int j = 0; j < 8; ++j) bw[c][j] = nw[c][j] = 0.f;
     if (!KEEP || at[c] >= d) continue;
     branch_weights(c, bw[c]);
-    weight8<VEC>(a.next_weight, a.next_weight_type, at[c], d, 1.f, nw[c]);
+    weight8<V>(a.next_weight, a.next_weight_type, at[c], d, 1.f, nw[c]);
   }
   __syncthreads();
   int s = 0, i = 0;
@@ -365,7 +343,7 @@ block_norm_ring_kernel(const RingParams R) {
     const uint8_t* py = pr + R.r_bytes;
     const uint8_t* py2 = py + R.y_bytes;
     const uint8_t* pg = py2 + R.y2_bytes;
-    if (!VEC) {
+    if (V != 8) {
       auto at_row = [&](const uint8_t*& p, const uint8_t* g) { p = edge(t) ? g : p + ((uintptr_t)g & 15); };
       at_row(pr, row(a.residual, rf, a.residual_stride, t));
       at_row(py, row(a.y, yf, a.y_stride, t));
@@ -382,10 +360,10 @@ block_norm_ring_kernel(const RingParams R) {
           for (int j = 0; j < 8; ++j) b[c][j] = 0.f;
           continue;
         }
-        unpack8<VEC>(py + at[c] * (yf ? 4 : 2), yf, d - at[c], b[c]);
+        load8<V>(py + at[c] * (yf ? 4 : 2), yf, d - at[c], b[c]);
         if (R.y2_bytes) {
           float v[8];
-          unpack8<VEC>(py2 + at[c] * (y2f ? 4 : 2), y2f, d - at[c], v);
+          load8<V>(py2 + at[c] * (y2f ? 4 : 2), y2f, d - at[c], v);
 #pragma unroll
           for (int j = 0; j < 8; ++j) b[c][j] += v[j];
         }
@@ -405,13 +383,13 @@ block_norm_ring_kernel(const RingParams R) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) b[c][j] *= m * bw[KEEP ? c : 0][j];
         if (R.g_bytes && at[c] < d) {
-          unpack8<VEC>(pg + at[c] * (gf ? 4 : 2), gf, d - at[c], v);
+          load8<V>(pg + at[c] * (gf ? 4 : 2), gf, d - at[c], v);
 #pragma unroll
           for (int j = 0; j < 8; ++j) b[c][j] *= a.gate_sigmoid ? sigmoid(v[j]) : v[j];
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[c][j] = 0.f;
-        if (at[c] < d) unpack8<VEC>(pr + at[c] * (rf ? 4 : 2), rf, d - at[c], r[c]);
+        if (at[c] < d) load8<V>(pr + at[c] * (rf ? 4 : 2), rf, d - at[c], r[c]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[c][j] += b[c][j];
       }
@@ -420,12 +398,12 @@ block_norm_ring_kernel(const RingParams R) {
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[c][j] = 0.f;
-        if (at[c] < d) unpack8<VEC>(pr + at[c] * (rf ? 4 : 2), rf, d - at[c], r[c]);
+        if (at[c] < d) load8<V>(pr + at[c] * (rf ? 4 : 2), rf, d - at[c], r[c]);
       }
     }
     if (a.out) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) store8<VEC>(a.out, a.residual_type, t * a.out_stride, c, d, r[c]);
+      for (int c = 0; c < 2; ++c) store8<V>(a.out, a.residual_type, t * a.out_stride, c, d, r[c]);
     }
     float n = 0.f;
     if (a.normed) {
@@ -444,10 +422,10 @@ block_norm_ring_kernel(const RingParams R) {
     if (a.normed) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        if (!KEEP && at[c] < d) weight8<VEC>(a.next_weight, a.next_weight_type, at[c], d, 1.f, nw[0]);
+        if (!KEEP && at[c] < d) weight8<V>(a.next_weight, a.next_weight_type, at[c], d, 1.f, nw[0]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[c][j] *= n * nw[KEEP ? c : 0][j];
-        store8<VEC>(a.normed, MOE_FP4_TYPE_BF16, t * d, c, d, r[c]);
+        store8<V>(a.normed, MOE_FP4_TYPE_BF16, t * d, c, d, r[c]);
       }
     }
     if (++s == R.slots) {
@@ -460,7 +438,7 @@ block_norm_ring_kernel(const RingParams R) {
 
 // The ring's layout and grid; false where the plain kernel is used: few rows, or
 // too wide ones.
-template <bool VEC>
+template <int V>
 bool ring_layout(const NormParams& P, RingParams* R, int* threads, int* ctas) {
   const moe_fp4_block_norm_args& a = P.a;
   const int chunks = (a.d + 7) / 8;
@@ -469,10 +447,10 @@ bool ring_layout(const NormParams& P, RingParams* R, int* threads, int* ctas) {
   // rows read element by element: by instructions, and the ring's fewer threads an
   // SM lose for narrow ones (bf16: 16384 x 501 25 us, plain 21; x 1501 61 and 63;
   // 8192 x 4001 83 and 93; 4096 x 7167 86 and 130)
-  if (!VEC && a.d < 1536) return false;
+  if (V != 8 && a.d < 1536) return false;
   auto bytes = [&](const void* p, int type) {
     const int n = a.d * (type == MOE_FP4_TYPE_F32 ? 4 : 2);
-    return p ? VEC ? n : (n + 30) / 16 * 16 : 0;
+    return p ? V == 8 ? n : (n + 30) / 16 * 16 : 0;
   };
   R->n = P;
   R->y_bytes = bytes(a.y, a.y_type);
@@ -492,33 +470,34 @@ bool ring_layout(const NormParams& P, RingParams* R, int* threads, int* ctas) {
   return R->slots >= 2;
 }
 
-template <bool VEC>
+template <int V>
 cudaError_t launch_ring(const RingParams& R, int threads, int ctas, cudaStream_t st) {
-  auto* k = threads <= kRingThreads ? block_norm_ring_kernel<true, VEC> : block_norm_ring_kernel<false, VEC>;
+  auto* k = threads <= kRingThreads ? block_norm_ring_kernel<true, V> : block_norm_ring_kernel<false, V>;
   const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(k), kRingSmem);
   if (e != cudaSuccess) return e;
   return launch_early(k, dim3(ctas), dim3(threads), R.slots * R.slot_bytes, st, R);
 }
 
-template <bool VEC>
+template <int V>
 cudaError_t launch_norm(const NormParams& P, cudaStream_t st) {
   RingParams R;
   int ring_threads, ctas;
-  if (ring_layout<VEC>(P, &R, &ring_threads, &ctas)) return launch_ring<VEC>(R, ring_threads, ctas, st);
+  if (ring_layout<V>(P, &R, &ring_threads, &ctas)) return launch_ring<V>(R, ring_threads, ctas, st);
   // a CTA a row: one chunk of 8 elements a thread up to 1024 threads (few rows are bound by latency), else two
   const int chunks = (P.a.d + 7) / 8, nc = chunks <= 1024 ? 1 : 2;
   const int threads = ((chunks + nc - 1) / nc + 31) / 32 * 32;
-  return launch_spread(nc == 1 ? block_norm_kernel<1, VEC> : block_norm_kernel<2, VEC>, (unsigned)P.a.T,
+  return launch_spread(nc == 1 ? block_norm_kernel<1, V> : block_norm_kernel<2, V>, (unsigned)P.a.T,
                        (unsigned)threads, st, P);
 }
 
 bool is_type(int t) { return t == MOE_FP4_TYPE_BF16 || t == MOE_FP4_TYPE_F32; }
 int64_t type_size(int t) { return t == MOE_FP4_TYPE_F32 ? 4 : 2; }
-// an operand of whole elements; *vec stays set if its rows start on 16 bytes
-bool operand_ok(const void* p, int type, int64_t stride, int64_t rows, int d, bool* vec) {
+// an operand of whole elements; *v goes down to what its rows' starts allow
+bool operand_ok(const void* p, int type, int64_t stride, int64_t rows, int d, int* v) {
   if (!is_type(type) || ((uintptr_t)p & (uintptr_t)(type_size(type) - 1))) return false;
   if (rows > 1 && (stride < d || stride >= (1LL << 32))) return false;
-  if (((uintptr_t)p & 15) || (rows > 1 && (stride * type_size(type)) % 16)) *vec = false;
+  const uintptr_t starts = (uintptr_t)p | (rows > 1 ? (uintptr_t)(stride * type_size(type)) : 0);
+  *v = std::min(*v, starts % 16 == 0 ? 8 : starts % (2 * type_size(type)) == 0 ? 2 : 1);
   return true;
 }
 
@@ -547,21 +526,22 @@ extern "C" int moe_fp4_block_norm(const moe_fp4_block_norm_args* args, void* cud
     return MOE_FP4_ERR_INVALID_ARG;
   if ((a.gate_shape != MOE_FP4_GATE_NONE) != (a.gate != nullptr) || (!a.normed && a.next_weight))
     return MOE_FP4_ERR_INVALID_ARG;
-  bool vec = a.d % 8 == 0;
-  if (!operand_ok(a.residual, a.residual_type, a.residual_stride, a.T, a.d, &vec)) return MOE_FP4_ERR_INVALID_ARG;
-  if (a.y && !operand_ok(a.y, a.y_type, a.y_stride, a.T, a.d, &vec)) return MOE_FP4_ERR_INVALID_ARG;
-  if (a.y2 && !operand_ok(a.y2, a.y2_type, a.y2_stride, a.T, a.d, &vec)) return MOE_FP4_ERR_INVALID_ARG;
-  if (a.post_weight && !operand_ok(a.post_weight, a.post_weight_type, a.d, 1, a.d, &vec))
+  int v = a.d % 8 == 0 ? 8 : a.d % 2 == 0 ? 2 : 1;
+  if (!operand_ok(a.residual, a.residual_type, a.residual_stride, a.T, a.d, &v)) return MOE_FP4_ERR_INVALID_ARG;
+  if (a.y && !operand_ok(a.y, a.y_type, a.y_stride, a.T, a.d, &v)) return MOE_FP4_ERR_INVALID_ARG;
+  if (a.y2 && !operand_ok(a.y2, a.y2_type, a.y2_stride, a.T, a.d, &v)) return MOE_FP4_ERR_INVALID_ARG;
+  if (a.post_weight && !operand_ok(a.post_weight, a.post_weight_type, a.d, 1, a.d, &v))
     return MOE_FP4_ERR_INVALID_ARG;
-  if (a.next_weight && !operand_ok(a.next_weight, a.next_weight_type, a.d, 1, a.d, &vec))
+  if (a.next_weight && !operand_ok(a.next_weight, a.next_weight_type, a.d, 1, a.d, &v))
     return MOE_FP4_ERR_INVALID_ARG;
-  bool any = true;  // a [T] gate is read one element a row
+  int any = 8;  // a [T] gate is read one element a row
   if (a.gate && !operand_ok(a.gate, a.gate_type, a.gate_stride, a.gate_shape == MOE_FP4_GATE_ELEMENT ? a.T : 1, a.d,
-                            a.gate_shape == MOE_FP4_GATE_TOKEN ? &any : &vec))
+                            a.gate_shape == MOE_FP4_GATE_TOKEN ? &any : &v))
     return MOE_FP4_ERR_INVALID_ARG;
-  if (a.out && !operand_ok(a.out, a.residual_type, a.out_stride, a.T, a.d, &vec)) return MOE_FP4_ERR_INVALID_ARG;
-  if (a.normed && !operand_ok(a.normed, MOE_FP4_TYPE_BF16, a.d, a.T, a.d, &vec)) return MOE_FP4_ERR_INVALID_ARG;
+  if (a.out && !operand_ok(a.out, a.residual_type, a.out_stride, a.T, a.d, &v)) return MOE_FP4_ERR_INVALID_ARG;
+  if (a.normed && !operand_ok(a.normed, MOE_FP4_TYPE_BF16, a.d, a.T, a.d, &v)) return MOE_FP4_ERR_INVALID_ARG;
   const NormParams P{a, 1.0f / sqrtf((float)a.d)};
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  return (vec ? launch_norm<true>(P, st) : launch_norm<false>(P, st)) == cudaSuccess ? MOE_FP4_OK : MOE_FP4_ERR_CUDA;
+  const cudaError_t e = v == 8 ? launch_norm<8>(P, st) : v == 2 ? launch_norm<2>(P, st) : launch_norm<1>(P, st);
+  return e == cudaSuccess ? MOE_FP4_OK : MOE_FP4_ERR_CUDA;
 }
