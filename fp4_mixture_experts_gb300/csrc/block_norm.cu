@@ -278,7 +278,7 @@ block_norm_ring_kernel(const RingParams R) {
   auto row = [&](const void* base, bool f, int64_t stride, int64_t t) {
     return static_cast<const uint8_t*>(base) + t * stride * (f ? 4 : 2);
   };
-  auto edge = [&](int64_t t) { return V != 8 && (t == 0 || t == T - 1); };
+  auto edge = [&](int64_t t) { return V == 1 && (t == 0 || t == T - 1); };
   // one thread: the operands of row t to slot s
   auto fill = [&](int64_t t, int s) {
     if (edge(t)) {
@@ -294,7 +294,7 @@ block_norm_ring_kernel(const RingParams R) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       bytes[i] = room[i];
-      if (V != 8 && room[i]) {
+      if (V == 1 && room[i]) {
         const uint32_t skip = (uint32_t)(uintptr_t)from[i] & 15;
         from[i] -= skip;
         bytes[i] = (skip + d * (wide[i] ? 4 : 2) + 15) & ~15u;
@@ -343,7 +343,7 @@ block_norm_ring_kernel(const RingParams R) {
     const uint8_t* py = pr + R.r_bytes;
     const uint8_t* py2 = py + R.y_bytes;
     const uint8_t* pg = py2 + R.y2_bytes;
-    if (V != 8) {
+    if (V == 1) {
       auto at_row = [&](const uint8_t*& p, const uint8_t* g) { p = edge(t) ? g : p + ((uintptr_t)g & 15); };
       at_row(pr, row(a.residual, rf, a.residual_stride, t));
       at_row(py, row(a.y, yf, a.y_stride, t));
@@ -444,10 +444,11 @@ bool ring_layout(const NormParams& P, RingParams* R, int* threads, int* ctas) {
   const int chunks = (a.d + 7) / 8;
   *threads = std::max(32, ((chunks + 1) / 2 + 31) / 32 * 32);
   if (*threads > 2 * kRingThreads) return false;
-  // rows read element by element: by instructions, and the ring's fewer threads an
-  // SM lose for narrow ones (bf16: 16384 x 501 25 us, plain 21; x 1501 61 and 63;
-  // 8192 x 4001 83 and 93; 4096 x 7167 86 and 130)
-  if (V != 8 && a.d < 1536) return false;
+  // rows read element by element are bound by instructions: the ring's fewer
+  // threads an SM pay for wide ones alone (bf16: 8192 x 3001 64 us, plain 64; x 4097
+  // 89 and 116; 4096 x 7167 86 and 122), and not at all by pairs (8192 x 5122 114
+  // and 91; 4096 x 7166 72 and 72)
+  if (V == 1 && a.d <= 4096) return false;
   auto bytes = [&](const void* p, int type) {
     const int n = a.d * (type == MOE_FP4_TYPE_F32 ? 4 : 2);
     return p ? V == 8 ? n : (n + 30) / 16 * 16 : 0;
@@ -482,7 +483,8 @@ template <int V>
 cudaError_t launch_norm(const NormParams& P, cudaStream_t st) {
   RingParams R;
   int ring_threads, ctas;
-  if (ring_layout<V>(P, &R, &ring_threads, &ctas)) return launch_ring<V>(R, ring_threads, ctas, st);
+  if constexpr (V != 2)
+    if (ring_layout<V>(P, &R, &ring_threads, &ctas)) return launch_ring<V>(R, ring_threads, ctas, st);
   // a CTA a row: one chunk of 8 elements a thread up to 1024 threads (few rows are bound by latency), else two
   const int chunks = (P.a.d + 7) / 8, nc = chunks <= 1024 ? 1 : 2;
   const int threads = ((chunks + nc - 1) / nc + 31) / 32 * 32;
