@@ -245,7 +245,7 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
 #pragma unroll
           for (int j = 0; j < kTokens; ++j) part[(c0 + j) * kPartPitch + e.q * 32 + lane] = __uint_as_float(v[j]);
         }
-      } else if (!e.item(P.y, tmem + b * NT, t.row0, t.n, f0, nf, 0, ok, [&](bool, bool last) {
+      } else if (!e.item(P.y, tmem + b * NT, t.row0, t.n, f0, nf, 0, ok, li, [&](bool, bool last) {
                    if (last && lane == 0) mbar_arrive(&acc_empty[b]);
                  })) {
         break;

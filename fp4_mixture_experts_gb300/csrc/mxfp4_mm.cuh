@@ -288,14 +288,15 @@ struct Ring {
 constexpr int kEpiWarps = 8;
 constexpr int kTokens = 32;  // tokens of a chunk = its columns
 
-// whether `ok` holds in all epilogue warps: they go on, or leave, together
-__device__ __forceinline__ bool all_of_epilogue(bool ok) {
+// whether `ok` holds in all the `warps` epilogue warps that share barrier `id`:
+// they go on, or leave, together
+__device__ __forceinline__ bool all_of_epilogue(bool ok, int id, int warps) {
   uint32_t all;
   asm volatile(
-      "{\n\t.reg .pred pin, pout;\n\tsetp.ne.u32 pin, %1, 0;\n\tbar.red.and.pred pout, 3, %2, pin;\n\t"
+      "{\n\t.reg .pred pin, pout;\n\tsetp.ne.u32 pin, %1, 0;\n\tbar.red.and.pred pout, %3, %2, pin;\n\t"
       "selp.u32 %0, 1, 0, pout;\n}"
       : "=r"(all)
-      : "r"(ok ? 1u : 0u), "r"(kEpiWarps * 32)
+      : "r"(ok ? 1u : 0u), "r"(warps * 32), "r"(id)
       : "memory");
   return all != 0;
 }
@@ -364,6 +365,27 @@ struct Epilogue {
     }
   }
 
+  // An item of one chunk: the groups take such items in turn (32 tokens x 8 over
+  // 128 experts, K = 512, N = 2048: 16.9 -> 15.2 us; 1024 x 8 over 256: 41.4 -> 39.2).
+  template <typename F>
+  __device__ __forceinline__ bool one_chunk(void* y, uint32_t taddr, int row0, int n, int f0, int nf, bool ok, int turn,
+                                            F&& after_reads) {
+    if ((turn & 1) != h) {
+      __syncwarp();
+      after_reads(true, true);
+      return ok;
+    }
+    uint32_t v[kTokens];
+    tmem_ld32_async(taddr + ((uint32_t)(q * 32) << 16), v);
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncwarp();
+    after_reads(true, true);
+    if (!all_of_epilogue(ok, 4 + h, kEpiWarps / 2)) return false;
+    put<false>(v, static_cast<uint8_t*>(y) + (size_t)row0 * ldy + (size_t)f0 * kEs, n, nf);
+    return true;
+  }
+
   // One item: n tokens from row0, its accumulator at taddr, features from f0
   // (nf of them in y).  Chunks are taken from `first` on, cyclically.
   // after_reads(round0, last): this group has read its chunks of the first
@@ -372,8 +394,9 @@ struct Epilogue {
   // accumulator ran out (not ok).
   template <typename F>
   __device__ __forceinline__ bool item(void* y, uint32_t taddr, int row0, int n, int f0, int nf, int first, bool ok,
-                                       F&& after_reads) {
+                                       int turn, F&& after_reads) {
     const int chunks = (n + kTokens - 1) / kTokens;
+    if (chunks == 1) return one_chunk(y, taddr, row0, n, f0, nf, ok, turn, after_reads);
     uint8_t* const y0 = static_cast<uint8_t*>(y) + (size_t)row0 * ldy + (size_t)f0 * kEs;
     taddr += (uint32_t)(q * 32) << 16;
     int i = h;
@@ -388,7 +411,7 @@ struct Epilogue {
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       after_reads(i == h, i + 4 >= chunks);
-      if (i == h && !all_of_epilogue(ok)) return false;
+      if (i == h && !all_of_epilogue(ok, 3, kEpiWarps)) return false;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         if (i + 2 * k >= chunks) break;

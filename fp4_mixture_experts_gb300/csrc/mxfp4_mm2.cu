@@ -334,7 +334,7 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
       // so its chunks are taken from there; accumulator 1's first 256 - kAcc1
       const int chunks = (t.n + kTokens - 1) / kTokens, from = kAcc1 / kTokens;
       const int start = b == 0 && chunks > from ? from : 0;
-      if (!e.item(P.y, tmem + b * kAcc1, t.row0, t.n, f0, nf, start, ok, [&](bool round0, bool last) {
+      if (!e.item(P.y, tmem + b * kAcc1, t.row0, t.n, f0, nf, start, ok, li, [&](bool round0, bool last) {
             if (lane != 0) return;
             if (round0) arrive_leader(&part_free[b]);
             if (last) arrive_leader(&acc_empty[b]);
