@@ -427,10 +427,13 @@ cudaError_t launch_mm(const moe_fp4_mm_dims& d, const uint8_t* a, const uint8_t*
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Bytes of the lists with which rows of x that are used several times are
-// quantised once; 0 where that does not pay: three launches more, so from 2^22
-// gathered elements, and two uses of a row, on.
+// quantised once; 0 where that does not pay, having three launches more: below
+// two uses of a row, 2^24 gathered elements and 2^13 gathered rows (4 uses, the
+// whole product: 16384 rows of 512 12.9 us, gathered rows 13.3; 32768 rows of 512
+// 16.5 and 19.6; 8192 of 2048 15.1 and 15.0, 16384 of 2048 18.3 and 20.5; 4681 of
+// 7168 24.3 and 22.7, 9362 of 7168 31.9 and 36.8).
 size_t once_bytes(const MxRows& R) {
-  if (!R.row_index || R.rows < 2 * R.x_rows || R.rows * R.K < (1LL << 22)) return 0;
+  if (!R.row_index || R.rows < 2 * R.x_rows || R.rows < (1 << 13) || R.rows * R.K < (1LL << 24)) return 0;
   return (size_t)(R.x_rows + 1 + R.rows) * sizeof(int32_t);
 }
 

@@ -346,7 +346,7 @@ def test_no_rows():
 def test_rows_used_several_times_are_quantised_once_with_the_same_bits():
     """a workspace that lets the call quantise each source row once and gather its codes"""
     rng = np.random.default_rng(21)
-    T, k, E, N, K = 1100, 8, 16, 96, 544
+    T, k, E, N, K = 2100, 8, 16, 96, 1056
     S = T * k
     counts = rng.multinomial(S, np.ones(E) / E)
     counts[3] += counts[4]
