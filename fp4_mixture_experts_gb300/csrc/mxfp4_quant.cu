@@ -67,33 +67,40 @@ __global__ void __launch_bounds__(kThreads) mxfp4_quantize_rows_kernel(const Qua
   const int src = source_row(P, r);
   if (src < 0 && lane == 0) atomicOr(&g_quant_err[0], kErrBadExpertId);
   const int64_t at = src * P.x_stride;
-  uint8_t* const tile = TILED ? tile_row(P, r, kt) : nullptr;
-  uint8_t* const codes = P.codes + (size_t)r * (P.K / 2);
-  for (int c0 = lane; c0 - lane < per_row; c0 += 64) {
-    uint32_t w[2][kPer];
+  uint32_t w[2][kPer];
+  auto load = [&](int c0) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) w[u][j] = 0;
       if (src >= 0 && c0 + 32 * u < per_row) load16_raw<F32, VEC>(P.x, at + (c0 + 32 * u) * kPer, w[u]);
     }
+  };
+  load(lane);
+  uint8_t* const tile = TILED ? tile_row(P, r, kt) : nullptr;  // while the loads are on their way
+  uint8_t* const codes = P.codes + (size_t)r * (P.K / 2);
+  for (int c0 = lane;;) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int c = c0 + 32 * u, b = c >> 1;
       uint32_t sb;
       const uint2 q = quantize16<F32>(w[u], sb);
+      if (TILED) {  // a word of four scales in every eighth lane, 0 past the end of K
+        sb <<= 8 * (b & 3);
+        sb |= __shfl_xor_sync(0xFFFFFFFFu, sb, 2);
+        sb |= __shfl_xor_sync(0xFFFFFFFFu, sb, 4);
+      }
       if (c >= per_row) continue;
       *reinterpret_cast<uint2*>(codes + c * (kPer / 2)) = q;
-      if (c & 1) continue;
       if (!TILED) {
-        P.scales[(size_t)r * nb + b] = (uint8_t)sb;
-      } else if (tile != nullptr) {
-        uint8_t* t = tile + (b >> 2) * 512;
-        t[b & 3] = (uint8_t)sb;
-        if (b == nb - 1)
-          for (int p = (b & 3) + 1; p < 4; ++p) t[p] = 0;
+        if ((c & 1) == 0) P.scales[(size_t)r * nb + b] = (uint8_t)sb;
+      } else if ((c & 7) == 0 && tile != nullptr) {
+        *reinterpret_cast<uint32_t*>(tile + (b >> 2) * 512) = sb;
       }
     }
+    c0 += 64;
+    if (c0 - lane >= per_row) break;
+    load(c0);
   }
 }
 
