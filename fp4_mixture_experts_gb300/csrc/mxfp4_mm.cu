@@ -372,12 +372,14 @@ cudaError_t launch_few(const moe_fp4_mm_dims& d, const MmParams& P, const MxRows
 
 // The kernel and tile of a product with more than a few rows: the one whose
 // time, rounds over the SMs x (stages x time of a stage + fixed time of an
-// item), is least.  Measured in us, over N = 1024 .. 16384, K = 1024 and 4096,
-// M = 16 .. 2048 and ragged groups of 1 .. 1024 rows: a stage takes 0.23, 0.24
-// and 0.29, an item 0.9, 1.2 and 3.2 beside them, with tiles of 128 weight rows
-// x 64 and 128 token rows on an SM and of 256 x 256 on a pair, whose launch
-// costs 1 more.  (M = 256, N = K = 4096: 9.4, 10.1 and 13.6 us; M = 2048: 36,
-// 26 and 24 us.)  The tiles of a group are estimated from the mean of the
+// item), is least.  Fitted in us to products of 64 .. 13073 rows, N = 512 .. 8192, K
+// = 128 .. 4096, with and without SwiGLU, and of ragged groups of 32 .. 1000 rows: a
+// stage takes 0.23, 0.24 and 0.25, an item 0.6, 1.05 and 2.2 (SwiGLU 2.8) beside
+// them, with tiles of 128 weight rows x 64 and 128 token rows on an SM and of 256 x
+// 256 on a pair; the kernels' fixed times differ by 0.15 and 1.3.  (The choice is
+// off the best of the three by 0.3% in the mean and 15% at most.  M = 256, N = K =
+// 4096: 9.4, 10.1 and 13.6 us; M = N = 4096, K = 2048: 35, 22 and 18; M = 8192, N =
+// 4096, K = 128: 24, 19 and 19.)  The tiles of a group are estimated from the mean of the
 // groups' rows, half a standard deviation of a uniform routing taken off.  A
 // dense product may split K over clusters of 2 or 4 CTAs (of 8, too few fit the
 // GPCs: 32 x 4096 x 2048 10 us), which costs 0.8 and 0.017 a token row.  (N = K =
@@ -394,7 +396,7 @@ Choice choose_tile(const moe_fp4_mm_dims& d, bool grouped) {
   const struct {
     int rows, wrows, sms;
     double stage, item, launch;
-  } kernels[] = {{64, 128, 1, 0.23, 0.9, 0}, {128, 128, 1, 0.24, 1.2, 0}, {256, 256, 2, 0.29, 3.2, 1}};
+  } kernels[] = {{64, 128, 1, 0.23, 0.6, 0}, {128, 128, 1, 0.24, 1.05, 0.15}, {256, 256, 2, 0.25, d.swiglu ? 2.8 : 2.2, 1.3}};
   for (const auto& k : kernels) {
     const double rows = grouped ? std::max(mean - 0.5 * std::sqrt(mean), 1.0) : mean;
     const double tiles = std::min(std::ceil(rows / k.rows) * d.E, (double)d.M);
