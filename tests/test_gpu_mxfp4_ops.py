@@ -215,6 +215,24 @@ def test_linear_long_k(M, N, K):
     dense(M, N, K, False, torch.float32, 5, f32=True)
 
 
+# odd sizes for which tiles of 128 token rows are chosen, and for which SM pairs are
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K,swiglu", [(290, 4095, 1056, False), (640, 2050, 96, True), (777, 4095, 2016, False),
+                                          (1999, 4096, 1056, False), (900, 2562, 2080, True), (2700, 1004, 2080, True)])
+def test_linear_larger_tiles(M, N, K, swiglu, dtype):
+    dense(M, N, K, swiglu, dtype, M)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("counts,N,K,swiglu", [([100, 120, 0, 130, 97, 1, 128, 129, 90], 2001, 544, False),
+                                               ([100, 120, 0, 130, 97, 1, 128, 129, 90], 2002, 544, True),
+                                               ([257, 0, 1, 513, 255, 31, 130, 96, 17], 1501, 1504, False),
+                                               ([257, 0, 1, 513, 255, 31, 130, 96, 17], 1498, 2080, True),
+                                               ([0, 256, 0, 512, 224, 33, 192, 64, 19], 4002, 544, False)])
+def test_grouped_larger_tiles(counts, N, K, swiglu, dtype):
+    grouped(counts, N, K, swiglu, dtype, N, before=3, after=2)
+
+
 def test_linear_equals_quantize_then_matmul():
     rng = np.random.default_rng(3)
     for M in (1, 9, 100, 600):
