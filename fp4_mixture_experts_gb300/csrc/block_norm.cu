@@ -238,6 +238,7 @@ struct RingParams {
   NormParams n;
   int slots, slot_bytes;                    // rows in the ring
   int y_bytes, y2_bytes, r_bytes, g_bytes;  // of a row in its slot; 0: not there
+  int fault;                                // CTA 0 never loads its first row
   uint64_t wait_ns;
 };
 
@@ -308,8 +309,10 @@ block_norm_ring_kernel(const RingParams R) {
       p += room[i];
     }
   };
+  int fills = 0;  // of thread 0
   if (tid == 0)
-    for (int i = 0; i < R.slots && blockIdx.x + i * step < T; ++i) fill(blockIdx.x + i * step, i);
+    for (; fills < R.slots && blockIdx.x + fills * step < T; ++fills)
+      if (!(R.fault && blockIdx.x == 0 && fills == 0)) fill(blockIdx.x + fills * step, fills);
   // what multiplies the branch (its weight, a channel gate, the scale), and the next norm's weight
   const int at[2] = {elem<V>(0, 0), elem<V>(1, 0)};
   auto branch_weights = [&](int c, float (&w)[8]) {
@@ -338,7 +341,8 @@ block_norm_ring_kernel(const RingParams R) {
       m = gf ? static_cast<const float*>(a.gate)[t] : bf16_to_f32(static_cast<const uint16_t*>(a.gate)[t]);
       if (a.gate_sigmoid) m = sigmoid(m);
     }
-    mbar_wait(&full[s], phase, abort_flag, &g_norm_err[0], kErrWaitTimeout, R.wait_ns);
+    // (every thread goes on to the CTA's sums, also if its wait ran out: it stores nothing then)
+    const bool ok = mbar_wait(&full[s], phase, abort_flag, &g_norm_err[0], kErrWaitTimeout, R.wait_ns);
     const uint8_t* pr = ring + (size_t)s * R.slot_bytes;
     const uint8_t* py = pr + R.r_bytes;
     const uint8_t* py2 = py + R.y_bytes;
@@ -401,7 +405,7 @@ block_norm_ring_kernel(const RingParams R) {
         if (at[c] < d) load8<V>(pr + at[c] * (rf ? 4 : 2), rf, d - at[c], r[c]);
       }
     }
-    if (a.out) {
+    if (a.out && ok) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) store8<V>(a.out, a.residual_type, t * a.out_stride, c, d, r[c]);
     }
@@ -418,8 +422,11 @@ block_norm_ring_kernel(const RingParams R) {
       __syncthreads();
     }
     // (a barrier has passed since the last read of the slot, and since the sums of row i - 1 were read)
-    if (tid == 0 && t + (int64_t)R.slots * step < T) fill(t + (int64_t)R.slots * step, s);
-    if (a.normed) {
+    if (tid == 0 && t + (int64_t)R.slots * step < T && !*abort_flag) {
+      fill(t + (int64_t)R.slots * step, s);
+      ++fills;
+    }
+    if (a.normed && ok) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         if (!KEEP && at[c] < d) weight8<V>(a.next_weight, a.next_weight_type, at[c], d, 1.f, nw[0]);
@@ -433,7 +440,12 @@ block_norm_ring_kernel(const RingParams R) {
       phase ^= 1;
     }
   }
-  // (every row that was filled has been waited for)
+  // every row that was filled has been waited for, unless a wait ran out: then no copy may outlive the CTA
+  __syncthreads();
+  if (tid == 0 && *abort_flag)
+    for (int q = std::max(fills - R.slots, 0); q < fills; ++q)
+      mbar_wait_drain(&full[q % R.slots], (q / R.slots) & 1, &g_norm_err[0], kErrWaitTimeout, R.wait_ns);
+  __syncthreads();
 }
 
 // The ring's layout and grid; false where the plain kernel is used: few rows, or
@@ -467,6 +479,7 @@ bool ring_layout(const NormParams& P, RingParams* R, int* threads, int* ctas) {
   *ctas = per_sm * num_sms();
   if (a.T < 4 * (int64_t)*ctas) return false;
   R->slots = std::min(kRingMaxSlots, kRingSmem / per_sm / R->slot_bytes);
+  R->fault = fault_site() == MOE_FP4_FAULT_TC_TOKEN_TILE;
   R->wait_ns = wait_limit_ns();
   return R->slots >= 2;
 }

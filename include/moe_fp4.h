@@ -483,7 +483,8 @@ int moe_fp4_ops_check(void* cuda_stream);
  * that call are incomplete, and moe_fp4_check reports MOE_FP4_ERR_DEVICE.
  * The products (moe_fp4_mxfp4_matmul, moe_fp4_mxfp4_linear) take
  * MOE_FP4_FAULT_TC_TOKEN_TILE too (the first CTA, or pair, never loads its first
- * stage; moe_fp4_ops_check reports it), and the limit.
+ * stage; moe_fp4_ops_check reports it), and the limit; so does moe_fp4_block_norm
+ * in its form for many rows (the first CTA never loads its first row).
  * MOE_FP4_FAULT_NONE (wait_limit_us ignored) restores normal operation.
  * Returns MOE_FP4_ERR_INVALID_ARG for an unknown site or a zero limit. */
 #define MOE_FP4_FAULT_NONE 0

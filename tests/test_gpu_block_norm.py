@@ -211,6 +211,26 @@ def test_many_rows_at_odd_addresses_in_place(d, off):
     moe.ops_check()
 
 
+@pytest.mark.parametrize("T,d", [(3000, 4096), (700, 7167)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(T, d):
+    """host-planted: the first CTA of the persistent form never loads its first row (no fault on the GPU)"""
+    rng = np.random.default_rng(T)
+    r, y = rand(rng, (T, d), BF), rand(rng, (T, d), F32)
+    want = moe.block_residual(r, y)
+    moe.ops_check()
+    moe.set_fault_injection(moe.FAULT_TC_TOKEN_TILE, 2000)
+    try:
+        moe.block_residual(r, y)
+        torch.cuda.synchronize()
+    finally:
+        moe.set_fault_injection(moe.FAULT_NONE)
+    with pytest.raises(moe.MoeFp4Error):
+        moe.ops_check()
+    again = moe.block_residual(r, y)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+    moe.ops_check()
+
+
 def test_offsets_beyond_32_bits():
     rng = np.random.default_rng(4)
     T, d = 140000, 16384
