@@ -53,7 +53,7 @@ struct Mm1Params {
   const void* x;             // rows: bf16, fp32 or codes
   int64_t x_rows, x_stride;  // stride in elements (codes: in elements too, two a byte)
   const int32_t* row_index;
-  int div, vec;              // vec: rows of x start on 16 bytes
+  int div, align;            // align: MxRows::align()
 };
 
 // SRC 0: bf16 rows, 1: fp32 rows, 2: codes with tiled scales
@@ -193,10 +193,12 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
         const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(Q.x) + (src + k) / 2);
         raw[0] = q.x, raw[1] = q.y;
         raw[2] = P.a_scales[(size_t)(k >> 7) * kSfTile + 16 * row + ((k >> 5) & 3)];
-      } else if (Q.vec) {
-        load16_raw<SRC == 1, true>(Q.x, src + k, raw);
+      } else if (Q.align == 32) {
+        load16_raw<SRC == 1, 32>(Q.x, src + k, raw);
+      } else if (Q.align == 16) {
+        load16_raw<SRC == 1, 16>(Q.x, src + k, raw);
       } else {
-        load16_raw<SRC == 1, false>(Q.x, src + k, raw);
+        load16_raw<SRC == 1, 0>(Q.x, src + k, raw);
       }
     };
     load(k0, next[0]);
@@ -302,7 +304,7 @@ cudaError_t launch_mm_few(const CUtensorMap& map_w, const MmParams& P, const MxR
   Q.x_stride = x->x_stride;
   Q.row_index = x->row_index;
   Q.div = x->div;
-  Q.vec = ((uintptr_t)x->x & 15) == 0 && (x->x_stride * (x->f32 ? 4 : 2)) % 16 == 0;
+  Q.align = x->align();
   return x->f32 ? launch_src<1>(map_w, Q, st) : launch_src<0>(map_w, Q, st);
 }
 

@@ -58,7 +58,7 @@ __device__ __forceinline__ int source_row(const QuantParams& P, int r) {
 // division and a group search in every thread, gathering 36,864 rows of 2048
 // took 63 us (27 so).  65536 x 4096: 96 us, the rate of a copy; tiled on a grid
 // that fills the SMs and strides, 109.
-template <bool F32, bool VEC, bool TILED>
+template <bool F32, int ALIGN, bool TILED>
 __global__ void __launch_bounds__(kThreads) mxfp4_quantize_rows_kernel(const QuantParams P) {
   griddep_begin();
   const int per_row = P.K / kPer, nb = P.K / 32, kt = (P.K + 127) / 128;
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreads) mxfp4_quantize_rows_kernel(const Qua
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) w[u][j] = 0;
-      if (src >= 0 && c0 + 32 * u < per_row) load16_raw<F32, VEC>(P.x, at + (c0 + 32 * u) * kPer, w[u]);
+      if (src >= 0 && c0 + 32 * u < per_row) load16_raw<F32, ALIGN>(P.x, at + (c0 + 32 * u) * kPer, w[u]);
     }
   };
   load(lane);
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) mxfp4_quantize_rows_kernel(const Qua
 }
 
 // Few or short rows: flat over the chunks of 16 elements
-template <bool F32, bool VEC, bool TILED>
+template <bool F32, int ALIGN, bool TILED>
 __global__ void __launch_bounds__(kThreads) mxfp4_quantize_flat_kernel(const QuantParams P) {
   griddep_begin();
   const int per_row = P.K / kPer, nb = P.K / 32, kt = (P.K + 127) / 128;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) mxfp4_quantize_flat_kernel(const Qua
     if (src < 0)
       atomicOr(&g_quant_err[0], kErrBadExpertId);
     else if (in)
-      load16_raw<F32, VEC>(P.x, src * P.x_stride + (int64_t)c * kPer, w);
+      load16_raw<F32, ALIGN>(P.x, src * P.x_stride + (int64_t)c * kPer, w);
     uint32_t sb;
     const uint2 q = quantize16<F32>(w, sb);
     if (!in) continue;
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) list_link_kernel(const QuantParams P
   next[r] = atomicExch(&head[s], r);
 }
 
-template <bool F32, bool VEC>
+template <bool F32, int ALIGN>
 __global__ void __launch_bounds__(kThreads)
 mxfp4_quantize_places_kernel(const QuantParams P, const int32_t* __restrict__ head, const int32_t* __restrict__ next) {
   griddep_begin();
@@ -205,7 +205,7 @@ mxfp4_quantize_places_kernel(const QuantParams P, const int32_t* __restrict__ he
 #pragma unroll
         for (int j = 0; j < kPer; ++j) w[u][j] = 0;
         if (s < (int)P.x_rows && c0 + 32 * u < per_row)
-          load16_raw<F32, VEC>(P.x, s * P.x_stride + (c0 + 32 * u) * kPer, w[u]);
+          load16_raw<F32, ALIGN>(P.x, s * P.x_stride + (c0 + 32 * u) * kPer, w[u]);
       }
       uint2 q[2];
       uint32_t sw[2];  // in every eighth lane, the word of four scales
@@ -309,31 +309,32 @@ int grid_for(int64_t threads, int per_sm) {
 
 namespace {
 
-template <bool F32, bool VEC, bool TILED>
+template <bool F32, int ALIGN, bool TILED>
 cudaError_t launch_quant(const QuantParams& P, cudaStream_t st) {
   // a warp a row where that fills the SMs (8 rows each at least) and most lanes
   if (P.K >= 512 && P.rows >= 8 * num_sms())
-    return launch_spread(mxfp4_quantize_rows_kernel<F32, VEC, TILED>, (unsigned)((P.rows + 7) / 8), kThreads, st, P);
-  return launch_spread(mxfp4_quantize_flat_kernel<F32, VEC, TILED>, (unsigned)grid_for(P.rows * (P.K / kPer), 8),
+    return launch_spread(mxfp4_quantize_rows_kernel<F32, ALIGN, TILED>, (unsigned)((P.rows + 7) / 8), kThreads, st, P);
+  return launch_spread(mxfp4_quantize_flat_kernel<F32, ALIGN, TILED>, (unsigned)grid_for(P.rows * (P.K / kPer), 8),
                        kThreads, st, P);
 }
 
+template <bool F32, int ALIGN>
+cudaError_t launch_quant(const QuantParams& P, bool tiled, cudaStream_t st) {
+  return tiled ? launch_quant<F32, ALIGN, true>(P, st) : launch_quant<F32, ALIGN, false>(P, st);
+}
+
 template <bool F32>
-cudaError_t launch_quant(const QuantParams& P, bool vec, bool tiled, cudaStream_t st) {
-  if (vec) return tiled ? launch_quant<F32, true, true>(P, st) : launch_quant<F32, true, false>(P, st);
-  return tiled ? launch_quant<F32, false, true>(P, st) : launch_quant<F32, false, false>(P, st);
+cudaError_t launch_quant(const QuantParams& P, int align, bool tiled, cudaStream_t st) {
+  return align == 32   ? launch_quant<F32, 32>(P, tiled, st)
+         : align == 16 ? launch_quant<F32, 16>(P, tiled, st)
+                       : launch_quant<F32, 0>(P, tiled, st);
 }
 
 }  // namespace
 
-static bool rows_vec(const MxRows& R) {
-  return ((uintptr_t)R.x & 15) == 0 && (R.x_stride * (R.f32 ? 4 : 2)) % 16 == 0;
-}
-
 cudaError_t launch_mxfp4_quantize(const MxRows& R, uint8_t* codes, uint8_t* scales, bool tiled, cudaStream_t st) {
   const QuantParams P{R.x, R.x_rows, R.x_stride, R.row_index, R.offsets, codes, scales, R.rows, R.K, R.div, R.groups};
-  const bool vec = rows_vec(R);
-  return R.f32 ? launch_quant<true>(P, vec, tiled, st) : launch_quant<false>(P, vec, tiled, st);
+  return R.f32 ? launch_quant<true>(P, R.align(), tiled, st) : launch_quant<false>(P, R.align(), tiled, st);
 }
 
 cudaError_t launch_mxfp4_quantize_once(const MxRows& R, int32_t* lists, uint8_t* codes, uint8_t* scales,
@@ -344,9 +345,13 @@ cudaError_t launch_mxfp4_quantize_once(const MxRows& R, int32_t* lists, uint8_t*
   cudaError_t e = launch_spread(list_init_kernel, blocks(R.x_rows + 1), kThreads, st, head, (int)R.x_rows + 1);
   if (e == cudaSuccess) e = launch_spread(list_link_kernel, blocks(R.rows), kThreads, st, P, head, next);
   if (e != cudaSuccess) return e;
-  const bool vec = rows_vec(R);
-  auto* k = R.f32 ? (vec ? mxfp4_quantize_places_kernel<true, true> : mxfp4_quantize_places_kernel<true, false>)
-                  : (vec ? mxfp4_quantize_places_kernel<false, true> : mxfp4_quantize_places_kernel<false, false>);
+  const int al = R.align();
+  auto* k = R.f32 ? (al == 32   ? mxfp4_quantize_places_kernel<true, 32>
+                     : al == 16 ? mxfp4_quantize_places_kernel<true, 16>
+                                : mxfp4_quantize_places_kernel<true, 0>)
+                  : (al == 32   ? mxfp4_quantize_places_kernel<false, 32>
+                     : al == 16 ? mxfp4_quantize_places_kernel<false, 16>
+                                : mxfp4_quantize_places_kernel<false, 0>);
   return launch_spread(k, blocks((R.x_rows + 1) * 32), kThreads, st, P, (const int32_t*)head, (const int32_t*)next);
 }
 

@@ -130,6 +130,22 @@ def test_quantize_strided_and_unaligned_rows(K, pad, shift, f32):
     np.testing.assert_array_equal(scales.cpu().numpy(), want_s)
 
 
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (4, 0), (8, 8), (1, 1)])
+def test_quantize_many_rows_at_every_alignment(pad, shift, f32):
+    R, K = 1300, 544
+    x = rows(np.random.default_rng(pad), R, K + 32, f32)[:, :K + pad + shift].contiguous()[:, shift:shift + K]
+    codes, scales = moe.mxfp4_quantize(x)
+    want_c, want_s = O.quantize(f64(x))
+    np.testing.assert_array_equal(codes.cpu().numpy(), want_c)
+    np.testing.assert_array_equal(scales.cpu().numpy(), want_s)
+    tiled_c, tiled_s = moe.mxfp4_quantize(x, tiled=True)
+    assert torch.equal(tiled_c, codes)
+    t = tiled_s.cpu().numpy().reshape(-1, (K + 127) // 128, 32, 4, 4)      # [tile, K / 128, row % 32, row / 32, block]
+    back = t.transpose(0, 3, 2, 1, 4).reshape(-1, (K + 127) // 128 * 4)[:R, :K // 32]
+    np.testing.assert_array_equal(back, want_s)
+
+
 @pytest.mark.parametrize("K", [32, 160, 512])
 def test_quantize_gathers_and_tiles_by_group(K):
     rng = np.random.default_rng(K)
