@@ -8,6 +8,8 @@
 // (round to nearest even, saturating) gives the code.  Two lanes share a
 // block, 16 elements each: loads of 16 bytes, one shuffle for amax, one
 // 8-byte store of codes.
+#include <algorithm>
+
 #include "moe_fp4_internal.cuh"
 #include "mxfp4_ops.cuh"
 
@@ -29,6 +31,7 @@ struct QuantParams {
   uint8_t* scales;
   int64_t rows;
   int K, div, groups;
+  int segments;  // warps a row (mxfp4_quantize_rows_kernel)
 };
 
 // The first byte of the tile word of (row, block 0) for a row r of the output,
@@ -53,16 +56,22 @@ __device__ __forceinline__ int source_row(const QuantParams& P, int r) {
   return s < P.x_rows ? s : -1;
 }
 
-// Many rows: a warp a row, what belongs to the row (its source, its place in
-// the tiles) once, 1024 elements a step.  Flat over the elements instead, with a
-// division and a group search in every thread, gathering 36,864 rows of 2048
-// took 63 us (27 so).  65536 x 4096: 96 us, the rate of a copy; tiled on a grid
-// that fills the SMs and strides, 109.
+// Many rows: a warp a row, or every segments-th 1024 elements of one, with what
+// belongs to the row (its source, its place in the tiles) looked up once.  Flat
+// over the elements instead, with a division and a group search in every thread,
+// gathering 36,864 rows of 2048 took 63 us (25 so).  65536 x 4096: 96 us, the rate
+// of a copy; tiled on a grid that fills the SMs and strides, 109.
 template <bool F32, int ALIGN, bool TILED>
 __global__ void __launch_bounds__(kThreads) mxfp4_quantize_rows_kernel(const QuantParams P) {
   griddep_begin();
   const int per_row = P.K / kPer, nb = P.K / 32, kt = (P.K + 127) / 128;
-  const int lane = threadIdx.x & 31, r = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  int r = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), c1 = 0;  // this warp's row, and its first chunk
+  if (P.segments > 1) {
+    const uint32_t id = r;
+    r = id / P.segments;
+    c1 = 64 * (id - r * P.segments);
+  }
   if (r >= (int)P.rows) return;
   const int src = source_row(P, r);
   if (src < 0 && lane == 0) atomicOr(&g_quant_err[0], kErrBadExpertId);
@@ -76,10 +85,10 @@ __global__ void __launch_bounds__(kThreads) mxfp4_quantize_rows_kernel(const Qua
       if (src >= 0 && c0 + 32 * u < per_row) load16_raw<F32, ALIGN>(P.x, at + (c0 + 32 * u) * kPer, w[u]);
     }
   };
-  load(lane);
+  load(c1 + lane);
   uint8_t* const tile = TILED ? tile_row(P, r, kt) : nullptr;  // while the loads are on their way
   uint8_t* const codes = P.codes + (size_t)r * (P.K / 2);
-  for (int c0 = lane;;) {
+  for (int c0 = c1 + lane;;) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int c = c0 + 32 * u, b = c >> 1;
@@ -98,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) mxfp4_quantize_rows_kernel(const Qua
         *reinterpret_cast<uint32_t*>(tile + (b >> 2) * 512) = sb;
       }
     }
-    c0 += 64;
+    c0 += 64 * P.segments;
     if (c0 - lane >= per_row) break;
     load(c0);
   }
@@ -312,8 +321,15 @@ namespace {
 template <bool F32, int ALIGN, bool TILED>
 cudaError_t launch_quant(const QuantParams& P, cudaStream_t st) {
   // a warp a row where that fills the SMs (8 rows each at least) and most lanes
-  if (P.K >= 512 && P.rows >= 8 * num_sms())
-    return launch_spread(mxfp4_quantize_rows_kernel<F32, ALIGN, TILED>, (unsigned)((P.rows + 7) / 8), kThreads, st, P);
+  if (P.K >= 512 && P.rows >= 8 * num_sms()) {
+    // Rows as they lie: a warp every 1024 elements (2000 x 16384, fp32: 23 us, 34 with a warp a row; 8192 x 4096,
+    // bf16: 13.2 and 15.2).  Gathered or grouped ones: up to 64 warps an SM, as each looks its row up (36864 rows of
+    // 2048: 26 us with a warp a row, 33 with two; 4000 of 7168: 11.0 with three, 12.1 and 12.8 with one and seven).
+    QuantParams Q = P;
+    const int64_t steps = (P.K + 64 * kPer - 1) / (64 * kPer);
+    Q.segments = (int)(P.row_index || P.offsets ? std::min(steps, (64 * num_sms() + P.rows - 1) / P.rows) : steps);
+    return launch_spread(mxfp4_quantize_rows_kernel<F32, ALIGN, TILED>, (unsigned)((P.rows * Q.segments + 7) / 8), kThreads, st, Q);
+  }
   return launch_spread(mxfp4_quantize_flat_kernel<F32, ALIGN, TILED>, (unsigned)grid_for(P.rows * (P.K / kPer), 8),
                        kThreads, st, P);
 }
