@@ -62,7 +62,10 @@ cudaError_t launch_spread(void (*kernel)(KArgs...), unsigned grid, unsigned thre
 // launch while the kernel before still runs, and begin with this (every
 // thread): wait until all work before has ended and is visible, then let the
 // next kernel be set up.  In this order: a kernel that starts early knows that
-// everything before the kernel ahead of it has ended.
+// everything before the kernel ahead of it has ended.  What the kernel ahead
+// writes is read by plain loads: the read-only ones (__ldg, ld.global.nc, what
+// the compiler makes of const __restrict__) are for memory that nobody writes
+// while the kernel runs, and may be moved ahead of the wait.
 __device__ __forceinline__ void griddep_begin() {
   griddep_wait();
   griddep_launch_dependents();
@@ -92,7 +95,7 @@ __device__ __forceinline__ void load16_raw(const void* x, int64_t at, uint32_t (
     const char* p = static_cast<const char*>(x) + at * (F32 ? 4 : 2);
 #pragma unroll
     for (int i = 0; i < (F32 ? 16 : 8); i += 8)
-      asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                    : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]), "=r"(w[i + 5]),
                      "=r"(w[i + 6]), "=r"(w[i + 7])
                    : "l"(p + 4 * i));
@@ -101,16 +104,16 @@ __device__ __forceinline__ void load16_raw(const void* x, int64_t at, uint32_t (
                          : reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
 #pragma unroll
     for (int i = 0; i < (F32 ? 4 : 2); ++i) {
-      const uint4 q = __ldg(p + i);
+      const uint4 q = p[i];
       w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
     }
   } else if (F32) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = __ldg(static_cast<const uint32_t*>(x) + at + i);
+    for (int i = 0; i < 16; ++i) w[i] = static_cast<const uint32_t*>(x)[at + i];
   } else {
     const uint16_t* p = static_cast<const uint16_t*>(x) + at;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = (uint32_t)__ldg(p + 2 * i) | ((uint32_t)__ldg(p + 2 * i + 1) << 16);
+    for (int i = 0; i < 8; ++i) w[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
   }
 }
 
@@ -162,12 +165,12 @@ __device__ __forceinline__ int find_group(const int32_t* off, int groups, int64_
   int lo = 0, hi = groups;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(off + mid) <= r)
+    if (off[mid] <= r)
       lo = mid;
     else
       hi = mid;
   }
-  const int64_t first = __ldg(off + lo), end = __ldg(off + lo + 1);
+  const int64_t first = off[lo], end = off[lo + 1];
   return first >= 0 && first <= r && r < end && end <= rows ? lo : -1;
 }
 
@@ -178,10 +181,10 @@ __device__ __forceinline__ int find_group_warp(const int32_t* off, int groups, i
   int below = 0;  // groups that begin at or before r
   for (int e0 = 0; e0 < groups; e0 += 32) {
     const int e = e0 + lane;
-    below += __popc(__ballot_sync(0xFFFFFFFFu, e < groups && __ldg(off + min(e, groups)) <= r));
+    below += __popc(__ballot_sync(0xFFFFFFFFu, e < groups && off[min(e, groups)] <= r));
   }
   if (below == 0) return -1;
-  const int b = __ldg(off + below - 1), end = __ldg(off + below);
+  const int b = off[below - 1], end = off[below];
   *first = b;
   return b >= 0 && b <= r && r < end && end <= rows ? below - 1 : -1;
 }

@@ -51,7 +51,7 @@ __device__ __forceinline__ uint8_t* tile_row(const QuantParams& P, int r, int kt
 // The source row of output row r, -1 for an index out of range.
 __device__ __forceinline__ int source_row(const QuantParams& P, int r) {
   if (!P.row_index) return r;
-  int s = __ldg(P.row_index + r);
+  int s = P.row_index[r];
   s = s < 0 ? -1 : s / P.div;
   return s < P.x_rows ? s : -1;
 }
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) list_link_kernel(const QuantParams P
 
 template <bool F32, int ALIGN>
 __global__ void __launch_bounds__(kThreads)
-mxfp4_quantize_places_kernel(const QuantParams P, const int32_t* __restrict__ head, const int32_t* __restrict__ next) {
+mxfp4_quantize_places_kernel(const QuantParams P, const int32_t* head, const int32_t* next) {
   griddep_begin();
   const int per_row = P.K / kPer, kt = (P.K + 127) / 128;
   const int lane = threadIdx.x & 31, s = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -242,8 +242,7 @@ mxfp4_quantize_places_kernel(const QuantParams P, const int32_t* __restrict__ he
 
 template <bool F32>
 __global__ void __launch_bounds__(kThreads)
-mxfp4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t total,
-                        void* __restrict__ out) {
+mxfp4_dequantize_kernel(const uint8_t* codes, const uint8_t* scales, int64_t total, void* out) {
   griddep_begin();
   // One thread: 8 elements, 4 bytes of codes, at kDequantRuns places loaded
   // together, in adjacent runs of the CTA; a CTA for each 8192 elements.  (65536
@@ -256,8 +255,8 @@ mxfp4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __rest
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
     const int64_t i = min(i0 + u * kThreads, total - 1);
-    c[u] = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
-    s[u] = e8m0_to_f32(__ldg(scales + (i >> 2)));
+    c[u] = reinterpret_cast<const uint32_t*>(codes)[i];
+    s[u] = e8m0_to_f32(scales[i >> 2]);
   }
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
@@ -289,8 +288,7 @@ mxfp4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __rest
 
 // one thread: the four scales of one row and tile, one word
 __global__ void __launch_bounds__(kThreads)
-tile_scales_kernel(const uint8_t* __restrict__ scales, int N, int nb, int rt, int kt, int swiglu, int64_t words,
-                   uint32_t* __restrict__ tiled) {
+tile_scales_kernel(const uint8_t* scales, int N, int nb, int rt, int kt, int swiglu, int64_t words, uint32_t* tiled) {
   griddep_begin();
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < words; i += (int64_t)gridDim.x * kThreads) {
     const int w = (int)(i & 127);                  // word of the tile: row (w % 4) * 32 + w / 4
