@@ -31,8 +31,9 @@
 // Warp roles: 0 the TMA producer, 1 the MMA issuer (and owner of tensor
 // memory), 4..11 the epilogue.  Two accumulators, so that the epilogue of one
 // item runs beside the MMAs of the next.  All waits are bounded; on a timeout
-// every role leaves its loop, and copies and MMAs in flight end before memory
-// is given back.
+// the producer and the issuer leave their loops, the epilogue goes through its
+// items without waits and stores, and copies and MMAs in flight end before
+// memory is given back.
 #include <cuda.h>
 
 #include <algorithm>
@@ -229,11 +230,12 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     E e(P, warp, lane);
     Item t{};
     int li = 0;
+    bool ok = true;  // no wait of this warp has run out
     for (int it = first; it < items; it += step, ++li) {
       item_at<NT>(t, it, P.mblocks, off, pre, P.E);
       const int b = li & 1, use = li >> 1;
       const int f0 = t.mb * E::kFeatures, nf = min(E::kFeatures, P.n_out - f0);
-      const bool ok = warp_wait(&acc_full[b], use & 1, abort_flag, P);
+      ok = ok && warp_wait(&acc_full[b], use & 1, abort_flag, P);
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       if (SPLIT) {
         // [token][weight row] to the stages' memory: all copies have landed and all MMAs that read it are done
@@ -245,10 +247,10 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
 #pragma unroll
           for (int j = 0; j < kTokens; ++j) part[(c0 + j) * kPartPitch + e.q * 32 + lane] = __uint_as_float(v[j]);
         }
-      } else if (!e.item(P.y, tmem + b * NT, t.row0, t.n, f0, nf, 0, ok, li, [&](bool, bool last) {
-                   if (last && lane == 0) mbar_arrive(&acc_empty[b]);
-                 })) {
-        break;
+      } else {
+        ok = e.item(P.y, tmem + b * NT, t.row0, t.n, f0, nf, 0, ok, li, [&](bool, bool last) {
+          if (last && lane == 0) mbar_arrive(&acc_empty[b]);
+        });
       }
     }
   }

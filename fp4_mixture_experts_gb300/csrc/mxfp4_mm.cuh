@@ -288,8 +288,10 @@ struct Ring {
 constexpr int kEpiWarps = 8;
 constexpr int kTokens = 32;  // tokens of a chunk = its columns
 
-// whether `ok` holds in all the `warps` epilogue warps that share barrier `id`:
-// they go on, or leave, together
+// Whether `ok` holds in all the `warps` epilogue warps that share barrier `id`.
+// This barrier has no time limit, so every epilogue warp comes to every one of
+// them: a warp whose wait ran out walks through all of its items still, without
+// waits and without stores (see Epilogue::item).
 __device__ __forceinline__ bool all_of_epilogue(bool ok, int id, int warps) {
   uint32_t all;
   asm volatile(
@@ -372,7 +374,7 @@ struct Epilogue {
                                             F&& after_reads) {
     if ((turn & 1) != h) {
       __syncwarp();
-      after_reads(true, true);
+      if (ok) after_reads(true, true);
       return ok;
     }
     uint32_t v[kTokens];
@@ -380,7 +382,7 @@ struct Epilogue {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncwarp();
-    after_reads(true, true);
+    if (ok) after_reads(true, true);
     if (!all_of_epilogue(ok, 4 + h, kEpiWarps / 2)) return false;
     put<false>(v, static_cast<uint8_t*>(y) + (size_t)row0 * ldy + (size_t)f0 * kEs, n, nf);
     return true;
@@ -390,8 +392,11 @@ struct Epilogue {
   // (nf of them in y).  Chunks are taken from `first` on, cyclically.
   // after_reads(round0, last): this group has read its chunks of the first
   // round (the item's chunks first .. first + 3), or, last, all of them.
-  // False, with nothing written, if some epilogue warp's wait for the
-  // accumulator ran out (not ok).
+  // False, with nothing written, if the wait for the accumulator ran out in a
+  // warp that takes chunks of the item (not ok).  The caller hands that result
+  // on as the next item's `ok`: which barriers an item has depends on its rows
+  // alone, so that no warp is left alone in one, and a warp that failed gives no
+  // accumulator back that others may still read.
   template <typename F>
   __device__ __forceinline__ bool item(void* y, uint32_t taddr, int row0, int n, int f0, int nf, int first, bool ok,
                                        int turn, F&& after_reads) {
@@ -410,7 +415,7 @@ struct Epilogue {
       asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      after_reads(i == h, i + 4 >= chunks);
+      if (ok) after_reads(i == h, i + 4 >= chunks);
       if (i == h && !all_of_epilogue(ok, 3, kEpiWarps)) return false;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {

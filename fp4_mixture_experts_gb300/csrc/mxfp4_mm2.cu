@@ -324,22 +324,22 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
     E e(P, warp, lane);
     Item t{};
     int li = 0;
+    bool ok = true;  // no wait of this warp has run out
     for (int it = first; it < items; it += step, ++li) {
       item_at<kNT>(t, it, mblocks2, off, pre, P.E);
       const int b = li & 1, use = li >> 1;
       const int f0 = (2 * t.mb + rank) * E::kFeatures, nf = max(0, min(E::kFeatures, P.n_out - f0));
-      const bool ok = warp_wait(&acc_full[b], use & 1, abort_flag, P);
+      ok = ok && warp_wait(&acc_full[b], use & 1, abort_flag, P);
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       // the columns shared with the other accumulator are read in the first round: accumulator 0's from kAcc1 on,
       // so its chunks are taken from there; accumulator 1's first 256 - kAcc1
       const int chunks = (t.n + kTokens - 1) / kTokens, from = kAcc1 / kTokens;
       const int start = b == 0 && chunks > from ? from : 0;
-      if (!e.item(P.y, tmem + b * kAcc1, t.row0, t.n, f0, nf, start, ok, li, [&](bool round0, bool last) {
-            if (lane != 0) return;
-            if (round0) arrive_leader(&part_free[b]);
-            if (last) arrive_leader(&acc_empty[b]);
-          }))
-        break;
+      ok = e.item(P.y, tmem + b * kAcc1, t.row0, t.n, f0, nf, start, ok, li, [&](bool round0, bool last) {
+        if (lane != 0) return;
+        if (round0) arrive_leader(&part_free[b]);
+        if (last) arrive_leader(&acc_empty[b]);
+      });
     }
   }
   __syncwarp();
