@@ -258,11 +258,11 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (SPLIT) {
-    cluster_sync();  // every CTA's partial sums are written
+    cluster_sync();  // every CTA's partial sums (and its abort flag) are written
     Item t{};
     if (first < items) {
       item_at<NT>(t, first, P.mblocks, off, pre, P.E);
-      sum_parts<F32, SW>(P, smem_u32(smem), rank, t.row0, t.n, t.mb, warp, lane);
+      sum_parts<F32, SW>(P, smem_u32(smem), smem_u32(const_cast<int*>(abort_flag)), rank, t.row0, t.n, t.mb, warp, lane);
     }
     cluster_sync();  // no CTA leaves while another may still read its sums
   }

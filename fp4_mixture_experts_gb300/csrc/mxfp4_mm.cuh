@@ -154,22 +154,36 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
       : "memory");
   return v;
 }
+// a word of it
+__device__ __forceinline__ uint32_t ld_cluster1(uint32_t addr, uint32_t rank) {
+  uint32_t v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.b32 %0, [a];\n}"
+      : "=r"(v)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
 
 // K split over a cluster: the CTAs' partial sums [token][weight row] (floats,
 // kPartPitch apart, at the same offset `part` in each) summed in rank order; a
 // warp a token, four rows a lane, CTA `rank` the tokens rank, rank + split, ...
+// Nothing is stored if a wait ran out in any of the CTAs (its abort flag, at
+// `abort` in each, is up): its sums are then missing or incomplete.
 constexpr int kPartPitch = kBM + 4;
 template <bool F32, bool SW>
-__device__ __forceinline__ void sum_parts(const MmParams& P, uint32_t part, int rank, int row0, int n, int mb, int warp,
-                                          int lane) {
+__device__ __forceinline__ void sum_parts(const MmParams& P, uint32_t part, uint32_t abort, int rank, int row0, int n,
+                                          int mb, int warp, int lane) {
   constexpr int kF = SW ? kBM / 2 : kBM, kOwn = SW ? 2 : 4;  // features of a tile, of a lane
   const int f = mb * kF + lane * kOwn, warps = blockDim.x >> 5;
+  const uint32_t failed = lane < P.split ? ld_cluster1(abort, lane) : 0;  // on its way with the first sums
   for (int t = rank + warp * P.split; t < n; t += warps * P.split) {
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int r = 0; r < P.split; ++r) {
       const float4 v = ld_cluster4(part + (t * kPartPitch + 4 * lane) * 4, r);
       s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
+    if (__any_sync(0xFFFFFFFFu, failed)) return;
     float o[4] = {s.x, s.y, s.z, s.w};
     if (SW) o[0] = swiglu(s.x, s.y), o[1] = swiglu(s.z, s.w);
     const size_t at = (size_t)(row0 + t) * P.n_out + f;

@@ -252,8 +252,8 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  cluster_sync();  // every CTA's partial sums are written
-  sum_parts<F32, SW>(P, smem_u32(part), rank, 0, P.M, mb, warp, lane);
+  cluster_sync();  // every CTA's partial sums (and its abort flag) are written
+  sum_parts<F32, SW>(P, smem_u32(part), smem_u32(const_cast<int*>(abort_flag)), rank, 0, P.M, mb, warp, lane);
   cluster_sync();  // no CTA leaves while another may still read its sums
   if (warp == 1) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");

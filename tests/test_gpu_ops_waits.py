@@ -56,3 +56,21 @@ def test_ragged_groups(counts, N, K, swiglu):
         right_or_untouched(out, want, before)
         assert torch.equal(moe.mxfp4_linear(x, w, wt, offsets=off, swiglu=swiglu), want)
     moe.ops_check()
+
+
+# few rows, and rows whose K is split over a cluster: nothing is stored for a tile whose sums are incomplete
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (3, 130, 96), (4, 256, 1024), (16, 1000, 8192), (40, 512, 2048),
+                                   (100, 1000, 4096)])
+def test_sums_over_a_cluster(M, N, K, swiglu):
+    rng = np.random.default_rng(M + N)
+    x = rows(rng, M, K)
+    w, ws = weights(rng, 1, N, K)
+    w, wt = gpu(w), moe.mxfp4_tile_scales(gpu(ws), swiglu)
+    want = moe.mxfp4_linear(x, w, wt, swiglu=swiglu)
+    before = torch.full_like(want, 7.0)
+    out = before.clone()
+    planted(lambda: moe.mxfp4_linear(x, w, wt, swiglu=swiglu, out=out))
+    right_or_untouched(out, want, before)
+    assert torch.equal(moe.mxfp4_linear(x, w, wt, swiglu=swiglu), want)
+    moe.ops_check()
