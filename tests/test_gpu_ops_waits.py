@@ -74,3 +74,25 @@ def test_sums_over_a_cluster(M, N, K, swiglu):
     right_or_untouched(out, want, before)
     assert torch.equal(moe.mxfp4_linear(x, w, wt, swiglu=swiglu), want)
     moe.ops_check()
+
+
+# the block end's form for many rows (with a norm after the row's sum and without, one warp and several a CTA)
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("T,d,post,following", [(3000, 4096, True, True), (7000, 520, False, True), (700, 7167, True, True),
+                                                (20000, 200, True, False), (13000, 64, True, True), (650, 16384, False, False)])
+def test_block_end(T, d, post, following, in_place):
+    rng = np.random.default_rng(T)
+    r, y = rows(rng, T, d), rows(rng, T, d, f32=True)
+    kw = dict(post_norm=post, next_norm=following)
+    want, want_n = moe.block_residual(r, y, **kw)
+    out = r.clone() if in_place else torch.full_like(r, 7.0)
+    before = out.clone()
+    normed = torch.full_like(r, 7.0) if following else None
+    planted(lambda: moe.block_residual(out if in_place else r, y, out=out, normed=normed, **kw))
+    right_or_untouched(out, want, before)
+    assert torch.equal(out[0], before[0])  # the withheld row itself
+    if following:
+        right_or_untouched(normed, want_n, torch.full_like(normed, 7.0))
+    again = moe.block_residual(r, y, **kw)
+    assert torch.equal(again[0], want) and (not following or torch.equal(again[1], want_n))
+    moe.ops_check()
