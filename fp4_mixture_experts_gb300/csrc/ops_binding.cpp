@@ -9,7 +9,6 @@
 
 #include <ATen/EmptyTensor.h>
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -115,20 +114,15 @@ const int32_t* indices(PyObject* o, const char* what, int64_t* numel) {
   return static_cast<const int32_t*>(t.data_ptr());
 }
 
-bool on_current_device(const at::Tensor& t) { return t.device().index() == c10::cuda::current_device(); }
-
-// A new tensor beside `like`, straight from PyTorch's allocator on the current
-// device (without the dispatcher: 1.4 -> 1.0 us each).
-at::Tensor fresh(at::IntArrayRef shape, at::ScalarType t, const at::Tensor& like) {
-  if (!on_current_device(like))
-    return at::empty(shape, at::TensorOptions().dtype(t).device(like.device()));
+// A new tensor on the current device, straight from PyTorch's allocator (without
+// the dispatcher: 1.4 -> 1.0 us each).
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType t) {
   return at::detail::empty_generic(shape, c10::GetAllocator(c10::kCUDA), c10::DispatchKeySet(c10::DispatchKey::CUDA), t,
                                    std::nullopt);
 }
 
-at::Tensor result(PyObject* out, int64_t rows, int64_t width, at::ScalarType t, const at::Tensor& like,
-                  const char* what) {
-  if (none(out)) return fresh({rows, width}, t, like);
+at::Tensor result(PyObject* out, int64_t rows, int64_t width, at::ScalarType t, const char* what) {
+  if (none(out)) return fresh({rows, width}, t);
   const at::Tensor& o = tensor(out, what);
   if (!o.is_cuda() || o.scalar_type() != t || !o.is_contiguous() || o.dim() != 2 || o.size(0) != rows ||
       o.size(1) != width)
@@ -137,21 +131,39 @@ at::Tensor result(PyObject* out, int64_t rows, int64_t width, at::ScalarType t, 
   return o;
 }
 
-// The stream of a call: the current one, or the one given, which is then the
-// current one while results and workspaces are allocated, so that their memory
-// is reused in that stream's order (a workspace is given back before its kernel
-// has run).
+// The GPU that all tensors among a call's arguments are on.
+c10::DeviceIndex gpu_of(PyObject* const* a, Py_ssize_t n) {
+  c10::DeviceIndex gpu = -1;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    PyObject* const o = a[i];  // (the check for a tensor takes ~0.1 us on anything else)
+    if (none(o) || PyBool_Check(o) || PyFloat_Check(o) || PyLong_Check(o) || THPDtype_Check(o)) continue;
+    if (!THPVariable_Check(o)) continue;
+    const c10::Device d = THPVariable_Unpack(o).device();
+    if (!d.is_cuda()) bad("GPU tensors are needed");
+    if (gpu >= 0 && d.index() != gpu) bad("all tensors must be on the same GPU");
+    gpu = d.index();
+  }
+  if (gpu < 0) bad("GPU tensors are needed");
+  return gpu;
+}
+
+// Where a call runs: on the GPU of its tensors, which is the current device
+// meanwhile (results are allocated, sizes looked up and kernels launched there),
+// and on that GPU's current stream or the one given, which is then the current
+// one while results and workspaces are allocated, so that their memory is reused
+// in that stream's order (a workspace is given back before its kernel has run).
 struct Stream {
+  std::optional<c10::cuda::CUDAGuard> device;
   std::optional<c10::cuda::CUDAStreamGuard> guard;
   void* handle;
-  Stream(PyObject* s, const at::Tensor& t) {
-    if (!t.is_cuda()) bad("GPU tensors are needed");
+  Stream(PyObject* s, c10::DeviceIndex gpu) {
+    if (gpu != c10::cuda::current_device()) device.emplace(gpu);
     if (none(s)) {
-      handle = c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
+      handle = c10::cuda::getCurrentCUDAStream(gpu).stream();
       return;
     }
     handle = reinterpret_cast<void*>(whole(s, "stream"));
-    guard.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), t.device().index()));
+    guard.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), gpu));
   }
 };
 
@@ -207,7 +219,7 @@ Weights weights_of(int64_t M, int64_t K, PyObject* w_, PyObject* scales_, bool g
 // x, row_index, index_div, offsets, tiled, codes, scales, stream
 NATIVE_BEGIN(quantize, 8)
   const at::Tensor& x = tensor(a[0], "x");
-  const Stream st(a[7], x);
+  const Stream st(a[7], gpu_of(a, nargs));
   const Rows r = rows_of(x, "x");
   if (r.width % 32 || r.width == 0) bad("K must be a multiple of 32");
   const bool tiled = truth(a[4]);
@@ -218,11 +230,11 @@ NATIVE_BEGIN(quantize, 8)
   const int64_t E = n_off - 1, K = r.width, kt = ceil_div(K, 128);
   at::Tensor codes, scales;
   if (none(a[5]))
-    codes = fresh({S, K / 2}, at::kByte, x);
+    codes = fresh({S, K / 2}, at::kByte);
   else
     codes = tensor(a[5], "codes"), bytes_of(codes, "codes", S * (K / 2));
   if (none(a[6]))
-    scales = tiled ? fresh({S / 128 + E, kt, 512}, at::kByte, x) : fresh({S, K / 32}, at::kByte, x);
+    scales = tiled ? fresh({S / 128 + E, kt, 512}, at::kByte) : fresh({S, K / 32}, at::kByte);
   else
     scales = tensor(a[6], "scales"), bytes_of(scales, "scales", tiled ? (S / 128 + E) * kt * 512 : S * (K / 32));
   if (K > INT32_MAX) bad("sizes beyond 2^31");
@@ -242,7 +254,7 @@ NATIVE_END
 // codes, scales, dtype, out, stream
 NATIVE_BEGIN(dequantize, 5)
   const at::Tensor& codes = tensor(a[0], "codes");
-  const Stream st(a[4], codes);
+  const Stream st(a[4], gpu_of(a, nargs));
   const at::ScalarType t = dtype_of(a[2]);
   if (codes.dim() < 1) bad("codes must be uint8 [.., K/2]");
   const int64_t half = codes.size(-1), n = codes.numel();
@@ -254,7 +266,7 @@ NATIVE_BEGIN(dequantize, 5)
   if (none(a[3])) {
     at::SmallVector<int64_t, 6> shape(codes.sizes().begin(), codes.sizes().end());
     shape.back() = 2 * half;
-    out = fresh(shape, t, codes);
+    out = fresh(shape, t);
   } else {
     out = tensor(a[3], "out");
     if (!out.is_cuda() || out.scalar_type() != t || !out.is_contiguous() || out.numel() != 2 * n)
@@ -269,14 +281,14 @@ NATIVE_END
 // scales, swiglu, out, stream
 NATIVE_BEGIN(tile_scales, 4)
   const at::Tensor& s = tensor(a[0], "scales");
-  const Stream st(a[3], s);
+  const Stream st(a[3], gpu_of(a, nargs));
   if (s.dim() != 2 && s.dim() != 3) bad("scales must be [E, N, K/32] or [N, K/32]");
   const int64_t E = s.dim() == 3 ? s.size(0) : 1, N = s.size(-2), nb = s.size(-1);
   if (E > INT32_MAX || N > INT32_MAX || nb > INT32_MAX / 32) bad("sizes beyond 2^31");
   const uint8_t* p = bytes_of(s, "scales", 0);
   at::Tensor out;
   if (none(a[2]))
-    out = fresh({E, ceil_div(N, 128), ceil_div(nb, 4), 512}, at::kByte, s);
+    out = fresh({E, ceil_div(N, 128), ceil_div(nb, 4), 512}, at::kByte);
   else
     out = tensor(a[2], "out"), bytes_of(out, "out", E * ceil_div(N, 128) * ceil_div(nb, 4) * 512);
   if (!ok(g_entry.tile_scales(p, (int32_t)E, (int32_t)N, (int32_t)(32 * nb), truth(a[1]),
@@ -289,7 +301,7 @@ NATIVE_END
 // a, a_scale, w, w_scale, offsets, swiglu, dtype, out, stream
 NATIVE_BEGIN(matmul, 9)
   const at::Tensor& x = tensor(a[0], "a");
-  const Stream st(a[8], x);
+  const Stream st(a[8], gpu_of(a, nargs));
   if (x.dim() != 2) bad("a must be uint8 [M, K/2]");
   const int64_t M = x.size(0), K = 2 * x.size(1);
   int64_t n_off = 0;
@@ -298,7 +310,7 @@ NATIVE_BEGIN(matmul, 9)
   const Weights W = weights_of(M, K, a[2], a[3], off != nullptr, n_off, truth(a[5]), t);
   const uint8_t* codes = bytes_of(x, "a", 0);
   const uint8_t* scales = bytes_of(tensor(a[1], "a_scale"), "a_scale (tiled)", W.a_scale_bytes);
-  const at::Tensor out = result(a[7], M, W.n_out, t, x, "out");
+  const at::Tensor out = result(a[7], M, W.n_out, t, "out");
   if (!ok(g_entry.matmul(&W.dims, codes, scales, off, W.w, W.scales, out.data_ptr(), st.handle),
           "moe_fp4_mxfp4_matmul"))
     return nullptr;
@@ -308,7 +320,7 @@ NATIVE_END
 // x, w, w_scale, offsets, row_index, index_div, swiglu, dtype, out, workspace, stream
 NATIVE_BEGIN(linear, 11)
   const at::Tensor& x = tensor(a[0], "x");
-  const Stream st(a[10], x);
+  const Stream st(a[10], gpu_of(a, nargs));
   const Rows r = rows_of(x, "x");
   int64_t M = r.rows, n_off = 0;
   const int32_t* off = indices(a[3], "offsets", &n_off);
@@ -323,22 +335,16 @@ NATIVE_BEGIN(linear, 11)
   void* ws = nullptr;
   size_t ws_bytes = 0;
   c10::DataPtr scratch;
-  at::Tensor scratch_elsewhere;  // rows on another device than the current one
   if (!none(a[9])) {
     const at::Tensor& given = tensor(a[9], "workspace");
     ws = bytes_of(given, "workspace", (int64_t)need);
     ws_bytes = (size_t)given.numel();
   } else if (off != nullptr || M > MOE_FP4_MXFP4_FEW_ROWS) {
     ws_bytes = index ? g_entry.gathered_workspace_bytes(&W.dims, r.rows) : need;
-    if (on_current_device(x)) {
-      scratch = c10::GetAllocator(c10::kCUDA)->allocate(ws_bytes);
-      ws = scratch.get();
-    } else {
-      scratch_elsewhere = fresh({(int64_t)ws_bytes}, at::kByte, x);
-      ws = scratch_elsewhere.data_ptr();
-    }
+    scratch = c10::GetAllocator(c10::kCUDA)->allocate(ws_bytes);
+    ws = scratch.get();
   }
-  const at::Tensor out = result(a[8], M, W.n_out, t, x, "out");
+  const at::Tensor out = result(a[8], M, W.n_out, t, "out");
   if (!ok(g_entry.linear(&W.dims, r.p, r.type, r.rows, r.stride, index, (int32_t)div, off, W.w, W.scales,
                          out.data_ptr(), ws, ws_bytes, st.handle),
           "moe_fp4_mxfp4_linear"))
@@ -358,7 +364,7 @@ void weight_of(PyObject* o, const char* what, int64_t d, const void** p, int32_t
 // x, weight, eps, out, stream
 NATIVE_BEGIN(rms_norm, 5)
   const at::Tensor& x = tensor(a[0], "x");
-  const Stream st(a[4], x);
+  const Stream st(a[4], gpu_of(a, nargs));
   const Rows r = rows_of(x, "x");
   moe_fp4_block_norm_args n{};
   if (r.width > INT32_MAX) bad("sizes beyond 2^31");
@@ -366,7 +372,7 @@ NATIVE_BEGIN(rms_norm, 5)
   n.residual = r.p, n.residual_type = r.type, n.residual_stride = r.stride;
   n.scale = 1.f, n.eps = (float)real(a[2], "eps");
   weight_of(a[1], "weight", r.width, &n.next_weight, &n.next_weight_type);
-  const at::Tensor out = result(a[3], r.rows, r.width, at::kBFloat16, x, "out");
+  const at::Tensor out = result(a[3], r.rows, r.width, at::kBFloat16, "out");
   n.normed = out.data_ptr();
   if (!ok(g_entry.block_norm(&n, st.handle), "moe_fp4_block_norm")) return nullptr;
   return THPVariable_Wrap(out);
@@ -375,7 +381,7 @@ NATIVE_END
 // residual, y, y2, post_norm, post_weight, gate, gate_sigmoid, scale, next_norm, next_weight, eps, out, normed, stream
 NATIVE_BEGIN(block_residual, 14)
   const at::Tensor& res = tensor(a[0], "residual");
-  const Stream st(a[13], res);
+  const Stream st(a[13], gpu_of(a, nargs));
   const Rows r = rows_of(res, "residual");
   const int64_t T = r.rows, d = r.width;
   if (d > INT32_MAX) bad("sizes beyond 2^31");
@@ -413,12 +419,12 @@ NATIVE_BEGIN(block_residual, 14)
   }
   n.scale = (float)real(a[7], "scale"), n.eps = (float)real(a[10], "eps");
   const bool in_place = a[11] == a[0];
-  const at::Tensor out = in_place ? res : result(a[11], T, d, res.scalar_type(), res, "out");
+  const at::Tensor out = in_place ? res : result(a[11], T, d, res.scalar_type(), "out");
   n.out = out.data_ptr(), n.out_stride = in_place ? r.stride : d;
   at::Tensor normed;
   if (truth(a[8])) {
     weight_of(a[9], "next_weight", d, &n.next_weight, &n.next_weight_type);
-    normed = result(a[12], T, d, at::kBFloat16, res, "normed");
+    normed = result(a[12], T, d, at::kBFloat16, "normed");
     n.normed = normed.data_ptr();
   } else if (!none(a[9]) || !none(a[12])) {
     bad("next_norm=False takes no next_weight and no normed");
