@@ -139,8 +139,8 @@ def block_residual(residual, y, y2=None, post_norm: bool = True, post_weight=Non
 
 
 def ops_check(stream=None) -> None:
-    """Synchronise and raise if a kernel of an earlier operator call on this device reported an error (a row index
-    out of range, or a pipeline wait that ran out); the error word is cleared."""
+    """Synchronise and raise if a kernel of an earlier operator call on this device, on any of its streams, reported an
+    error (a row index out of range, or a pipeline wait that ran out); each error is reported by one check."""
     rc = load_library().moe_fp4_ops_check(_binding._stream(stream))
     if rc != 0:
         raise MoeFp4Error(rc, "moe_fp4_ops_check")

@@ -528,13 +528,7 @@ bool operand_ok(const void* p, int type, int64_t stride, int64_t rows, int d, in
 
 }  // namespace
 
-cudaError_t ops_norm_error(int32_t* word, bool clear, cudaStream_t st) {
-  if (clear) {
-    const int32_t zero = 0;
-    return cudaMemcpyToSymbolAsync(g_norm_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
-  }
-  return cudaMemcpyFromSymbolAsync(word, g_norm_err, sizeof(*word), 0, cudaMemcpyDeviceToHost, st);
-}
+cudaError_t ops_norm_error(int32_t** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_norm_err); }
 
 }  // namespace moe_fp4
 

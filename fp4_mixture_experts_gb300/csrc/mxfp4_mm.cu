@@ -443,13 +443,7 @@ size_t once_bytes(const MxRows& R) {
 
 }  // namespace
 
-cudaError_t ops_mm_error(int32_t* word, bool clear, cudaStream_t st) {
-  if (clear) {
-    const int32_t zero = 0;
-    return cudaMemcpyToSymbolAsync(g_mm_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
-  }
-  return cudaMemcpyFromSymbolAsync(word, g_mm_err, sizeof(*word), 0, cudaMemcpyDeviceToHost, st);
-}
+cudaError_t ops_mm_error(int32_t** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_mm_err); }
 
 }  // namespace moe_fp4
 

@@ -308,12 +308,6 @@ cudaError_t launch_mm_few(const CUtensorMap& map_w, const MmParams& P, const MxR
   return x->f32 ? launch_src<1>(map_w, Q, st) : launch_src<0>(map_w, Q, st);
 }
 
-cudaError_t ops_mm1_error(int32_t* word, bool clear, cudaStream_t st) {
-  if (clear) {
-    const int32_t zero = 0;
-    return cudaMemcpyToSymbolAsync(g_mm1_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
-  }
-  return cudaMemcpyFromSymbolAsync(word, g_mm1_err, sizeof(*word), 0, cudaMemcpyDeviceToHost, st);
-}
+cudaError_t ops_mm1_error(int32_t** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_mm1_err); }
 
 }  // namespace moe_fp4

@@ -387,12 +387,6 @@ cudaError_t launch_mm_pairs(const CUtensorMap& map_w, const CUtensorMap& map_a, 
                   : launch_as<false, false>(map_w, map_a, map_a128, map_ws, map_as, P, pairs, st);
 }
 
-cudaError_t ops_mm2_error(int32_t* word, bool clear, cudaStream_t st) {
-  if (clear) {
-    const int32_t zero = 0;
-    return cudaMemcpyToSymbolAsync(g_mm2_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
-  }
-  return cudaMemcpyFromSymbolAsync(word, g_mm2_err, sizeof(*word), 0, cudaMemcpyDeviceToHost, st);
-}
+cudaError_t ops_mm2_error(int32_t** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_mm2_err); }
 
 }  // namespace moe_fp4

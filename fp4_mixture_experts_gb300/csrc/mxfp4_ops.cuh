@@ -31,12 +31,12 @@ cudaError_t launch_mxfp4_quantize(const MxRows& R, uint8_t* codes, uint8_t* scal
 // is quantised once.  lists: x_rows + 1 + rows integers.
 cudaError_t launch_mxfp4_quantize_once(const MxRows& R, int32_t* lists, uint8_t* codes, uint8_t* scales,
                                        cudaStream_t st);
-// the error words of the operators' kernels (one in each translation unit): read, or cleared
-cudaError_t ops_quant_error(int32_t* word, bool clear, cudaStream_t st);
-cudaError_t ops_mm_error(int32_t* word, bool clear, cudaStream_t st);
-cudaError_t ops_mm1_error(int32_t* word, bool clear, cudaStream_t st);
-cudaError_t ops_mm2_error(int32_t* word, bool clear, cudaStream_t st);
-cudaError_t ops_norm_error(int32_t* word, bool clear, cudaStream_t st);
+// the error words of the operators' kernels on the current device (one in each translation unit)
+cudaError_t ops_quant_error(int32_t** word);
+cudaError_t ops_mm_error(int32_t** word);
+cudaError_t ops_mm1_error(int32_t** word);
+cudaError_t ops_mm2_error(int32_t** word);
+cudaError_t ops_norm_error(int32_t** word);
 
 #ifdef __CUDACC__
 

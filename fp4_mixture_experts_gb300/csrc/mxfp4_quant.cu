@@ -9,6 +9,7 @@
 // block, 16 elements each: loads of 16 bytes, one shuffle for amax, one
 // 8-byte store of codes.
 #include <algorithm>
+#include <mutex>
 
 #include "moe_fp4_internal.cuh"
 #include "mxfp4_ops.cuh"
@@ -307,6 +308,20 @@ tile_scales_kernel(const uint8_t* scales, int N, int nb, int rt, int kt, int swi
   }
 }
 
+// The error words of all the operators, taken: each read and cleared in one
+// step, so that an error which another stream raises meanwhile is in this check or
+// in the next.
+constexpr int kErrorWords = 5;
+struct ErrorWords {
+  int32_t* word[kErrorWords];
+};
+__device__ int32_t g_taken_err;
+__global__ void take_errors_kernel(const ErrorWords w) {
+  int32_t bits = 0;
+  for (int i = 0; i < kErrorWords; ++i) bits |= atomicExch(w.word[i], 0);
+  g_taken_err = bits;
+}
+
 int grid_for(int64_t threads, int per_sm) {
   const int64_t blocks = (threads + kThreads - 1) / kThreads, cap = (int64_t)num_sms() * per_sm;
   return (int)(blocks < cap ? blocks : cap);
@@ -369,13 +384,7 @@ cudaError_t launch_mxfp4_quantize_once(const MxRows& R, int32_t* lists, uint8_t*
   return launch_spread(k, blocks((R.x_rows + 1) * 32), kThreads, st, P, (const int32_t*)head, (const int32_t*)next);
 }
 
-cudaError_t ops_quant_error(int32_t* word, bool clear, cudaStream_t st) {
-  if (clear) {
-    const int32_t zero = 0;
-    return cudaMemcpyToSymbolAsync(g_quant_err, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st);
-  }
-  return cudaMemcpyFromSymbolAsync(word, g_quant_err, sizeof(*word), 0, cudaMemcpyDeviceToHost, st);
-}
+cudaError_t ops_quant_error(int32_t** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_quant_err); }
 
 int check_mx_rows(const MxRows& R) {
   if (R.K <= 0 || R.K % 32 != 0 || R.K > 32768 || R.rows < 0 || R.x_rows < 0 || R.div < 1) return MOE_FP4_ERR_INVALID_ARG;
@@ -449,19 +458,19 @@ int moe_fp4_mxfp4_tile_scales(const uint8_t* scales, int32_t E, int32_t N, int32
 
 int moe_fp4_ops_check(void* cuda_stream) {
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  cudaError_t (*const words[])(int32_t*, bool, cudaStream_t) = {ops_quant_error, ops_mm_error, ops_mm1_error,
-                                                              ops_mm2_error, ops_norm_error};
+  ErrorWords words;
+  cudaError_t (*const address[])(int32_t**) = {ops_quant_error, ops_mm_error, ops_mm1_error, ops_mm2_error, ops_norm_error};
+  for (int i = 0; i < kErrorWords; ++i)
+    if (address[i](&words.word[i]) != cudaSuccess) return MOE_FP4_ERR_CUDA;
+  static std::mutex one_check;  // g_taken_err is one word
+  const std::lock_guard<std::mutex> lock(one_check);
+  take_errors_kernel<<<1, 1, 0, st>>>(words);
   int32_t bits = 0;
-  for (auto word : words) {
-    int32_t w = 0;
-    if (word(&w, false, st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess) return MOE_FP4_ERR_CUDA;
-    bits |= w;
-  }
-  if (bits == 0) return MOE_FP4_OK;
-  for (auto word : words)
-    if (word(nullptr, true, st) != cudaSuccess) return MOE_FP4_ERR_CUDA;
-  if (cudaStreamSynchronize(st) != cudaSuccess) return MOE_FP4_ERR_CUDA;
-  return MOE_FP4_ERR_DEVICE;
+  if (cudaGetLastError() != cudaSuccess ||
+      cudaMemcpyFromSymbolAsync(&bits, g_taken_err, sizeof(bits), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
+    return MOE_FP4_ERR_CUDA;
+  return bits == 0 ? MOE_FP4_OK : MOE_FP4_ERR_DEVICE;
 }
 
 }  // extern "C"

@@ -321,8 +321,8 @@ int moe_fp4_forward_mx(const moe_fp4_dims* dims, const void* x_bf16, const float
  * expert) and the end of a block (norm, gate, residual, next norm).  As for
  * the layer: device buffers owned by the caller, work enqueued on the given
  * stream, nothing allocated, nothing synchronised, arguments checked on the
- * host before anything is enqueued.  They keep no state between calls but an
- * error word (moe_fp4_ops_check).  Their kernels are launched with programmatic
+ * host before anything is enqueued.  They keep no state between calls but a
+ * device's error words (moe_fp4_ops_check).  Their kernels are launched with programmatic
  * dependent launch: each is set up while the kernel before it on the stream
  * still runs and waits on the device until all work before has ended and is
  * visible, so that ordinary stream order holds; and each lets a kernel that the
@@ -458,10 +458,13 @@ typedef struct moe_fp4_block_norm_args {
 } moe_fp4_block_norm_args;
 int moe_fp4_block_norm(const moe_fp4_block_norm_args* args, void* cuda_stream);
 
-/* Synchronises the stream and reads the error word of the operators above on
- * the current device: 1 = a row index out of range, 2 = a pipeline wait gave
- * up after 2 s (results incomplete).  Returns MOE_FP4_OK, MOE_FP4_ERR_DEVICE
- * or MOE_FP4_ERR_CUDA, and clears the word.  Not during a stream capture. */
+/* Synchronises the stream and takes the errors of the operators above on the
+ * current device: 1 = a row index out of range, 2 = a pipeline wait gave up
+ * after 2 s (results incomplete).  Returns MOE_FP4_OK, MOE_FP4_ERR_DEVICE or
+ * MOE_FP4_ERR_CUDA.  The error words are one set for all streams and threads of
+ * a device: a check reports what calls on any of them have raised so far, and
+ * each error is reported by one check, so that callers who share a device
+ * share its checks too.  Not during a stream capture. */
 int moe_fp4_ops_check(void* cuda_stream);
 
 /* Fault injection, for tests of the failure path only (the layer's own
