@@ -431,14 +431,17 @@ cudaError_t launch_mm(const moe_fp4_mm_dims& d, const uint8_t* a, const uint8_t*
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Bytes of the lists with which rows of x that are used several times are
-// quantised once; 0 where that does not pay, having three launches more: below
-// two uses of a row, 2^24 gathered elements and 2^13 gathered rows (4 uses, the
-// whole product: 16384 rows of 512 12.9 us, gathered rows 13.3; 32768 rows of 512
-// 16.5 and 19.6; 8192 of 2048 15.1 and 15.0, 16384 of 2048 18.3 and 20.5; 4681 of
-// 7168 24.3 and 22.7, 9362 of 7168 31.9 and 36.8).
+// quantised once; 0 where that does not pay, having two launches more.  Quantiser and
+// a product of 64 features, every row gathered / each source row once, us: 36864 rows of 2048
+// with 8 uses each 32.1 / 23.5, 65536 of 512 with 2 uses 35.7 / 31.6, 32768 of 512 with 4 19.8 /
+// 16.9, 9362 of 7168 with 4 30.0 / 26.0, 16384 of 1024 with 8 12.9 / 13.5; below the bounds
+// 16384 of 512 with 8 11.9 / 12.3, 8192 of 4096 with 8 18.4 / 20.5, 65536 of 256 with 4 24.0 / 25.3.
+// Beyond a mean of 32 uses most places would be on the shared list.
 size_t once_bytes(const MxRows& R) {
-  if (!R.row_index || R.rows < 2 * R.x_rows || R.rows < (1 << 13) || R.rows * R.K < (1LL << 24)) return 0;
-  return (size_t)(R.x_rows + 1 + R.rows) * sizeof(int32_t);
+  if (!R.row_index || R.rows < 2 * R.x_rows || R.rows > 32 * R.x_rows || R.K < 512) return 0;
+  const int64_t n = R.rows * R.K;
+  if (!(R.rows >= (1 << 14) && n >= (1LL << 24)) && !(R.rows >= (1 << 13) && n >= (3LL << 24))) return 0;
+  return (size_t)once_lists(R) * sizeof(int32_t);
 }
 
 }  // namespace

@@ -3,6 +3,8 @@
 
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "moe_fp4_internal.cuh"
 
 namespace moe_fp4 {
@@ -28,7 +30,10 @@ struct MxRows {
 int check_mx_rows(const MxRows& R);  // a moe_fp4_status
 cudaError_t launch_mxfp4_quantize(const MxRows& R, uint8_t* codes, uint8_t* scales, bool tiled, cudaStream_t st);
 // The same result (tiled) for rows that are used several times: every row of x
-// is quantised once.  lists: x_rows + 1 + rows integers.
+// is quantised once, with up to once_cap of its uses, twice the mean; the others
+// one by one.  lists: once_lists integers.
+inline int once_cap(const MxRows& R) { return (int)std::min<int64_t>(32, 2 * ((R.rows + R.x_rows - 1) / R.x_rows)); }
+inline int64_t once_lists(const MxRows& R) { return R.x_rows + 1 + R.x_rows * once_cap(R) + R.rows; }
 cudaError_t launch_mxfp4_quantize_once(const MxRows& R, int32_t* lists, uint8_t* codes, uint8_t* scales,
                                        cudaStream_t st);
 // the error words of the operators' kernels on the current device (one in each translation unit)
