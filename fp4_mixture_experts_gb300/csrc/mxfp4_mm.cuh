@@ -129,6 +129,15 @@ __device__ __forceinline__ uint32_t pack_bf16(uint32_t lo, uint32_t hi) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
+// silu(g) u.  For results in fp32 with the sigmoid to a few 2^-24: the fast one's
+// error grows with |g|, 2^-18 of the result at 50.  Results in bf16 lose nothing
+// by it.  (In fp32, 4096 x 4096 x 4096: 34.7 us, 33.5 with the fast one, 42 with expf and
+// a rounded quotient; 8192 x 8192 x 512: 62, 55 and 102.)
+template <bool F32>
+__device__ __forceinline__ float gated(float g, float u) {
+  return F32 ? g * sigmoid(g) * u : swiglu(g, u);
+}
+
 // Lanes l and l ^ d hold two bf16 each, (a0, a1) and (b0, b1): the lower lane
 // gets (a0, b0), the upper (a1, b1); sel is 0x5410 in the lower, 0x3276 in the upper.
 __device__ __forceinline__ uint32_t swap_pair(uint32_t p, int d, uint32_t sel) {
@@ -185,7 +194,7 @@ __device__ __forceinline__ void sum_parts(const MmParams& P, uint32_t part, uint
     }
     if (__any_sync(0xFFFFFFFFu, failed)) return;
     float o[4] = {s.x, s.y, s.z, s.w};
-    if (SW) o[0] = swiglu(s.x, s.y), o[1] = swiglu(s.z, s.w);
+    if (SW) o[0] = gated<F32>(s.x, s.y), o[1] = gated<F32>(s.z, s.w);
     const size_t at = (size_t)(row0 + t) * P.n_out + f;
     if (!F32 && P.vec) {
 #pragma unroll
@@ -352,7 +361,7 @@ struct Epilogue {
 #pragma unroll
       for (int j = 0; j < kTokens; j += 2) {
         const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j] : v[j + 1], 1);
-        s[j / 2] = swiglu(__uint_as_float(odd ? other : v[j]), __uint_as_float(odd ? v[j + 1] : other));
+        s[j / 2] = gated<F32>(__uint_as_float(odd ? other : v[j]), __uint_as_float(odd ? v[j + 1] : other));
       }
       if (F32 || !vec) {
         const int f = q * 16 + (lane >> 1);

@@ -76,6 +76,24 @@ __device__ __forceinline__ void griddep_begin() {
   griddep_launch_dependents();
 }
 
+// 1 / (1 + e^-g) to a few 2^-24 of the value for every g.  With t = e^-|g|, at
+// most 1, it is r = 1 / (1 + t), or t r for negative g: nothing overflows.  t is 2^h (1 + l ln 2), where
+// h + l is -|g| log2 e as a rounded product and what it leaves (a rounded
+// argument alone makes an error that grows with |g|, 2^-18 at 80); r is the
+// approximate reciprocal after one Newton step.
+__device__ __forceinline__ float sigmoid(float g) {
+  constexpr float kLog2e = 1.4426950408889634f, kRest = (float)(1.4426950408889634 - (double)kLog2e);
+  float a, t, r;
+  asm("max.NaN.f32 %0, %1, 0fC3480000;" : "=f"(a) : "f"(-fabsf(g)));  // -200: t is 0 there, and l not inf - inf
+  const float h = a * kLog2e, l = fmaf(a, kRest, fmaf(a, kLog2e, -h));
+  asm("ex2.approx.f32 %0, %1;" : "=f"(t) : "f"(h));
+  t = fmaf(t, l * 0.6931471805599453f, t);
+  const float y = 1.f + t;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+  r = fmaf(r, fmaf(-y, r, 1.f), r);
+  return g < 0.f ? t * r : r;
+}
+
 // eight fp32 values -> eight E2M1 codes, element 0 in the low nibble
 __device__ __forceinline__ uint32_t e2m1x8(const float* v) {
   uint32_t r;
