@@ -82,7 +82,14 @@ double real(PyObject* o, const char* what) {
   return v;
 }
 
-bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject* o, const char* what) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    bad(std::string(what) + " must be true or false");
+  }
+  return v == 1;
+}
 
 // rows: 2-D on the GPU, contiguous along a row; rows may be strided
 struct Rows {
@@ -222,7 +229,7 @@ NATIVE_BEGIN(quantize, 8)
   const Stream st(a[7], gpu_of(a, nargs));
   const Rows r = rows_of(x, "x");
   if (r.width % 32 || r.width == 0) bad("K must be a multiple of 32");
-  const bool tiled = truth(a[4]);
+  const bool tiled = truth(a[4], "tiled");
   int64_t S = r.rows, n_off = 2;
   const int32_t* index = indices(a[1], "row_index", &S);
   const int32_t* off = indices(a[3], "offsets", &n_off);
@@ -291,7 +298,7 @@ NATIVE_BEGIN(tile_scales, 4)
     out = fresh({E, ceil_div(N, 128), ceil_div(nb, 4), 512}, at::kByte);
   else
     out = tensor(a[2], "out"), bytes_of(out, "out", E * ceil_div(N, 128) * ceil_div(nb, 4) * 512);
-  if (!ok(g_entry.tile_scales(p, (int32_t)E, (int32_t)N, (int32_t)(32 * nb), truth(a[1]),
+  if (!ok(g_entry.tile_scales(p, (int32_t)E, (int32_t)N, (int32_t)(32 * nb), truth(a[1], "swiglu"),
                               static_cast<uint8_t*>(out.data_ptr()), st.handle),
           "moe_fp4_mxfp4_tile_scales"))
     return nullptr;
@@ -307,7 +314,7 @@ NATIVE_BEGIN(matmul, 9)
   int64_t n_off = 0;
   const int32_t* off = indices(a[4], "offsets", &n_off);
   const at::ScalarType t = dtype_of(a[6]);
-  const Weights W = weights_of(M, K, a[2], a[3], off != nullptr, n_off, truth(a[5]), t);
+  const Weights W = weights_of(M, K, a[2], a[3], off != nullptr, n_off, truth(a[5], "swiglu"), t);
   const uint8_t* codes = bytes_of(x, "a", 0);
   const uint8_t* scales = bytes_of(tensor(a[1], "a_scale"), "a_scale (tiled)", W.a_scale_bytes);
   const at::Tensor out = result(a[7], M, W.n_out, t, "out");
@@ -328,7 +335,7 @@ NATIVE_BEGIN(linear, 11)
   const int64_t div = whole(a[5], "index_div");
   if (div < 1 || div > INT32_MAX) bad("index_div must be at least 1");
   const at::ScalarType t = dtype_of(a[7]);
-  const Weights W = weights_of(M, r.width, a[1], a[2], off != nullptr, n_off, truth(a[6]), t);
+  const Weights W = weights_of(M, r.width, a[1], a[2], off != nullptr, n_off, truth(a[6], "swiglu"), t);
   const size_t need = g_entry.linear_workspace_bytes(&W.dims);
   if (need == 0) return ok(MOE_FP4_ERR_UNSUPPORTED, "moe_fp4_mxfp4_linear"), nullptr;
   // the workspace: none for few rows, the one given, or scratch memory for this call
@@ -396,12 +403,12 @@ NATIVE_BEGIN(block_residual, 14)
     if (y2.rows != T || y2.width != d) bad("y2 must have residual's shape");
     n.y2 = y2.p, n.y2_type = y2.type, n.y2_stride = y2.stride;
   }
-  n.post_norm = truth(a[3]);
+  n.post_norm = truth(a[3], "post_norm");
   weight_of(a[4], "post_weight", d, &n.post_weight, &n.post_weight_type);
   if (!none(a[5])) {
     const at::Tensor& g = tensor(a[5], "gate");
     const int64_t dim = g.dim(), s0 = dim > 0 ? g.size(0) : 0, s1 = dim == 2 ? g.size(1) : 1;
-    n.gate_sigmoid = truth(a[6]);
+    n.gate_sigmoid = truth(a[6], "gate_sigmoid");
     n.gate_stride = d;
     if (dim == 2 && s0 == T && s1 == d && !(T > 1 && d == 1)) {
       const Rows e = rows_of(g, "gate");
@@ -422,7 +429,7 @@ NATIVE_BEGIN(block_residual, 14)
   const at::Tensor out = in_place ? res : result(a[11], T, d, res.scalar_type(), "out");
   n.out = out.data_ptr(), n.out_stride = in_place ? r.stride : d;
   at::Tensor normed;
-  if (truth(a[8])) {
+  if (truth(a[8], "next_norm")) {
     weight_of(a[9], "next_weight", d, &n.next_weight, &n.next_weight_type);
     normed = result(a[12], T, d, at::kBFloat16, "normed");
     n.normed = normed.data_ptr();
