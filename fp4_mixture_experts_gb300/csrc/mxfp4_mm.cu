@@ -330,8 +330,8 @@ int check_mm(const moe_fp4_mm_dims& d) {
       (d.y_type != MOE_FP4_TYPE_BF16 && d.y_type != MOE_FP4_TYPE_F32))
     return MOE_FP4_ERR_INVALID_ARG;
   // item counts and tensor-map extents stay below 2^31
-  const int64_t mb = (d.N + 127) / 128;
-  if ((int64_t)d.M * d.K >= (1LL << 35) || ((int64_t)d.M / 64 + d.E) * mb >= (1LL << 30)) return MOE_FP4_ERR_UNSUPPORTED;
+  const int64_t mb = ((int64_t)d.N + 127) / 128;
+  if (d.N > kMaxFeatures || (int64_t)d.M * d.K >= (1LL << 35) || ((int64_t)d.M / 64 + d.E) * mb >= (1LL << 30)) return MOE_FP4_ERR_UNSUPPORTED;
   return MOE_FP4_OK;
 }
 

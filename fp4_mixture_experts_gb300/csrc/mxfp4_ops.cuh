@@ -10,6 +10,7 @@
 namespace moe_fp4 {
 
 constexpr int kMaxGroups = 1024;
+constexpr int kMaxFeatures = INT32_MAX - 255;  // a tile past them is still counted in 32 bits
 
 // rows to quantise: row r is row (row_index ? row_index[r] / div : r) of x
 struct MxRows {

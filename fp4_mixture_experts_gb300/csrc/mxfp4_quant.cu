@@ -480,7 +480,7 @@ int moe_fp4_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_
 
 int moe_fp4_mxfp4_tile_scales(const uint8_t* scales, int32_t E, int32_t N, int32_t K, int swiglu, uint8_t* tiled,
                               void* cuda_stream) {
-  if (!scales || !tiled || ((uintptr_t)tiled & 15) || E < 1 || E > kMaxGroups || N < 1 || K <= 0 || K % 32 != 0 ||
+  if (!scales || !tiled || ((uintptr_t)tiled & 15) || E < 1 || E > kMaxGroups || N < 1 || N > kMaxFeatures || K <= 0 || K % 32 != 0 ||
       K > 32768 || (swiglu && N % 2 != 0))
     return MOE_FP4_ERR_INVALID_ARG;
   const int rt = (N + 127) / 128, kt = (K + 127) / 128;

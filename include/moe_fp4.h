@@ -383,13 +383,14 @@ size_t moe_fp4_mxfp4_tiled_scale_bytes(int64_t rows, int32_t groups, int32_t K);
  * weights' layout of the products, once when weights are loaded: uint8
  * [E][ceil(N/128)][ceil(K/128)][512], tiles as above, zeros past the ends.
  * swiglu = 1: for a product with SwiGLU (N = 2I, gate rows then up rows), the
- * rows of a tile are gate and up rows in turn.  tiled 16-byte aligned. */
+ * rows of a tile are gate and up rows in turn.  N at most 2^31 - 256; tiled
+ * 16-byte aligned. */
 int moe_fp4_mxfp4_tile_scales(const uint8_t* scales, int32_t E, int32_t N, int32_t K, int swiglu, uint8_t* tiled,
                               void* cuda_stream);
 
 /* Sizes and form of a product: a has M rows, w is E matrices of N rows. */
 typedef struct moe_fp4_mm_dims {
-  int32_t M, N, K, E;   /* M >= 0, N >= 1, K a multiple of 32 up to 32768, 1 <= E <= 1024 */
+  int32_t M, N, K, E;   /* M >= 0, 1 <= N <= 2^31 - 256, K a multiple of 32 up to 32768, 1 <= E <= 1024 */
   int32_t swiglu;       /* 0: y [M, N]; 1: N = 2I even, y [M, I] = silu(first I features) * last I */
   int32_t y_type;       /* MOE_FP4_TYPE_BF16 or MOE_FP4_TYPE_F32 */
 } moe_fp4_mm_dims;
