@@ -125,8 +125,8 @@ __device__ __forceinline__ void store8(void* base, int type, int64_t row_at, int
 }
 
 // For results in bf16, many at a time: its error (2^-18 of the value at |g| = 80)
-// is far below their rounding.  (A gate of every element, 16384 x 7168: 261 us,
-// 274 with the other one.)
+// is far below their rounding.  (A gate of every element, 16384 x 7168: 263 us,
+// 286 with the other one.)
 __device__ __forceinline__ float fast_sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
 
 // sum over the CTA, the same in every thread; `part` holds 32 floats.  What a
@@ -147,8 +147,14 @@ __device__ __forceinline__ float cta_sum(float s, float* part) {
   return t;
 }
 
-template <int NC, int V>
-__global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams P) {
+// GATE: whether there is a gate of elements (of every one, or of channels in the
+// form for few rows), and for which results: in bf16 its sigmoid is the fast one.
+// (A kernel of its own for each: with both sigmoids in the loop, and none
+// needed, 16384 x 7168 takes 204 us, 200 so.)
+enum class Gate { none, bf16, f32 };
+
+template <int NC, int V, Gate GATE>
+__global__ void __launch_bounds__(1024, NC == 1 && V > 1 ? 2 : 1) block_norm_kernel(const NormParams P) {
   griddep_begin();
   __shared__ float part[2][32];
   const moe_fp4_block_norm_args& a = P.a;
@@ -171,7 +177,7 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams P) {
       }
     }
     float m = a.scale;
-    if (a.gate_shape == MOE_FP4_GATE_TOKEN) {
+    if (GATE == Gate::none && a.gate_shape == MOE_FP4_GATE_TOKEN) {
       const float g = a.gate_type == MOE_FP4_TYPE_F32 ? static_cast<const float*>(a.gate)[t]
                                                       : bf16_to_f32(static_cast<const uint16_t*>(a.gate)[t]);
       m *= a.gate_sigmoid ? sigmoid(g) : g;
@@ -194,10 +200,11 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams P) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) b[c][j] *= v[j];
       }
-      if (a.gate_shape >= MOE_FP4_GATE_CHANNEL) {
+      if (GATE != Gate::none) {
         load8<V>(a.gate, a.gate_type, a.gate_shape == MOE_FP4_GATE_ELEMENT ? t * a.gate_stride : 0, c, d, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) b[c][j] *= a.gate_sigmoid ? sigmoid(v[j]) : v[j];
+        for (int j = 0; j < 8; ++j)
+          b[c][j] *= !a.gate_sigmoid ? v[j] : GATE == Gate::f32 ? sigmoid(v[j]) : fast_sigmoid(v[j]);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) r[c][j] += b[c][j];
@@ -235,7 +242,7 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams P) {
 // first and the last row, beside which memory may be another's, are read where
 // they are.
 constexpr int kRingThreads = 512;      // with the weights in registers; 1024 read them again for every row
-constexpr int kRingSmThreads = 640;    // on an SM: 88 registers a thread are 5 warps of each of its quarters
+constexpr int kRingSmThreads = 640;    // on an SM, in CTAs of up to 512: 5 warps of each of its quarters, 96 registers a thread
 constexpr int kRingMaxSlots = 8;
 constexpr int kRingSmem = 200 * 1024;
 
@@ -261,8 +268,8 @@ __device__ __forceinline__ void weight8(const void* w, int type, int at, int d, 
   for (int j = 0; j < 8; ++j) v[j] *= to;
 }
 
-template <bool KEEP, int V>
-__global__ void __launch_bounds__(KEEP ? kRingThreads : 2 * kRingThreads, 1)
+template <bool KEEP, int V, Gate GATE>
+__global__ void __launch_bounds__(KEEP ? kRingSmThreads : 2 * kRingThreads, 1)
 block_norm_ring_kernel(const RingParams R) {
   griddep_begin();
   extern __shared__ __align__(128) uint8_t ring[];
@@ -322,7 +329,7 @@ block_norm_ring_kernel(const RingParams R) {
   const int at[2] = {elem<V>(0, 0), elem<V>(1, 0)};
   auto branch_weights = [&](int c, float (&w)[8]) {
     weight8<V>(a.post_weight, a.post_weight_type, at[c], d, a.scale, w);
-    if (a.gate_shape != MOE_FP4_GATE_CHANNEL) return;
+    if (GATE != Gate::none || a.gate_shape != MOE_FP4_GATE_CHANNEL) return;
     float g[8];
     load8<V>(static_cast<const uint8_t*>(a.gate) + (size_t)at[c] * (gf ? 4 : 2), gf, d - at[c], g);
 #pragma unroll
@@ -341,13 +348,13 @@ block_norm_ring_kernel(const RingParams R) {
   // Once a wait has run out the CTA stores nothing any more: the slots are not filled again, and a barrier that is a
   // phase behind would let later rows pass.  A thread knows it of its own waits, and behind a sum (of this row or an
   // earlier one) of those of all the threads that were in it, which raised the flag before its barrier; every thread
-  // goes on through the sums' barriers.  (16384 x 7168, fp32 + bf16 branch: 202 us, 200 without the flag's reads.)
+  // goes on through the sums' barriers.
   bool ok = true;
   int s = 0, i = 0;
   uint32_t phase = 0;
   for (int64_t t = blockIdx.x; t < T; t += step, ++i) {
     float m = 1.f;
-    if (a.gate_shape == MOE_FP4_GATE_TOKEN) {
+    if (GATE == Gate::none && a.gate_shape == MOE_FP4_GATE_TOKEN) {
       m = gf ? static_cast<const float*>(a.gate)[t] : bf16_to_f32(static_cast<const uint16_t*>(a.gate)[t]);
       if (a.gate_sigmoid) m = sigmoid(m);
     }
@@ -396,10 +403,11 @@ block_norm_ring_kernel(const RingParams R) {
         if (!KEEP && at[c] < d) branch_weights(c, bw[0]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) b[c][j] *= m * bw[KEEP ? c : 0][j];
-        if (R.g_bytes && at[c] < d) {
+        if (GATE != Gate::none && at[c] < d) {
           load8<V>(pg + at[c] * (gf ? 4 : 2), gf, d - at[c], v);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) b[c][j] *= !a.gate_sigmoid ? v[j] : rf ? sigmoid(v[j]) : fast_sigmoid(v[j]);
+          for (int j = 0; j < 8; ++j)
+            b[c][j] *= !a.gate_sigmoid ? v[j] : GATE == Gate::f32 ? sigmoid(v[j]) : fast_sigmoid(v[j]);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[c][j] = 0.f;
@@ -495,25 +503,36 @@ bool ring_layout(const NormParams& P, RingParams* R, int* threads, int* ctas) {
   return R->slots >= 2;
 }
 
-template <int V>
+template <int V, Gate GATE>
 cudaError_t launch_ring(const RingParams& R, int threads, int ctas, cudaStream_t st) {
-  auto* k = threads <= kRingThreads ? block_norm_ring_kernel<true, V> : block_norm_ring_kernel<false, V>;
+  auto* k = threads <= kRingThreads ? block_norm_ring_kernel<true, V, GATE> : block_norm_ring_kernel<false, V, GATE>;
   const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(k), kRingSmem);
   if (e != cudaSuccess) return e;
   return launch_early(k, dim3(ctas), dim3(threads), R.slots * R.slot_bytes, st, R);
 }
 
-template <int V>
-cudaError_t launch_norm(const NormParams& P, cudaStream_t st) {
-  RingParams R;
-  int ring_threads, ctas;
-  if constexpr (V != 2)
-    if (ring_layout<V>(P, &R, &ring_threads, &ctas)) return launch_ring<V>(R, ring_threads, ctas, st);
+template <int V, Gate GATE>
+cudaError_t launch_rows(const NormParams& P, cudaStream_t st) {
   // a CTA a row: one chunk of 8 elements a thread up to 1024 threads (few rows are bound by latency), else two
   const int chunks = (P.a.d + 7) / 8, nc = chunks <= 1024 ? 1 : 2;
   const int threads = ((chunks + nc - 1) / nc + 31) / 32 * 32;
-  return launch_spread(nc == 1 ? block_norm_kernel<1, V> : block_norm_kernel<2, V>, (unsigned)P.a.T,
+  return launch_spread(nc == 1 ? block_norm_kernel<1, V, GATE> : block_norm_kernel<2, V, GATE>, (unsigned)P.a.T,
                        (unsigned)threads, st, P);
+}
+
+template <int V>
+cudaError_t launch_norm(const NormParams& P, cudaStream_t st) {
+  const bool f32 = P.a.residual_type == MOE_FP4_TYPE_F32;
+  RingParams R;
+  int threads, ctas;
+  if constexpr (V != 2)
+    if (ring_layout<V>(P, &R, &threads, &ctas))
+      return P.a.gate_shape != MOE_FP4_GATE_ELEMENT ? launch_ring<V, Gate::none>(R, threads, ctas, st)
+             : f32                                  ? launch_ring<V, Gate::f32>(R, threads, ctas, st)
+                                                    : launch_ring<V, Gate::bf16>(R, threads, ctas, st);
+  return P.a.gate_shape < MOE_FP4_GATE_CHANNEL ? launch_rows<V, Gate::none>(P, st)
+         : f32                                 ? launch_rows<V, Gate::f32>(P, st)
+                                               : launch_rows<V, Gate::bf16>(P, st);
 }
 
 bool is_type(int t) { return t == MOE_FP4_TYPE_BF16 || t == MOE_FP4_TYPE_F32; }

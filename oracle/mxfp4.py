@@ -12,10 +12,6 @@ import numpy as np
 MAGNITUDES = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
 
 
-def bf16_to_f64(bits: np.ndarray) -> np.ndarray:
-    return (bits.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
-
-
 def quantize(x: np.ndarray):
     """codes uint8 [R, K/2] and scales uint8 [R, K/32] of rows x [R, K] (values exact in fp64)"""
     x = np.asarray(x, dtype=np.float64)
