@@ -14,7 +14,8 @@ residual stream after the block and its norm before the next one.  Per token
 The routed experts run as the layer (`forward`: bf16 activations), or, with
 mxfp4_experts, as MXFP4 x MXFP4 products grouped by expert (`mxfp4_linear` with
 the offsets and sorted slots of `route`): W13 with SwiGLU from the tokens, W2
-from its rows, and the weighted sum of each token's k rows.
+from its rows, and the weighted sum of each token's k rows (that sum in PyTorch's
+own operations, several passes over the rows in fp32; the layer has its own).
 
 prepare() lays the scales out once, when the weights are loaded.  Everything
 runs on the current stream.

@@ -11,7 +11,7 @@
 // a CTA a row its loads stop while the sums are reduced and the row is written
 // (16384 x 7168, fp32 + bf16 branch, bf16 residual: 298 us, 4.7 TB/s).  There
 // persistent CTAs keep a ring of rows in shared memory that bulk copies fill
-// ahead, and the weights in registers: 201 us, 7.0 TB/s, the rate of a copy.
+// ahead, and the weights in registers: 200 us, 7.1 TB/s, the rate of a copy.
 #include <algorithm>
 
 #include "moe_fp4_internal.cuh"
@@ -477,7 +477,7 @@ bool ring_layout(const NormParams& P, RingParams* R, int* threads, int* ctas) {
   if (*threads > 2 * kRingThreads) return false;
   // rows read element by element are bound by instructions: the ring's fewer
   // threads an SM pay for wide ones alone (bf16: 8192 x 3001 64 us, plain 64; x 4097
-  // 89 and 116; 4096 x 7167 86 and 122), and not at all by pairs (8192 x 5122 114
+  // 89 and 116; 4096 x 7167 81 and 122), and not at all by pairs (8192 x 5122 114
   // and 91; 4096 x 7166 72 and 72)
   if (V == 1 && a.d <= 4096) return false;
   auto bytes = [&](const void* p, int type) {
@@ -490,8 +490,8 @@ bool ring_layout(const NormParams& P, RingParams* R, int* threads, int* ctas) {
   R->r_bytes = bytes(a.residual, a.residual_type);
   R->g_bytes = a.gate_shape == MOE_FP4_GATE_ELEMENT ? bytes(a.gate, a.gate_type) : 0;
   R->slot_bytes = (R->y_bytes + R->y2_bytes + R->r_bytes + R->g_bytes + 127) / 128 * 128;
-  // as many CTAs an SM as run there (4096 x 5120, bf16: two of 320 threads 37 us,
-  // one 54) with 2 rows in the ring (two are enough, 8192 x 3584, fp32: two CTAs of
+  // as many CTAs an SM as run there (4096 x 5120, bf16: two of 320 threads 33 us,
+  // one 50) with 2 rows in the ring (two are enough, 8192 x 3584, fp32: two CTAs of
   // 2 rows 95 us, one of 4 154)
   int per_sm = std::max(1, kRingSmThreads / *threads);
   while (per_sm > 1 && kRingSmem / per_sm / R->slot_bytes < 2) --per_sm;

@@ -362,7 +362,9 @@ MmParams params(const moe_fp4_mm_dims& d, const uint8_t* as, const int32_t* offs
   return P;
 }
 
-// few rows of one matrix have a kernel of their own, which quantises them itself
+// Few rows of one matrix have a kernel of their own, which quantises them itself and needs no workspace: that, the
+// interface's promise, decides, whatever N is.  16 x 4096 x 4096 takes 5.8 us in it, 17 rows in the others 6.2; one row
+// 4.8.  With a wide N it is the slower one: 16 x 16384 x 4096 11.1 us, 17 rows 8.7.
 bool few_rows(const moe_fp4_mm_dims& d, const int32_t* offsets) { return !offsets && d.M <= kFewRows; }
 
 cudaError_t launch_few(const moe_fp4_mm_dims& d, const MmParams& P, const MxRows* x, const uint8_t* codes,

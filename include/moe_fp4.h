@@ -327,7 +327,11 @@ int moe_fp4_forward_mx(const moe_fp4_dims* dims, const void* x_bf16, const float
  * still runs and waits on the device until all work before has ended and is
  * visible, so that ordinary stream order holds; and each lets a kernel that the
  * caller launches early be set up while it runs (such a kernel must wait on the
- * device, griddepcontrol.wait, as any early-launched kernel must). */
+ * device, griddepcontrol.wait, as any early-launched kernel must).  A quantiser,
+ * read-back, scale layout or block end of fewer CTAs than the SMs hold asks for
+ * shared memory that it does not use (up to 225 KB a CTA), which spreads its CTAs
+ * over the SMs; kernels of other streams that need shared memory do not run
+ * beside them on an SM for those microseconds. */
 
 /* Element types of the operators' unquantised operands and results. */
 #define MOE_FP4_TYPE_BF16 0
