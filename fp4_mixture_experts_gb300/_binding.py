@@ -49,6 +49,9 @@ EXPORTED_SYMBOLS = (
     "moe_fp4_mxfp4_linear",
     "moe_fp4_block_norm",
     "moe_fp4_ops_check",
+    "moe_fp4_fp8_tile_scales",
+    "moe_fp4_fp8_linear_workspace_bytes",
+    "moe_fp4_fp8_linear",
 )
 
 
@@ -123,6 +126,9 @@ def load_library():
             ("mxfp4_gathered_workspace_bytes", [P, i64], size),
             ("mxfp4_linear", [P, P, i32, i64, i64, P, i32, P, P, P, P, P, size, P], i32),
             ("block_norm", [P, P], i32),
+            ("fp8_tile_scales", [P, i32, i32, i32, i32, P, P], i32),
+            ("fp8_linear_workspace_bytes", [P], size),
+            ("fp8_linear", [P, P, i32, i64, i64, P, P, P, P, P, size, P], i32),
             ("ops_check", [P], i32)):
         fn = getattr(lib, "moe_fp4_" + name)
         fn.argtypes, fn.restype = args, res

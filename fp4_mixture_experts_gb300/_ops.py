@@ -52,7 +52,8 @@ class _Unloaded:
                                "fp4_mixture_experts_gb300.build` (there is no fallback implementation)") from e
         native.bind(tuple(ctypes.cast(getattr(lib, "moe_fp4_" + n), ctypes.c_void_p).value for n in (
             "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_tile_scales", "mxfp4_matmul", "mxfp4_linear",
-            "mxfp4_linear_workspace_bytes", "mxfp4_gathered_workspace_bytes", "block_norm")), _raise)
+            "mxfp4_linear_workspace_bytes", "mxfp4_gathered_workspace_bytes", "block_norm", "fp8_tile_scales",
+            "fp8_linear_workspace_bytes", "fp8_linear")), _raise)
         _native, _BF16 = native, torch.bfloat16
         return getattr(native, name)
 
@@ -115,6 +116,27 @@ def mxfp4_linear(x, w, w_scale, offsets=None, row_index=None, index_div: int = 1
     offsets) and mxfp4_matmul in one call, the same bits."""
     f = _native.linear
     return f(x, w, w_scale, offsets, row_index, index_div, swiglu, dtype or _BF16, out, workspace, _handle(stream))
+
+
+def fp8_tile_scales(scales, N: int, K: int, swiglu: bool = False, out=None, stream=None):
+    """E8M0 weight scales uint8 [E, ceil(N/128), ceil(K/128)] (or without E), one for each 128 x 128 of w [E, N, K], in
+    the layout of fp8_linear, uint8 [E, ceil(N/128), ceil(K/128), 512]: once, when weights are loaded.  swiglu: for
+    products with SwiGLU."""
+    return _native.fp8_tile_scales(scales, N, K, swiglu, out, _handle(stream))
+
+
+def fp8_linear_workspace_bytes(M: int, N: int, K: int, E: int = 1) -> int:
+    """Bytes of fp8_linear's workspace."""
+    return int(load_library().moe_fp4_fp8_linear_workspace_bytes(ctypes.byref(MmDims(M, N, K, E, 0, 0))))
+
+
+def fp8_linear(x, w, w_scale, offsets=None, swiglu: bool = False, dtype=None, out=None, workspace=None, stream=None):
+    """y = x_q w^T of rows x [M, K] (bf16 or fp32, K a multiple of 32; rows may be strided), quantised in the call to
+    E4M3 with a power-of-two scale for each 128 elements, and weights w float8_e4m3fn [E, N, K] or [N, K] with scales
+    of fp8_tile_scales.  offsets (int32 [E + 1]): rows [off[e], off[e+1]) use w[e]; rows in no group are left as they
+    were.  Returns [M, N], or with swiglu silu(first half) * second half [M, N/2]: bf16, or dtype=torch.float32."""
+    f = _native.fp8_linear
+    return f(x, w, w_scale, offsets, swiglu, dtype or _BF16, out, workspace, _handle(stream))
 
 
 def rms_norm(x, weight=None, eps: float = 1e-6, out=None, stream=None):

@@ -51,12 +51,13 @@ __device__ int32_t g_mm_err[4];
 
 constexpr int kThreads = 384;
 
-template <int NT>
+template <typename F, int NT>
 struct Cfg {
   static constexpr int kATile = kBM * 128;
   static constexpr int kBTile = NT * 128;
-  static constexpr int kStage = kATile + kBTile + 4 * kSfTile;
-  static constexpr int kSfCols = 16;                         // tensor-memory columns of a stage's scales
+  static constexpr int kSf = 2 * F::kSfTiles;                // scale tiles of a stage
+  static constexpr int kStage = kATile + kBTile + kSf * kSfTile;
+  static constexpr int kSfCols = 4 * kSf;                    // tensor-memory columns of them
   static constexpr int kGroupBytes = 2 * (kMaxGroups + 1) * 4;
   static constexpr int kFixed = 1024 + 512 + kGroupBytes;
   static constexpr int kByMem = (kSmemMax - kFixed) / kStage;
@@ -71,12 +72,12 @@ struct Cfg {
 // SPLIT: a dense product with too few tiles for the SMs.  The CTAs of a cluster
 // share one tile's K; their partial sums meet in rank order through distributed
 // shared memory, each CTA summing every split-th token.
-template <int NT, bool F32, bool SW, bool SPLIT>
+template <typename F, int NT, bool F32, bool SW, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a, MmParams P) {
   P.err = &g_mm_err[0];
-  using C = Cfg<NT>;
-  constexpr int kStages = C::kStages;
+  using C = Cfg<F, NT>;
+  constexpr int kStages = C::kStages, kStageK = F::kStageK, kSf = F::kSfTiles;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* tail = smem + kStages * C::kStage;
@@ -138,19 +139,19 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
       auto load_w = [&](int ks, int s) {  // and announce the stage's bytes
         if (elect_one()) {
           uint8_t* st = smem + s * C::kStage;
-          const uint32_t sf_bytes = min(2, P.kt - 2 * ks) * kSfTile;
+          const uint32_t sf_bytes = min(kSf, P.kt - kSf * ks) * kSfTile;
           mbar_expect_tx(&full[s], C::kATile + C::kBTile + 2 * sf_bytes);
           tma_load_4d(st, &map_w, ks * 128, 0, wrow, t.g, &full[s]);
-          bulk_load(st + C::kATile + C::kBTile, ws + ks * 2 * kSfTile, sf_bytes, &full[s]);
+          bulk_load(st + C::kATile + C::kBTile, ws + ks * kSf * kSfTile, sf_bytes, &full[s]);
         }
         __syncwarp();
       };
       auto load_a = [&](int ks, int s) {
         if (elect_one()) {
           uint8_t* st = smem + s * C::kStage;
-          const uint32_t sf_bytes = min(2, P.kt - 2 * ks) * kSfTile;
+          const uint32_t sf_bytes = min(kSf, P.kt - kSf * ks) * kSfTile;
           tma_load_2d(st + C::kATile, &map_a, ks * 128, t.row0, &full[s]);
-          bulk_load(st + C::kATile + C::kBTile + 2 * kSfTile, as + ks * 2 * kSfTile, sf_bytes, &full[s]);
+          bulk_load(st + C::kATile + C::kBTile + kSf * kSfTile, as + ks * kSf * kSfTile, sf_bytes, &full[s]);
         }
         __syncwarp();
       };
@@ -191,7 +192,9 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
       if (!warp_wait(&acc_empty[b], (use & 1) ^ 1, abort_flag, P)) break;
       const uint32_t d_tmem = tmem + b * NT;
       const int n_mma = (t.n + 15) & ~15;
-      const uint32_t id0 = idesc_mxf4(kBM, n_mma, 0), id1 = idesc_mxf4(kBM, n_mma, 1);
+      uint32_t id[4];
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) id[kk] = idesc_mx<F>(kBM, n_mma, kk);
       const uint32_t shift = (t.local & 127) >> 5;  // a 64-row tile may start in the middle of a scale tile
       for (int ks = k0; ks < k1; ++ks, ring.next()) {
         if (!warp_wait(&full[ring.s], ring.phase, abort_flag, P)) {
@@ -204,17 +207,18 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
           const uint32_t a_lo = lo | kDescLoSw128, b_lo = (lo + (C::kATile >> 4)) | kDescLoSw128;
           const uint32_t sf_lo = lo + ((C::kATile + C::kBTile) >> 4);
           const uint32_t sf_t = sf_base + ring.s * C::kSfCols;
-          // the weights' two K chunks (128 elements each), then the token rows'; a chunk past the end of K copies
+          // the weights' K chunks (128 elements each), then the token rows'; a chunk past the end of K copies
           // what the stage holds, and no MMA uses it
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_cp_scales<1>(sf_t + 4 * i, sf_lo + i * (kSfTile >> 4));
-          const int steps = (P.K - ks * kStageK + 63) / 64;
+          for (int i = 0; i < 2 * kSf; ++i) tmem_cp_scales<1>(sf_t + 4 * i, sf_lo + i * (kSfTile >> 4));
+          const int steps = (P.K - ks * kStageK + F::kMmaK - 1) / F::kMmaK;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
+          for (int kk = 0; kk < 4; ++kk) {
+            const int sf = 4 * (kk * F::kMmaK / 128);  // columns of this MMA's scale tile
             if (kk < steps)
-              umma_mxf4<1>(d_tmem, desc(a_lo + 2 * kk, kDescHiSw128), desc(b_lo + 2 * kk, kDescHiSw128),
-                           (kk & 1) ? id1 : id0, sf_t + 4 * (kk >> 1), sf_t + 8 + 4 * (kk >> 1) + shift,
-                           kk > 0 ? 1u : (uint32_t)(ks - k0));
+              umma_mx<F, 1>(d_tmem, desc(a_lo + 2 * kk, kDescHiSw128), desc(b_lo + 2 * kk, kDescHiSw128), id[kk],
+                            sf_t + sf, sf_t + 4 * kSf + sf + shift, kk > 0 ? 1u : (uint32_t)(ks - k0));
+          }
           umma_commit(&empty[ring.s]);
           if (ks == k1 - 1) umma_commit(&acc_full[b]);
         }
@@ -272,56 +276,64 @@ mm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
   }
 }
 
+template <typename F>
+constexpr int code_bytes(int K) {  // of a row
+  return F::kMmaK == 64 ? K / 2 : K;
+}
+
+template <typename F>
 bool make_w_map(const moe_fp4_mm_dims& d, const uint8_t* w, CUtensorMap* map) {
   const uint32_t pair = d.swiglu ? 2 : 1;
-  const uint64_t row = (uint64_t)d.K / 2;
+  const uint64_t row = code_bytes<F>(d.K);
   const uint64_t dims[4] = {row, pair, (uint64_t)d.N / pair, (uint64_t)d.E};
   const uint64_t strides[3] = {(d.N / pair) * row, row, (uint64_t)d.N * row};
   const uint32_t box[4] = {128, pair, 128 / pair, 1};
   return make_map_4d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, w, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+template <typename F>
 bool make_a_map(const moe_fp4_mm_dims& d, const uint8_t* a, int rows, CUtensorMap* map) {
-  const uint64_t row = (uint64_t)d.K / 2;
+  const uint64_t row = code_bytes<F>(d.K);
   return make_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, a, row, d.M, row, 128, rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int NT, bool F32, bool SW>
+template <typename F, int NT, bool F32, bool SW>
 cudaError_t launch_as(const CUtensorMap& map_w, const CUtensorMap& map_a, const MmParams& P, int items,
                       cudaStream_t st) {
-  auto* k = P.split > 1 ? mm_kernel<NT, F32, SW, true> : mm_kernel<NT, F32, SW, false>;
-  const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(k), Cfg<NT>::kSmem);
+  auto* k = P.split > 1 ? mm_kernel<F, NT, F32, SW, true> : mm_kernel<F, NT, F32, SW, false>;
+  const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(k), Cfg<F, NT>::kSmem);
   if (e != cudaSuccess) return e;
   const int grid = P.split > 1 ? items * P.split : std::min(items, num_sms());
-  return launch_cluster_early(k, grid, P.split, kThreads, Cfg<NT>::kSmem, st, map_w, map_a, P);
+  return launch_cluster_early(k, grid, P.split, kThreads, Cfg<F, NT>::kSmem, st, map_w, map_a, P);
 }
 
-template <int NT>
+template <typename F, int NT>
 cudaError_t launch_nt(const moe_fp4_mm_dims& d, const uint8_t* a, const uint8_t* w, const MmParams& P,
                       cudaStream_t st) {
   CUtensorMap map_w, map_a;
-  if (!make_w_map(d, w, &map_w) || !make_a_map(d, a, NT, &map_a)) return cudaErrorInvalidValue;
+  if (!make_w_map<F>(d, w, &map_w) || !make_a_map<F>(d, a, NT, &map_a)) return cudaErrorInvalidValue;
   // exactly, or for groups at most
   const int64_t tiles = P.offsets ? (int64_t)d.M / NT + std::min(d.E, d.M) : ((int64_t)d.M + NT - 1) / NT;
   const int items = (int)std::min<int64_t>(tiles * P.mblocks, INT32_MAX);
   if (P.f32)
-    return P.swiglu ? launch_as<NT, true, true>(map_w, map_a, P, items, st)
-                    : launch_as<NT, true, false>(map_w, map_a, P, items, st);
-  return P.swiglu ? launch_as<NT, false, true>(map_w, map_a, P, items, st)
-                  : launch_as<NT, false, false>(map_w, map_a, P, items, st);
+    return P.swiglu ? launch_as<F, NT, true, true>(map_w, map_a, P, items, st)
+                    : launch_as<F, NT, true, false>(map_w, map_a, P, items, st);
+  return P.swiglu ? launch_as<F, NT, false, true>(map_w, map_a, P, items, st)
+                  : launch_as<F, NT, false, false>(map_w, map_a, P, items, st);
 }
 
+template <typename F>
 cudaError_t launch_pairs(const moe_fp4_mm_dims& d, const uint8_t* a, const uint8_t* w, const MmParams& P,
                          cudaStream_t st) {
   CUtensorMap map_w, map_a, map_a128, map_ws, map_as;
   const uint64_t ws_tiles = (uint64_t)d.E * P.mblocks * P.kt, as_tiles = (uint64_t)(d.M / 128 + d.E) * P.kt;
-  if (!make_w_map(d, w, &map_w) || !make_a_map(d, a, 32, &map_a) || !make_a_map(d, a, 128, &map_a128) ||
-      !make_map_2d(&map_ws, CU_TENSOR_MAP_DATA_TYPE_INT32, P.w_scales, kSfTile / 4, ws_tiles, kSfTile, kSfTile / 4, 2,
+  if (!make_w_map<F>(d, w, &map_w) || !make_a_map<F>(d, a, 32, &map_a) || !make_a_map<F>(d, a, 128, &map_a128) ||
+      !make_map_2d(&map_ws, CU_TENSOR_MAP_DATA_TYPE_INT32, P.w_scales, kSfTile / 4, ws_tiles, kSfTile, kSfTile / 4, F::kSfTiles,
                    CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !make_map_2d(&map_as, CU_TENSOR_MAP_DATA_TYPE_INT32, P.a_scales, kSfTile / 4, as_tiles, kSfTile, kSfTile / 4, 2,
+      !make_map_2d(&map_as, CU_TENSOR_MAP_DATA_TYPE_INT32, P.a_scales, kSfTile / 4, as_tiles, kSfTile, kSfTile / 4, F::kSfTiles,
                    CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
-  return launch_mm_pairs(map_w, map_a, map_a128, map_ws, map_as, P, st);
+  return launch_mm_pairs<F>(map_w, map_a, map_a128, map_ws, map_as, P, st);
 }
 
 int check_mm(const moe_fp4_mm_dims& d) {
@@ -367,11 +379,12 @@ MmParams params(const moe_fp4_mm_dims& d, const uint8_t* as, const int32_t* offs
 // 4.8.  With a wide N it is the slower one: 16 x 16384 x 4096 11.1 us, 17 rows 8.7.
 bool few_rows(const moe_fp4_mm_dims& d, const int32_t* offsets) { return !offsets && d.M <= kFewRows; }
 
+template <typename F>
 cudaError_t launch_few(const moe_fp4_mm_dims& d, const MmParams& P, const MxRows* x, const uint8_t* codes,
                        const uint8_t* w, cudaStream_t st) {
   CUtensorMap map_w;
-  if (!make_w_map(d, w, &map_w)) return cudaErrorInvalidValue;
-  return launch_mm_few(map_w, P, x, codes, st);
+  if (!make_w_map<F>(d, w, &map_w)) return cudaErrorInvalidValue;
+  return launch_mm_few<F>(map_w, P, x, codes, st);
 }
 
 // The kernel and tile of a product with more than a few rows: the one whose
@@ -392,8 +405,9 @@ struct Choice {
   int rows, split;
 };
 
+template <typename F>
 Choice choose_tile(const moe_fp4_mm_dims& d, bool grouped) {
-  const int nks = (d.K + kStageK - 1) / kStageK, sms = num_sms();
+  const int nks = (d.K + F::kStageK - 1) / F::kStageK, sms = num_sms();
   const double mean = (double)d.M / d.E;
   double best = 0;
   Choice choice{0, 1};
@@ -416,17 +430,18 @@ Choice choose_tile(const moe_fp4_mm_dims& d, bool grouped) {
 }
 
 // rows_ahead: the kernel ahead of this one quantises the rows, to a and as
+template <typename F>
 cudaError_t launch_mm(const moe_fp4_mm_dims& d, const uint8_t* a, const uint8_t* as, const int32_t* offsets,
                       const uint8_t* w, const uint8_t* ws, void* y, bool rows_ahead, cudaStream_t st) {
   MmParams P = params(d, as, offsets, ws, y);
   P.rows_ahead = rows_ahead;
-  if (few_rows(d, offsets)) return launch_few(d, P, nullptr, a, w, st);
-  const Choice c = choose_tile(d, offsets != nullptr);
+  if (few_rows(d, offsets)) return launch_few<F>(d, P, nullptr, a, w, st);
+  const Choice c = choose_tile<F>(d, offsets != nullptr);
   P.split = c.split;
   switch (c.rows) {
-    case 64: return launch_nt<64>(d, a, w, P, st);
-    case 128: return launch_nt<128>(d, a, w, P, st);
-    default: return launch_pairs(d, a, w, P, st);
+    case 64: return launch_nt<F, 64>(d, a, w, P, st);
+    case 128: return launch_nt<F, 128>(d, a, w, P, st);
+    default: return launch_pairs<F>(d, a, w, P, st);
   }
 }
 
@@ -466,7 +481,7 @@ int moe_fp4_mxfp4_matmul(const moe_fp4_mm_dims* dims, const uint8_t* a, const ui
   rc = check_mm_pointers(d, w, w_scales, y, offsets);
   if (rc != MOE_FP4_OK) return rc;
   if (!a || !a_scales || ((uintptr_t)a & 15) || ((uintptr_t)a_scales & 15)) return MOE_FP4_ERR_INVALID_ARG;
-  return launch_mm(d, a, a_scales, offsets, w, w_scales, y, false, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
+  return launch_mm<Fp4>(d, a, a_scales, offsets, w, w_scales, y, false, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
              ? MOE_FP4_OK
              : MOE_FP4_ERR_CUDA;
 }
@@ -505,7 +520,7 @@ int moe_fp4_mxfp4_linear(const moe_fp4_mm_dims* dims, const void* x, int x_type,
   if (rc != MOE_FP4_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   if (few_rows(d, offsets))
-    return launch_few(d, params(d, nullptr, nullptr, w_scales, y), &R, nullptr, w, st) == cudaSuccess ? MOE_FP4_OK
+    return launch_few<Fp4>(d, params(d, nullptr, nullptr, w_scales, y), &R, nullptr, w, st) == cudaSuccess ? MOE_FP4_OK
                                                                                                      : MOE_FP4_ERR_CUDA;
   if (!workspace || ((uintptr_t)workspace & 255)) return MOE_FP4_ERR_INVALID_ARG;
   if (workspace_bytes < moe_fp4_mxfp4_linear_workspace_bytes(dims)) return MOE_FP4_ERR_WORKSPACE;
@@ -517,7 +532,38 @@ int moe_fp4_mxfp4_linear(const moe_fp4_mm_dims* dims, const void* x, int x_type,
           ? launch_mxfp4_quantize_once(R, reinterpret_cast<int32_t*>(codes + base), codes, scales, st)
           : launch_mxfp4_quantize(R, codes, scales, true, st);
   if (e != cudaSuccess) return MOE_FP4_ERR_CUDA;
-  return launch_mm(d, codes, scales, offsets, w, w_scales, y, true, st) == cudaSuccess ? MOE_FP4_OK : MOE_FP4_ERR_CUDA;
+  return launch_mm<Fp4>(d, codes, scales, offsets, w, w_scales, y, true, st) == cudaSuccess ? MOE_FP4_OK : MOE_FP4_ERR_CUDA;
+}
+
+size_t moe_fp4_fp8_linear_workspace_bytes(const moe_fp4_mm_dims* dims) {
+  if (!dims || check_mm(*dims) != MOE_FP4_OK) return 0;
+  return align256((size_t)dims->M * dims->K) + moe_fp4_mxfp4_tiled_scale_bytes(dims->M, dims->E, dims->K);
+}
+
+int moe_fp4_fp8_linear(const moe_fp4_mm_dims* dims, const void* x, int x_type, int64_t x_rows, int64_t x_stride,
+                       const int32_t* offsets, const uint8_t* w, const uint8_t* w_scales, void* y, void* workspace,
+                       size_t workspace_bytes, void* cuda_stream) {
+  if (!dims || (x_type != MOE_FP4_TYPE_BF16 && x_type != MOE_FP4_TYPE_F32)) return MOE_FP4_ERR_INVALID_ARG;
+  const moe_fp4_mm_dims d = *dims;
+  int rc = check_mm(d);
+  if (rc != MOE_FP4_OK) return rc;
+  const MxRows R{x, x_rows, x_stride, nullptr, offsets, d.M, d.K, 1, d.E, x_type == MOE_FP4_TYPE_F32};
+  rc = check_mx_rows(R);
+  if (rc != MOE_FP4_OK || d.M == 0) return rc;
+  rc = check_mm_pointers(d, w, w_scales, y, offsets);
+  if (rc != MOE_FP4_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (few_rows(d, offsets))
+    return launch_few<Fp8>(d, params(d, nullptr, nullptr, w_scales, y), &R, nullptr, w, st) == cudaSuccess
+               ? MOE_FP4_OK
+               : MOE_FP4_ERR_CUDA;
+  if (!workspace || ((uintptr_t)workspace & 255)) return MOE_FP4_ERR_INVALID_ARG;
+  if (workspace_bytes < moe_fp4_fp8_linear_workspace_bytes(dims)) return MOE_FP4_ERR_WORKSPACE;
+  uint8_t* codes = static_cast<uint8_t*>(workspace);
+  uint8_t* scales = codes + align256((size_t)d.M * d.K);
+  if (launch_fp8_quantize(R, codes, scales, st) != cudaSuccess) return MOE_FP4_ERR_CUDA;
+  return launch_mm<Fp8>(d, codes, scales, offsets, w, w_scales, y, true, st) == cudaSuccess ? MOE_FP4_OK
+                                                                                           : MOE_FP4_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -14,10 +14,21 @@ namespace moe_fp4 {
 namespace mm {
 
 constexpr int kBM = 128;        // weight rows of a CTA's tile
-constexpr int kStageK = 256;    // K elements per stage: 128 bytes of codes a row
 constexpr int kSfTile = 512;    // bytes of one scale tile: 128 rows x 4 scales (K = 128)
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSmemMax = 227 * 1024;
+
+// The operands' format.  A stage of the ring holds 128 bytes of codes a row of
+// either operand and the scale tiles that belong to them, four MMAs' worth.
+//   Fp4  E2M1 codes, a scale for 32 elements: kind::mxf4, K = 64 an MMA
+//   Fp8  E4M3 codes, a scale for 128 elements: kind::mxf8f6f4, K = 32 an MMA, which
+//        takes a scale for 32; a tile's row holds the same one four times
+struct Fp4 {
+  static constexpr int kStageK = 256, kMmaK = 64, kSfTiles = 2;  // scale tiles (128 rows, K = 128) of an operand and stage
+};
+struct Fp8 {
+  static constexpr int kStageK = 128, kMmaK = 32, kSfTiles = 1;
+};
 
 struct MmParams {
   const uint8_t* a_scales;   // tiled, grouped
@@ -63,30 +74,35 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-template <int CTAS>
-__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+template <typename F, int CTAS>
+__device__ __forceinline__ void umma_mx(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                           uint32_t sfb, uint32_t acc) {
-  if (CTAS == 1)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
-            d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-        : "memory");
+#define MOE_UMMA(kind)                                                                                     \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\ttcgen05.mma." kind                       \
+               " [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d_tmem),                                        \
+               "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)                                     \
+               : "memory")
+  constexpr bool kFp4 = F::kMmaK == 64;
+  if (kFp4 && CTAS == 1)
+    MOE_UMMA("cta_group::1.kind::mxf4.block_scale.scale_vec::2X");
+  else if (kFp4)
+    MOE_UMMA("cta_group::2.kind::mxf4.block_scale.scale_vec::2X");
+  else if (CTAS == 1)
+    MOE_UMMA("cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X");
   else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
-            d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-        : "memory");
+    MOE_UMMA("cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X");
+#undef MOE_UMMA
 }
 
-// Instruction descriptor of kind::mxf4: A and B E2M1 (1), E8M0 scales; `half`:
-// which two bytes of the scale words the K = 64 of this instruction uses.
-__device__ __forceinline__ uint32_t idesc_mxf4(int M, int N, uint32_t half) {
-  return ((2 * half) << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
-         ((uint32_t)(M >> 4) << 24) | ((2 * half) << 29);
+// Instruction descriptor of MMA kk of a stage: A and B E2M1 (1) or E4M3 (0), E8M0
+// scales, and which bytes of the scale words belong to its K: two of them (mxf4)
+// or one.
+template <typename F>
+__device__ __forceinline__ uint32_t idesc_mx(int M, int N, int kk) {
+  constexpr bool kFp4 = F::kMmaK == 64;
+  const uint32_t sf = kFp4 ? 2 * (kk & 1) : kk, format = kFp4 ? 1 : 0;
+  return (sf << 4) | (format << 7) | (format << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(M >> 4) << 24) | (sf << 29);
 }
 
 // Shared-memory descriptors as two words: the high one is fixed by the layout,
@@ -478,12 +494,15 @@ cudaError_t launch_cluster_early(void (*kernel)(KArgs...), int grid, int cluster
 }
 
 // the kernel for few rows of one matrix, M <= kFewRows (mxfp4_mm1.cu): rows x
-// to quantise, or (x null) their codes with P.a_scales
+// to quantise, or (x null, Fp4 only) their codes with P.a_scales
 constexpr int kFewRows = MOE_FP4_MXFP4_FEW_ROWS;
+template <typename F>
 cudaError_t launch_mm_few(const CUtensorMap& map_w, const mm::MmParams& P, const MxRows* x, const uint8_t* codes,
                           cudaStream_t st);
 // the pair kernel (mxfp4_mm2.cu); the boxes of map_a have 32 rows, those of
-// map_a128 128; map_ws and map_as: scale tiles as rows of 512 bytes, boxes of 2
+// map_a128 128; map_ws and map_as: scale tiles as rows of 512 bytes, boxes of
+// F::kSfTiles
+template <typename F>
 cudaError_t launch_mm_pairs(const CUtensorMap& map_w, const CUtensorMap& map_a, const CUtensorMap& map_a128,
                             const CUtensorMap& map_ws, const CUtensorMap& map_as, const mm::MmParams& P,
                             cudaStream_t st);

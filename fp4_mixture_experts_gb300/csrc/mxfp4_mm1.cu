@@ -35,18 +35,19 @@ constexpr int kWriters = 8;
 constexpr int kRows = kFewRows;
 constexpr int kATile = kBM * 128;
 constexpr int kBTile = kRows * 128;
-constexpr int kStage = kATile + kBTile + 4 * kSfTile;
 // Ring stages: 5 where a CTA has no more (two CTAs then fit an SM, and the next
 // launch is set up while this one runs), else 10.
-template <int S>
+template <typename F, int S>
 struct Cfg {
+  static constexpr int kSf = 2 * F::kSfTiles;                 // scale tiles of a stage
+  static constexpr int kStage = kATile + kBTile + kSf * kSfTile;
+  static_assert(kStage % 1024 == 0, "stages stay 1 KB aligned for the 128-byte swizzle");
   static constexpr int kOffPart = S * kStage;
   static constexpr int kOffBar = kOffPart + kRows * kPartPitch * 4;
   static constexpr int kSmem = kOffBar + 512 + 1024;
   static_assert(kSmem <= (S <= 5 ? kSmemMax / 2 : kSmemMax) && kRows + 16 * S <= 256, "layout");
 };
 constexpr uint32_t kCols1 = 256;     // tensor memory: 16 accumulator columns, 16 of scales a stage
-static_assert(kStage % 1024 == 0, "stages stay 1 KB aligned for the 128-byte swizzle");
 
 struct Mm1Params {
   MmParams m;
@@ -57,15 +58,18 @@ struct Mm1Params {
 };
 
 // SRC 0: bf16 rows, 1: fp32 rows, 2: codes with tiled scales
-template <int kStages, int SRC, bool F32, bool SW>
+template <typename F, int kStages, int SRC, bool F32, bool SW>
 __global__ void __launch_bounds__(kThreads, kStages <= 5 ? 2 : 1)
 mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
   MmParams& P = Q.m;
   P.err = &g_mm1_err[0];
+  using C = Cfg<F, kStages>;
+  constexpr int kStage = C::kStage, kStageK = F::kStageK, kSf = F::kSfTiles;
+  static_assert(SRC != 2 || F::kMmaK == 64, "codes");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* part = reinterpret_cast<float*>(smem + Cfg<kStages>::kOffPart);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg<kStages>::kOffBar);  // [stage]: weights landed
+  float* part = reinterpret_cast<float*>(smem + C::kOffPart);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kOffBar);  // [stage]: weights landed
   uint64_t* written = full + kStages;                            // [stage]: rows written
   uint64_t* empty = written + kStages;                           // [stage]: its MMAs completed
   uint64_t* acc_full = empty + kStages;
@@ -80,10 +84,10 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
   auto load_weights = [&](int ks, int s) {
     if (elect_one()) {
       uint8_t* st = smem + s * kStage;
-      const uint32_t sf_bytes = min(2, P.kt - 2 * ks) * kSfTile;
+      const uint32_t sf_bytes = min(kSf, P.kt - kSf * ks) * kSfTile;
       mbar_expect_tx(&full[s], kATile + sf_bytes);
       tma_load_4d(st, &map_w, ks * 128, 0, mb * (SW ? 64 : 128), 0, &full[s]);
-      bulk_load(st + kATile + kBTile, P.w_scales + ((size_t)mb * P.kt + 2 * ks) * kSfTile, sf_bytes, &full[s]);
+      bulk_load(st + kATile + kBTile, P.w_scales + ((size_t)mb * P.kt + kSf * ks) * kSfTile, sf_bytes, &full[s]);
     }
     __syncwarp();
   };
@@ -131,7 +135,9 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
   } else if (warp == 1) {
     Ring<kStages> ring;
     const uint32_t lo0 = desc_lo(smem_u32(smem));
-    const uint32_t id0 = idesc_mxf4(kBM, kRows, 0), id1 = idesc_mxf4(kBM, kRows, 1);
+    uint32_t id[4];
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) id[kk] = idesc_mx<F>(kBM, kRows, kk);
     for (int ks = k0; ks < k1; ++ks, ring.next()) {
       if (!warp_wait(&written[ring.s], ring.phase, abort_flag, P) ||
           !warp_wait(&full[ring.s], ring.phase, abort_flag, P))
@@ -141,17 +147,18 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
         const uint32_t lo = lo0 + ring.s * (kStage >> 4);
         const uint32_t a_lo = lo | kDescLoSw128, b_lo = (lo + (kATile >> 4)) | kDescLoSw128;
         const uint32_t sf_lo = lo + ((kATile + kBTile) >> 4);
-        const uint32_t sf_t = sf_base + ring.s * 16;
+        const uint32_t sf_t = sf_base + ring.s * 8 * kSf;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)  // weights' two K chunks, then the rows'
+        for (int i = 0; i < 2 * kSf; ++i)  // weights' K chunks, then the rows'
           tmem_cp_scales<1>(sf_t + 4 * i, sf_lo + i * (kSfTile >> 4));
-        const int steps = (P.K - ks * kStageK + 63) / 64;
+        const int steps = (P.K - ks * kStageK + F::kMmaK - 1) / F::kMmaK;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
+        for (int kk = 0; kk < 4; ++kk) {
+          const int sf = 4 * (kk * F::kMmaK / 128);  // columns of this MMA's scale tile
           if (kk < steps)
-            umma_mxf4<1>(tmem, desc(a_lo + 2 * kk, kDescHiSw128), desc(b_lo + 2 * kk, kDescHiSw128),
-                         (kk & 1) ? id1 : id0, sf_t + 4 * (kk >> 1), sf_t + 8 + 4 * (kk >> 1),
-                         kk > 0 ? 1u : (uint32_t)(ks - k0));
+            umma_mx<F, 1>(tmem, desc(a_lo + 2 * kk, kDescHiSw128), desc(b_lo + 2 * kk, kDescHiSw128), id[kk], sf_t + sf,
+                          sf_t + 4 * kSf + sf, kk > 0 ? 1u : (uint32_t)(ks - k0));
+        }
         umma_commit(&empty[ring.s]);
       }
       __syncwarp();
@@ -161,14 +168,15 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
     mbar_wait_drain(acc_full, 0, P.err, kErrWaitTimeout, P.wait_ns);
   } else if (warp >= 4) {
     // ---------------- writers: rows into the stages ----------------
-    // A pass covers 256 chunks of 16 elements (8 bytes of codes): 16 a row and
-    // stage, so that with few rows one pass covers several stages.  A pass's
-    // rows are loaded two passes before they are quantised.
+    // A pass covers 256 chunks of 16 elements (8 bytes of FP4 codes, 16 of FP8): 16
+    // (8) a row and stage, so that with few rows one pass covers several stages.  A
+    // pass's rows are loaded two passes before they are quantised.
     const int tid = threadIdx.x - 128;
-    int per_log = 4;                                           // chunks of a stage: its rows, rounded up to a
-    while ((16 << (per_log - 4)) < 16 * P.M) ++per_log;        // power of two, times 16
+    constexpr int kChunkLog = kStageK == 256 ? 4 : 3;          // log2 of the chunks of a row and stage
+    int per_log = kChunkLog;                                   // chunks of a stage: its rows, rounded up to a
+    while ((1 << (per_log - kChunkLog)) < P.M) ++per_log;      // power of two, times those
     const int group = min(1 << (8 - per_log), 4);              // stages of a pass
-    const int sub = tid >> per_log, c = tid & 15, row = (tid & ((1 << per_log) - 1)) >> 4;
+    const int sub = tid >> per_log, c = tid & ((1 << kChunkLog) - 1), row = (tid & ((1 << per_log) - 1)) >> kChunkLog;
     const bool mine = sub < group && row < P.M;
     int64_t src = -1;                                          // first element of this thread's row, -1: a zero row
     if (mine) {
@@ -215,7 +223,10 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
       }
       load(ks + 2 * group, next[1]);
       uint2 q;
-      if (SRC == 2) {
+      uint4 q8;
+      if (F::kMmaK == 32) {
+        q8 = quantize16_fp8<SRC == 1>(cur, sb);
+      } else if (SRC == 2) {
         q = make_uint2(cur[0], cur[1]);
         sb = cur[2];
       } else {
@@ -229,8 +240,14 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
       if (mine && sub < here) {
         uint8_t* st = smem + (ring.s + sub < kStages ? ring.s + sub : ring.s + sub - kStages) * kStage;
         // 128-byte swizzle: the 16-byte chunk at (c / 2) ^ (row % 8); past the end of K codes and scales are 0
-        *reinterpret_cast<uint2*>(st + kATile + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8) = q;
-        if ((c & 1) == 0) st[kATile + kBTile + (2 + (c >> 3)) * kSfTile + 16 * row + ((c >> 1) & 3)] = (uint8_t)sb;
+        if (F::kMmaK == 32) {
+          *reinterpret_cast<uint4*>(st + kATile + row * 128 + ((c ^ (row & 7)) << 4)) = q8;
+          if (c == 0)
+            *reinterpret_cast<uint32_t*>(st + kATile + kBTile + kSfTile + 16 * row) = sb * 0x01010101u;
+        } else {
+          *reinterpret_cast<uint2*>(st + kATile + row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8) = q;
+          if ((c & 1) == 0) st[kATile + kBTile + (2 + (c >> 3)) * kSfTile + 16 * row + ((c >> 1) & 3)] = (uint8_t)sb;
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
@@ -261,43 +278,44 @@ mm1_kernel(const __grid_constant__ CUtensorMap map_w, Mm1Params Q) {
   }
 }
 
-template <int S, int SRC, bool F32, bool SW>
+template <typename F, int S, int SRC, bool F32, bool SW>
 cudaError_t launch_as(const CUtensorMap& map_w, const Mm1Params& Q, cudaStream_t st) {
-  auto* k = mm1_kernel<S, SRC, F32, SW>;
-  const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(k), Cfg<S>::kSmem);
+  auto* k = mm1_kernel<F, S, SRC, F32, SW>;
+  const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(k), Cfg<F, S>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_cluster_early(k, Q.m.mblocks * Q.m.split, Q.m.split, kThreads, Cfg<S>::kSmem, st, map_w, Q);
+  return launch_cluster_early(k, Q.m.mblocks * Q.m.split, Q.m.split, kThreads, Cfg<F, S>::kSmem, st, map_w, Q);
 }
 
-template <int SRC, bool F32, bool SW>
+template <typename F, int SRC, bool F32, bool SW>
 cudaError_t launch_stages(const CUtensorMap& map_w, const Mm1Params& Q, cudaStream_t st) {
-  const int nks = (Q.m.K + kStageK - 1) / kStageK;
-  return (nks + Q.m.split - 1) / Q.m.split <= 5 ? launch_as<5, SRC, F32, SW>(map_w, Q, st)
-                                                : launch_as<10, SRC, F32, SW>(map_w, Q, st);
+  const int nks = (Q.m.K + F::kStageK - 1) / F::kStageK;
+  return (nks + Q.m.split - 1) / Q.m.split <= 5 ? launch_as<F, 5, SRC, F32, SW>(map_w, Q, st)
+                                                : launch_as<F, 10, SRC, F32, SW>(map_w, Q, st);
 }
 
-template <int SRC>
+template <typename F, int SRC>
 cudaError_t launch_src(const CUtensorMap& map_w, const Mm1Params& Q, cudaStream_t st) {
   if (Q.m.f32)
-    return Q.m.swiglu ? launch_stages<SRC, true, true>(map_w, Q, st) : launch_stages<SRC, true, false>(map_w, Q, st);
-  return Q.m.swiglu ? launch_stages<SRC, false, true>(map_w, Q, st) : launch_stages<SRC, false, false>(map_w, Q, st);
+    return Q.m.swiglu ? launch_stages<F, SRC, true, true>(map_w, Q, st) : launch_stages<F, SRC, true, false>(map_w, Q, st);
+  return Q.m.swiglu ? launch_stages<F, SRC, false, true>(map_w, Q, st) : launch_stages<F, SRC, false, false>(map_w, Q, st);
 }
 
 }  // namespace
 
+template <typename F>
 cudaError_t launch_mm_few(const CUtensorMap& map_w, const MmParams& P, const MxRows* x, const uint8_t* codes,
                           cudaStream_t st) {
   Mm1Params Q{};
   Q.m = P;
   // CTAs of a cluster: as many as the SMs take, with two stages of K each at least
-  const int nks = (P.K + kStageK - 1) / kStageK;
+  const int nks = (P.K + F::kStageK - 1) / F::kStageK;
   Q.m.split = 1;
   while (Q.m.split < 8 && 2 * Q.m.split * P.mblocks <= num_sms() && 4 * Q.m.split <= nks) Q.m.split *= 2;
   if (x == nullptr) {
     Q.x = codes;
     Q.x_rows = P.M;
     Q.x_stride = P.K;
-    return launch_src<2>(map_w, Q, st);
+    return launch_src<Fp4, 2>(map_w, Q, st);
   }
   Q.x = x->x;
   Q.x_rows = x->x_rows;
@@ -305,8 +323,11 @@ cudaError_t launch_mm_few(const CUtensorMap& map_w, const MmParams& P, const MxR
   Q.row_index = x->row_index;
   Q.div = x->div;
   Q.align = x->align();
-  return x->f32 ? launch_src<1>(map_w, Q, st) : launch_src<0>(map_w, Q, st);
+  return x->f32 ? launch_src<F, 1>(map_w, Q, st) : launch_src<F, 0>(map_w, Q, st);
 }
+
+template cudaError_t launch_mm_few<Fp4>(const CUtensorMap&, const MmParams&, const MxRows*, const uint8_t*, cudaStream_t);
+template cudaError_t launch_mm_few<Fp8>(const CUtensorMap&, const MmParams&, const MxRows*, const uint8_t*, cudaStream_t);
 
 cudaError_t ops_mm1_error(int32_t** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_mm1_err); }
 

@@ -55,17 +55,23 @@ constexpr int kNT = 256;                                 // token rows per item
 constexpr int kBoxRows = 32;                             // token rows per small TMA box; a large one has 128
 constexpr int kATile = kBM * 128;
 constexpr int kBTile = kNT / 2 * 128;                    // this CTA's half
-constexpr int kStage = kATile + kBTile + 6 * kSfTile;    // scales: 2 weight tiles, 2 x 2 token tiles
 constexpr int kFixed = 1024 + 512 + 2 * (kMaxGroups + 1) * 4;
-constexpr int kStages = (kSmemMax - kFixed) / kStage;
-constexpr int kSmem2 = kStages * kStage + kFixed;
 constexpr uint32_t kAcc1 = 184;                          // first column of accumulator 1
 constexpr uint32_t kSfBase = 440;
-constexpr uint32_t kSfCols = 24;
 constexpr int kSfSlots = 3;
-static_assert(kStage % 1024 == 0 && kStages >= 4, "ring");
+template <typename F>
+struct Cfg {
+  static constexpr int kSf = F::kSfTiles;
+  // scales of a stage: weight tiles, and token tiles of two 128 rows (to whole KB)
+  static constexpr int kStage = kATile + kBTile + (3 * kSf + (kSf & 1)) * kSfTile;
+  static constexpr int kStages = (kSmemMax - kFixed) / kStage;
+  static constexpr int kSmem = kStages * kStage + kFixed;
+  static constexpr uint32_t kSfCols = 12 * kSf;
+  static_assert(kStage % 1024 == 0 && kStages >= 4, "ring");
+  static_assert(kSfBase + kSfSlots * kSfCols <= kTmemCols, "tensor memory columns");
+};
 static_assert(kNT - kAcc1 <= 128 - 32 && kNT - kAcc1 / 32 * 32 <= 128, "the shared columns are in the first round's reads");
-static_assert(kSfBase >= kAcc1 + kNT && kSfBase + kSfSlots * kSfCols <= kTmemCols, "tensor memory columns");
+static_assert(kSfBase >= kAcc1 + kNT, "tensor memory columns");
 
 // Arrive on the barrier at the same offset in the leader CTA: this warp's reads
 // of tensor memory have ended (tcgen05.wait::ld, the fence before it), and that
@@ -118,12 +124,14 @@ __device__ __forceinline__ void commit_one(uint64_t* bar) {
                : "memory");
 }
 
-template <bool F32, bool SW>
+template <typename F, bool F32, bool SW>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
            const __grid_constant__ CUtensorMap map_a128, const __grid_constant__ CUtensorMap map_ws,
            const __grid_constant__ CUtensorMap map_as, MmParams P) {
   P.err = &g_mm2_err[0];
+  constexpr int kStage = Cfg<F>::kStage, kStages = Cfg<F>::kStages, kStageK = F::kStageK, kSf = F::kSfTiles;
+  constexpr uint32_t kSfCols = Cfg<F>::kSfCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* tail = smem + kStages * kStage;
@@ -214,12 +222,12 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
                 tma2_load_2d(st + kATile + i * kBoxRows * 128, &map_a, ks * 128, arow + i * kBoxRows, bar);
           }
         } else if (elect_one()) {
-          // two tiles (K = 256) a box; the second of the last stage may be the next row tile's: not used then
+          // a stage's tiles a box; the second (Fp4) of the last stage may be the next row tile's: not used then
           uint8_t* sf = st + kATile + kBTile;
-          expect_tx_cl(bar, 6 * kSfTile);
-          tma2_load_2d(sf, &map_ws, 0, ws + 2 * ks, bar);
-          tma2_load_2d(sf + 2 * kSfTile, &map_as, 0, as + 2 * ks, bar);
-          tma2_load_2d(sf + 4 * kSfTile, &map_as, 0, as + P.kt + 2 * ks, bar);
+          expect_tx_cl(bar, 3 * kSf * kSfTile);
+          tma2_load_2d(sf, &map_ws, 0, ws + kSf * ks, bar);
+          tma2_load_2d(sf + kSf * kSfTile, &map_as, 0, as + kSf * ks, bar);
+          tma2_load_2d(sf + 2 * kSf * kSfTile, &map_as, 0, as + P.kt + kSf * ks, bar);
         }
         __syncwarp();
       }
@@ -249,7 +257,9 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
             (shared && !warp_wait(&part_free[b ^ 1], ((li - 1) >> 1) & 1, abort_flag, P)))
           break;
         const uint32_t d_tmem = tmem + b * kAcc1;
-        const uint32_t id0 = idesc_mxf4(2 * kBM, n_mma, 0), id1 = idesc_mxf4(2 * kBM, n_mma, 1);
+        uint32_t id[4];
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) id[kk] = idesc_mx<F>(2 * kBM, n_mma, kk);
         for (int ks = 0; ks < nks; ++ks, ring.next(), slot.next()) {
           if (!warp_wait(&sf_full[slot.s], slot.phase, abort_flag, P)) {
             ok = false;
@@ -260,13 +270,14 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
             const uint32_t lo = lo0 + ring.s * (kStage >> 4);
             const uint32_t a_lo = lo | kDescLoSw128, b_lo = (lo + (kATile >> 4)) | kDescLoSw128;
             const uint32_t sf_t = tmem + kSfBase + slot.s * kSfCols;
-            const int steps = (P.K - ks * kStageK + 63) / 64;
+            const int steps = (P.K - ks * kStageK + F::kMmaK - 1) / F::kMmaK;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
+            for (int kk = 0; kk < 4; ++kk) {
+              const int c = kk * F::kMmaK / 128;  // this MMA's scale tile
               if (kk < steps)
-                umma_mxf4<2>(d_tmem, desc(a_lo + 2 * kk, kDescHiSw128), desc(b_lo + 2 * kk, kDescHiSw128),
-                             (kk & 1) ? id1 : id0, sf_t + 4 * (kk >> 1), sf_t + 8 + 8 * (kk >> 1),
-                             kk > 0 ? 1u : (uint32_t)ks);
+                umma_mx<F, 2>(d_tmem, desc(a_lo + 2 * kk, kDescHiSw128), desc(b_lo + 2 * kk, kDescHiSw128), id[kk],
+                              sf_t + 4 * c, sf_t + 4 * kSf + 8 * c, kk > 0 ? 1u : (uint32_t)ks);
+            }
             commit_both(&empty[ring.s]);
             if (ks == nks - 1) commit_both(&acc_full[b]);
           }
@@ -304,10 +315,10 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
             const uint32_t sf_lo = lo0 + ring.s * (kStage >> 4);
             const uint32_t sf_t = tmem + kSfBase + slot.s * kSfCols;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < kSf; ++c) {
               tmem_cp_scales<2>(sf_t + 4 * c, sf_lo + c * (kSfTile >> 4));
-              tmem_cp_scales<2>(sf_t + 8 + 8 * c, sf_lo + (2 + c) * (kSfTile >> 4));
-              tmem_cp_scales<2>(sf_t + 12 + 8 * c, sf_lo + (4 + c) * (kSfTile >> 4));
+              tmem_cp_scales<2>(sf_t + 4 * kSf + 8 * c, sf_lo + (kSf + c) * (kSfTile >> 4));
+              tmem_cp_scales<2>(sf_t + 4 * kSf + 4 + 8 * c, sf_lo + (2 * kSf + c) * (kSfTile >> 4));
             }
             commit_one(&sf_full[slot.s]);
           }
@@ -364,28 +375,34 @@ mm2_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
 
 namespace {
 
-template <bool F32, bool SW>
+template <typename F, bool F32, bool SW>
 cudaError_t launch_as(const CUtensorMap& map_w, const CUtensorMap& map_a, const CUtensorMap& map_a128,
                       const CUtensorMap& map_ws, const CUtensorMap& map_as, const MmParams& P, int pairs,
                       cudaStream_t st) {
-  const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(mm2_kernel<F32, SW>), kSmem2);
+  const cudaError_t e = ensure_smem_optin(reinterpret_cast<const void*>(mm2_kernel<F, F32, SW>), Cfg<F>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_early(mm2_kernel<F32, SW>, dim3(2 * pairs), dim3(kThreads), kSmem2, st, map_w, map_a, map_a128, map_ws,
+  return launch_early(mm2_kernel<F, F32, SW>, dim3(2 * pairs), dim3(kThreads), Cfg<F>::kSmem, st, map_w, map_a, map_a128, map_ws,
                       map_as, P);
 }
 
 }  // namespace
 
+template <typename F>
 cudaError_t launch_mm_pairs(const CUtensorMap& map_w, const CUtensorMap& map_a, const CUtensorMap& map_a128,
                             const CUtensorMap& map_ws, const CUtensorMap& map_as, const MmParams& P, cudaStream_t st) {
   const int64_t most = ((int64_t)P.M / kNT + std::min(P.E, P.M)) * ((P.mblocks + 1) / 2);
   const int pairs = (int)std::min<int64_t>(most, num_sms() / 2);
   if (P.f32)
-    return P.swiglu ? launch_as<true, true>(map_w, map_a, map_a128, map_ws, map_as, P, pairs, st)
-                    : launch_as<true, false>(map_w, map_a, map_a128, map_ws, map_as, P, pairs, st);
-  return P.swiglu ? launch_as<false, true>(map_w, map_a, map_a128, map_ws, map_as, P, pairs, st)
-                  : launch_as<false, false>(map_w, map_a, map_a128, map_ws, map_as, P, pairs, st);
+    return P.swiglu ? launch_as<F, true, true>(map_w, map_a, map_a128, map_ws, map_as, P, pairs, st)
+                    : launch_as<F, true, false>(map_w, map_a, map_a128, map_ws, map_as, P, pairs, st);
+  return P.swiglu ? launch_as<F, false, true>(map_w, map_a, map_a128, map_ws, map_as, P, pairs, st)
+                  : launch_as<F, false, false>(map_w, map_a, map_a128, map_ws, map_as, P, pairs, st);
 }
+
+template cudaError_t launch_mm_pairs<Fp4>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                                          const CUtensorMap&, const MmParams&, cudaStream_t);
+template cudaError_t launch_mm_pairs<Fp8>(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                                          const CUtensorMap&, const MmParams&, cudaStream_t);
 
 cudaError_t ops_mm2_error(int32_t** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_mm2_err); }
 

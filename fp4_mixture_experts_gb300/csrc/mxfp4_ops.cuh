@@ -37,6 +37,8 @@ inline int once_cap(const MxRows& R) { return (int)std::min<int64_t>(32, 2 * ((R
 inline int64_t once_lists(const MxRows& R) { return R.x_rows + 1 + R.x_rows * once_cap(R) + R.rows; }
 cudaError_t launch_mxfp4_quantize_once(const MxRows& R, int32_t* lists, uint8_t* codes, uint8_t* scales,
                                        cudaStream_t st);
+// E4M3 form of rows (no row_index) with a scale for 128 elements, tiled; by groups with offsets
+cudaError_t launch_fp8_quantize(const MxRows& R, uint8_t* codes, uint8_t* scales, cudaStream_t st);
 // the error words of the operators' kernels on the current device (one in each translation unit)
 cudaError_t ops_quant_error(int32_t** word);
 cudaError_t ops_mm_error(int32_t** word);
@@ -180,6 +182,54 @@ __device__ __forceinline__ uint2 quantize16(const uint32_t (&w)[16], uint32_t& s
     }
   }
   return make_uint2(e2m1x8(v), e2m1x8(v + 8));
+}
+
+// four fp32 values, in [-448, 448], -> four E4M3 codes, to nearest even
+__device__ __forceinline__ uint32_t e4m3x4(const float* v) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]));
+  return r;
+}
+
+// The E4M3 codes of 16 elements as load16_raw leaves them, by eight lanes (8 i ..
+// 8 i + 7) that hold a block of 128 together (whole warp; every lane takes part),
+// and the block's scale byte: e + 127 with the least e >= -127 for which amax <= 448
+// 2^e.  448 is 1.75 2^8, so e is the exponent of amax minus 8, and one more for
+// mantissas above 1.75.  x 2^-e is exact but where it underflows to the code 0.
+template <bool F32>
+__device__ __forceinline__ uint4 quantize16_fp8(const uint32_t (&w)[16], uint32_t& scale) {
+  uint32_t amax = 0;  // bits of the largest magnitude as fp32
+  if (F32) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) amax = max(amax, w[j] & 0x7FFFFFFFu);
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
+    amax = max(m << 16, m & 0xFFFF0000u);
+  }
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+  const uint32_t ef = (amax >> 23) + ((amax & 0x7FFFFFu) > 0x600000u ? 1u : 0u);
+  scale = amax >= 0x7F800000u ? 255u : (ef > 8u ? ef - 8u : 0u);
+  if (scale == 255u) return make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  const float inv = __uint_as_float((254u - scale) << 23);  // 2^(127 - scale), normal for scale in [0, 247]
+  uint32_t q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = (F32 ? __uint_as_float(w[4 * i + j])
+                  : __uint_as_float(j & 1 ? w[2 * i + j / 2] & 0xFFFF0000u : w[2 * i + j / 2] << 16)) * inv;
+    q[i] = e4m3x4(v);
+  }
+  return make_uint4(q[0], q[1], q[2], q[3]);
 }
 
 // The group that holds row r: the last e with off[e] <= r, if r < off[e + 1];

@@ -35,6 +35,9 @@ struct Entry {
   decltype(&moe_fp4_mxfp4_linear_workspace_bytes) linear_workspace_bytes;
   decltype(&moe_fp4_mxfp4_gathered_workspace_bytes) gathered_workspace_bytes;
   decltype(&moe_fp4_block_norm) block_norm;
+  decltype(&moe_fp4_fp8_tile_scales) fp8_tile_scales;
+  decltype(&moe_fp4_fp8_linear_workspace_bytes) fp8_linear_workspace_bytes;
+  decltype(&moe_fp4_fp8_linear) fp8_linear;
 } g_entry;
 PyObject* g_raise = nullptr;  // called with (status, entry point); raises
 
@@ -101,7 +104,7 @@ struct Rows {
 Rows rows_of(const at::Tensor& t, const char* what) {
   if (!t.is_cuda() || t.dim() != 2) bad(std::string(what) + " must be a 2-D GPU tensor");
   const int64_t R = t.size(0), K = t.size(1);
-  if ((t.stride(1) != 1 && K > 1) || (t.stride(0) < K && R > 1))
+  if (R > 0 && ((t.stride(1) != 1 && K > 1) || (t.stride(0) < K && R > 1)))
     bad(std::string(what) + " must have contiguous, separate rows");
   return {R, K, R > 1 ? t.stride(0) : K, type_of(t, what), t.data_ptr()};
 }
@@ -109,6 +112,12 @@ Rows rows_of(const at::Tensor& t, const char* what) {
 uint8_t* bytes_of(const at::Tensor& t, const char* what, int64_t numel) {
   if (t.scalar_type() != at::kByte || !t.is_cuda() || !t.is_contiguous() || t.numel() < numel)
     bad(std::string(what) + " must be a contiguous uint8 GPU tensor of at least " + std::to_string(numel) + " elements");
+  return static_cast<uint8_t*>(t.data_ptr());
+}
+
+uint8_t* e4m3_of(const at::Tensor& t, const char* what) {
+  if (t.scalar_type() != at::kFloat8_e4m3fn || !t.is_cuda() || !t.is_contiguous())
+    bad(std::string(what) + " must be a contiguous float8_e4m3fn GPU tensor");
   return static_cast<uint8_t*>(t.data_ptr());
 }
 
@@ -192,18 +201,21 @@ struct Weights {
 };
 
 Weights weights_of(int64_t M, int64_t K, PyObject* w_, PyObject* scales_, bool grouped, int64_t n_offsets, bool swiglu,
-                   at::ScalarType t) {
+                   at::ScalarType t, bool fp8 = false) {
   const at::Tensor& w = tensor(w_, "w");
-  if ((w.dim() != 2 && w.dim() != 3) || w.size(-1) * 2 != K)
-    bad("w must be uint8 [E, N, K/2] or [N, K/2] with K = " + std::to_string(K));
+  if ((w.dim() != 2 && w.dim() != 3) || w.size(-1) * (fp8 ? 1 : 2) != K)
+    bad(fp8 ? "w must be float8_e4m3fn [E, N, K] or [N, K] with K = " + std::to_string(K)
+            : "w must be uint8 [E, N, K/2] or [N, K/2] with K = " + std::to_string(K));
   const int64_t E = w.dim() == 3 ? w.size(0) : 1, N = w.size(-2);
   if (grouped ? n_offsets != E + 1 : E != 1) bad("several matrices need offsets, of E + 1 elements");
   if (swiglu && N % 2) bad("swiglu needs an even number of features");
   if (M > INT32_MAX || N > INT32_MAX || E > INT32_MAX || K > INT32_MAX) bad("sizes beyond 2^31");
   const int64_t kt = ceil_div(K, 128);
   return {{(int32_t)M, (int32_t)N, (int32_t)K, (int32_t)E, swiglu, t == at::kFloat ? MOE_FP4_TYPE_F32 : MOE_FP4_TYPE_BF16},
-          bytes_of(w, "w", 0),
-          bytes_of(tensor(scales_, "w_scale"), "w_scale (tiled, by mxfp4_tile_scales)", E * ceil_div(N, 128) * kt * 512),
+          fp8 ? e4m3_of(w, "w") : bytes_of(w, "w", 0),
+          bytes_of(tensor(scales_, "w_scale"),
+                   fp8 ? "w_scale (tiled, by fp8_tile_scales)" : "w_scale (tiled, by mxfp4_tile_scales)",
+                   E * ceil_div(N, 128) * kt * 512),
           swiglu ? N / 2 : N, (M / 128 + E) * kt * 512};
 }
 
@@ -359,6 +371,57 @@ NATIVE_BEGIN(linear, 11)
   return THPVariable_Wrap(out);
 NATIVE_END
 
+// scales, N, K, swiglu, out, stream
+NATIVE_BEGIN(fp8_tile_scales, 6)
+  const at::Tensor& s = tensor(a[0], "scales");
+  const Stream st(a[5], gpu_of(a, nargs));
+  const int64_t N = whole(a[1], "N"), K = whole(a[2], "K");
+  if (N < 1 || N > INT32_MAX || K < 1 || K > INT32_MAX) bad("N and K must be a matrix's sizes");
+  const int64_t rt = ceil_div(N, 128), kt = ceil_div(K, 128);
+  if ((s.dim() != 2 && s.dim() != 3) || s.size(-2) != rt || s.size(-1) != kt)
+    bad("scales must be uint8 [E, ceil(N/128), ceil(K/128)], or without E");
+  const int64_t E = s.dim() == 3 ? s.size(0) : 1;
+  if (E > INT32_MAX) bad("sizes beyond 2^31");
+  const uint8_t* p = bytes_of(s, "scales", 0);
+  at::Tensor out;
+  if (none(a[4]))
+    out = fresh({E, rt, kt, 512}, at::kByte);
+  else
+    out = tensor(a[4], "out"), bytes_of(out, "out", E * rt * kt * 512);
+  if (!ok(g_entry.fp8_tile_scales(p, (int32_t)E, (int32_t)N, (int32_t)K, truth(a[3], "swiglu"),
+                                  static_cast<uint8_t*>(out.data_ptr()), st.handle),
+          "moe_fp4_fp8_tile_scales"))
+    return nullptr;
+  return THPVariable_Wrap(out);
+NATIVE_END
+
+// x, w, w_scale, offsets, swiglu, dtype, out, workspace, stream
+NATIVE_BEGIN(fp8_linear, 9)
+  const at::Tensor& x = tensor(a[0], "x");
+  const Stream st(a[8], gpu_of(a, nargs));
+  const Rows r = rows_of(x, "x");
+  int64_t n_off = 0;
+  const int32_t* off = indices(a[3], "offsets", &n_off);
+  const at::ScalarType t = dtype_of(a[5]);
+  const Weights W = weights_of(r.rows, r.width, a[1], a[2], off != nullptr, n_off, truth(a[4], "swiglu"), t, true);
+  const size_t need = g_entry.fp8_linear_workspace_bytes(&W.dims);
+  if (need == 0) return ok(MOE_FP4_ERR_UNSUPPORTED, "moe_fp4_fp8_linear"), nullptr;
+  void* ws = nullptr;
+  c10::DataPtr scratch;
+  if (!none(a[7])) {
+    ws = bytes_of(tensor(a[7], "workspace"), "workspace", (int64_t)need);
+  } else if (off != nullptr || r.rows > MOE_FP4_MXFP4_FEW_ROWS) {
+    scratch = c10::GetAllocator(c10::kCUDA)->allocate(need);
+    ws = scratch.get();
+  }
+  const at::Tensor out = result(a[6], r.rows, W.n_out, t, "out");
+  if (!ok(g_entry.fp8_linear(&W.dims, r.p, r.type, r.rows, r.stride, off, W.w, W.scales, out.data_ptr(), ws, need,
+                             st.handle),
+          "moe_fp4_fp8_linear"))
+    return nullptr;
+  return THPVariable_Wrap(out);
+NATIVE_END
+
 void weight_of(PyObject* o, const char* what, int64_t d, const void** p, int32_t* type) {
   if (none(o)) return;
   const at::Tensor& w = tensor(o, what);
@@ -478,6 +541,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(bind),   METHOD(quantize), METHOD(dequantize), METHOD(tile_scales),
                          METHOD(matmul), METHOD(linear),   METHOD(rms_norm),   METHOD(block_residual),
+                         METHOD(fp8_tile_scales), METHOD(fp8_linear),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -435,6 +435,40 @@ int moe_fp4_mxfp4_linear(const moe_fp4_mm_dims* dims, const void* x, int x_type,
                          const uint8_t* w_scales, void* y, void* workspace, size_t workspace_bytes,
                          void* cuda_stream);
 
+/* ---- Products with weights in 8-bit floating point ------------------------
+ * E4M3 codes (OCP 8-bit, no infinities), one E8M0 scale for each 128 x 128 of a
+ * weight matrix and for each 128 elements of a row of x, which is quantised in
+ * the call: for 128 consecutive elements, with amax their largest magnitude,
+ *   scale byte  s = e + 127, e the least integer >= -127 with amax <= 448 2^e
+ *               (0 for an all-zero block)
+ *   codes       E4M3 of x / 2^e, rounded to nearest (ties to the even code)
+ * A block holding an infinity or a NaN becomes NaN.  K need not be a multiple
+ * of 128: the last block of a row is then a shorter one. */
+
+/* Weight scales [E, ceil(N/128), ceil(K/128)] in the product's layout, once when
+ * weights are loaded: uint8 [E][ceil(N/128)][ceil(K/128)][512], tiles as for
+ * MXFP4 with the same byte for the four times 32 elements of a block, zeros past
+ * the end.  swiglu = 1: for a product with SwiGLU (N = 2I, gate rows then up
+ * rows); N and K as in moe_fp4_mm_dims, tiled 16-byte aligned. */
+int moe_fp4_fp8_tile_scales(const uint8_t* scales, int32_t E, int32_t N, int32_t K, int swiglu, uint8_t* tiled,
+                            void* cuda_stream);
+
+/* Device workspace of moe_fp4_fp8_linear (codes and scales of the quantised
+ * rows; 256-byte aligned base); 0 for unsupported sizes.  None is used by at most
+ * MOE_FP4_MXFP4_FEW_ROWS rows without offsets: it may be NULL. */
+size_t moe_fp4_fp8_linear_workspace_bytes(const moe_fp4_mm_dims* dims);
+
+/* y[m, n] = sum_K x_q[m, K] w_e[n, K], with SwiGLU, groups (offsets), sizes and y
+ * as for moe_fp4_mxfp4_matmul: tcgen05.mma kind::mxf8f6f4, products of codes and
+ * scales exact, fp32 sums, one rounding to y_type; the same call gives the same
+ * bits.
+ *   x         bf16 or fp32, x_rows >= M rows, row r at element r * x_stride
+ *   w         E4M3 codes [E, N, K], 16-byte aligned
+ *   w_scales  of moe_fp4_fp8_tile_scales, 16-byte aligned */
+int moe_fp4_fp8_linear(const moe_fp4_mm_dims* dims, const void* x, int x_type, int64_t x_rows, int64_t x_stride,
+                       const int32_t* offsets, const uint8_t* w, const uint8_t* w_scales, void* y, void* workspace,
+                       size_t workspace_bytes, void* cuda_stream);
+
 /* The end of a block in one pass over its rows.  With b = y (+ y2):
  *   post_norm:  b = b * rsqrt(mean(b^2) + eps)
  *   b = b * post_weight                      (NULL: 1)
@@ -489,8 +523,8 @@ int moe_fp4_ops_check(void* cuda_stream);
  *                                 loads its first weight stage.
  * Nothing faults, traps or hangs: the waiting threads give up, the outputs of
  * that call are incomplete, and moe_fp4_check reports MOE_FP4_ERR_DEVICE.
- * The products (moe_fp4_mxfp4_matmul, moe_fp4_mxfp4_linear) take
- * MOE_FP4_FAULT_TC_TOKEN_TILE too (the first CTA, or pair, never loads its first
+ * The products (moe_fp4_mxfp4_matmul, moe_fp4_mxfp4_linear, moe_fp4_fp8_linear)
+ * take MOE_FP4_FAULT_TC_TOKEN_TILE too (the first CTA, or pair, never loads its first
  * stage; moe_fp4_ops_check reports it), and the limit; so does moe_fp4_block_norm
  * in its form for many rows (the first CTA never loads its first row).
  * MOE_FP4_FAULT_NONE (wait_limit_us ignored) restores normal operation.
