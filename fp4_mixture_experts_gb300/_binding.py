@@ -52,6 +52,8 @@ EXPORTED_SYMBOLS = (
     "moe_fp4_fp8_tile_scales",
     "moe_fp4_fp8_linear_workspace_bytes",
     "moe_fp4_fp8_linear",
+    "moe_fp4_latent_decode_workspace_bytes",
+    "moe_fp4_latent_decode",
 )
 
 
@@ -129,6 +131,8 @@ def load_library():
             ("fp8_tile_scales", [P, i32, i32, i32, i32, P, P], i32),
             ("fp8_linear_workspace_bytes", [P], size),
             ("fp8_linear", [P, P, i32, i64, i64, P, P, P, P, P, size, P], i32),
+            ("latent_decode_workspace_bytes", [i32], size),
+            ("latent_decode", [P, P, size, P], i32),
             ("ops_check", [P], i32)):
         fn = getattr(lib, "moe_fp4_" + name)
         fn.argtypes, fn.restype = args, res

@@ -34,6 +34,12 @@ class BlockNormArgs(ctypes.Structure):
                                                 "normed")])
 
 
+class LatentDecodeArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "H", "page", "pages", "width")] + [("scale", ctypes.c_float)] +
+                [(n, ctypes.c_int64) for n in ("q_stride", "q_head_stride", "table_stride")] +
+                [(n, ctypes.c_void_p) for n in ("q", "cache", "table", "lengths", "out")])
+
+
 def _raise(status, entry):
     raise MoeFp4Error(status, entry)
 
@@ -53,7 +59,7 @@ class _Unloaded:
         native.bind(tuple(ctypes.cast(getattr(lib, "moe_fp4_" + n), ctypes.c_void_p).value for n in (
             "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_tile_scales", "mxfp4_matmul", "mxfp4_linear",
             "mxfp4_linear_workspace_bytes", "mxfp4_gathered_workspace_bytes", "block_norm", "fp8_tile_scales",
-            "fp8_linear_workspace_bytes", "fp8_linear")), _raise)
+            "fp8_linear_workspace_bytes", "fp8_linear", "latent_decode_workspace_bytes", "latent_decode")), _raise)
         _native, _BF16 = native, torch.bfloat16
         return getattr(native, name)
 
@@ -137,6 +143,23 @@ def fp8_linear(x, w, w_scale, offsets=None, swiglu: bool = False, dtype=None, ou
     were.  Returns [M, N], or with swiglu silu(first half) * second half [M, N/2]: bf16, or dtype=torch.float32."""
     f = _native.fp8_linear
     return f(x, w, w_scale, offsets, swiglu, dtype or _BF16, out, workspace, _handle(stream))
+
+
+def latent_decode_workspace_bytes(H: int) -> int:
+    """Bytes of latent_decode's workspace on the current device."""
+    return int(load_library().moe_fp4_latent_decode_workspace_bytes(H))
+
+
+def latent_decode(q, cache, block_table, lengths, scale, out=None, workspace=None, stream=None):
+    """Latent attention of one new token a sequence in its absorbed form, over a paged cache: bf16 [B, H, 512],
+
+      out[b, h] = sum_j softmax(scale q[b, h] . c_j) c_j[:512],   j < lengths[b]
+
+    q bf16 [B, H, 576] (latent part, rotary part; heads that start on 16 bytes), cache bf16 [pages, page, 576] (page a
+    multiple of 16), block_table int32 [B, width]: the pages of each sequence, lengths int32 [B].  What the cache holds
+    behind a sequence's end is not used; a sequence of no tokens gets zeros.  Lengths that the table does not hold and
+    pages outside the cache are reported by ops_check."""
+    return _native.latent_decode(q, cache, block_table, lengths, scale, out, workspace, _handle(stream))
 
 
 def rms_norm(x, weight=None, eps: float = 1e-6, out=None, stream=None):

@@ -38,6 +38,8 @@ struct Entry {
   decltype(&moe_fp4_fp8_tile_scales) fp8_tile_scales;
   decltype(&moe_fp4_fp8_linear_workspace_bytes) fp8_linear_workspace_bytes;
   decltype(&moe_fp4_fp8_linear) fp8_linear;
+  decltype(&moe_fp4_latent_decode_workspace_bytes) latent_decode_workspace_bytes;
+  decltype(&moe_fp4_latent_decode) latent_decode;
 } g_entry;
 PyObject* g_raise = nullptr;  // called with (status, entry point); raises
 
@@ -516,6 +518,83 @@ NATIVE_BEGIN(block_residual, 14)
   return both;
 NATIVE_END
 
+const at::Tensor& bf16_of(PyObject* o, const char* what, int64_t dim) {
+  const at::Tensor& t = tensor(o, what);
+  if (t.scalar_type() != at::kBFloat16 || !t.is_cuda() || t.dim() != dim)
+    bad(std::string(what) + " must be a bf16 GPU tensor of " + std::to_string(dim) + " dimensions");
+  return t;
+}
+
+// [T, H, W]: the last dimension contiguous, rows that start on 16 bytes; the strides of a dimension of one element do
+// not matter
+struct Heads {
+  int64_t rows, heads, width, stride, head_stride;
+  void* p;
+};
+
+Heads heads_of(PyObject* o, const char* what, int64_t width) {
+  const at::Tensor& t = bf16_of(o, what, 3);
+  if (t.size(2) != width) bad(std::string(what) + " must have " + std::to_string(width) + " elements a head");
+  const int64_t T = t.size(0), H = t.size(1);
+  Heads h{T, H, width, T > 1 ? t.stride(0) : H * width, H > 1 ? t.stride(1) : width, t.data_ptr()};
+  if (T == 0 || H == 0) return h;
+  if (t.stride(2) != 1 || h.stride < width || h.head_stride < width || h.stride % 8 || h.head_stride % 8 ||
+      reinterpret_cast<uintptr_t>(h.p) % 16)
+    bad(std::string(what) + " must have contiguous heads, apart, that start on 16 bytes");
+  return h;
+}
+
+const int32_t* table_of(PyObject* o, const char* what, int64_t rows, int64_t* width, int64_t* stride) {
+  const at::Tensor& t = tensor(o, what);
+  if (t.scalar_type() != at::kInt || !t.is_cuda() || t.dim() != 2 || t.size(0) != rows ||
+      (rows > 0 && ((t.stride(1) != 1 && t.size(1) > 1) || (t.stride(0) < t.size(1) && rows > 1))))
+    bad(std::string(what) + " must be an int32 GPU tensor of " + std::to_string(rows) + " separate, contiguous rows");
+  *width = t.size(1);
+  *stride = rows > 1 ? t.stride(0) : t.size(1);
+  return static_cast<const int32_t*>(t.data_ptr());
+}
+
+// q, cache, block_table, lengths, scale, out, workspace, stream
+NATIVE_BEGIN(latent_decode, 8)
+  const Stream st(a[7], gpu_of(a, nargs));
+  const Heads q = heads_of(a[0], "q", 576);
+  const at::Tensor& c = bf16_of(a[1], "cache", 3);
+  if (c.size(2) != 576 || !c.is_contiguous()) bad("cache must be contiguous [pages, page, 576]");
+  int64_t width, n = 0;
+  moe_fp4_latent_decode_args d{};
+  d.table = table_of(a[2], "block_table", q.rows, &width, &d.table_stride);
+  if (none(a[3])) bad("lengths must be a contiguous 1-D int32 GPU tensor");
+  d.lengths = indices(a[3], "lengths", &n);
+  if (n != q.rows) bad("lengths must have an element for each sequence");
+  if (q.rows > INT32_MAX || q.heads > INT32_MAX || c.size(0) > INT32_MAX || c.size(1) > INT32_MAX || width > INT32_MAX)
+    bad("sizes beyond 2^31");
+  d.B = (int32_t)q.rows, d.H = (int32_t)q.heads, d.width = (int32_t)width;
+  d.pages = (int32_t)c.size(0), d.page = (int32_t)c.size(1);
+  d.scale = (float)real(a[4], "scale");
+  d.q = q.p, d.q_stride = q.stride, d.q_head_stride = q.head_stride, d.cache = c.data_ptr();
+  const size_t need = g_entry.latent_decode_workspace_bytes(d.H);
+  if (need == 0) bad("q must have 1 to " + std::to_string(MOE_FP4_LATENT_MAX_HEADS) + " heads");
+  void* ws;
+  c10::DataPtr scratch;
+  if (!none(a[6])) {
+    ws = bytes_of(tensor(a[6], "workspace"), "workspace", (int64_t)need);
+  } else {
+    scratch = c10::GetAllocator(c10::kCUDA)->allocate(need);
+    ws = scratch.get();
+  }
+  at::Tensor out;
+  if (none(a[5])) {
+    out = fresh({q.rows, q.heads, 512}, at::kBFloat16);
+  } else {
+    out = bf16_of(a[5], "out", 3);
+    if (!out.is_contiguous() || out.size(0) != q.rows || out.size(1) != q.heads || out.size(2) != 512)
+      bad("out must be contiguous [B, H, 512]");
+  }
+  d.out = out.data_ptr();
+  if (!ok(g_entry.latent_decode(&d, ws, need, st.handle), "moe_fp4_latent_decode")) return nullptr;
+  return THPVariable_Wrap(out);
+NATIVE_END
+
 // addresses (in Entry's order), raise
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   constexpr Py_ssize_t n = sizeof(Entry) / sizeof(void*);
@@ -541,7 +620,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(bind),   METHOD(quantize), METHOD(dequantize), METHOD(tile_scales),
                          METHOD(matmul), METHOD(linear),   METHOD(rms_norm),   METHOD(block_residual),
-                         METHOD(fp8_tile_scales), METHOD(fp8_linear),
+                         METHOD(fp8_tile_scales), METHOD(fp8_linear), METHOD(latent_decode),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

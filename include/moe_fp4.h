@@ -469,6 +469,46 @@ int moe_fp4_fp8_linear(const moe_fp4_mm_dims* dims, const void* x, int x_type, i
                        const int32_t* offsets, const uint8_t* w, const uint8_t* w_scales, void* y, void* workspace,
                        size_t workspace_bytes, void* cuda_stream);
 
+/* ---- Latent attention ------------------------------------------------------
+ * Attention whose keys and values come from one latent vector a token (512
+ * elements) and one rotary key that all heads share (64). */
+#define MOE_FP4_LATENT_MAX_HEADS 1024
+
+/* Absorbed form, one new token a sequence, over a paged cache of the latent
+ * vectors: with c_j the 576 elements of token j of a sequence,
+ *   s_j = scale q . c_j,   out = sum_j softmax(s)_j c_j[0 .. 511]
+ * for j < lengths[b]; a sequence of no tokens gets zeros.  fp32 scores,
+ * statistics and sums; P is rounded to bf16 for its product, the result once to
+ * bf16.  What the cache holds behind a sequence's end is not used, whatever it
+ * is; its values up to there are to be finite (an infinity or a NaN reaches every
+ * head of the sequence).  The same call gives the same bits.
+ *   q        bf16 [B, H, 576] (latent part, rotary part), element strides
+ *            q_stride and q_head_stride: multiples of 8, base 16-byte aligned
+ *   cache    bf16 [pages, page, 576], contiguous, 16-byte aligned; page a multiple
+ *            of 16 (64 and its multiples are read in one copy a tile)
+ *   table    int32 [B, width], row stride table_stride: page of tokens [i page,
+ *            (i + 1) page) of the sequence; entries behind its end are not read
+ *   lengths  int32 [B], tokens in the cache (the new one included)
+ *   out      bf16 [B, H, 512], contiguous, 16-byte aligned
+ * A length below 0 or above width * page is taken as the nearest of the two, a page
+ * outside the cache reads as zeros; both set error bit 1 (moe_fp4_ops_check).
+ * pages * page and width * page below 2^31. */
+typedef struct moe_fp4_latent_decode_args {
+  int32_t B, H, page, pages, width;  /* B >= 0; H 1 .. 1024 */
+  float scale;
+  int64_t q_stride, q_head_stride, table_stride;
+  const void *q, *cache;
+  const int32_t *table, *lengths;
+  void* out;
+} moe_fp4_latent_decode_args;
+
+/* Device workspace of moe_fp4_latent_decode (the pieces of sequences that several
+ * SMs share; 256-byte aligned base), for the current device; 0 for unsupported
+ * sizes.  It holds nothing between calls; calls that may overlap need one each. */
+size_t moe_fp4_latent_decode_workspace_bytes(int32_t H);
+int moe_fp4_latent_decode(const moe_fp4_latent_decode_args* args, void* workspace, size_t workspace_bytes,
+                          void* cuda_stream);
+
 /* The end of a block in one pass over its rows.  With b = y (+ y2):
  *   post_norm:  b = b * rsqrt(mean(b^2) + eps)
  *   b = b * post_weight                      (NULL: 1)
@@ -524,8 +564,8 @@ int moe_fp4_ops_check(void* cuda_stream);
  * Nothing faults, traps or hangs: the waiting threads give up, the outputs of
  * that call are incomplete, and moe_fp4_check reports MOE_FP4_ERR_DEVICE.
  * The products (moe_fp4_mxfp4_matmul, moe_fp4_mxfp4_linear, moe_fp4_fp8_linear)
- * take MOE_FP4_FAULT_TC_TOKEN_TILE too (the first CTA, or pair, never loads its first
- * stage; moe_fp4_ops_check reports it), and the limit; so does moe_fp4_block_norm
+ * and moe_fp4_latent_decode take MOE_FP4_FAULT_TC_TOKEN_TILE too (the first CTA, or
+ * pair, never loads its first stage; moe_fp4_ops_check reports it), and the limit; so does moe_fp4_block_norm
  * in its form for many rows (the first CTA never loads its first row).
  * MOE_FP4_FAULT_NONE (wait_limit_us ignored) restores normal operation.
  * Returns MOE_FP4_ERR_INVALID_ARG for an unknown site or a zero limit. */

@@ -6,9 +6,8 @@ Error bound: codes and scales are exact, and so is every product of two values
 An instruction adds 32 aligned products to the accumulator, K / 32 instructions
 follow one another: with each of these additions off by at most 2^-23 of S = sum
 |a w|, an fp32 result is within (K / 32 + 32) 2^-23 S of the definition, and the
-sum over a cluster of up to 8 CTAs adds 8 roundings; bf16 adds 2^-8 |y| (half a
-step, 2^-9, and the fp32 error's way over a rounding boundary).  SwiGLU: as for
-the MXFP4 products.
+sum over a cluster of up to 8 CTAs adds 8 roundings; bf16 adds half a step, 2^-8
+of the value with its fp32 error.  SwiGLU: as for the MXFP4 products.
 """
 import numpy as np
 import pytest
