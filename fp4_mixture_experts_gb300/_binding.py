@@ -54,6 +54,7 @@ EXPORTED_SYMBOLS = (
     "moe_fp4_fp8_linear",
     "moe_fp4_latent_decode_workspace_bytes",
     "moe_fp4_latent_decode",
+    "moe_fp4_latent_attention",
 )
 
 
@@ -133,6 +134,7 @@ def load_library():
             ("fp8_linear", [P, P, i32, i64, i64, P, P, P, P, P, size, P], i32),
             ("latent_decode_workspace_bytes", [i32], size),
             ("latent_decode", [P, P, size, P], i32),
+            ("latent_attention", [P, P], i32),
             ("ops_check", [P], i32)):
         fn = getattr(lib, "moe_fp4_" + name)
         fn.argtypes, fn.restype = args, res

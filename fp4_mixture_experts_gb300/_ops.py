@@ -34,6 +34,13 @@ class BlockNormArgs(ctypes.Structure):
                                                 "normed")])
 
 
+class LatentAttentionArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "H", "causal")] + [("scale", ctypes.c_float)] +
+                [(n, ctypes.c_int64) for n in ("Tq", "Tk", "q_stride", "q_head_stride", "kv_stride", "kv_head_stride",
+                                               "rope_stride")] +
+                [(n, ctypes.c_void_p) for n in ("q", "kv", "k_rope", "q_offsets", "k_offsets", "out")])
+
+
 class LatentDecodeArgs(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_int32) for n in ("B", "H", "page", "pages", "width")] + [("scale", ctypes.c_float)] +
                 [(n, ctypes.c_int64) for n in ("q_stride", "q_head_stride", "table_stride")] +
@@ -59,7 +66,8 @@ class _Unloaded:
         native.bind(tuple(ctypes.cast(getattr(lib, "moe_fp4_" + n), ctypes.c_void_p).value for n in (
             "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_tile_scales", "mxfp4_matmul", "mxfp4_linear",
             "mxfp4_linear_workspace_bytes", "mxfp4_gathered_workspace_bytes", "block_norm", "fp8_tile_scales",
-            "fp8_linear_workspace_bytes", "fp8_linear", "latent_decode_workspace_bytes", "latent_decode")), _raise)
+            "fp8_linear_workspace_bytes", "fp8_linear", "latent_decode_workspace_bytes", "latent_decode",
+            "latent_attention")), _raise)
         _native, _BF16 = native, torch.bfloat16
         return getattr(native, name)
 
@@ -160,6 +168,19 @@ def latent_decode(q, cache, block_table, lengths, scale, out=None, workspace=Non
     behind a sequence's end is not used; a sequence of no tokens gets zeros.  Lengths that the table does not hold and
     pages outside the cache are reported by ops_check."""
     return _native.latent_decode(q, cache, block_table, lengths, scale, out, workspace, _handle(stream))
+
+
+def latent_attention(q, kv, k_rope, q_offsets, k_offsets, scale, causal: bool = True, out=None, stream=None):
+    """Latent attention in its expanded form for the new tokens of a ragged batch: bf16 [Tq, H, 128],
+
+      out[i, h] = sum_j softmax(scale (q[i, h, :128] . kv[j, h, :128] + q[i, h, 128:] . k_rope[j])) kv[j, h, 128:]
+
+    q bf16 [Tq, H, 192], kv bf16 [Tk, H, 256] (keys and values of a head side by side, as the latent vectors' up
+    projection writes them), k_rope bf16 [Tk, 64]; heads and rows start on 16 bytes.  Sequence b has queries
+    [q_offsets[b], q_offsets[b+1]) and keys [k_offsets[b], k_offsets[b+1]) (int32 [B + 1]); causal: its last query sees
+    all keys, each one before it one less.  A query that sees no key gets zeros, queries of no sequence are left as
+    they were.  Values are to be finite; scale is positive."""
+    return _native.latent_attention(q, kv, k_rope, q_offsets, k_offsets, scale, causal, out, _handle(stream))
 
 
 def rms_norm(x, weight=None, eps: float = 1e-6, out=None, stream=None):

@@ -40,6 +40,7 @@ struct Entry {
   decltype(&moe_fp4_fp8_linear) fp8_linear;
   decltype(&moe_fp4_latent_decode_workspace_bytes) latent_decode_workspace_bytes;
   decltype(&moe_fp4_latent_decode) latent_decode;
+  decltype(&moe_fp4_latent_attention) latent_attention;
 } g_entry;
 PyObject* g_raise = nullptr;  // called with (status, entry point); raises
 
@@ -595,6 +596,42 @@ NATIVE_BEGIN(latent_decode, 8)
   return THPVariable_Wrap(out);
 NATIVE_END
 
+// q, kv, k_rope, q_offsets, k_offsets, scale, causal, out, stream
+NATIVE_BEGIN(latent_attention, 9)
+  const Stream st(a[8], gpu_of(a, nargs));
+  const Heads q = heads_of(a[0], "q", 192), kv = heads_of(a[1], "kv", 256);
+  const at::Tensor& rope = bf16_of(a[2], "k_rope", 2);
+  if (kv.heads != q.heads) bad("kv must have q's heads");
+  if (rope.size(0) != kv.rows || rope.size(1) != 64) bad("k_rope must be [Tk, 64]");
+  moe_fp4_latent_attention_args d{};
+  d.rope_stride = kv.rows > 1 ? rope.stride(0) : 64;
+  if (kv.rows > 0 && (rope.stride(1) != 1 || d.rope_stride < 64 || d.rope_stride % 8 ||
+                      reinterpret_cast<uintptr_t>(rope.data_ptr()) % 16))
+    bad("k_rope must have contiguous rows, apart, that start on 16 bytes");
+  int64_t nq = 0, nk = 0;
+  if (none(a[3]) || none(a[4])) bad("q_offsets and k_offsets must be contiguous 1-D int32 GPU tensors");
+  d.q_offsets = indices(a[3], "q_offsets", &nq), d.k_offsets = indices(a[4], "k_offsets", &nk);
+  if (nq < 1 || nq != nk) bad("q_offsets and k_offsets must have B + 1 elements each");
+  if (q.heads < 1 || q.heads > MOE_FP4_LATENT_MAX_HEADS)
+    bad("q must have 1 to " + std::to_string(MOE_FP4_LATENT_MAX_HEADS) + " heads");
+  if (nq > INT32_MAX) bad("sizes beyond 2^31");
+  d.B = (int32_t)(nq - 1), d.H = (int32_t)q.heads, d.Tq = q.rows, d.Tk = kv.rows;
+  d.scale = (float)real(a[5], "scale"), d.causal = truth(a[6], "causal");
+  d.q = q.p, d.q_stride = q.stride, d.q_head_stride = q.head_stride;
+  d.kv = kv.p, d.kv_stride = kv.stride, d.kv_head_stride = kv.head_stride, d.k_rope = rope.data_ptr();
+  at::Tensor out;
+  if (none(a[7])) {
+    out = fresh({q.rows, q.heads, 128}, at::kBFloat16);
+  } else {
+    out = bf16_of(a[7], "out", 3);
+    if (!out.is_contiguous() || out.size(0) != q.rows || out.size(1) != q.heads || out.size(2) != 128)
+      bad("out must be contiguous [Tq, H, 128]");
+  }
+  d.out = out.data_ptr();
+  if (!ok(g_entry.latent_attention(&d, st.handle), "moe_fp4_latent_attention")) return nullptr;
+  return THPVariable_Wrap(out);
+NATIVE_END
+
 // addresses (in Entry's order), raise
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   constexpr Py_ssize_t n = sizeof(Entry) / sizeof(void*);
@@ -620,7 +657,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(bind),   METHOD(quantize), METHOD(dequantize), METHOD(tile_scales),
                          METHOD(matmul), METHOD(linear),   METHOD(rms_norm),   METHOD(block_residual),
-                         METHOD(fp8_tile_scales), METHOD(fp8_linear), METHOD(latent_decode),
+                         METHOD(fp8_tile_scales), METHOD(fp8_linear), METHOD(latent_decode), METHOD(latent_attention),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

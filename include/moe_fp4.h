@@ -509,6 +509,33 @@ size_t moe_fp4_latent_decode_workspace_bytes(int32_t H);
 int moe_fp4_latent_decode(const moe_fp4_latent_decode_args* args, void* workspace, size_t workspace_bytes,
                           void* cuda_stream);
 
+/* Expanded form, for the new tokens of a ragged batch: sequence b has queries
+ * [q_offsets[b], q_offsets[b+1]) and keys [k_offsets[b], k_offsets[b+1]) (those of
+ * its cached tokens and of the new ones), nq and nk of them; for query i
+ *   s_j = scale (q_i[0 .. 127] . kn_j + q_i[128 .. 191] . kr_j)
+ *   out_i = sum_j softmax(s)_j v_j        over j < nk; causal: j <= i + nk - nq
+ * for every head; a query that sees no key gets zeros, queries of no sequence are
+ * left as they were.  fp32 scores, statistics and sums; P is rounded to bf16 for
+ * its product, the result once to bf16.  Values (v) are to be finite; what a
+ * sequence's neighbours hold does not reach it.  The same call gives the same bits.
+ *   q         bf16 [Tq, H, 192], element strides q_stride, q_head_stride
+ *   kv        bf16 [Tk, H, 256]: kn and v of a head side by side
+ *   k_rope    bf16 [Tk, 64], the heads' shared rotary key kr
+ *   q_offsets, k_offsets  int32 [B + 1] on the device, not decreasing (taken into
+ *             [0, Tq] and [0, Tk])
+ *   out       bf16 [Tq, H, 128], contiguous
+ * All bases 16-byte aligned, strides multiples of 8 elements; scale positive. */
+typedef struct moe_fp4_latent_attention_args {
+  int32_t B, H, causal;              /* B >= 0; H 1 .. 1024 */
+  float scale;
+  int64_t Tq, Tk;
+  int64_t q_stride, q_head_stride, kv_stride, kv_head_stride, rope_stride;
+  const void *q, *kv, *k_rope;
+  const int32_t *q_offsets, *k_offsets;
+  void* out;
+} moe_fp4_latent_attention_args;
+int moe_fp4_latent_attention(const moe_fp4_latent_attention_args* args, void* cuda_stream);
+
 /* The end of a block in one pass over its rows.  With b = y (+ y2):
  *   post_norm:  b = b * rsqrt(mean(b^2) + eps)
  *   b = b * post_weight                      (NULL: 1)
@@ -564,7 +591,7 @@ int moe_fp4_ops_check(void* cuda_stream);
  * Nothing faults, traps or hangs: the waiting threads give up, the outputs of
  * that call are incomplete, and moe_fp4_check reports MOE_FP4_ERR_DEVICE.
  * The products (moe_fp4_mxfp4_matmul, moe_fp4_mxfp4_linear, moe_fp4_fp8_linear)
- * and moe_fp4_latent_decode take MOE_FP4_FAULT_TC_TOKEN_TILE too (the first CTA, or
+ * and latent attention take MOE_FP4_FAULT_TC_TOKEN_TILE too (the first CTA, or
  * pair, never loads its first stage; moe_fp4_ops_check reports it), and the limit; so does moe_fp4_block_norm
  * in its form for many rows (the first CTA never loads its first row).
  * MOE_FP4_FAULT_NONE (wait_limit_us ignored) restores normal operation.

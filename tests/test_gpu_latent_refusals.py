@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import fp4_mixture_experts_gb300 as moe
-from tests.test_gpu_ops_refusals import F32, I32, U8, z
+from tests.test_gpu_ops_refusals import BOTH, F32, I32, U8, z
 
 pytestmark = pytest.mark.gpu
 
@@ -15,7 +15,37 @@ def decode(**kw):
     return moe.latent_decode(**{**t, **kw})
 
 
+def attention(**kw):
+    t = {"q": z(8, 4, 192), "kv": z(9, 4, 256), "k_rope": z(9, 64), "q_offsets": z(3, dtype=I32), "k_offsets": z(3, dtype=I32),
+         "scale": 0.1}
+    return moe.latent_attention(**{**t, **kw})
+
+
 REFUSED = {
+    "attention: q of fp32": lambda: attention(q=z(8, 4, 192, dtype=F32)),
+    "attention: q's width": lambda: attention(q=z(8, 4, 128)),
+    "attention: q of two dimensions": lambda: attention(q=z(32, 192)),
+    "attention: no heads": lambda: attention(q=z(8, 0, 192), kv=z(9, 0, 256)),
+    "attention: many heads": lambda: attention(q=z(8, 1025, 192), kv=z(9, 1025, 256)),
+    "attention: other heads": lambda: attention(kv=z(9, 1, 256)),
+    "attention: one head for all": lambda: attention(kv=z(9, 1, 256).expand(9, 4, 256)),
+    "attention: q off 16 bytes": lambda: attention(q=z(8, 4, 196)[:, :, 4:]),
+    "attention: q's columns apart": lambda: attention(q=z(8, 192, 4).transpose(1, 2)),
+    "attention: kv's width": lambda: attention(kv=z(9, 4, 320)),
+    "attention: k_rope's rows": lambda: attention(k_rope=z(8, 64)),
+    "attention: k_rope's width": lambda: attention(k_rope=z(9, 32)),
+    "attention: k_rope of heads": lambda: attention(k_rope=z(9, 4, 64)),
+    "attention: k_rope off 16 bytes": lambda: attention(k_rope=z(9, 68)[:, 4:]),
+    "attention: k_rope's columns apart": lambda: attention(k_rope=z(64, 9).t()),
+    "attention: offsets' number": lambda: attention(q_offsets=z(2, dtype=I32)),
+    "attention: no offsets' elements": lambda: attention(q_offsets=z(0, dtype=I32), k_offsets=z(0, dtype=I32)),
+    "attention: offsets' type": lambda: attention(k_offsets=z(3, dtype=torch.int64)),
+    "attention: no offsets": lambda: attention(q_offsets=None),
+    "attention: scale": lambda: attention(scale=None),
+    "attention: causal neither": lambda: attention(causal=BOTH),
+    "attention: out's shape": lambda: attention(out=z(8, 4, 192)),
+    "attention: out's type": lambda: attention(out=z(8, 4, 128, dtype=F32)),
+    "attention: out's strides": lambda: attention(out=z(4, 8, 128).transpose(0, 1)),
     "decode: q of fp32": lambda: decode(q=z(2, 16, 576, dtype=F32)),
     "decode: q's width": lambda: decode(q=z(2, 16, 512)),
     "decode: q of two dimensions": lambda: decode(q=z(32, 576)),
@@ -54,7 +84,8 @@ def test_refused(name):
 
 def test_sizes_that_the_library_refuses():
     for call in (lambda: decode(cache=z(8, 40, 576)), lambda: decode(cache=z(8, 8, 576)), lambda: decode(cache=z(0, 64, 576)),
-                 lambda: decode(block_table=z(2, 0, dtype=I32)), lambda: decode(scale=float("nan"))):
+                 lambda: decode(block_table=z(2, 0, dtype=I32)), lambda: decode(scale=float("nan")),
+                 lambda: attention(scale=0.0), lambda: attention(scale=-1.0), lambda: attention(scale=float("nan"))):
         with pytest.raises(moe.MoeFp4Error):
             call()
     moe.ops_check()

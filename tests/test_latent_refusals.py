@@ -12,7 +12,7 @@ from torch._subclasses.fake_tensor import FakeTensorMode
 
 import fp4_mixture_experts_gb300 as moe
 from fp4_mixture_experts_gb300 import build as build_mod
-from fp4_mixture_experts_gb300._ops import LatentDecodeArgs
+from fp4_mixture_experts_gb300._ops import LatentAttentionArgs, LatentDecodeArgs
 from tests.test_early_launch_loads import CSRC, code
 
 FAKE = 0x100000  # never dereferenced
@@ -51,6 +51,29 @@ def test_decode(lib):
     assert call(B=0, q=None, cache=None, work=None) == 0
 
 
+def test_attention(lib):
+    base = dict(B=2, H=16, causal=1, scale=0.1, Tq=40, Tk=60, q_stride=16 * 192, q_head_stride=192, kv_stride=16 * 256,
+                kv_head_stride=256, rope_stride=64, q=FAKE, kv=FAKE, k_rope=FAKE, q_offsets=FAKE, k_offsets=FAKE, out=FAKE)
+
+    def call(**kw):
+        a = LatentAttentionArgs()
+        for k, v in {**base, **kw}.items():
+            setattr(a, k, v)
+        return lib.moe_fp4_latent_attention(ctypes.byref(a), None)
+
+    assert lib.moe_fp4_latent_attention(None, None) == -1
+    for bad in (dict(B=-1), dict(H=0), dict(H=1025), dict(causal=2), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
+                dict(scale=float("inf")), dict(Tq=-1), dict(Tk=-1), dict(q=None), dict(kv=None), dict(k_rope=None),
+                dict(q_offsets=None), dict(k_offsets=None), dict(out=None), dict(q=FAKE + 8), dict(kv=FAKE + 8),
+                dict(k_rope=FAKE + 8), dict(out=FAKE + 8), dict(q_offsets=FAKE + 2), dict(k_offsets=FAKE + 2), dict(q_stride=188),
+                dict(q_stride=196), dict(q_head_stride=184), dict(kv_stride=248), dict(kv_head_stride=260), dict(rope_stride=56),
+                dict(rope_stride=66), dict(q_stride=1 << 39)):
+        assert call(**bad) == -1, bad
+    for big in (dict(Tq=2**31), dict(Tk=2**31), dict(Tq=2**31 - 1000, H=1024), dict(B=2**31 - 1, Tq=2**30)):
+        assert call(**big) == -2, big
+    assert call(Tq=0, q=None, kv=None, out=None) == 0 and call(B=0, q=None) == 0
+
+
 def on(device, *shape, dtype=BF):
     with FakeTensorMode():
         return torch.empty(*shape, dtype=dtype, device=device)
@@ -62,8 +85,19 @@ def decode(**other):
     return moe.latent_decode(**{**t, **other})
 
 
+def attention(**other):
+    t = {"q": on("cuda:0", 8, 4, 192), "kv": on("cuda:0", 9, 4, 256), "k_rope": on("cuda:0", 9, 64), "scale": 0.1,
+         "q_offsets": on("cuda:0", 3, dtype=I32), "k_offsets": on("cuda:0", 3, dtype=I32)}
+    return moe.latent_attention(**{**t, **other})
+
+
 def calls(o):
     return {
+        "attention kv": lambda: attention(kv=on(o, 9, 4, 256)),
+        "attention k_rope": lambda: attention(k_rope=on(o, 9, 64)),
+        "attention q_offsets": lambda: attention(q_offsets=on(o, 3, dtype=I32)),
+        "attention k_offsets": lambda: attention(k_offsets=on(o, 3, dtype=I32)),
+        "attention out": lambda: attention(out=on(o, 8, 4, 128)),
         "decode cache": lambda: decode(cache=on(o, 8, 64, 576)),
         "decode block_table": lambda: decode(block_table=on(o, 2, 4, dtype=I32)),
         "decode lengths": lambda: decode(lengths=on(o, 2, dtype=I32)),
