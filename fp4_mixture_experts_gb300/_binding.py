@@ -55,6 +55,7 @@ EXPORTED_SYMBOLS = (
     "moe_fp4_latent_decode_workspace_bytes",
     "moe_fp4_latent_decode",
     "moe_fp4_latent_attention",
+    "moe_fp4_page_slots",
 )
 
 
@@ -135,6 +136,7 @@ def load_library():
             ("latent_decode_workspace_bytes", [i32], size),
             ("latent_decode", [P, P, size, P], i32),
             ("latent_attention", [P, P], i32),
+            ("page_slots", [P, P], i32),
             ("ops_check", [P], i32)):
         fn = getattr(lib, "moe_fp4_" + name)
         fn.argtypes, fn.restype = args, res

@@ -11,6 +11,7 @@ be given so that a call allocates nothing (a captured graph).
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple
 
 from . import _binding
 from ._binding import MoeFp4Error, load_library
@@ -32,6 +33,13 @@ class BlockNormArgs(ctypes.Structure):
                 [("scale", ctypes.c_float), ("eps", ctypes.c_float)] +
                 [(n, ctypes.c_void_p) for n in ("residual", "y", "y2", "gate", "post_weight", "next_weight", "out",
                                                 "normed")])
+
+
+class PageSlotsArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("B", "page", "width")] +
+                [(n, ctypes.c_int64) for n in ("tokens", "free_count", "table_stride")] +
+                [(n, ctypes.c_void_p) for n in ("lengths", "new_tokens", "free_pages", "table", "slots", "positions",
+                                                "out_lengths", "q_offsets", "k_offsets", "taken")])
 
 
 class LatentAttentionArgs(ctypes.Structure):
@@ -67,7 +75,7 @@ class _Unloaded:
             "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_tile_scales", "mxfp4_matmul", "mxfp4_linear",
             "mxfp4_linear_workspace_bytes", "mxfp4_gathered_workspace_bytes", "block_norm", "fp8_tile_scales",
             "fp8_linear_workspace_bytes", "fp8_linear", "latent_decode_workspace_bytes", "latent_decode",
-            "latent_attention")), _raise)
+            "latent_attention", "page_slots")), _raise)
         _native, _BF16 = native, torch.bfloat16
         return getattr(native, name)
 
@@ -181,6 +189,29 @@ def latent_attention(q, kv, k_rope, q_offsets, k_offsets, scale, causal: bool = 
     all keys, each one before it one less.  A query that sees no key gets zeros, queries of no sequence are left as
     they were.  Values are to be finite; scale is positive."""
     return _native.latent_attention(q, kv, k_rope, q_offsets, k_offsets, scale, causal, out, _handle(stream))
+
+
+class PageSlots(NamedTuple):
+    """What page_slots returns (GPU tensors)."""
+    slots: object      # int64 [tokens]: page * page_size + place in it
+    positions: object  # int32 [tokens]
+    lengths: object    # int32 [B], with the new tokens
+    q_offsets: object  # int32 [B + 1], of the new tokens
+    k_offsets: object  # int32 [B + 1], of all tokens
+    taken: object      # int32 []: pages taken from the front of free_pages
+
+
+def page_slots(lengths, new_tokens, block_table, free_pages, page_size: int, tokens: int, out: PageSlots | None = None,
+               stream=None) -> PageSlots:
+    """Places of a batch's new tokens in a paged cache.  Request b has lengths[b] tokens and gets new_tokens[b] more (int32
+    [B], B up to 8192); the pages that they need are taken from the front of free_pages (int32), request after request,
+    and entered in block_table (int32 [B, width], in place).  tokens: the size of slots and positions, at least the
+    number of new tokens; behind the last one slots are -1.  out: an earlier result of the same sizes, to be
+    overwritten.  Requests that their rows do not hold, too few free pages or too many tokens are reported by
+    ops_check, their tokens' slots are -1."""
+    f = _native.page_slots
+    return PageSlots(*f(lengths, new_tokens, block_table, free_pages, page_size, tokens, *(out or (None,) * 6),
+                        _handle(stream)))
 
 
 def rms_norm(x, weight=None, eps: float = 1e-6, out=None, stream=None):

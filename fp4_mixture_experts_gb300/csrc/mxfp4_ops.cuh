@@ -47,6 +47,7 @@ cudaError_t ops_mm2_error(int32_t** word);
 cudaError_t ops_norm_error(int32_t** word);
 cudaError_t latent_decode_error(int32_t** word);
 cudaError_t latent_attention_error(int32_t** word);
+cudaError_t page_slots_error(int32_t** word);
 
 #ifdef __CUDACC__
 

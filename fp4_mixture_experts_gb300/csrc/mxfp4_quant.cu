@@ -341,7 +341,7 @@ tile_scales_kernel(const uint8_t* scales, int N, int nb, int rt, int kt, int swi
 // The error words of all the operators, taken: each read and cleared in one
 // step, so that an error which another stream raises meanwhile is in this check or
 // in the next.
-constexpr int kErrorWords = 7;
+constexpr int kErrorWords = 8;
 struct ErrorWords {
   int32_t* word[kErrorWords];
 };
@@ -496,7 +496,8 @@ int moe_fp4_ops_check(void* cuda_stream) {
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   ErrorWords words;
   cudaError_t (*const address[])(int32_t**) = {ops_quant_error, ops_mm_error, ops_mm1_error, ops_mm2_error, ops_norm_error,
-                                               latent_decode_error, latent_attention_error};
+                                               latent_decode_error, latent_attention_error,
+                                               page_slots_error};
   for (int i = 0; i < kErrorWords; ++i)
     if (address[i](&words.word[i]) != cudaSuccess) return MOE_FP4_ERR_CUDA;
   static std::mutex one_check;  // g_taken_err is one word

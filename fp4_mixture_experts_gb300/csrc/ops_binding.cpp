@@ -41,6 +41,7 @@ struct Entry {
   decltype(&moe_fp4_latent_decode_workspace_bytes) latent_decode_workspace_bytes;
   decltype(&moe_fp4_latent_decode) latent_decode;
   decltype(&moe_fp4_latent_attention) latent_attention;
+  decltype(&moe_fp4_page_slots) page_slots;
 } g_entry;
 PyObject* g_raise = nullptr;  // called with (status, entry point); raises
 
@@ -632,6 +633,51 @@ NATIVE_BEGIN(latent_attention, 9)
   return THPVariable_Wrap(out);
 NATIVE_END
 
+// lengths, new_tokens, block_table, free_pages, page_size, tokens, then the results or None: slots, positions, lengths,
+// q_offsets, k_offsets, taken; stream
+NATIVE_BEGIN(page_slots, 13)
+  const Stream st(a[12], gpu_of(a, nargs));
+  moe_fp4_page_slots_args d{};
+  int64_t B = 0, n = 0, width;
+  for (int i : {0, 1, 3})
+    if (none(a[i])) bad("lengths, new_tokens and free_pages must be contiguous 1-D int32 GPU tensors");
+  d.lengths = indices(a[0], "lengths", &B), d.new_tokens = indices(a[1], "new_tokens", &n);
+  if (n != B) bad("new_tokens must have an element for each of lengths");
+  d.table = const_cast<int32_t*>(table_of(a[2], "block_table", B, &width, &d.table_stride));
+  d.free_pages = indices(a[3], "free_pages", &d.free_count);
+  const int64_t page = whole(a[4], "page_size");
+  d.tokens = whole(a[5], "tokens");
+  if (d.tokens < 0 || d.tokens > INT32_MAX) bad("tokens must be 0 to 2^31 - 1");
+  if (B > INT32_MAX || width > INT32_MAX || page > INT32_MAX) bad("sizes beyond 2^31");
+  if (page < 1) bad("page_size must be at least 1");
+  d.B = (int32_t)B, d.page = (int32_t)page, d.width = (int32_t)width;
+  const struct {
+    const char* what;
+    int64_t size;  // -1: no dimension
+    at::ScalarType type;
+  } results[6] = {{"slots", d.tokens, at::kLong}, {"positions", d.tokens, at::kInt}, {"lengths", B, at::kInt},
+                  {"q_offsets", B + 1, at::kInt}, {"k_offsets", B + 1, at::kInt},    {"taken", -1, at::kInt}};
+  at::Tensor out[6];
+  for (int i = 0; i < 6; ++i) {
+    const int64_t size = results[i].size;
+    const at::IntArrayRef shape(&size, size < 0 ? 0 : 1);
+    if (none(a[6 + i])) {
+      out[i] = fresh(shape, results[i].type);
+    } else {
+      out[i] = tensor(a[6 + i], results[i].what);
+      if (out[i].scalar_type() != results[i].type || !out[i].is_cuda() || !out[i].is_contiguous() || out[i].sizes() != shape)
+        bad(std::string("out's ") + results[i].what + " must be as of a call of these sizes");
+    }
+  }
+  d.slots = static_cast<int64_t*>(out[0].data_ptr());
+  int32_t** const to[5] = {&d.positions, &d.out_lengths, &d.q_offsets, &d.k_offsets, &d.taken};
+  for (int i = 0; i < 5; ++i) *to[i] = static_cast<int32_t*>(out[i + 1].data_ptr());
+  if (!ok(g_entry.page_slots(&d, st.handle), "moe_fp4_page_slots")) return nullptr;
+  PyObject* res = PyTuple_New(6);
+  for (int i = 0; i < 6; ++i) PyTuple_SET_ITEM(res, i, THPVariable_Wrap(out[i]));
+  return res;
+NATIVE_END
+
 // addresses (in Entry's order), raise
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   constexpr Py_ssize_t n = sizeof(Entry) / sizeof(void*);
@@ -657,7 +703,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
 #define METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(bind),   METHOD(quantize), METHOD(dequantize), METHOD(tile_scales),
                          METHOD(matmul), METHOD(linear),   METHOD(rms_norm),   METHOD(block_residual),
-                         METHOD(fp8_tile_scales), METHOD(fp8_linear), METHOD(latent_decode), METHOD(latent_attention),
+                         METHOD(fp8_tile_scales), METHOD(fp8_linear), METHOD(latent_decode), METHOD(latent_attention), METHOD(page_slots),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -536,6 +536,32 @@ typedef struct moe_fp4_latent_attention_args {
 } moe_fp4_latent_attention_args;
 int moe_fp4_latent_attention(const moe_fp4_latent_attention_args* args, void* cuda_stream);
 
+/* Block tables and slots of a batch's new tokens in a paged cache.  Request b has
+ * n = lengths[b] tokens in the cache and gets t = new_tokens[b] more; tokens are
+ * numbered through in the requests' order.  The pages that its tokens n .. n + t - 1
+ * need beyond its ceil(n / page) own ones are taken from free_pages, request after
+ * request, and entered in its row of the table.
+ *   slots      int64 [tokens]: table page * page + place in it, of each new token
+ *   positions  int32 [tokens]: n, n + 1, ...
+ *   out_lengths int32 [B]: n + t
+ *   q_offsets, k_offsets  int32 [B + 1]: where a request's new tokens, and all its
+ *              tokens, begin if they are laid side by side
+ *   taken      int32: pages taken, the first ones of free_pages
+ * A batch of fewer than `tokens` new tokens (a padded one) gets slot -1 and position
+ * 0 behind its last.  Negative lengths (taken as 0), a request that its row of the
+ * table does not hold, more new tokens than `tokens` and too few free pages set error
+ * bit 1 (moe_fp4_ops_check); tokens without a place get slot -1, requests are kept to
+ * what their rows hold.  The outputs overlap no input; table is written in place. */
+typedef struct moe_fp4_page_slots_args {
+  int32_t B, page, width;            /* B 0 .. 8192, width * page below 2^31 */
+  int64_t tokens, free_count, table_stride;
+  const int32_t *lengths, *new_tokens, *free_pages;
+  int32_t* table;                    /* [B, width], row stride table_stride */
+  int64_t* slots;
+  int32_t *positions, *out_lengths, *q_offsets, *k_offsets, *taken;
+} moe_fp4_page_slots_args;
+int moe_fp4_page_slots(const moe_fp4_page_slots_args* args, void* cuda_stream);
+
 /* The end of a block in one pass over its rows.  With b = y (+ y2):
  *   post_norm:  b = b * rsqrt(mean(b^2) + eps)
  *   b = b * post_weight                      (NULL: 1)
