@@ -1,13 +1,14 @@
-"""A whole MoE block around the layer, as a serving loop runs it:
+"""A decoder layer's two blocks, as a serving loop runs them:
 
+    residual, normed = attention_forward(residual, normed, attention_weights, cache, block_table, pages, prompt)
     residual, normed = block_forward(residual, normed, weights, k)
 
-takes the residual stream and its norm before the block, and returns the
+The MoE block (block_forward) takes the residual stream and its norm before the block, and returns the
 residual stream after the block and its norm before the next one.  Per token
 
     logits = normed . w_gate^T                                   (router)
     routed = the routed experts' outputs, weighted
-    shared = W2s (silu(W1s normed) * W3s normed)                 (mxfp4_linear, twice)
+    shared = W2s (silu(W1s normed) * W3s normed)                 (mxfp4_linear or fp8_linear, twice)
     residual' = residual + scale * gate * norm(routed + shared)  (block_residual)
     normed' = norm(residual')
 
@@ -17,6 +18,18 @@ the offsets and sorted slots of `route`): W13 with SwiGLU from the tokens, W2
 from its rows, and the weighted sum of each token's k rows (that sum in PyTorch's
 own operations, several passes over the rows in fp32; the layer has its own).
 
+The attention block (attention_forward) writes the new tokens' latent vectors to
+the paged cache and attends, every projection an FP8 product:
+
+    q', c, kr = W_down normed;  q', c = norm(q'), norm(c);  kr = rotary(kr)
+    q = W_q q', its rotary part turned;  cache[slots] = (c, kr)
+    prompt:  kv = W_kv c of all the sequences' tokens;  o = latent_attention(q, kv, kr)
+    decode:  ql = W_k[h] q of each head;  o = W_v[h] latent_decode((ql, qr), cache)  (products grouped by head)
+    residual' = residual + W_o o;  normed' = norm(residual')     (block_residual)
+
+(the rotary turn, the concatenations and the cache's scatter and gather in
+PyTorch's own operations).
+
 prepare() lays the scales out once, when the weights are loaded.  Everything
 runs on the current stream.
 """
@@ -25,13 +38,17 @@ from __future__ import annotations
 from dataclasses import dataclass
 
 from ._binding import forward, route, router
-from ._ops import block_residual, mxfp4_linear, mxfp4_tile_scales, rms_norm
+from ._ops import (PageSlots, block_residual, fp8_linear, fp8_tile_scales, latent_attention, latent_decode, mxfp4_linear,
+                   mxfp4_tile_scales, rms_norm)
+
+NOPE, ROPE, VALUE, LATENT = 128, 64, 128, 512   # of a head: without and with positions, values; of a token: the latent vector
 
 
 @dataclass
 class BlockWeights:
     """Weights of one block (GPU tensors).  Codes and row-major scales as in the layer; the *_tiled scales are
-    prepare()'s.  Shared expert and gates may be missing."""
+    prepare()'s.  Shared expert and gates may be missing.  The shared expert may be in FP8 instead: float8_e4m3fn
+    [2Is, d] and [d, Is] with scales [rows / 128, columns / 128] (rounded up)."""
     w_gate: object                    # bf16 [E, d]
     w13: object                       # uint8 [E, 2I, d/2]
     w13_scale: object                 # uint8 [E, 2I, d/32]
@@ -51,9 +68,17 @@ class BlockWeights:
     shared_w13_tiled: object = None
     shared_w2_tiled: object = None
 
+    @property
+    def shared_fp8(self) -> bool:
+        import torch
+        return self.shared_w13.dtype == torch.float8_e4m3fn
+
     def prepare(self, mxfp4_experts: bool = False) -> "BlockWeights":
         """The scales of the products' operands in their layout, once."""
-        if self.shared_w13 is not None:
+        if self.shared_w13 is not None and self.shared_fp8:
+            self.shared_w13_tiled = fp8_tile_scales(self.shared_w13_scale, *self.shared_w13.shape, swiglu=True)
+            self.shared_w2_tiled = fp8_tile_scales(self.shared_w2_scale, *self.shared_w2.shape)
+        elif self.shared_w13 is not None:
             self.shared_w13_tiled = mxfp4_tile_scales(self.shared_w13_scale, swiglu=True)
             self.shared_w2_tiled = mxfp4_tile_scales(self.shared_w2_scale)
         if mxfp4_experts:
@@ -90,8 +115,106 @@ def block_forward(residual, normed, weights: BlockWeights, k: int, mxfp4_experts
                          workspace=workspace)
     shared = None
     if weights.shared_w13 is not None:
-        h = mxfp4_linear(normed, weights.shared_w13, weights.shared_w13_tiled, swiglu=True)
-        shared = mxfp4_linear(h, weights.shared_w2, weights.shared_w2_tiled)
+        linear = fp8_linear if weights.shared_fp8 else mxfp4_linear
+        h = linear(normed, weights.shared_w13, weights.shared_w13_tiled, swiglu=True)
+        shared = linear(h, weights.shared_w2, weights.shared_w2_tiled)
     return block_residual(residual, routed, y2=shared, post_norm=weights.post_norm is not None,
                           post_weight=weights.post_norm, gate=None if weights.gate is None else weights.gate[None],
                           scale=weights.scale, next_weight=weights.next_norm, eps=eps)
+
+
+@dataclass
+class AttentionWeights:
+    """Weights of one attention block of H heads (GPU tensors): matrices float8_e4m3fn, scales uint8 (E8M0) for each 128
+    x 128 of a matrix; r is the width of the queries' latent vector.  The *_tiled scales are prepare()'s."""
+    w_down: object        # [r + 576, d]: the queries' latent vector, the tokens' and their rotary key
+    w_down_scale: object
+    q_norm: object        # [r]
+    kv_norm: object       # [512]
+    w_q: object           # [192 H, r]: a head's 128 and 64
+    w_q_scale: object
+    w_kv: object          # [256 H, 512]: a head's keys and values of a latent vector (prompts)
+    w_kv_scale: object
+    w_k: object           # [H, 512, 128]: a head's query into the latent space (its keys' matrix, transposed)
+    w_k_scale: object
+    w_v: object           # [H, 128, 512]: a head's values of a latent vector
+    w_v_scale: object
+    w_o: object           # [d, 128 H]
+    w_o_scale: object
+    next_norm: object     # [d], of the norm before the next block
+    rope_base: float = 10000.0
+    w_down_tiled: object = None
+    w_q_tiled: object = None
+    w_kv_tiled: object = None
+    w_k_tiled: object = None
+    w_v_tiled: object = None
+    w_o_tiled: object = None
+
+    @property
+    def heads(self) -> int:
+        return self.w_k.shape[0]
+
+    def prepare(self) -> "AttentionWeights":
+        """The scales of the products' operands in their layout, once."""
+        for name in ("w_down", "w_q", "w_kv", "w_k", "w_v", "w_o"):
+            w = getattr(self, name)
+            setattr(self, name + "_tiled", fp8_tile_scales(getattr(self, name + "_scale"), w.shape[-2], w.shape[-1]))
+        return self
+
+
+def rotary(x, positions, base: float = 10000.0):
+    """bf16 x [T, 64] or [T, H, 64] turned by the tokens' positions (int32 [T]): elements 2 i and 2 i + 1 are a pair, turned
+    by position base^(-i / 32).  Angles in 64 bits: at position 10^6 those in 32 are 1/16 apart."""
+    import torch
+    i = torch.arange(ROPE // 2, dtype=torch.float64, device=x.device)
+    angle = positions.double()[:, None] * base ** (-i / (ROPE // 2))
+    cos, sin = angle.cos().float(), angle.sin().float()
+    if x.dim() == 3:
+        cos, sin = cos[:, None], sin[:, None]
+    a, b = x[..., 0::2].float(), x[..., 1::2].float()
+    return torch.stack([a * cos - b * sin, a * sin + b * cos], -1).flatten(-2).to(x.dtype)
+
+
+def cached_rows(cache, block_table, pages: PageSlots, tokens: int):
+    """The latent vectors of all tokens of a batch's sequences, side by side in the requests' order: [tokens, 576];
+    tokens: their number (pages.k_offsets' last)."""
+    import torch
+    i = torch.arange(tokens, dtype=torch.int32, device=cache.device)
+    b = torch.searchsorted(pages.k_offsets[1:], i, right=True)
+    at = (i - pages.k_offsets[b]).long()
+    size = cache.shape[1]
+    return cache[block_table[b, at // size].long(), at % size]
+
+
+def attention_forward(residual, normed, weights: AttentionWeights, cache, block_table, pages: PageSlots, prompt: bool,
+                      cached_tokens: int | None = None, eps: float = 1e-6, workspace=None):
+    """One attention block on residual [T, d] (bf16 or fp32) and its norm normed (bf16 [T, d]); returns (residual',
+    normed').  pages is page_slots' result for these T tokens (none of them without a slot), whose latent vectors are
+    written to cache (bf16 [pages, page, 576]).  prompt: any number of new tokens a sequence, the expanded form;
+    cached_tokens, for sequences with tokens in the cache already, is the number of all their tokens (pages.k_offsets'
+    last; None: all tokens are new).  Otherwise one new token a sequence, the absorbed form; workspace is
+    latent_decode's."""
+    import torch
+    W, T, H = weights, normed.shape[0], weights.heads
+    scale = (NOPE + ROPE) ** -0.5
+    down = fp8_linear(normed, W.w_down, W.w_down_tiled)
+    r = down.shape[1] - LATENT - ROPE
+    c = rms_norm(down[:, r:r + LATENT], W.kv_norm, eps=eps)
+    new = torch.cat([c, rotary(down[:, r + LATENT:], pages.positions, W.rope_base)], 1)
+    cache.view(-1, LATENT + ROPE).index_copy_(0, pages.slots, new)
+    q = fp8_linear(rms_norm(down[:, :r], W.q_norm, eps=eps), W.w_q, W.w_q_tiled).view(T, H, NOPE + ROPE)
+    turned = rotary(q[..., NOPE:], pages.positions, W.rope_base)
+    if prompt:
+        rows = new if cached_tokens is None else cached_rows(cache, block_table, pages, cached_tokens)
+        kv = fp8_linear(rows[:, :LATENT], W.w_kv, W.w_kv_tiled).view(-1, H, NOPE + VALUE)
+        q = torch.cat([q[..., :NOPE], turned], 2)
+        o = latent_attention(q, kv, rows[:, LATENT:], pages.q_offsets, pages.k_offsets, scale)
+    else:
+        by_head = torch.arange(H + 1, dtype=torch.int32, device=q.device) * T
+        ql = fp8_linear(q[..., :NOPE].transpose(0, 1).reshape(H * T, NOPE), W.w_k, W.w_k_tiled, offsets=by_head)
+        q = torch.cat([ql.view(H, T, LATENT), turned.transpose(0, 1)], 2).transpose(0, 1)
+        ol = latent_decode(q, cache, block_table, pages.lengths, scale, workspace=workspace)
+        o = fp8_linear(ol.transpose(0, 1).reshape(H * T, LATENT), W.w_v, W.w_v_tiled, offsets=by_head)
+        o = o.view(H, T, VALUE).transpose(0, 1)
+    y = fp8_linear(o.reshape(T, H * VALUE), W.w_o, W.w_o_tiled)
+    return block_residual(residual, y, post_norm=False, next_weight=W.next_norm, eps=eps)

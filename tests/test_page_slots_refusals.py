@@ -48,7 +48,7 @@ def test_arguments(lib):
 
 def on(device, *shape, dtype=I32):
     with FakeTensorMode():
-        return torch.empty(*shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def calls(o):
