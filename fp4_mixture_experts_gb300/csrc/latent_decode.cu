@@ -25,8 +25,9 @@
 // sums (fp32) and its maximum and sum in the workspace, which a second kernel
 // joins in the ranges' order.  The same lengths give the same bits.
 //
-// Warps: 0 and 1 load (tokens; 0 the queries too), 2 issues the MMAs, 4..7 are the
-// softmax, the rescaling and the results.  Waits are bounded; a piece whose wait ran
+// Warps: 0 and 1 load (tokens; 0 the queries too), 2 issues the MMAs, 3 writes the
+// results of sequences without tokens, 4..7 are the softmax, the rescaling and the
+// results.  Waits are bounded; a piece whose wait ran
 // out stores nothing, and a sequence with such a piece is not joined.
 #include <algorithm>
 #include <numeric>
@@ -45,7 +46,7 @@ constexpr int kThreads = 256;
 constexpr int kTile = 64;                     // tokens of a tile
 constexpr int kHeads = 64;                    // heads of a CTA, at most
 constexpr int kSlab = kTile * 128;
-constexpr int kSlabs = kRow / 64, kValueSlabs = kLatent / 64;
+constexpr int kSlabs = kRow / 64;
 constexpr int kStage = kSlabs * kSlab;
 constexpr int kStages = 2;
 constexpr int kOffQ = kStages * kStage;
@@ -56,8 +57,7 @@ static_assert(kSmem <= kSmemMax, "shared memory");
 constexpr uint32_t kCols = 512;
 constexpr uint32_t kColS = 4 * kHeads;        // O^T: 4 x 64 columns, then two buffers of S
 constexpr float kGrow = 8.f;                  // log2 of what P may grow to
-constexpr int kMinTiles = 4;                  // of a range
-constexpr int kMaxRanges = 256;               // (threads of the join kernel, at most)
+constexpr int kMaxRanges = 256;
 
 struct DecodeParams {
   const int32_t* table;
@@ -67,7 +67,7 @@ struct DecodeParams {
   int4* cut;           // [range]: the sequence at its start, tiles of it before, all of its tiles, tiles of a range
   int32_t* done;       // [slot]: its piece is in the workspace
   float2* ml;          // [slot][heads]: maximum (log2) and sum
-  float* sums;         // [slot][heads][512]
+  float* sums;         // [slot][4 x 128 elements][32 heads][4 x 32 elements][8 x 4 heads][32 elements][4 heads]
   int64_t table_stride;
   int B, H, groups, heads;  // heads: of a group
   int page, width, pages, box;  // box: tokens of a copy
@@ -85,10 +85,15 @@ __device__ __forceinline__ int length_at(const DecodeParams& P, int b) {
 }
 __device__ __forceinline__ int tiles_of(int n) { return n / kTile + (n % kTile != 0); }
 
-// Tiles of a range: the ranges' even share, a few at least.
+// Tiles of a range: the ranges' even share.  Fewer and longer ranges where that
+// leaves many pieces of few sequences: a tile takes about 1.25 us, a piece of a
+// sequence 0.1 us in its joining, so that sqrt(0.08 tiles) of a sequence are best.  (72
+// tiles, 64 heads, in ranges of 1, 2, 3, 4, 8: 19.3, 16.7, 17.7, 18.5, 23.5 us; 256
+// tiles, of 2, 3, 4, 6, 8: 25.7, 24.5, 21.8, 23.1, 25.1.)
 __device__ __forceinline__ int64_t share(const DecodeParams& P, int64_t total) {
   const int64_t even = (total + P.ranges - 1) / P.ranges;
-  return even > kMinTiles ? even : kMinTiles;
+  const int64_t best = (int64_t)(sqrtf(0.08f * (float)(total / P.B)) + 0.5f);
+  return max(even, max(best, (int64_t)1));
 }
 
 // The pieces of this CTA's range, sequence by sequence; every warp walks them with
@@ -97,66 +102,101 @@ struct Walk {
   int b, t0, left;     // sequence, its first tile here, tiles left of the range
   int nt, len, all;    // of the piece: tiles, length of the sequence and its tiles
   int base, mine;
-  __device__ __forceinline__ void start(int b_, int t_, int left_) {
-    b = b_, t0 = t_, left = left_, nt = 0, base = -32;
+  __device__ __forceinline__ void load(const DecodeParams& P) {
+    base = b;
+    const int i = b + (threadIdx.x & 31);
+    mine = i < P.B ? length_at(P, i) : 0;
+  }
+  // from tile t_ of sequence b_, whose length is known
+  __device__ __forceinline__ void start(const DecodeParams& P, int b_, int t_, int len_, int left_) {
+    b = b_, t0 = t_, len = len_, left = left_, nt = 0;
+    load(P);  // (needed for the second piece)
   }
   __device__ __forceinline__ bool next(const DecodeParams& P) {
-    if (nt > 0) ++b, t0 = 0;
-    for (; left > 0 && b < P.B; ++b, t0 = 0) {
-      if (b >= base + 32) {
-        base = b;
-        const int i = b + (threadIdx.x & 31);
-        mine = i < P.B ? length_at(P, i) : 0;
-      }
-      len = __shfl_sync(0xFFFFFFFFu, mine, b - base);
-      all = tiles_of(len);
-      if (all == 0) continue;
-      nt = min(all - t0, left);
-      left -= nt;
-      return true;
+    if (left <= 0) return false;
+    if (nt > 0) {
+      t0 = 0;
+      do {
+        if (++b >= P.B) return false;
+        if (b >= base + 32) load(P);
+        len = __shfl_sync(0xFFFFFFFFu, mine, b - base);
+      } while (len == 0);
     }
-    return false;
+    all = tiles_of(len);
+    nt = min(all - t0, left);
+    left -= nt;
+    return true;
   }
 };
 
-// The sum of v over the block; scratch: a word of 64 bits for each warp.
-__device__ int64_t block_sum(int64_t v, int64_t* scratch) {
-  const int warp = threadIdx.x >> 5;
+// Inclusive sums of v over the block's threads; *total: over all of them.
+// scratch: a word of 64 bits for each warp.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64_t* total) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, s);
-  if ((threadIdx.x & 31) == 0) scratch[warp] = v;
+  for (int s = 1; s < 32; s <<= 1) {
+    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, s);
+    if (lane >= s) v += u;
+  }
+  if (lane == 31) scratch[warp] = v;
   __syncthreads();
-  int64_t sum = 0;
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) sum += scratch[w];
+  int64_t all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == warp) v += all;
+    all += scratch[w];
+  }
   __syncthreads();
-  return sum;
+  *total = all;
+  return v;
 }
 
-// Where tile number `at` (below the total) is: its sequence, and its number there.
-__device__ void find_tile(const DecodeParams& P, int64_t at, int64_t* scratch, int* b_out, int* t_out) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t before = 0;
-  for (int b0 = 0; b0 < P.B; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    const int n = b < P.B ? tiles_of(length_at(P, b)) : 0;
-    int64_t c = n;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, c, s);
-      if (lane >= s) c += v;
+// A range: its sequence at the start, that one's tiles before it and length, its tiles.
+struct Range {
+  int b, t, len, left;
+};
+
+// This CTA's range, to *out in shared memory; whole block.  With up to kThreads
+// sequences their lengths are loaded once and summed up once.
+__device__ void find_range(const DecodeParams& P, int range, bool names, int64_t* scratch, Range* out) {
+  int64_t total = 0, upto = 0;
+  int mine = 0;
+  bool bad = false;
+  if (P.B <= kThreads) {
+    if ((int)threadIdx.x < P.B) mine = length_at(P, threadIdx.x), bad = mine != P.lengths[threadIdx.x];
+    upto = block_scan(tiles_of(mine), scratch, &total);
+  } else {
+    for (int b = threadIdx.x; b < P.B; b += kThreads) {
+      const int n = length_at(P, b);
+      bad |= n != P.lengths[b];
+      upto += tiles_of(n);
     }
-    if (lane == 31) scratch[warp] = c;
-    __syncthreads();
-    int64_t first = before, all = before;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) first += scratch[w];
-      all += scratch[w];
+    block_scan(upto, scratch, &total);
+  }
+  if (bad && blockIdx.x == 0) atomicOr(P.err, kErrBadExpertId);
+  const int64_t per = share(P, total), first = per * range;
+  if (first >= total) {
+    if (threadIdx.x == 0) {
+      *out = Range{0, 0, 0, 0};
+      if (names) P.cut[range] = make_int4(0, 0, 0, 0);
     }
-    first += c - n;
-    if (n > 0 && first <= at && at < first + n) *b_out = b, *t_out = (int)(at - first);
-    __syncthreads();
-    before = all;
-    if (before > at) break;
+  } else {
+    int64_t before = 0;
+    for (int b0 = 0; b0 < P.B; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      int64_t all = total;
+      if (P.B > kThreads) {
+        mine = b < P.B ? length_at(P, b) : 0;
+        upto = block_scan(tiles_of(mine), scratch, &all);
+      }
+      const int64_t end = before + upto, begin = end - tiles_of(mine);
+      if (begin <= first && first < end) {
+        *out = Range{b, (int)(first - begin), mine, (int)min(per, total - first)};
+        if (names) P.cut[range] = make_int4(b, (int)(first - begin), tiles_of(mine), (int)per);
+      }
+      before += all;
+      if (before > first) break;
+    }
   }
   __syncthreads();
 }
@@ -178,7 +218,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   uint64_t* mma_done = o_free + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* where = reinterpret_cast<int*>(tmem_slot + 2);                // [2]
+  Range* where = reinterpret_cast<Range*>(tmem_slot + 2);
   float* factor = reinterpret_cast<float*>(smem + kOffTail + 256);   // [heads]
   int64_t* scratch = reinterpret_cast<int64_t*>(smem + kOffTail + 512);
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
@@ -206,30 +246,11 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   const int head0 = group * P.heads, live = min(P.heads, P.H - head0);  // this CTA's heads
   const int slot0 = (2 * range) * P.groups + group;
   if (threadIdx.x < 2) P.done[slot0 + threadIdx.x * P.groups] = 0;
-  // this range's tiles
-  int64_t mine = 0;
-  bool bad = false;
-  for (int b = threadIdx.x; b < P.B; b += kThreads) {
-    const int n = length_at(P, b);
-    bad |= n != P.lengths[b];
-    mine += tiles_of(n);
-  }
-  if (bad && blockIdx.x == 0) atomicOr(P.err, kErrBadExpertId);
   tmem_fence_before();
-  const int64_t total = block_sum(mine, scratch);
+  find_range(P, range, group == 0, scratch, where);
   tmem_fence_after();
-  const int64_t per = share(P, total), first = per * range, last = min(total, first + per);
-  const int left = (int)max(last - first, (int64_t)0);
-  if (left > 0) find_tile(P, first, scratch, &where[0], &where[1]);
-  if (group == 0 && threadIdx.x == 0)
-    P.cut[range] = left > 0 ? make_int4(where[0], where[1], tiles_of(length_at(P, where[0])), (int)per) : make_int4(0, 0, 0, 0);
-  // sequences of no tokens
-  for (int b = blockIdx.x; b < P.B; b += gridDim.x)
-    if (length_at(P, b) == 0)
-      for (int64_t i = threadIdx.x; i < (int64_t)P.H * (kLatent / 8); i += kThreads)
-        reinterpret_cast<uint4*>(P.out + (int64_t)b * P.H * kLatent)[i] = make_uint4(0, 0, 0, 0);
   Walk w;
-  w.start(left > 0 ? where[0] : P.B, left > 0 ? where[1] : 0, left);
+  w.start(P, where->b, where->t, where->len, where->left);
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
   const Waits wait{abort_flag, P.err, P.wait_ns};
   const int n_mma = (live + 15) & ~15;
@@ -240,17 +261,6 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     int g = 0, piece = 0;
     bool ok = true;
     while (ok && w.next(P)) {
-      if (warp == 0) {
-        ok = wait(q_empty, (piece & 1) ^ 1);
-        if (!ok) break;
-        if (elect_one()) {
-          mbar_expect_tx(q_full, kSlabs * kHeads * 128);
-          for (int s = 0; s < kSlabs; ++s)
-            tma_load_3d(smem + kOffQ + s * kHeads * 128, &map_q, s * 64, head0, w.b, q_full);
-        }
-        __syncwarp();
-        ++piece;
-      }
       // the tokens' first row in the cache, for copy `lane` of a tile; a tile ahead.  A page outside the cache reads
       // as zeros.
       const int none = P.pages * P.page;
@@ -293,6 +303,19 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           }
           __syncwarp();
         }
+        if (warp == 0 && i == 0) {  // behind the first tile: its way is longer
+          ok = wait(q_empty, (piece & 1) ^ 1);
+          if (!ok) {
+            ++g;
+            break;
+          }
+          if (elect_one()) {
+            mbar_expect_tx(q_full, kSlabs * kHeads * 128);
+            tma_load_4d(smem + kOffQ, &map_q, 0, head0, w.b, 0, q_full);
+          }
+          __syncwarp();
+          ++piece;
+        }
         row = next;
       }
     }
@@ -306,7 +329,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     // ---------------- MMAs ----------------
     const uint32_t base = smem_u32(smem);
     const uint32_t q_lo = desc_lo(base + kOffQ, 16), p_lo = desc_lo(base + kOffP, 16);
-    const uint32_t id_qk = idesc_bf16(kHeads, kTile, false, false), id_pv = idesc_bf16(128, n_mma, true, false);
+    const uint32_t id_pv = idesc_bf16(128, n_mma, true, false);
     int g0 = 0, piece = 0;
     bool ok = true;
     while (ok && w.next(P)) {
@@ -314,6 +337,8 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       if (!ok) break;
       int qi = 0, pi = 0;  // tiles whose scores, whose sums have been issued
       uint64_t since = 0;
+      // tokens of a tile, to whole MMA steps: the sequence's last one may have fewer
+      auto tokens16 = [&](int i) { return min(kTile, (w.len - (w.t0 + i) * kTile + 15) & ~15); };
       while (pi < w.nt) {
         const int gq = g0 + qi, gp = g0 + pi;
         if (qi < w.nt && qi < pi + 2 && mbar_test(&kv_full[gq % kStages], (gq / kStages) & 1) &&
@@ -321,7 +346,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           tmem_fence_after();
           if (elect_one()) {
             const uint32_t k_lo = desc_lo(base + (gq % kStages) * kStage, 16);
-            const uint32_t d = tmem + kColS + (gq & 1) * kTile;
+            const uint32_t d = tmem + kColS + (gq & 1) * kTile, id_qk = idesc_bf16(kHeads, tokens16(qi), false, false);
 #pragma unroll
             for (int k = 0; k < kRow / 16; ++k) {
               const uint32_t at = ((k / 4) * kSlab + (k % 4) * 32) >> 4;
@@ -337,12 +362,14 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           tmem_fence_after();
           if (elect_one()) {
             const uint32_t v_lo = desc_lo(base + (gp % kStages) * kStage, kSlab);
+            const int steps = tokens16(pi) / 16;
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
+              if (k < steps)
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                umma_ss(tmem + j * kHeads, desc(v_lo + ((2 * j * kSlab + k * 2048) >> 4)), desc(p_lo + ((k * 32) >> 4)),
-                        id_pv, pi > 0 || k > 0);
+                for (int j = 0; j < 4; ++j)
+                  umma_ss(tmem + j * kHeads, desc(v_lo + ((2 * j * kSlab + k * 2048) >> 4)), desc(p_lo + ((k * 32) >> 4)),
+                          id_pv, pi > 0 || k > 0);
             umma_commit(pv_done);
             umma_commit(&kv_empty[gp % kStages]);
           }
@@ -370,7 +397,13 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     if (elect_one()) umma_commit(mma_done);
     __syncwarp();
     wait.drain(mma_done, 0);
-  } else if (warp >= 4) {
+  } else if (warp == 3) {
+    // ---------------- sequences of no tokens ----------------
+    for (int b = blockIdx.x; b < P.B; b += gridDim.x)
+      if (length_at(P, b) == 0)
+        for (int64_t i = lane; i < (int64_t)P.H * (kLatent / 8); i += 32)
+          reinterpret_cast<uint4*>(P.out + (int64_t)b * P.H * kLatent)[i] = make_uint4(0, 0, 0, 0);
+  } else {
     // ---------------- softmax, rescaling, results ----------------
     const int q = warp & 3, tid = threadIdx.x - 128;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
@@ -392,13 +425,12 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         tmem_fence_before();
         __syncwarp();
         if (lane == 0 && ok) mbar_arrive(&s_free[g & 1]);
-        // rows behind the sequence's end count as zeros: whatever is there must not meet a zero of P
-        if (n < kTile && ok) {
-          uint8_t* st = smem + (g % kStages) * kStage;
-          for (int c = tid; c < (kTile - n) * kValueSlabs * 8; c += 128) {
-            const int row = n + c / (kValueSlabs * 8), s = (c >> 3) % kValueSlabs;
-            *reinterpret_cast<uint4*>(st + s * kSlab + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
+        // Rows behind the sequence's end that the last MMA step takes in are zeros: whatever is there must not meet a
+        // zero of P.
+        if (n % 16 != 0 && ok) {
+          uint8_t* st = smem + (g % kStages) * kStage + (tid >> 4) * kSlab + (tid & 7) * 16;
+          for (int row = n + ((tid >> 3) & 1); row < ((n + 15) & ~15); row += 2)
+            *reinterpret_cast<uint4*>(st + row * 128) = make_uint4(0, 0, 0, 0);
         }
         float s[2][16], top[2] = {-INFINITY, -INFINITY};
         if (rows_live) {
@@ -489,30 +521,74 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
       const bool all_ok = !any_at_barrier(!ok, 1, 128);
       tmem_fence_after();
       if (all_ok) {
-        const int dim0 = q * 32 + lane;
-        uint16_t* const out = P.out + ((int64_t)w.b * P.H + head0) * kLatent + dim0;
-        float* const sums = P.sums + (int64_t)slot * P.heads * kLatent + dim0;
-        for (int c0 = 0; c0 < 4 * kHeads; c0 += 32) {
-          const int h0 = c0 & (kHeads - 1), dim = (c0 / kHeads) * 128;
-          if (h0 >= live) continue;
-          uint32_t o[32];
-          tmem_ld32(tmem + lanes + c0, o);
-          tmem_wait_ld();
+        // 32 heads at a time, two quarters of the latent vector
+        const int halves = (P.heads + 31) / 32;
+#pragma unroll 1
+        for (int c = 0; c < 2 * halves; ++c) {
+          const int h0 = c / 2 * 32, j0 = (c & 1) * 2;
+          if (h0 >= live) break;
+          uint32_t o[2][32];
           if (whole) {
+            // Elements lie across lanes, heads across columns; a head's elements are wanted side by side.  Read as
+            // fragments of 8 x 8 and stored transposed to this warp's rows of P, [head][32 elements] (16-byte chunk c of
+            // head h at c ^ (h / 2) % 4), then 16 bytes a lane.
+            const int i0 = lane >> 3, column = 8 * i0 + (lane & 7);  // the matrix and head whose address this lane gives
+            uint8_t* const turn = smem + kOffP + q * 2048;
+            float2 f[4];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (h0 + j < live)
-                out[(int64_t)(h0 + j) * kLatent + dim] = f32_to_bf16_rn(__uint_as_float(o[j]) * factor[h0 + j]);
+            for (int i = 0; i < 4; ++i) f[i] = *reinterpret_cast<const float2*>(factor + h0 + 8 * i + 2 * (lane & 3));
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                tmem_ld_rows16_half(tmem + lanes + ((uint32_t)(16 * h) << 16) + (j0 + u) * kHeads + h0, o[u] + 16 * h);
+            tmem_wait_ld();
+            uint16_t* const out = P.out + ((int64_t)w.b * P.H + head0 + h0 + (lane >> 2)) * kLatent + j0 * 128 + q * 32 + (lane & 3) * 8;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+              for (int c8 = 0; c8 < 4; ++c8) {  // elements 8 c8 .. 8 c8 + 7 of the 32
+                uint32_t p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int at = 16 * (c8 >> 1) + 4 * i + 2 * (c8 & 1);
+                  p[i] = pack_bf16(__uint_as_float(o[u][at]) * f[i].x, __uint_as_float(o[u][at + 1]) * f[i].y);
+                }
+                stmatrix4_trans(turn + column * 64 + ((c8 ^ ((column >> 1) & 3)) << 4), p[0], p[1], p[2], p[3]);
+              }
+              __syncwarp();
+              uint4 v[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int h = i * 8 + (lane >> 2);
+                v[i] = *reinterpret_cast<const uint4*>(turn + h * 64 + (((lane & 3) ^ ((h >> 1) & 3)) << 4));
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (h0 + i * 8 + (lane >> 2) < live) *reinterpret_cast<uint4*>(out + i * 8 * kLatent + u * 128) = v[i];
+              __syncwarp();
+            }
           } else {
+            // [quarter of the latent vector][32 heads][warp][4 heads] of 32 elements x 4 heads: 16 bytes a lane
+            float4* const sums = reinterpret_cast<float4*>(P.sums) +
+                                 ((((int64_t)slot * 4 + j0) * halves + h0 / 32) * 4 + q) * 8 * 32 + lane;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (h0 + j < live) sums[(int64_t)(h0 + j) * kLatent + dim] = __uint_as_float(o[j]);
+            for (int u = 0; u < 2; ++u) tmem_ld32(tmem + lanes + (j0 + u) * kHeads + h0, o[u]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int j = 0; j < 32; j += 4)
+                if (h0 + j < live)
+                  sums[u * halves * 4 * 8 * 32 + j / 4 * 32] =
+                      make_float4(__uint_as_float(o[u][j]), __uint_as_float(o[u][j + 1]), __uint_as_float(o[u][j + 2]),
+                                  __uint_as_float(o[u][j + 3]));
           }
         }
         if (!whole && rows_live && (lane & 3) == 0) {
 #pragma unroll
           for (int r = 0; r < 2; ++r)
-            if (r0 + 8 * r < live) P.ml[(int64_t)slot * P.heads + r0 + 8 * r] = make_float2(m[r], l[r]);
+            P.ml[(int64_t)slot * P.heads + r0 + 8 * r] = make_float2(m[r], l[r]);
         }
       }
       tmem_fence_before();
@@ -532,74 +608,119 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   }
 }
 
-// The pieces of cut sequences, joined: a CTA a sequence and head at a time, four
-// groups of 128 threads that take the pieces in turn, four elements a thread.
-__global__ void __launch_bounds__(512) latent_join_kernel(DecodeParams P) {
+// The pieces of cut sequences, joined: an item is four heads and a quarter of the
+// latent vector of a sequence, an element and four heads a thread, as the pieces
+// lie, every fourth piece a part of the CTA.  A part's lanes find the factors of its
+// pieces (to its own maximum), 32 at a time; the parts meet in shared memory.
+template <int kJoinParts>
+__global__ void __launch_bounds__(128 * kJoinParts) latent_join_kernel(DecodeParams P) {
   griddep_begin();
   __shared__ int4 list[kMaxRanges];  // sequence, first and last range, first slot's number
   __shared__ uint32_t found[kMaxRanges / 32];
-  __shared__ float4 part[4][128];
-  __shared__ float part_l[4];
   // A range that starts inside a sequence cuts it, the first such one names it; in the ranges' order, the same list
   // in every CTA.
-  const int rr = threadIdx.x;
-  int4 cut = make_int4(0, 0, 0, 0);
-  if (rr < P.ranges) cut = P.cut[rr];
-  const bool names = cut.y > 0 && cut.y <= cut.w;
-  const uint32_t mask = __ballot_sync(0xFFFFFFFFu, names);
-  if (rr < kMaxRanges && (rr & 31) == 0) found[rr >> 5] = mask;
-  __syncthreads();
-  int count = 0, at = __popc(mask & ((1u << (rr & 31)) - 1));
-  for (int i = 0; i < kMaxRanges / 32; ++i) {
-    if (i < rr >> 5) at += __popc(found[i]);
-    count += __popc(found[i]);
-  }
-  if (names) {
-    const int64_t start = (int64_t)rr * cut.w - cut.y;
-    list[at] = make_int4(cut.x, rr - 1, (int)((start + cut.z - 1) / cut.w), 2 * (rr - 1) + (cut.y < cut.w ? 1 : 0));
+  __shared__ float4 part_o[kJoinParts][128];
+  __shared__ float part_top[kJoinParts][4], part_l[kJoinParts][4];
+  constexpr int kThreads = 128 * kJoinParts, kRounds = (kMaxRanges + kThreads - 1) / kThreads;
+  int at[kRounds], count = 0;
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int r = i * kThreads + threadIdx.x;
+    int4 cut = make_int4(0, 0, 0, 0);
+    if (r < P.ranges) cut = P.cut[r];
+    const bool names = cut.y > 0 && cut.y <= cut.w;
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, names);
+    if (r < kMaxRanges && (r & 31) == 0) found[r >> 5] = mask;
+    at[i] = names ? __popc(mask & ((1u << (r & 31)) - 1)) : -1;
   }
   __syncthreads();
-  const int tid = threadIdx.x & 127, part_of = threadIdx.x >> 7;
-  for (int item = blockIdx.x; item < count * P.H; item += gridDim.x) {
-    const int4 c = list[item / P.H];
-    const int h = item % P.H, group = h / P.heads, hh = h % P.heads;
+#pragma unroll
+  for (int k = 0; k < kMaxRanges / 32; ++k) {
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i)
+      if (at[i] >= 0 && k < (i * kThreads + (int)threadIdx.x) >> 5) at[i] += __popc(found[k]);
+    count += __popc(found[k]);
+  }
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i)
+    if (at[i] >= 0) {
+      const int r = i * kThreads + threadIdx.x;
+      const int4 cut = P.cut[r];
+      const int64_t start = (int64_t)r * cut.w - cut.y;
+      list[at[i]] = make_int4(cut.x, r - 1, (int)((start + cut.z - 1) / cut.w), 2 * (r - 1) + (cut.y < cut.w ? 1 : 0));
+    }
+  __syncthreads();
+  const int lane = threadIdx.x & 31, q = (threadIdx.x >> 5) & 3, part = threadIdx.x >> 7, halves = (P.heads + 31) / 32;
+  const int quads = P.heads / 4, items = count * P.groups * quads * 4;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    int i = item;
+    const int j0 = i & 3;
+    i >>= 2;
+    const int quad = i % quads;
+    i /= quads;
+    const int group = i % P.groups;
+    const int4 c = list[i / P.groups];
+    const int h0 = quad * 4, live = min(P.heads, P.H - group * P.heads);
+    if (h0 >= live) continue;
     const int first = c.y, last = c.z;
     auto slot_of = [&](int r) { return (int64_t)(r == first ? c.w : 2 * r) * P.groups + group; };
-    float top = -INFINITY;
+    float o[4] = {0.f, 0.f, 0.f, 0.f}, l[4] = {0.f, 0.f, 0.f, 0.f};
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     bool complete = true;
-    for (int r = first; r <= last; ++r) {
-      const int64_t s = slot_of(r);
-      complete &= P.done[s] != 0;
-      top = fmaxf(top, P.ml[s * P.heads + hh].x);
-    }
-    if (!complete) continue;  // a wait ran out; the same in all threads
-    if (top == -INFINITY) top = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int r = first + part_of; r <= last; r += 4) {
-      const int64_t s = slot_of(r) * P.heads + hh;
-      const float2 ml = P.ml[s];
-      const float f = exp2f(ml.x - top);
-      const float4 v = reinterpret_cast<const float4*>(P.sums + s * kLatent)[tid];
-      o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
-      l += f * ml.y;
-    }
-    part[part_of][tid] = o;
-    if (tid == 0) part_l[part_of] = l;
-    __syncthreads();
-    if (threadIdx.x < 128) {
-      l = 0.f;
-      o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 v = part[i][tid];
-        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
-        l += part_l[i];
+    const float4* const sums = reinterpret_cast<const float4*>(P.sums) + (quad & 7) * 32 + lane;
+    for (int r0 = first + part; r0 <= last; r0 += 32 * kJoinParts) {
+      const int r = r0 + lane * kJoinParts, n = min(32, (last - r0) / kJoinParts + 1);
+      float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, s[4] = {0.f, 0.f, 0.f, 0.f}, f[4];
+      if (r <= last) {
+        complete &= P.done[slot_of(r)] != 0;
+        const float4* const ml = reinterpret_cast<const float4*>(P.ml + slot_of(r) * P.heads + h0);
+        const float4 a = ml[0], b = ml[1];
+        m[0] = a.x, m[1] = a.z, m[2] = b.x, m[3] = b.z;
+        s[0] = a.y, s[1] = a.w, s[2] = b.y, s[3] = b.w;
       }
-      const float inv = 1.f / l;
-      reinterpret_cast<uint2*>(P.out + ((int64_t)c.x * P.H + h) * kLatent)[tid] =
-          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        float to = fmaxf(top[h], m[h]);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) to = fmaxf(to, __shfl_xor_sync(0xFFFFFFFFu, to, d));
+        const float off = to == -INFINITY ? 0.f : to, was = exp2f(top[h] - off);
+        f[h] = exp2f(m[h] - off);
+        o[h] *= was;
+        l[h] = l[h] * was + f[h] * s[h];
+        top[h] = to;
+      }
+#pragma unroll 8
+      for (int k = 0; k < n; ++k) {
+        const float4 v = sums[((slot_of(r0 + k * kJoinParts) * 4 + j0) * halves + h0 / 32) * 4 * 8 * 32 + q * 8 * 32];
+        o[0] += __shfl_sync(0xFFFFFFFFu, f[0], k) * v.x;
+        o[1] += __shfl_sync(0xFFFFFFFFu, f[1], k) * v.y;
+        o[2] += __shfl_sync(0xFFFFFFFFu, f[2], k) * v.z;
+        o[3] += __shfl_sync(0xFFFFFFFFu, f[3], k) * v.w;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], d);
+      if (q == 0 && lane == 0) part_top[part][h] = top[h], part_l[part][h] = l[h];
+    }
+    part_o[part][q * 32 + lane] = make_float4(o[0], o[1], o[2], o[3]);
+    if (__syncthreads_or(!complete)) continue;  // a wait ran out (what is written above is not read)
+    // a part adds up a head of the four, or all
+#pragma unroll
+    for (int h = part; h < 4; h += kJoinParts) {
+      float all = -INFINITY, sum = 0.f, den = 0.f;
+#pragma unroll
+      for (int p = 0; p < kJoinParts; ++p) all = fmaxf(all, part_top[p][h]);
+      if (all == -INFINITY) all = 0.f;
+#pragma unroll
+      for (int p = 0; p < kJoinParts; ++p) {
+        const float f = exp2f(part_top[p][h] - all);
+        sum += f * reinterpret_cast<const float*>(&part_o[p][q * 32 + lane])[h];
+        den += f * part_l[p][h];
+      }
+      if (h0 + h < live)
+        P.out[((int64_t)c.x * P.H + group * P.heads + h0 + h) * kLatent + j0 * 128 + q * 32 + lane] = f32_to_bf16_rn(sum / den);
     }
     __syncthreads();
   }
@@ -639,7 +760,7 @@ size_t moe_fp4_latent_decode_workspace_bytes(int32_t H) {
   if (H < 1 || H > MOE_FP4_LATENT_MAX_HEADS) return 0;
   const Shape s = shape_of(H);
   return align256(kMaxRanges * sizeof(int4)) + align256(s.slots * sizeof(int32_t)) + align256(s.slots * s.heads * sizeof(float2)) +
-         (size_t)s.slots * s.heads * kLatent * sizeof(float);
+         (size_t)s.slots * ((s.heads + 31) & ~31) * kLatent * sizeof(float);
 }
 
 int moe_fp4_latent_decode(const moe_fp4_latent_decode_args* args, void* workspace, size_t workspace_bytes,
@@ -676,20 +797,24 @@ int moe_fp4_latent_decode(const moe_fp4_latent_decode_args* args, void* workspac
   P.fault = fault_site() == MOE_FP4_FAULT_TC_TOKEN_TILE;
   P.wait_ns = wait_limit_ns();
   CUtensorMap map_q, map_c;
-  const uint64_t qd[3] = {kRow, (uint64_t)a.H, (uint64_t)a.B}, qs[2] = {(uint64_t)a.q_head_stride * 2, (uint64_t)a.q_stride * 2};
-  const uint32_t qb[3] = {64, kHeads, 1};
+  const uint64_t qd[4] = {64, (uint64_t)a.H, (uint64_t)a.B, kSlabs};
+  const uint64_t qs[3] = {(uint64_t)a.q_head_stride * 2, (uint64_t)a.q_stride * 2, 128};
+  const uint32_t qb[4] = {64, kHeads, 1, kSlabs};
   const uint64_t cd[3] = {64, (uint64_t)a.pages * a.page, kSlabs}, cs[2] = {kRow * 2, 128};
   const uint32_t cb[3] = {64, (uint32_t)P.box, P.box == kTile ? (uint32_t)kSlabs : 1u};
-  if (!make_map_3d(&map_q, a.q, qd, qs, qb) || !make_map_3d(&map_c, a.cache, cd, cs, cb)) return MOE_FP4_ERR_CUDA;
+  if (!make_map_4d(&map_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) || !make_map_3d(&map_c, a.cache, cd, cs, cb)) return MOE_FP4_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   if (ensure_smem_optin(reinterpret_cast<const void*>(latent_decode_kernel), kSmem) != cudaSuccess) return MOE_FP4_ERR_CUDA;
   if (launch_early(latent_decode_kernel, dim3(s.ranges * s.groups), dim3(kThreads), kSmem, st, map_q, map_c, P) != cudaSuccess)
     return MOE_FP4_ERR_CUDA;
   // at most a sequence is cut for each range but the first
-  const int64_t items = (int64_t)std::min(a.B, s.ranges - 1) * a.H;
+  const int64_t items = (int64_t)std::min(a.B, s.ranges - 1) * s.groups * s.heads;  // a quarter of four heads each
   if (items == 0) return MOE_FP4_OK;
-  return launch_early(latent_join_kernel, dim3((unsigned)std::min<int64_t>(items, 2 * num_sms())), dim3(512), 0, st, P) ==
-                 cudaSuccess
+  // Four parts share a sequence's pieces where there are many: the ranges are 8 and more a sequence.  (One of 512 tiles
+  // in 128 pieces, 16 heads: 27 us, 52 with one part; 32 of 72 tiles, 64 heads: 68 and 56.)
+  const bool many = s.ranges >= 8 * a.B;
+  const unsigned grid = (unsigned)std::min<int64_t>(items, (many ? 4 : 16) * num_sms());
+  return launch_early(many ? latent_join_kernel<4> : latent_join_kernel<1>, dim3(grid), dim3(many ? 512 : 128), 0, st, P) == cudaSuccess
              ? MOE_FP4_OK
              : MOE_FP4_ERR_CUDA;
 }
