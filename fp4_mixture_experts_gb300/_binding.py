@@ -54,6 +54,7 @@ EXPORTED_SYMBOLS = (
     "moe_fp4_fp8_linear",
     "moe_fp4_latent_decode_workspace_bytes",
     "moe_fp4_latent_decode",
+    "moe_fp4_latent_attention_workspace_bytes",
     "moe_fp4_latent_attention",
     "moe_fp4_page_slots",
 )
@@ -135,7 +136,8 @@ def load_library():
             ("fp8_linear", [P, P, i32, i64, i64, P, P, P, P, P, size, P], i32),
             ("latent_decode_workspace_bytes", [i32], size),
             ("latent_decode", [P, P, size, P], i32),
-            ("latent_attention", [P, P], i32),
+            ("latent_attention_workspace_bytes", [], size),
+            ("latent_attention", [P, P, size, P], i32),
             ("page_slots", [P, P], i32),
             ("ops_check", [P], i32)):
         fn = getattr(lib, "moe_fp4_" + name)

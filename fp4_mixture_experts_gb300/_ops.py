@@ -75,7 +75,7 @@ class _Unloaded:
             "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_tile_scales", "mxfp4_matmul", "mxfp4_linear",
             "mxfp4_linear_workspace_bytes", "mxfp4_gathered_workspace_bytes", "block_norm", "fp8_tile_scales",
             "fp8_linear_workspace_bytes", "fp8_linear", "latent_decode_workspace_bytes", "latent_decode",
-            "latent_attention", "page_slots")), _raise)
+            "latent_attention_workspace_bytes", "latent_attention", "page_slots")), _raise)
         _native, _BF16 = native, torch.bfloat16
         return getattr(native, name)
 
@@ -178,7 +178,12 @@ def latent_decode(q, cache, block_table, lengths, scale, out=None, workspace=Non
     return _native.latent_decode(q, cache, block_table, lengths, scale, out, workspace, _handle(stream))
 
 
-def latent_attention(q, kv, k_rope, q_offsets, k_offsets, scale, causal: bool = True, out=None, stream=None):
+def latent_attention_workspace_bytes() -> int:
+    """Bytes of latent_attention's workspace on the current device."""
+    return int(load_library().moe_fp4_latent_attention_workspace_bytes())
+
+
+def latent_attention(q, kv, k_rope, q_offsets, k_offsets, scale, causal: bool = True, out=None, workspace=None, stream=None):
     """Latent attention in its expanded form for the new tokens of a ragged batch: bf16 [Tq, H, 128],
 
       out[i, h] = sum_j softmax(scale (q[i, h, :128] . kv[j, h, :128] + q[i, h, 128:] . k_rope[j])) kv[j, h, 128:]
@@ -188,7 +193,7 @@ def latent_attention(q, kv, k_rope, q_offsets, k_offsets, scale, causal: bool = 
     [q_offsets[b], q_offsets[b+1]) and keys [k_offsets[b], k_offsets[b+1]) (int32 [B + 1]); causal: its last query sees
     all keys, each one before it one less.  A query that sees no key gets zeros, queries of no sequence are left as
     they were.  Values are to be finite; scale is positive."""
-    return _native.latent_attention(q, kv, k_rope, q_offsets, k_offsets, scale, causal, out, _handle(stream))
+    return _native.latent_attention(q, kv, k_rope, q_offsets, k_offsets, scale, causal, out, workspace, _handle(stream))
 
 
 class PageSlots(NamedTuple):

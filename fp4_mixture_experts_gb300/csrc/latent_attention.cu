@@ -20,11 +20,17 @@
 // until then P may grow up to 2^8, which costs bf16 nothing.
 //
 // Shared memory: Q 2 x 3 slabs of [128][64] (96 KB), keys two stages of 3 slabs,
-// values one of 2.  Warps: 0 loads, 1 issues the MMAs (and clears what the last tile
-// of values holds behind the sequence's end: a zero of P must not meet an infinity
-// there), 4..7 and 8..11 are the tiles' softmax and results.  Items are dealt out to
-// one CTA an SM, long ones of a sequence first.  Waits are bounded; results are
-// stored only by warps none of whose waits ran out.
+// values one of 2.  Warps: 0 loads, 1 issues the MMAs (and clears what the last MMA
+// step of values holds behind the sequence's end: a zero of P must not meet an
+// infinity there), 2 finds the pieces of work and hands them to the others, 4..7 and
+// 8..11 are the tiles' softmax and results.  Items are dealt out to
+// one CTA an SM; where there are few, by their cost: all items' steps are numbered
+// through, in the order of sequences, heads and queries, and cut into even ranges,
+// wherever that is in an item of some length; its pieces leave their sums (fp32),
+// maxima and row sums in the workspace, which a second kernel joins in the ranges'
+// order.  The same lengths
+// give the same bits.  Waits are bounded; results are stored only by warps none of
+// whose waits ran out.
 #include <algorithm>
 
 #include "latent.cuh"
@@ -52,67 +58,245 @@ constexpr uint32_t kCols = 512;               // S of both tiles, O of both
 constexpr uint32_t kColO = 256;
 constexpr float kGrow = 8.f;                  // log2 of what P may grow to
 
+constexpr int kMinSplit = 8;                  // steps of an item that may be cut
+constexpr int kCut = 4;                       // where: at multiples of this
+constexpr int kMaxRanges = 256;
+constexpr int kRows = 2 * kQ;                 // queries of an item
+
 struct AttentionParams {
   const int32_t* q_offsets;
   const int32_t* k_offsets;
   uint16_t* out;
   int32_t* err;
+  int4* info;          // [range]: flags, first query, queries and head of the item that its last piece leaves unfinished
+  int32_t* done;       // [slot][8]: a warp's part of the piece is in the workspace
+  float2* ml;          // [slot][queries]: maximum (log2) and sum
+  float4* sums;        // [slot][32][queries] of 4 elements
   int B, H, Tq, Tk;
-  int causal;
+  int ranges, causal;
   float scale_log2;
   int fault;
   uint64_t wait_ns;
 };
+// a range: it has pieces; the first one begins inside its item; the last one ends before its item does; it is the first
+constexpr int kHasPieces = 1, kContinues = 2, kUnfinished = 4, kOnePiece = 8;
 
-// The items of a CTA, in ascending number: tile number x heads, tiles numbered
-// through over the sequences.  Whole warp; 32 sequences at a time.
-struct Items {
-  int item, step;
-  int base;               // first sequence of the 32 in the lanes
-  int before;             // tiles before them
-  int q0_, nq_, c_, end_; // this lane's sequence: first query, queries, its tiles, tiles up to its end
-  // the item
-  int h, q0, rows, k0, nk, lim[2], n[2];  // lim: keys that the first query of a tile sees; n: tiles of keys
-  __device__ __forceinline__ void start(int first, int step_) {
-    item = first - step_, step = step_, base = -32, before = 0, c_ = 0, end_ = 0;
+struct Sequence {
+  int q0, nq, k0, nk;
+};
+__device__ __forceinline__ Sequence sequence_at(const AttentionParams& P, int b) {
+  Sequence s{};
+  if (b < P.B) {
+    s.q0 = min(max(P.q_offsets[b], 0), P.Tq), s.nq = max(0, min(P.q_offsets[b + 1], P.Tq) - s.q0);
+    s.k0 = min(max(P.k_offsets[b], 0), P.Tk), s.nk = max(0, min(P.k_offsets[b + 1], P.Tk) - s.k0);
   }
-  __device__ __forceinline__ bool next(const AttentionParams& P) {
-    const int lane = threadIdx.x & 31;
-    item += step;
-    const int tile = item / P.H;
-    h = item - tile * P.H;
-    while (tile >= __shfl_sync(0xFFFFFFFFu, end_, 31)) {
-      before = __shfl_sync(0xFFFFFFFFu, end_, 31);
-      base += 32;
-      if (base >= P.B) return false;
-      const int b = base + lane;
-      q0_ = b < P.B ? min(max(P.q_offsets[b], 0), P.Tq) : 0;
-      nq_ = b < P.B ? max(0, min(P.q_offsets[b + 1], P.Tq) - q0_) : 0;
-      c_ = (nq_ + 2 * kQ - 1) / (2 * kQ);
-      int s = c_;
+  return s;
+}
+__device__ __forceinline__ int items_of(const Sequence& s) { return s.nq / kRows + (s.nq % kRows != 0); }
+
+// Steps (tiles of keys) of item t of a sequence's head: what its last query sees.
+__device__ __forceinline__ int steps_of(const AttentionParams& P, const Sequence& s, int t) {
+  const int64_t last = min((int64_t)s.nq, (int64_t)(t + 1) * kRows);
+  const int64_t keys = P.causal ? max(last + s.nk - s.nq, (int64_t)0) : s.nk;
+  return (int)((keys + kK - 1) / kK);
+}
+
+// An item costs its steps and one more for its beginning and end.  Cost of the
+// items before t of a sequence's head, t <= items_of(s): under a causal mask item u
+// < items - 1 has max(0, 2 (u + 1) + ceil((nk - nq) / 128)) steps.
+__device__ __forceinline__ int64_t cost_before(const AttentionParams& P, const Sequence& s, int t) {
+  if (t == 0) return 0;
+  const int items = items_of(s);
+  if (!P.causal) return (int64_t)t * (steps_of(P, s, 0) + 1);
+  const int64_t off = (int64_t)s.nk - s.nq, a = off >= 0 ? (off + kK - 1) / kK : -(-off / kK);
+  const int64_t u1 = min(t, items - 1);             // u + 1 = 1 .. u1, from u0 on above 0
+  const int64_t u0 = a >= 0 ? 1 : -a / 2 + 1;
+  int64_t cost = t;
+  if (u0 <= u1) cost += u1 * (u1 + 1) - (u0 - 1) * u0 + a * (u1 - u0 + 1);
+  if (t == items) cost += steps_of(P, s, items - 1);
+  return cost;
+}
+
+// A place in the work of all items, in the order of sequences, heads and items: an
+// item and a step in it.  Only items of more than kMinSplit steps are cut, at
+// multiples of kCut (the places of several ranges may then be the same one).
+struct Place {
+  int b, h, t, x;
+};
+
+// A CTA's share of the work: where it begins (with that sequence) and ends; or, with
+// many items, every gridDim.x-th whole one.
+struct Range {
+  Place from, to;
+  Sequence first;
+  int strided;
+};
+constexpr int kManyItems = 6;  // items a CTA
+
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64_t* total) {  // inclusive
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, s, d);
-        if (lane >= d) s += v;
-      }
-      end_ = before + s;
+  for (int s = 1; s < 32; s <<= 1) {
+    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, s);
+    if (lane >= s) v += u;
+  }
+  if (lane == 31) scratch[warp] = v;
+  __syncthreads();
+  int64_t all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == warp) v += all;
+    all += scratch[w];
+  }
+  __syncthreads();
+  *total = all;
+  return v;
+}
+
+// This CTA's range, to *out in shared memory; whole block.
+//
+// With kManyItems items for each CTA they stay whole and are dealt out in turn, a
+// sequence's last queries first, its heads side by side: what runs at the same time
+// then reads the same keys (8192 tokens, 64 heads, 13.5 items a CTA: 1129 us, 1285 with
+// even ranges of whole heads; 4608 tokens, 7.6 items: 393 and 449).
+__device__ void find_range(const AttentionParams& P, int range, int64_t* scratch, Range* out) {
+  int64_t total = 0, sum = 0, items = 0;
+  Sequence s{};
+  int64_t each = 0, upto = 0;  // a head's cost of this thread's sequence; the sequences' up to it
+  if (threadIdx.x == 0) out->from = out->to = Place{P.B, 0, 0, 0};
+  if (P.B <= kThreads) {
+    s = sequence_at(P, threadIdx.x);
+    block_scan((int64_t)items_of(s) * P.H, scratch, &items);
+  } else {
+    for (int b = threadIdx.x; b < P.B; b += kThreads) {
+      s = sequence_at(P, b);
+      items += (int64_t)items_of(s) * P.H;
+      sum += cost_before(P, s, items_of(s)) * P.H;
     }
-    const int l = __popc(__ballot_sync(0xFFFFFFFFu, end_ <= tile));
-    const int b = base + l;
-    // the sequence's tiles from its end on: under a causal mask the long ones come first
-    const int t = __shfl_sync(0xFFFFFFFFu, end_, l) - 1 - tile;
-    const int nq = __shfl_sync(0xFFFFFFFFu, nq_, l);
-    q0 = __shfl_sync(0xFFFFFFFFu, q0_, l) + t * 2 * kQ;
-    rows = min(2 * kQ, nq - t * 2 * kQ);
-    k0 = min(max(P.k_offsets[b], 0), P.Tk);
-    nk = max(0, min(P.k_offsets[b + 1], P.Tk) - k0);
-    k0 = uniform(k0), nk = uniform(nk);
+    block_scan(items, scratch, &items);
+  }
+  const bool strided = items >= kManyItems * gridDim.x;
+  if (threadIdx.x == 0) out->strided = strided;
+  if (!strided) {
+    if (P.B <= kThreads) {
+      each = cost_before(P, s, items_of(s));
+      upto = block_scan(each * P.H, scratch, &total);
+    } else {
+      block_scan(sum, scratch, &total);
+    }
+    const int64_t even = total / P.ranges, rest = total % P.ranges;
+    int64_t at[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) at[i] = even * (range + i) + min((int64_t)(range + i), rest);
+    int64_t before = 0;
+    for (int b0 = 0; b0 < P.B; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      int64_t all = total;
+      if (P.B > kThreads) {
+        s = sequence_at(P, b);
+        each = cost_before(P, s, items_of(s));
+        upto = block_scan(each * P.H, scratch, &all);
+      }
+      const int64_t end = before + upto, begin = end - each * P.H;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (!(begin <= at[i] && at[i] < end)) continue;
+        const int64_t y = at[i] - begin, h = y / each, z = y - h * each;
+        int lo = 0, hi = items_of(s);  // the last item that begins at or before z
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (cost_before(P, s, mid) <= z)
+            lo = mid;
+          else
+            hi = mid;
+        }
+        const int n = steps_of(P, s, lo);
+        const int x = (int)min(z - cost_before(P, s, lo), (int64_t)n - 1);
+        (i == 0 ? out->from : out->to) = Place{b, (int)h, lo, n > kMinSplit ? x - x % kCut : 0};
+        if (i == 0) out->first = s;
+      }
+      before += all;
+      if (before > at[1]) break;
+    }
+  } else if (threadIdx.x == 0) {
+    out->from = Place{0, 0, 0, 0};
+    out->first = sequence_at(P, 0);
+  }
+  __syncthreads();
+}
+
+// A piece of an item, as the warps hand it on in shared memory.
+struct Piece {
+  int h, q0, rows, k0, nk;  // rows 0: no more pieces
+  int n, from, to;          // steps of the item, of the piece
+  int lim[2], upto[2];      // of either tile: keys that its first query sees, where its steps end
+  int slot;                 // of its sums, if it is not the whole item
+};
+constexpr int kHanded = 3;  // pieces on their way
+
+// The pieces of a CTA's share, item by item; one warp walks them and holds 32
+// sequences, one a lane.
+struct Pieces {
+  Place at, end;      // at.t counts a sequence's items of all heads where they are dealt out in turn
+  bool begun, strided;
+  int base;
+  Sequence mine, s;   // this lane's sequence, the current one
+  __device__ __forceinline__ void load(const AttentionParams& P) {
+    base = at.b;
+    mine = sequence_at(P, base + (threadIdx.x & 31));
+  }
+  __device__ __forceinline__ void start(const AttentionParams& P, const Range& r) {
+    at = r.from, end = r.to, s = r.first, strided = r.strided, begun = false;
+    if (strided) at.t = (int)blockIdx.x - (int)gridDim.x;
+    load(P);  // (needed from the second sequence on)
+  }
+  __device__ __forceinline__ void next_sequence(const AttentionParams& P) {
+    if (++at.b >= base + 32) load(P);
+    s.q0 = __shfl_sync(0xFFFFFFFFu, mine.q0, at.b - base), s.nq = __shfl_sync(0xFFFFFFFFu, mine.nq, at.b - base);
+    s.k0 = __shfl_sync(0xFFFFFFFFu, mine.k0, at.b - base), s.nk = __shfl_sync(0xFFFFFFFFu, mine.nk, at.b - base);
+  }
+  __device__ __forceinline__ bool next(const AttentionParams& P, Piece& p) {
+    int t;
+    bool last = false;
+    if (strided) {
+      at.t += gridDim.x;
+      int count;
+      while (at.b < P.B && at.t >= (count = items_of(s) * P.H)) {
+        at.t -= count;
+        next_sequence(P);
+      }
+      if (at.b >= P.B) return false;
+      const int row = at.t / P.H;
+      p.h = at.t - row * P.H;
+      t = items_of(s) - 1 - row;
+    } else {
+      if (begun) {
+        if (at.b == end.b && at.h == end.h && at.t == end.t) return false;
+        at.x = 0;
+        if (++at.t >= items_of(s)) {
+          at.t = 0;
+          if (++at.h == P.H) {
+            at.h = 0;
+            do next_sequence(P);
+            while (at.b < P.B && s.nq == 0);
+          }
+        }
+      }
+      begun = true;
+      last = at.b == end.b && at.h == end.h && at.t == end.t;
+      if (at.b >= P.B || (last && at.x == end.x)) return false;
+      p.h = at.h, t = at.t;
+    }
+    p.n = steps_of(P, s, t);
+    p.q0 = s.q0 + t * kRows, p.rows = min(kRows, s.nq - t * kRows);
+    p.k0 = s.k0, p.nk = s.nk;
+    p.from = at.x, p.to = last ? end.x : p.n;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int r = min(rows, (i + 1) * kQ) - i * kQ;  // queries of the tile
-      lim[i] = P.causal ? t * 2 * kQ + i * kQ + 1 + nk - nq : nk;
-      const int most = P.causal ? min(nk, lim[i] + r - 1) : nk;  // what its last one sees
-      n[i] = r > 0 && most > 0 ? (most + kK - 1) / kK : 0;
+      const int r = min(p.rows, (i + 1) * kQ) - i * kQ;  // queries of the tile
+      p.lim[i] = P.causal ? t * kRows + i * kQ + 1 + s.nk - s.nq : s.nk;
+      const int most = P.causal ? min(s.nk, p.lim[i] + r - 1) : s.nk;  // what its last one sees
+      p.upto[i] = r > 0 && most > 0 ? min((most + kK - 1) / kK, p.to) : 0;
     }
     return true;
   }
@@ -149,8 +333,13 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
   uint64_t* o_full = p_full + 2;        // [tile]
   uint64_t* o_free = o_full + 2;        // [tile], four warps
   uint64_t* mma_done = o_free + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  uint64_t* piece_full = mma_done + 1;  // [handed]
+  uint64_t* piece_empty = piece_full + kHanded;  // [handed], ten warps
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(piece_empty + kHanded);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  Range* share = reinterpret_cast<Range*>(smem + kOffTail + 256);
+  int64_t* scratch = reinterpret_cast<int64_t*>(smem + kOffTail + 512);
+  Piece* handed = reinterpret_cast<Piece*>(smem + kOffTail + 640);   // [handed]
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -160,6 +349,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     for (int t = 0; t < 2; ++t)
       mbar_init(&s_full[t], 1), mbar_init(&p_full[t], 4), mbar_init(&o_full[t], 1), mbar_init(&o_free[t], 4);
     mbar_init(mma_done, 1);
+    for (int s = 0; s < kHanded; ++s) mbar_init(&piece_full[s], 1), mbar_init(&piece_empty[s], 10);
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -170,23 +360,34 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   griddep_begin();
+  const int slot0 = 2 * blockIdx.x;
+  if (threadIdx.x < 16) P.done[slot0 * 8 + threadIdx.x] = 0;
   tmem_fence_before();
-  __syncthreads();
+  find_range(P, blockIdx.x, scratch, share);
   tmem_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
   const Waits wait{abort_flag, P.err, P.wait_ns};
-  Items w;
-  w.start(blockIdx.x, gridDim.x);
+  // the next piece, from the warp that walks them; false: there is none, or a wait ran out
+  int seen_pieces = 0;
+  bool ok = true;
+  Piece w;
+  auto next_piece = [&] {
+    const int s = seen_pieces % kHanded;
+    if (!(ok = wait(&piece_full[s], (seen_pieces / kHanded) & 1))) return false;
+    w = handed[s];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&piece_empty[s]);
+    ++seen_pieces;
+    return w.rows > 0;
+  };
 
   if (warp < 4) {
     set_registers_fewer<kRegsFew>();
     if (warp == 0) {
       // ---------------- loads ----------------
       int items = 0, g = 0;  // items with keys, tiles of keys
-      bool ok = true;
-      while (ok && w.next(P)) {
-        const int n = max(w.n[0], w.n[1]);
-        if (n == 0) continue;
+      while (ok && next_piece()) {
+        if (w.from >= w.to) continue;
         if (!(ok = wait(q_empty, (items & 1) ^ 1))) break;
         const int tiles = w.rows > kQ ? 2 : 1;
         if (elect_one()) {
@@ -197,10 +398,10 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         }
         __syncwarp();
         ++items;
-        for (int i = 0; i < n; ++i, ++g) {
+        for (int i = w.from; i < w.to; ++i, ++g) {
           const int s = g % kKStages;
           if (!(ok = wait(&k_empty[s], ((g / kKStages) & 1) ^ 1))) break;
-          if (!(P.fault && blockIdx.x == 0 && g == 0) && elect_one()) {
+          if (!(P.fault && g == 0 && w.from == 0 && w.h == 0) && elect_one()) {
             uint8_t* st = smem + kOffK + s * kKStage;
             mbar_expect_tx(&k_full[s], kKStage);
             tma_load_3d(st, &map_kv, 0, w.h, w.k0 + i * kK, &k_full[s]);
@@ -228,12 +429,12 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     } else if (warp == 1) {
       // ---------------- MMAs ----------------
       const uint32_t base = smem_u32(smem);
-      constexpr uint32_t id_qk = idesc_bf16(kQ, kK, false, false), id_pv = idesc_bf16(kQ, kValue, false, true);
+      constexpr uint32_t id_pv = idesc_bf16(kQ, kValue, false, true);
       int items = 0, g = 0, use[2] = {0, 0}, turn[2] = {0, 0};  // of O's and of P's barriers
-      bool ok = true;
-      auto qk = [&](int t, int gk) {
+      auto keys16 = [&](int i) { return min(kK, (w.nk - i * kK + 15) & ~15); };  // of a tile, to whole MMA steps
+      auto qk = [&](int t, int gk, int i) {
         if (elect_one()) {
-          const uint32_t q_lo = desc_lo(base + t * kQSlabs * kSlab, 16);
+          const uint32_t q_lo = desc_lo(base + t * kQSlabs * kSlab, 16), id_qk = idesc_bf16(kQ, keys16(i), false, false);
           const uint32_t k_lo = desc_lo(base + kOffK + (gk % kKStages) * kKStage, 16);
 #pragma unroll
           for (int k = 0; k < (kNope + kRope) / 16; ++k) {
@@ -244,26 +445,25 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         }
         __syncwarp();
       };
-      while (ok && w.next(P)) {
-        const int n = max(w.n[0], w.n[1]);
-        if (n == 0) continue;
-        const bool clean = n * kK > w.nk;  // the last tile's end is behind the sequence's
+      while (ok && next_piece()) {
+        if (w.from >= w.to) continue;
         if (!(ok = wait(q_full, items & 1)) || !(ok = wait(&k_full[g % kKStages], (g / kKStages) & 1))) break;
         tmem_fence_after();
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          if (w.n[t] > 0) qk(t, g);
+          if (w.from < w.upto[t]) qk(t, g, w.from);
         if (elect_one()) {
           umma_commit(&k_empty[g % kKStages]);
-          if (n == 1) umma_commit(q_empty);
+          if (w.to - w.from == 1) umma_commit(q_empty);
         }
         __syncwarp();
-        for (int i = 0; i < n && ok; ++i, ++g) {
+        for (int i = w.from; i < w.to && ok; ++i, ++g) {
           if (!(ok = wait(v_full, g & 1))) break;
-          if (clean && i == n - 1) {
-            const int from = w.nk - i * kK;
-            for (int c = lane; c < (kK - from) * kVSlabs * 8; c += 32) {
-              const int row = from + c / (kVSlabs * 8), s = (c >> 3) % kVSlabs;
+          const int keys = w.nk - i * kK, steps = keys16(i) / 16;
+          if (keys < kK && keys % 16 != 0) {
+            // rows behind the sequence's end that the last MMA step takes in are zeros
+            for (int c = lane; c < (16 * steps - keys) * kVSlabs * 8; c += 32) {
+              const int row = keys + c / (kVSlabs * 8), s = (c >> 3) % kVSlabs;
               *reinterpret_cast<uint4*>(smem + kOffV + s * kSlab + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async();
@@ -271,9 +471,9 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
           }
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (i >= w.n[t] || !ok) continue;
+            if (i >= w.upto[t] || !ok) continue;
             ok = wait(&p_full[t], turn[t] & 1);
-            if (ok && i == 0) ok = wait(&o_free[t], (use[t] & 1) ^ 1), ++use[t];
+            if (ok && i == w.from) ok = wait(&o_free[t], (use[t] & 1) ^ 1), ++use[t];
             if (!ok) break;
             ++turn[t];
             tmem_fence_after();
@@ -281,22 +481,23 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
               const uint32_t v_lo = desc_lo(base + kOffV, kSlab);
 #pragma unroll
               for (int k = 0; k < kK / 16; ++k)
-                tc::umma_tmem_a(tmem + kColO + t * kValue, tmem + t * kK + 8 * k, desc(v_lo + ((k * 2048) >> 4)), id_pv,
-                                i > 0 || k > 0);
-              if (i == w.n[t] - 1) umma_commit(&o_full[t]);
+                if (k < steps)
+                  tc::umma_tmem_a(tmem + kColO + t * kValue, tmem + t * kK + 8 * k, desc(v_lo + ((k * 2048) >> 4)), id_pv,
+                                  i > w.from || k > 0);
+              if (i == w.upto[t] - 1) umma_commit(&o_full[t]);
             }
             __syncwarp();
-            if (i + 1 < w.n[t]) {
+            if (i + 1 < w.upto[t]) {
               if (!(ok = wait(&k_full[(g + 1) % kKStages], ((g + 1) / kKStages) & 1))) break;
               tmem_fence_after();
-              qk(t, g + 1);
+              qk(t, g + 1, i + 1);
             }
           }
           if (!ok) break;
           if (elect_one()) {
             umma_commit(v_empty);
-            if (i + 1 < n) umma_commit(&k_empty[(g + 1) % kKStages]);
-            if (i + 2 == n) umma_commit(q_empty);
+            if (i + 1 < w.to) umma_commit(&k_empty[(g + 1) % kKStages]);
+            if (i + 2 == w.to) umma_commit(q_empty);
           }
           __syncwarp();
         }
@@ -306,6 +507,36 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
       if (elect_one()) umma_commit(mma_done);
       __syncwarp();
       wait.drain(mma_done, 0);
+    } else if (warp == 2) {
+      // ---------------- the share's pieces ----------------
+      Pieces all;
+      all.start(P, *share);
+      int count = 0, flags = 0;
+      int4 unfinished = make_int4(0, 0, 0, 0);
+      while (true) {
+        Piece p{};
+        const bool more = all.next(P, p);
+        const int s = count % kHanded;
+        if (more) {
+          p.slot = slot0 + (count > 0 ? 1 : 0);
+          flags |= kHasPieces | (count == 0 && p.from > 0 ? kContinues : 0);
+          if (p.to < p.n) {
+            flags |= kUnfinished | (count == 0 ? kOnePiece : 0);
+            unfinished = make_int4(0, p.q0, p.rows, p.h);
+          }
+        }
+        if (!ok || !(ok = wait(&piece_empty[s], ((count / kHanded) & 1) ^ 1))) {
+          if (!more) break;
+          continue;  // (the flags are needed still)
+        }
+        if (lane == 0) {
+          handed[s] = p;
+          mbar_arrive(&piece_full[s]);
+        }
+        ++count;
+        if (!more) break;
+      }
+      if (lane == 0) P.info[blockIdx.x] = make_int4(flags, unfinished.y, unfinished.z, unfinished.w);
     }
   } else {
     set_registers_more<kRegsMany>();
@@ -314,12 +545,11 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + t * kK + lanes, o_col = tmem + kColO + t * kValue + lanes;
     int turn = 0, use = 0;
-    bool ok = true;
-    while (ok && w.next(P)) {
+    while (ok && next_piece()) {
       const int here = min(w.rows - t * kQ, kQ);  // queries of the tile
       const int seen = P.causal ? min(w.nk, w.lim[t] + row) : w.nk;  // keys that this query sees
       float m = -INFINITY, l = 0.f;
-      for (int i = 0; i < w.n[t]; ++i, ++turn) {
+      for (int i = w.from; i < w.upto[t]; ++i, ++turn) {
         if (!(ok = wait(&s_full[t], turn & 1))) break;
         tmem_fence_after();
         uint32_t s[4][32];
@@ -342,7 +572,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
           const float to = fmaxf(m, top);
           const float f = to == m ? 1.f : exp2_fast(m - to);  // the first maximum: 0
           m = to, l *= f;
-          if (i > 0) {
+          if (i > w.from) {
             // this warp's lanes of O; the MMAs before this S have ended
 #pragma unroll 1
             for (int c = 0; c < kValue; c += 32) {
@@ -377,35 +607,48 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         if (lane == 0) mbar_arrive(&p_full[t]);
       }
       if (!ok) break;
-      if (here <= 0) continue;
+      const bool whole = w.from == 0 && w.to == w.n, any = w.from < w.upto[t], mine = row < here;
       uint16_t* const out = P.out + ((int64_t)(w.q0 + t * kQ + row) * P.H + w.h) * kValue;
-      const bool mine = row < here;
-      if (w.n[t] == 0) {
+      if (whole && !any) {
         if (mine)
           for (int c = 0; c < kValue; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
         continue;
       }
-      if (!(ok = wait(&o_full[t], use & 1))) break;
-      ++use;
-      tmem_fence_after();
-      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // a query that sees nothing: zeros
+      if (any) {
+        if (!(ok = wait(&o_full[t], use & 1))) break;
+        ++use;
+        tmem_fence_after();
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // a query that sees nothing: zeros
+        float4* const sums = P.sums + (int64_t)w.slot * (kValue / 4) * kRows + t * kQ + row;
 #pragma unroll 1
-      for (int c = 0; c < kValue; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(o_col + c, o);
-        tmem_wait_ld();
+        for (int c = 0; c < kValue; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_col + c, o);
+          tmem_wait_ld();
+          if (whole) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          uint32_t v[4];
+            for (int j = 0; j < 32; j += 8) {
+              uint32_t v[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            v[k] = pack_bf16(__uint_as_float(o[j + 2 * k]) * inv, __uint_as_float(o[j + 2 * k + 1]) * inv);
-          if (mine) *reinterpret_cast<uint4*>(out + c + j) = make_uint4(v[0], v[1], v[2], v[3]);
+              for (int k = 0; k < 4; ++k)
+                v[k] = pack_bf16(__uint_as_float(o[j + 2 * k]) * inv, __uint_as_float(o[j + 2 * k + 1]) * inv);
+              if (mine) *reinterpret_cast<uint4*>(out + c + j) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              sums[(c + j) / 4 * kRows] = make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
+                                                      __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
+          }
         }
+        tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[t]);
       }
-      tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&o_free[t]);
+      if (!whole) {
+        P.ml[(int64_t)w.slot * kRows + t * kQ + row] = make_float2(m, l);
+        if (lane == 0) P.done[w.slot * 8 + warp - 4] = 1;
+      }
     }
   }
   __syncwarp();
@@ -414,6 +657,71 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
   if (warp == 1) {
     tmem_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
+  }
+}
+
+// The pieces of items that several ranges share, joined in the ranges' order: a
+// CTA an item and eight elements of its queries' results, a query a thread.
+constexpr int kJoinChunks = kValue / 8;
+__global__ void __launch_bounds__(kRows) latent_attention_join_kernel(AttentionParams P) {
+  griddep_begin();
+  __shared__ int flags[kMaxRanges];
+  __shared__ uint32_t found[kMaxRanges / 32];
+  const int r0 = threadIdx.x;  // (kRows threads, a range each)
+  const int4 info = r0 < P.ranges ? P.info[r0] : make_int4(0, 0, 0, 0);
+  flags[r0] = info.x;
+  // an item's first piece: it begins the item and leaves it unfinished
+  const bool first = (info.x & kUnfinished) && !((info.x & kContinues) && (info.x & kOnePiece));
+  const uint32_t mask = __ballot_sync(0xFFFFFFFFu, first);
+  if ((r0 & 31) == 0) found[r0 >> 5] = mask;
+  __syncthreads();
+  int count = 0;
+#pragma unroll
+  for (int k = 0; k < kMaxRanges / 32; ++k) count += __popc(found[k]);
+  const int row = threadIdx.x, warp = threadIdx.x >> 5;
+  for (int item = blockIdx.x; item < count * kJoinChunks; item += gridDim.x) {
+    int skip = item / kJoinChunks, r = 0;
+    const int c = item % kJoinChunks;
+    for (int k = 0; k < kMaxRanges / 32; ++k) {
+      const int here = __popc(found[k]);
+      if (skip < here) {
+        r = 32 * k + __fns(found[k], 0, skip + 1);
+        break;
+      }
+      skip -= here;
+    }
+    const int4 what = P.info[r];
+    float o[8] = {}, l = 0.f, top = -INFINITY;
+    bool complete = true;
+    auto add = [&](int64_t slot) {
+      complete &= P.done[slot * 8 + warp] != 0;
+      const float2 ml = P.ml[slot * kRows + row];
+      const float4* const s = P.sums + (slot * (kValue / 4) + 2 * c) * kRows + row;
+      const float4 a = s[0], b = s[kRows];
+      const float to = fmaxf(top, ml.x), off = to == -INFINITY ? 0.f : to;
+      const float f = exp2f(ml.x - off), was = exp2f(top - off);
+      // (a piece without a step for the query's tile holds no sums)
+      const bool has = ml.x > -INFINITY || ml.y != 0.f;
+      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = o[j] * was + (has ? f * v[j] : 0.f);
+      l = l * was + f * ml.y;
+      top = to;
+    };
+    add(2 * r + ((flags[r] & kOnePiece) ? 0 : 1));
+    while (true) {  // the first pieces of the ranges behind, up to the one that ends the item
+      do ++r;
+      while (r < P.ranges && !(flags[r] & kHasPieces));
+      if (r >= P.ranges) break;
+      add(2 * r);
+      if (!((flags[r] & kUnfinished) && (flags[r] & kOnePiece))) break;
+    }
+    if (!complete || row >= what.z) continue;  // a wait ran out; behind the item's last query
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    uint32_t v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
+    *reinterpret_cast<uint4*>(P.out + ((int64_t)(what.y + row) * P.H + what.w) * kValue + 8 * c) = make_uint4(v[0], v[1], v[2], v[3]);
   }
 }
 
@@ -428,6 +736,9 @@ cudaError_t ready() {
   return enough ? ensure_smem_optin(k, kSmem) : cudaErrorLaunchOutOfResources;
 }
 
+int most_ranges() { return std::min(kMaxRanges, num_sms()); }
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+
 }  // namespace
 
 cudaError_t latent_attention_error(int32_t** word) {
@@ -438,7 +749,16 @@ cudaError_t latent_attention_error(int32_t** word) {
 
 using namespace moe_fp4;
 
-extern "C" int moe_fp4_latent_attention(const moe_fp4_latent_attention_args* args, void* cuda_stream) {
+extern "C" {
+
+size_t moe_fp4_latent_attention_workspace_bytes(void) {
+  const size_t slots = 2 * (size_t)most_ranges();
+  return align256(kMaxRanges * sizeof(int4)) + align256(slots * 8 * sizeof(int32_t)) + slots * kRows * sizeof(float2) +
+         slots * kRows * kValue * sizeof(float);
+}
+
+int moe_fp4_latent_attention(const moe_fp4_latent_attention_args* args, void* workspace, size_t workspace_bytes,
+                             void* cuda_stream) {
   if (!args) return MOE_FP4_ERR_INVALID_ARG;
   const moe_fp4_latent_attention_args a = *args;
   if (a.B < 0 || a.H < 1 || a.H > MOE_FP4_LATENT_MAX_HEADS || a.Tq < 0 || a.Tk < 0 || !(a.scale > 0.f) || a.scale > 3e38f ||
@@ -446,7 +766,7 @@ extern "C" int moe_fp4_latent_attention(const moe_fp4_latent_attention_args* arg
     return MOE_FP4_ERR_INVALID_ARG;
   // items and TMA coordinates are counted in 32 bits
   const int64_t tiles = a.Tq / (2 * kQ) + std::min<int64_t>(a.B, a.Tq);
-  if (a.Tq > INT32_MAX - 4 * kQ || a.Tk > INT32_MAX - 2 * kK || (tiles + num_sms()) * a.H >= (1LL << 30)) return MOE_FP4_ERR_UNSUPPORTED;
+  if (a.Tq > INT32_MAX - 4 * kQ || a.Tk > INT32_MAX - 2 * kK || tiles * a.H >= (1LL << 30)) return MOE_FP4_ERR_UNSUPPORTED;
   if (a.B == 0 || a.Tq == 0) return MOE_FP4_OK;
   const auto rows = [](const void* p, int64_t stride, int64_t head_stride, int64_t width) {
     return p && ((uintptr_t)p & 15) == 0 && stride >= width && head_stride >= width && stride % 8 == 0 && head_stride % 8 == 0 &&
@@ -457,6 +777,8 @@ extern "C" int moe_fp4_latent_attention(const moe_fp4_latent_attention_args* arg
     return MOE_FP4_ERR_INVALID_ARG;
   if (a.Tk > 0 && (!rows(a.kv, a.kv_stride, a.kv_head_stride, kNope + kValue) || !rows(a.k_rope, a.rope_stride, kRope, kRope)))
     return MOE_FP4_ERR_INVALID_ARG;
+  if (!workspace || ((uintptr_t)workspace & 255)) return MOE_FP4_ERR_INVALID_ARG;
+  if (workspace_bytes < moe_fp4_latent_attention_workspace_bytes()) return MOE_FP4_ERR_WORKSPACE;
   AttentionParams P{};
   P.q_offsets = a.q_offsets, P.k_offsets = a.k_offsets, P.out = static_cast<uint16_t*>(a.out);
   P.B = a.B, P.H = a.H, P.Tq = (int)a.Tq, P.Tk = (int)a.Tk, P.causal = a.causal;
@@ -476,9 +798,28 @@ extern "C" int moe_fp4_latent_attention(const moe_fp4_latent_attention_args* arg
     map_kv = map_rope = map_q;  // nothing is loaded through them
   }
   if (ready() != cudaSuccess) return MOE_FP4_ERR_CUDA;
-  const int grid = (int)std::min<int64_t>(num_sms(), tiles * a.H);
-  return launch_early(latent_attention_kernel, dim3(grid), dim3(kThreads), kSmem, static_cast<cudaStream_t>(cuda_stream), map_q,
-                      map_kv, map_rope, P) == cudaSuccess
+  // ranges for all SMs if items may be cut, else for the items that there may be
+  const bool cut = a.Tk > kMinSplit * kK;
+  P.ranges = cut ? most_ranges() : (int)std::min<int64_t>(most_ranges(), tiles * a.H);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const size_t slots = 2 * (size_t)most_ranges();
+  P.info = reinterpret_cast<int4*>(ws);
+  ws += align256(kMaxRanges * sizeof(int4));
+  P.done = reinterpret_cast<int32_t*>(ws);
+  ws += align256(slots * 8 * sizeof(int32_t));
+  P.ml = reinterpret_cast<float2*>(ws);
+  P.sums = reinterpret_cast<float4*>(ws + slots * kRows * sizeof(float2));
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  if (launch_early(latent_attention_kernel, dim3(P.ranges), dim3(kThreads), kSmem, st, map_q, map_kv, map_rope, P) != cudaSuccess)
+    return MOE_FP4_ERR_CUDA;
+  if (!cut) return MOE_FP4_OK;
+  // an item is cut for each range but the first, at most
+  const int64_t items = std::min<int64_t>(P.ranges - 1, tiles * a.H) * kJoinChunks;
+  if (items == 0) return MOE_FP4_OK;
+  return launch_early(latent_attention_join_kernel, dim3((unsigned)std::min<int64_t>(items, 8 * num_sms())), dim3(kRows), 0, st,
+                      P) == cudaSuccess
              ? MOE_FP4_OK
              : MOE_FP4_ERR_CUDA;
 }
+
+}  // extern "C"

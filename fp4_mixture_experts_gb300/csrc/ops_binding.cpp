@@ -40,6 +40,7 @@ struct Entry {
   decltype(&moe_fp4_fp8_linear) fp8_linear;
   decltype(&moe_fp4_latent_decode_workspace_bytes) latent_decode_workspace_bytes;
   decltype(&moe_fp4_latent_decode) latent_decode;
+  decltype(&moe_fp4_latent_attention_workspace_bytes) latent_attention_workspace_bytes;
   decltype(&moe_fp4_latent_attention) latent_attention;
   decltype(&moe_fp4_page_slots) page_slots;
 } g_entry;
@@ -597,9 +598,9 @@ NATIVE_BEGIN(latent_decode, 8)
   return THPVariable_Wrap(out);
 NATIVE_END
 
-// q, kv, k_rope, q_offsets, k_offsets, scale, causal, out, stream
-NATIVE_BEGIN(latent_attention, 9)
-  const Stream st(a[8], gpu_of(a, nargs));
+// q, kv, k_rope, q_offsets, k_offsets, scale, causal, out, workspace, stream
+NATIVE_BEGIN(latent_attention, 10)
+  const Stream st(a[9], gpu_of(a, nargs));
   const Heads q = heads_of(a[0], "q", 192), kv = heads_of(a[1], "kv", 256);
   const at::Tensor& rope = bf16_of(a[2], "k_rope", 2);
   if (kv.heads != q.heads) bad("kv must have q's heads");
@@ -629,7 +630,16 @@ NATIVE_BEGIN(latent_attention, 9)
       bad("out must be contiguous [Tq, H, 128]");
   }
   d.out = out.data_ptr();
-  if (!ok(g_entry.latent_attention(&d, st.handle), "moe_fp4_latent_attention")) return nullptr;
+  const size_t need = g_entry.latent_attention_workspace_bytes();
+  void* ws;
+  c10::DataPtr scratch;
+  if (!none(a[8])) {
+    ws = bytes_of(tensor(a[8], "workspace"), "workspace", (int64_t)need);
+  } else {
+    scratch = c10::GetAllocator(c10::kCUDA)->allocate(need);
+    ws = scratch.get();
+  }
+  if (!ok(g_entry.latent_attention(&d, ws, need, st.handle), "moe_fp4_latent_attention")) return nullptr;
   return THPVariable_Wrap(out);
 NATIVE_END
 

@@ -534,7 +534,12 @@ typedef struct moe_fp4_latent_attention_args {
   const int32_t *q_offsets, *k_offsets;
   void* out;
 } moe_fp4_latent_attention_args;
-int moe_fp4_latent_attention(const moe_fp4_latent_attention_args* args, void* cuda_stream);
+/* Device workspace of moe_fp4_latent_attention (pieces of items that SMs share;
+ * 256-byte aligned base), for the current device.  It holds nothing between calls;
+ * calls that may overlap need one each. */
+size_t moe_fp4_latent_attention_workspace_bytes(void);
+int moe_fp4_latent_attention(const moe_fp4_latent_attention_args* args, void* workspace, size_t workspace_bytes,
+                             void* cuda_stream);
 
 /* Block tables and slots of a batch's new tokens in a paged cache.  Request b has
  * n = lengths[b] tokens in the cache and gets t = new_tokens[b] more; tokens are

@@ -111,6 +111,23 @@ def test_scores_that_grow_and_that_are_far_apart():
         check_all(moe.latent_attention(*t, scale), *t, True, scale, what=f"scale {scale}")
 
 
+# items of many keys, cut over the SMs: few queries behind long prefixes, ends of pieces at the items' ends, tiles that see
+# fewer keys than their item, more queries than keys, more sequences than a block's threads
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("q_lens,k_lens,H", [([1], [20000], 1), ([130], [9000], 3), ([3, 200, 1], [7000, 300, 30000], 2),
+                                             ([2500], [2500], 5), ([300, 1, 0, 64] * 10, [3000, 1, 9, 1200] * 10, 3),
+                                             ([4000], [1500], 2), ([1, 2] * 250 + [600], [1, 3] * 250 + [4000], 2),
+                                             ([255] * 7, [1100] * 7, 24), ([1] * 30, [1024 + i for i in range(30)], 1)])
+def test_items_cut_over_the_sms(q_lens, k_lens, H, causal):
+    t = make(q_lens, k_lens, H, seed=len(q_lens), before=2, after=9)
+    ws = torch.full((moe.latent_attention_workspace_bytes(),), 255, dtype=torch.uint8, device=DEV)
+    out = moe.latent_attention(*t, SCALE, causal=causal, workspace=ws)
+    check_all(out, *t, causal, heads=(0, H - 1))
+    ws.fill_(1)
+    assert torch.equal(out[2:2 + sum(q_lens)], moe.latent_attention(*t, SCALE, causal=causal, workspace=ws)[2:2 + sum(q_lens)])
+    moe.ops_check()
+
+
 def test_many_items_an_sm():
     t = make([2000, 1100], [2000, 2300], 64, seed=5)
     out = moe.latent_attention(*t, SCALE)
@@ -162,7 +179,7 @@ def test_offsets_outside_the_rows_are_taken_into_them():
     assert torch.equal(moe.latent_attention(*t[:3], qo, ko, SCALE), want)
 
 
-@pytest.mark.parametrize("q_lens,k_lens,H", [([300], [300], 1), ([2000, 100], [2000, 3000], 24)])
+@pytest.mark.parametrize("q_lens,k_lens,H", [([300], [300], 1), ([2000, 100], [2000, 3000], 24), ([100, 300], [20000, 4000], 1)])
 def test_a_wait_that_runs_out_stores_nothing_wrong(q_lens, k_lens, H):
     t = make(q_lens, k_lens, H)
     want = moe.latent_attention(*t, SCALE)

@@ -43,6 +43,8 @@ REFUSED = {
     "attention: no offsets": lambda: attention(q_offsets=None),
     "attention: scale": lambda: attention(scale=None),
     "attention: causal neither": lambda: attention(causal=BOTH),
+    "attention: small workspace": lambda: attention(workspace=z(moe.latent_attention_workspace_bytes() - 1, dtype=U8)),
+    "attention: workspace's type": lambda: attention(workspace=z(1 << 26)),
     "attention: out's shape": lambda: attention(out=z(8, 4, 192)),
     "attention: out's type": lambda: attention(out=z(8, 4, 128, dtype=F32)),
     "attention: out's strides": lambda: attention(out=z(4, 8, 128).transpose(0, 1)),

@@ -55,13 +55,15 @@ def test_attention(lib):
     base = dict(B=2, H=16, causal=1, scale=0.1, Tq=40, Tk=60, q_stride=16 * 192, q_head_stride=192, kv_stride=16 * 256,
                 kv_head_stride=256, rope_stride=64, q=FAKE, kv=FAKE, k_rope=FAKE, q_offsets=FAKE, k_offsets=FAKE, out=FAKE)
 
-    def call(**kw):
+    def call(work=FAKE, size=1 << 30, **kw):
         a = LatentAttentionArgs()
         for k, v in {**base, **kw}.items():
             setattr(a, k, v)
-        return lib.moe_fp4_latent_attention(ctypes.byref(a), None)
+        return lib.moe_fp4_latent_attention(ctypes.byref(a), work, size, None)
 
-    assert lib.moe_fp4_latent_attention(None, None) == -1
+    assert lib.moe_fp4_latent_attention(None, FAKE, 1 << 30, None) == -1
+    assert call(work=None) == -1 and call(work=FAKE + 16) == -1
+    assert call(size=moe.latent_attention_workspace_bytes() - 1) == -3
     for bad in (dict(B=-1), dict(H=0), dict(H=1025), dict(causal=2), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
                 dict(scale=float("inf")), dict(Tq=-1), dict(Tk=-1), dict(q=None), dict(kv=None), dict(k_rope=None),
                 dict(q_offsets=None), dict(k_offsets=None), dict(out=None), dict(q=FAKE + 8), dict(kv=FAKE + 8),
@@ -98,6 +100,7 @@ def calls(o):
         "attention q_offsets": lambda: attention(q_offsets=on(o, 3, dtype=I32)),
         "attention k_offsets": lambda: attention(k_offsets=on(o, 3, dtype=I32)),
         "attention out": lambda: attention(out=on(o, 8, 4, 128)),
+        "attention workspace": lambda: attention(workspace=on(o, 1 << 26, dtype=U8)),
         "decode cache": lambda: decode(cache=on(o, 8, 64, 576)),
         "decode block_table": lambda: decode(block_table=on(o, 2, 4, dtype=I32)),
         "decode lengths": lambda: decode(lengths=on(o, 2, dtype=I32)),
