@@ -19,10 +19,11 @@
 // warp multiplies its lanes of O, in tensor memory, before it gives P to the MMAs;
 // until then P may grow up to 2^8, which costs bf16 nothing.
 //
-// Shared memory: Q 2 x 3 slabs of [128][64] (96 KB), keys two stages of 3 slabs,
-// values one of 2.  Warps: 0 loads, 1 issues the MMAs (and clears what the last MMA
-// step of values holds behind the sequence's end: a zero of P must not meet an
-// infinity there), 2 finds the pieces of work and hands them to the others, 4..7 and
+// Shared memory: Q 2 x 3 slabs of [128][64] (96 KB) and a ring of 8 slabs, through
+// which 3 of keys and 2 of values go for each step, given back in that order.  (Two
+// stages of keys and one of values take the same 128 KB, but a step's values are
+// then on their way only when the last one's are used: 8192 tokens, 64 heads 1130 us,
+// 1080 without any softmax.)  Warps: 0 loads, 1 issues the MMAs, 2 finds the pieces of work and hands them to the others, 4..7 and
 // 8..11 are the tiles' softmax and results.  Items are dealt out to
 // one CTA an SM; where there are few, by their cost: all items' steps are numbered
 // through, in the order of sequences, heads and queries, and cut into even ranges,
@@ -47,11 +48,10 @@ constexpr int kThreads = 384;
 constexpr int kQ = 128, kK = 128;             // queries and keys of a tile
 constexpr int kSlab = 128 * 128;              // [128 rows][64 elements]
 constexpr int kQSlabs = 3, kVSlabs = 2;
-constexpr int kKStages = 2;
-constexpr int kKStage = kQSlabs * kSlab, kVStage = kVSlabs * kSlab;
-constexpr int kOffK = 2 * kQSlabs * kSlab;
-constexpr int kOffV = kOffK + kKStages * kKStage;
-constexpr int kOffTail = kOffV + kVStage;
+constexpr int kStepSlabs = kQSlabs + kVSlabs;  // of keys, then of values, of a step
+constexpr int kRing = 8;                      // slabs
+constexpr int kOffRing = 2 * kQSlabs * kSlab;
+constexpr int kOffTail = kOffRing + kRing * kSlab;
 constexpr int kSmem = kOffTail + 1024 + 1024;
 static_assert(kSmem <= kSmemMax, "shared memory");
 constexpr uint32_t kCols = 512;               // S of both tiles, O of both
@@ -231,6 +231,7 @@ struct Piece {
   int n, from, to;          // steps of the item, of the piece
   int lim[2], upto[2];      // of either tile: keys that its first query sees, where its steps end
   int slot;                 // of its sums, if it is not the whole item
+  int g;                    // steps of the pieces before it
 };
 constexpr int kHanded = 3;  // pieces on their way
 
@@ -324,11 +325,11 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + kOffTail);
   uint64_t* q_empty = q_full + 1;
-  uint64_t* k_full = q_empty + 1;       // [stage]
-  uint64_t* k_empty = k_full + kKStages;
-  uint64_t* v_full = k_empty + kKStages;
-  uint64_t* v_empty = v_full + 1;
-  uint64_t* s_full = v_empty + 1;       // [tile]
+  uint64_t* k_full = q_empty + 1;       // [step % 2]: the step's keys have landed,
+  uint64_t* v_full = k_full + 2;        // its values,
+  uint64_t* k_empty = v_full + 2;       // and are given back
+  uint64_t* v_empty = k_empty + 2;
+  uint64_t* s_full = v_empty + 2;       // [tile]
   uint64_t* p_full = s_full + 2;        // [tile], four warps
   uint64_t* o_full = p_full + 2;        // [tile]
   uint64_t* o_free = o_full + 2;        // [tile], four warps
@@ -337,15 +338,14 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
   uint64_t* piece_empty = piece_full + kHanded;  // [handed], ten warps
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(piece_empty + kHanded);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  Range* share = reinterpret_cast<Range*>(smem + kOffTail + 256);
+  Range* share = reinterpret_cast<Range*>(smem + kOffTail + 320);
   int64_t* scratch = reinterpret_cast<int64_t*>(smem + kOffTail + 512);
   Piece* handed = reinterpret_cast<Piece*>(smem + kOffTail + 640);   // [handed]
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1), mbar_init(q_empty, 1);
-    for (int s = 0; s < kKStages; ++s) mbar_init(&k_full[s], 1), mbar_init(&k_empty[s], 1);
-    mbar_init(v_full, 1), mbar_init(v_empty, 1);
+    for (int s = 0; s < 8; ++s) mbar_init(&k_full[s], 1);  // (the four pairs)
     for (int t = 0; t < 2; ++t)
       mbar_init(&s_full[t], 1), mbar_init(&p_full[t], 4), mbar_init(&o_full[t], 1), mbar_init(&o_free[t], 4);
     mbar_init(mma_done, 1);
@@ -385,7 +385,15 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     set_registers_fewer<kRegsFew>();
     if (warp == 0) {
       // ---------------- loads ----------------
-      int items = 0, g = 0;  // items with keys, tiles of keys
+      int items = 0, g = 0;  // items with keys, steps
+      // the step's slab j goes where the ring's eighth slab before it was
+      auto given_back = [&](int j) {
+        const int n = g * kStepSlabs + j - kRing, gn = n / kStepSlabs;
+        if (n < 0) return true;
+        return wait(n - gn * kStepSlabs < kQSlabs ? &k_empty[gn & 1] : &v_empty[gn & 1], (gn >> 1) & 1);
+      };
+      auto place = [&](int j) { return smem + kOffRing + (g * kStepSlabs + j) % kRing * kSlab; };
+      int k_steps = 0, v_steps = 0;  // announced
       while (ok && next_piece()) {
         if (w.from >= w.to) continue;
         if (!(ok = wait(q_empty, (items & 1) ^ 1))) break;
@@ -398,48 +406,49 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         }
         __syncwarp();
         ++items;
-        for (int i = w.from; i < w.to; ++i, ++g) {
-          const int s = g % kKStages;
-          if (!(ok = wait(&k_empty[s], ((g / kKStages) & 1) ^ 1))) break;
-          if (!(P.fault && g == 0 && w.from == 0 && w.h == 0) && elect_one()) {
-            uint8_t* st = smem + kOffK + s * kKStage;
-            mbar_expect_tx(&k_full[s], kKStage);
-            tma_load_3d(st, &map_kv, 0, w.h, w.k0 + i * kK, &k_full[s]);
-            tma_load_3d(st + kSlab, &map_kv, 64, w.h, w.k0 + i * kK, &k_full[s]);
-            tma_load_3d(st + 2 * kSlab, &map_rope, 0, 0, w.k0 + i * kK, &k_full[s]);
+        for (int i = w.from; i < w.to && ok; ++i, ++g) {
+          const int row = w.k0 + i * kK;
+          const bool withheld = P.fault && g == 0 && w.from == 0 && w.h == 0;
+          for (int j = 0; j < kStepSlabs; ++j) {
+            if (!(ok = given_back(j))) break;
+            uint64_t* const bar = j < kQSlabs ? &k_full[g & 1] : &v_full[g & 1];
+            if (j == 0 && withheld) continue;
+            if (elect_one()) {
+              if (j == 0 || (j == 1 && withheld)) mbar_expect_tx(bar, kQSlabs * kSlab);
+              if (j == kQSlabs) mbar_expect_tx(bar, kVSlabs * kSlab);
+              // 0, 1: keys, 2: their rotary part, 3, 4: values (which lie behind the keys)
+              if (j == kQSlabs - 1)
+                tma_load_3d(place(j), &map_rope, 0, 0, row, bar);
+              else
+                tma_load_3d(place(j), &map_kv, (j < kQSlabs ? j : j - 1) * 64, w.h, row, bar);
+            }
+            __syncwarp();
+            if (j == 0 || (j == 1 && withheld)) ++k_steps;
+            if (j == kQSlabs) ++v_steps;
           }
-          __syncwarp();
-          if (!(ok = wait(v_empty, (g & 1) ^ 1))) {
-            ++g;  // its keys are under way
-            break;
-          }
-          if (elect_one()) {
-            mbar_expect_tx(v_full, kVStage);
-            tma_load_3d(smem + kOffV, &map_kv, 128, w.h, w.k0 + i * kK, v_full);
-            tma_load_3d(smem + kOffV + kSlab, &map_kv, 192, w.h, w.k0 + i * kK, v_full);
-          }
-          __syncwarp();
         }
       }
       // every issued copy has landed before shared memory is given back
       __syncwarp();
-      for (int q = max(0, g - kKStages); q < g; ++q) wait.drain(&k_full[q % kKStages], (q / kKStages) & 1);
-      if (g > 0) wait.drain(v_full, (g - 1) & 1);
+      for (int q = max(0, k_steps - 2); q < k_steps; ++q) wait.drain(&k_full[q & 1], (q >> 1) & 1);
+      for (int q = max(0, v_steps - 2); q < v_steps; ++q) wait.drain(&v_full[q & 1], (q >> 1) & 1);
       if (items > 0) wait.drain(q_full, (items - 1) & 1);
     } else if (warp == 1) {
       // ---------------- MMAs ----------------
       const uint32_t base = smem_u32(smem);
-      constexpr uint32_t id_pv = idesc_bf16(kQ, kValue, false, true);
-      int items = 0, g = 0, use[2] = {0, 0}, turn[2] = {0, 0};  // of O's and of P's barriers
+      constexpr uint32_t id_pv = idesc_bf16(kQ, kValue, false, true), id_pv_half = idesc_bf16(kQ, kValue / 2, false, true);
+      int items = 0, g = 0, use[2] = {0, 0}, turn[2] = {0, 0};  // items, steps, turns of O's and of P's barriers
       auto keys16 = [&](int i) { return min(kK, (w.nk - i * kK + 15) & ~15); };  // of a tile, to whole MMA steps
-      auto qk = [&](int t, int gk, int i) {
+      // S of tile t with the keys of step gk of the ring, the item's i
+      auto qk = [&](int t, int gk, uint32_t id_qk) {
         if (elect_one()) {
-          const uint32_t q_lo = desc_lo(base + t * kQSlabs * kSlab, 16), id_qk = idesc_bf16(kQ, keys16(i), false, false);
-          const uint32_t k_lo = desc_lo(base + kOffK + (gk % kKStages) * kKStage, 16);
+          const uint32_t q_lo = desc_lo(base + t * kQSlabs * kSlab, 16);
 #pragma unroll
-          for (int k = 0; k < (kNope + kRope) / 16; ++k) {
-            const uint32_t at = ((k / 4) * kSlab + (k % 4) * 32) >> 4;
-            umma_ss(tmem + t * kK, desc(q_lo + at), desc(k_lo + at), id_qk, k > 0);
+          for (int j = 0; j < kQSlabs; ++j) {
+            const uint32_t k_lo = desc_lo(base + kOffRing + (gk * kStepSlabs + j) % kRing * kSlab, 16);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_ss(tmem + t * kK, desc(q_lo + ((j * kSlab + k * 32) >> 4)), desc(k_lo + ((k * 32) >> 4)), id_qk, j > 0 || k > 0);
           }
           umma_commit(&s_full[t]);
         }
@@ -447,28 +456,25 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
       };
       while (ok && next_piece()) {
         if (w.from >= w.to) continue;
-        if (!(ok = wait(q_full, items & 1)) || !(ok = wait(&k_full[g % kKStages], (g / kKStages) & 1))) break;
+        if (!(ok = wait(q_full, items & 1) && wait(&k_full[g & 1], (g >> 1) & 1))) break;
         tmem_fence_after();
+        uint32_t id_qk = idesc_bf16(kQ, keys16(w.from), false, false);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          if (w.from < w.upto[t]) qk(t, g, w.from);
+          if (w.from < w.upto[t]) qk(t, g, id_qk);
         if (elect_one()) {
-          umma_commit(&k_empty[g % kKStages]);
+          umma_commit(&k_empty[g & 1]);
           if (w.to - w.from == 1) umma_commit(q_empty);
         }
         __syncwarp();
         for (int i = w.from; i < w.to && ok; ++i, ++g) {
-          if (!(ok = wait(v_full, g & 1))) break;
-          const int keys = w.nk - i * kK, steps = keys16(i) / 16;
-          if (keys < kK && keys % 16 != 0) {
-            // rows behind the sequence's end that the last MMA step takes in are zeros
-            for (int c = lane; c < (16 * steps - keys) * kVSlabs * 8; c += 32) {
-              const int row = keys + c / (kVSlabs * 8), s = (c >> 3) % kVSlabs;
-              *reinterpret_cast<uint4*>(smem + kOffV + s * kSlab + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async();
-            __syncwarp();
-          }
+          const bool more = i + 1 < w.to;
+          const int steps = keys16(i) / 16;
+          if (more) id_qk = idesc_bf16(kQ, keys16(i + 1), false, false);
+          const uint32_t nv = g * kStepSlabs + kQSlabs;  // the values' slabs
+          const uint32_t v_at[2] = {base + kOffRing + nv % kRing * kSlab, base + kOffRing + (nv + 1) % kRing * kSlab};
+          // (not earlier: they may still be on their way while the keys' MMAs run)
+          if (!(ok = wait(&v_full[g & 1], (g >> 1) & 1))) break;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (i >= w.upto[t] || !ok) continue;
@@ -478,25 +484,37 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
             ++turn[t];
             tmem_fence_after();
             if (elect_one()) {
-              const uint32_t v_lo = desc_lo(base + kOffV, kSlab);
+              const uint32_t o = tmem + kColO + t * kValue, p = tmem + t * kK;
+              if (v_at[1] > v_at[0] && steps == kK / 16) {
+                const uint32_t v_lo = desc_lo(v_at[0], kSlab);
 #pragma unroll
-              for (int k = 0; k < kK / 16; ++k)
-                if (k < steps)
-                  tc::umma_tmem_a(tmem + kColO + t * kValue, tmem + t * kK + 8 * k, desc(v_lo + ((k * 2048) >> 4)), id_pv,
-                                  i > w.from || k > 0);
+                for (int k = 0; k < kK / 16; ++k)
+                  tc::umma_tmem_a(o, p + 8 * k, desc(v_lo + ((k * 2048) >> 4)), id_pv, i > w.from || k > 0);
+              } else {
+                // the ring's last slab and its first, or the sequence's last keys: half of the values at a time.  (A condition
+                // on every MMA of the usual case costs 3% of a long prompt.)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                  const uint32_t v_lo = desc_lo(v_at[u], kSlab);
+#pragma unroll 1
+                  for (int k = 0; k < steps; ++k)
+                    tc::umma_tmem_a(o + u * kValue / 2, p + 8 * k, desc(v_lo + ((k * 2048) >> 4)), id_pv_half, i > w.from || k > 0);
+                }
+              }
               if (i == w.upto[t] - 1) umma_commit(&o_full[t]);
+              // the values are given back behind their last reader, ahead of the keys of the next step
+              if (t == 1 || i >= w.upto[1]) umma_commit(&v_empty[g & 1]);
             }
             __syncwarp();
             if (i + 1 < w.upto[t]) {
-              if (!(ok = wait(&k_full[(g + 1) % kKStages], ((g + 1) / kKStages) & 1))) break;
+              if (!(ok = wait(&k_full[(g + 1) & 1], ((g + 1) >> 1) & 1))) break;
               tmem_fence_after();
-              qk(t, g + 1, i + 1);
+              qk(t, g + 1, id_qk);
             }
           }
           if (!ok) break;
-          if (elect_one()) {
-            umma_commit(v_empty);
-            if (i + 1 < w.to) umma_commit(&k_empty[(g + 1) % kKStages]);
+          if (more && elect_one()) {
+            umma_commit(&k_empty[(g + 1) & 1]);
             if (i + 2 == w.to) umma_commit(q_empty);
           }
           __syncwarp();
@@ -511,7 +529,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
       // ---------------- the share's pieces ----------------
       Pieces all;
       all.start(P, *share);
-      int count = 0, flags = 0;
+      int count = 0, steps = 0, flags = 0;
       int4 unfinished = make_int4(0, 0, 0, 0);
       while (true) {
         Piece p{};
@@ -519,6 +537,8 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         const int s = count % kHanded;
         if (more) {
           p.slot = slot0 + (count > 0 ? 1 : 0);
+          p.g = steps;
+          steps += p.to - p.from;
           flags |= kHasPieces | (count == 0 && p.from > 0 ? kContinues : 0);
           if (p.to < p.n) {
             flags |= kUnfinished | (count == 0 ? kOnePiece : 0);
@@ -601,6 +621,17 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
           tc::tmem_st32(s_col + 32 * half, p);
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const int keys = w.nk - i * kK;
+        if (keys < kK && keys % 16 != 0) {
+          // Rows behind the sequence's end that the last MMA step takes in are zeros: whatever is there must not meet a
+          // zero of P.  (Both tiles' warps may write them.)
+          const int g = w.g + i - w.from, nv = g * kStepSlabs + kQSlabs;
+          if (!(ok = wait(&v_full[g & 1], (g >> 1) & 1))) break;
+          uint8_t* const v = smem + kOffRing + (nv + ((warp >> 1) & 1)) % kRing * kSlab + (lane & 7) * 16;
+          for (int r = keys + (lane >> 3) + 4 * (warp & 1); r < ((keys + 15) & ~15); r += 8)
+            *reinterpret_cast<uint4*>(v + r * 128) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async();
+        }
         tmem_wait_st();
         tmem_fence_before();
         __syncwarp();
