@@ -5,6 +5,8 @@
 
 #include <cuda.h>
 
+#include <cmath>
+
 #include "moe_fp4_internal.cuh"
 #include "mxfp4_ops.cuh"
 #include "ptx_sm103.cuh"
@@ -171,6 +173,10 @@ __device__ __forceinline__ bool any_at_barrier(bool v, int id, int threads) {
 }
 
 }  // namespace latent
+
+constexpr int kMaxSequences = 1 << 24;  // every CTA looks through them
+// the scale, and its multiple that exp2 takes
+inline bool finite_scale(float scale) { return std::isfinite(scale * 1.4426950408889634f); }
 
 bool make_map_3d(CUtensorMap* m, const void* base, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
                  const uint32_t (&box)[3]);  // bf16, 128-byte swizzle

@@ -84,14 +84,17 @@ constexpr int kHasPieces = 1, kContinues = 2, kUnfinished = 4, kOnePiece = 8;
 struct Sequence {
   int q0, nq, k0, nk;
 };
-__device__ __forceinline__ Sequence sequence_at(const AttentionParams& P, int b) {
-  Sequence s{};
-  if (b < P.B) {
-    s.q0 = min(max(P.q_offsets[b], 0), P.Tq), s.nq = max(0, min(P.q_offsets[b + 1], P.Tq) - s.q0);
-    s.k0 = min(max(P.k_offsets[b], 0), P.Tk), s.nk = max(0, min(P.k_offsets[b + 1], P.Tk) - s.k0);
-  }
+// its four offsets as they are, and taken into the rows
+__device__ __forceinline__ int4 offsets_at(const AttentionParams& P, int b) {
+  return b < P.B ? make_int4(P.q_offsets[b], P.q_offsets[b + 1], P.k_offsets[b], P.k_offsets[b + 1]) : make_int4(0, 0, 0, 0);
+}
+__device__ __forceinline__ Sequence sequence_of(const AttentionParams& P, int4 o) {
+  Sequence s;
+  s.q0 = min(max(o.x, 0), P.Tq), s.nq = max(0, min(o.y, P.Tq) - s.q0);
+  s.k0 = min(max(o.z, 0), P.Tk), s.nk = max(0, min(o.w, P.Tk) - s.k0);
   return s;
 }
+__device__ __forceinline__ Sequence sequence_at(const AttentionParams& P, int b) { return sequence_of(P, offsets_at(P, b)); }
 __device__ __forceinline__ int items_of(const Sequence& s) { return s.nq / kRows + (s.nq % kRows != 0); }
 
 // Steps (tiles of keys) of item t of a sequence's head: what its last query sees.
@@ -133,24 +136,31 @@ struct Range {
 };
 constexpr int kManyItems = 6;  // items a CTA
 
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64_t* total) {  // inclusive
+// Inclusive sums over the block's threads; *total: over all of them.  scratch: two
+// words for each warp.
+__device__ __forceinline__ longlong2 block_scan(longlong2 v, longlong2* scratch, longlong2* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) {
-    const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, s);
-    if (lane >= s) v += u;
+    const long long x = __shfl_up_sync(0xFFFFFFFFu, v.x, s), y = __shfl_up_sync(0xFFFFFFFFu, v.y, s);
+    if (lane >= s) v.x += x, v.y += y;
   }
   if (lane == 31) scratch[warp] = v;
   __syncthreads();
-  int64_t all = 0;
+  longlong2 all = make_longlong2(0, 0);
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w == warp) v += all;
-    all += scratch[w];
+    if (w == warp) v.x += all.x, v.y += all.y;
+    all.x += scratch[w].x, all.y += scratch[w].y;
   }
   __syncthreads();
   *total = all;
   return v;
+}
+
+// a / b, by a division of 32 bits where that does
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (uint64_t)a >> 32 == 0 && (uint64_t)b >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // This CTA's range, to *out in shared memory; whole block.
@@ -159,49 +169,43 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64
 // sequence's last queries first, its heads side by side: what runs at the same time
 // then reads the same keys (8192 tokens, 64 heads, 13.5 items a CTA: 1129 us, 1285 with
 // even ranges of whole heads; 4608 tokens, 7.6 items: 393 and 449).
-__device__ void find_range(const AttentionParams& P, int range, int64_t* scratch, Range* out) {
-  int64_t total = 0, sum = 0, items = 0;
+__device__ void find_range(const AttentionParams& P, int range, longlong2* scratch, Range* out) {
+  const bool once = P.B <= kThreads;  // each sequence has its thread
   Sequence s{};
-  int64_t each = 0, upto = 0;  // a head's cost of this thread's sequence; the sequences' up to it
+  longlong2 sum = make_longlong2(0, 0), total, upto;  // items, and their cost
+  int64_t each = 0;                                   // a head's cost of this thread's sequence
   if (threadIdx.x == 0) out->from = out->to = Place{P.B, 0, 0, 0};
-  if (P.B <= kThreads) {
-    s = sequence_at(P, threadIdx.x);
-    block_scan((int64_t)items_of(s) * P.H, scratch, &items);
-  } else {
-    for (int b = threadIdx.x; b < P.B; b += kThreads) {
-      s = sequence_at(P, b);
-      items += (int64_t)items_of(s) * P.H;
-      sum += cost_before(P, s, items_of(s)) * P.H;
-    }
-    block_scan(items, scratch, &items);
+  auto look = [&](int b) {
+    s = sequence_at(P, b);
+    each = cost_before(P, s, items_of(s));
+    return make_longlong2((long long)items_of(s) * P.H, each * P.H);
+  };
+  for (int b = threadIdx.x; b < (once ? kThreads : P.B); b += kThreads) {
+    const longlong2 v = look(b);
+    sum.x += v.x, sum.y += v.y;
   }
-  const bool strided = items >= kManyItems * gridDim.x;
+  upto = block_scan(sum, scratch, &total);
+  const bool strided = total.x >= (long long)kManyItems * gridDim.x;
   if (threadIdx.x == 0) out->strided = strided;
-  if (!strided) {
-    if (P.B <= kThreads) {
-      each = cost_before(P, s, items_of(s));
-      upto = block_scan(each * P.H, scratch, &total);
-    } else {
-      block_scan(sum, scratch, &total);
+  if (strided) {
+    if (threadIdx.x == 0) {
+      out->from = Place{0, 0, 0, 0};
+      out->first = sequence_at(P, 0);
     }
-    const int64_t even = total / P.ranges, rest = total % P.ranges;
+  } else {
+    const int64_t even = quotient(total.y, P.ranges), rest = total.y - even * P.ranges;
     int64_t at[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) at[i] = even * (range + i) + min((int64_t)(range + i), rest);
     int64_t before = 0;
     for (int b0 = 0; b0 < P.B; b0 += kThreads) {
-      const int b = b0 + threadIdx.x;
-      int64_t all = total;
-      if (P.B > kThreads) {
-        s = sequence_at(P, b);
-        each = cost_before(P, s, items_of(s));
-        upto = block_scan(each * P.H, scratch, &all);
-      }
-      const int64_t end = before + upto, begin = end - each * P.H;
-#pragma unroll
+      longlong2 all = total;
+      if (!once) upto = block_scan(look(b0 + threadIdx.x), scratch, &all);
+      const int64_t end = before + upto.y, begin = end - each * P.H;
+#pragma unroll 1
       for (int i = 0; i < 2; ++i) {
         if (!(begin <= at[i] && at[i] < end)) continue;
-        const int64_t y = at[i] - begin, h = y / each, z = y - h * each;
+        const int64_t y = at[i] - begin, h = quotient(y, each), z = y - h * each;
         int lo = 0, hi = items_of(s);  // the last item that begins at or before z
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
@@ -212,15 +216,12 @@ __device__ void find_range(const AttentionParams& P, int range, int64_t* scratch
         }
         const int n = steps_of(P, s, lo);
         const int x = (int)min(z - cost_before(P, s, lo), (int64_t)n - 1);
-        (i == 0 ? out->from : out->to) = Place{b, (int)h, lo, n > kMinSplit ? x - x % kCut : 0};
+        (i == 0 ? out->from : out->to) = Place{b0 + (int)threadIdx.x, (int)h, lo, n > kMinSplit ? x - x % kCut : 0};
         if (i == 0) out->first = s;
       }
-      before += all;
+      before += all.y;
       if (before > at[1]) break;
     }
-  } else if (threadIdx.x == 0) {
-    out->from = Place{0, 0, 0, 0};
-    out->first = sequence_at(P, 0);
   }
   __syncthreads();
 }
@@ -241,10 +242,11 @@ struct Pieces {
   Place at, end;      // at.t counts a sequence's items of all heads where they are dealt out in turn
   bool begun, strided;
   int base;
-  Sequence mine, s;   // this lane's sequence, the current one
+  int4 mine;          // this lane's sequence's offsets (as loaded: nothing waits for them here)
+  Sequence s;         // the current one
   __device__ __forceinline__ void load(const AttentionParams& P) {
     base = at.b;
-    mine = sequence_at(P, base + (threadIdx.x & 31));
+    mine = offsets_at(P, base + (threadIdx.x & 31));
   }
   __device__ __forceinline__ void start(const AttentionParams& P, const Range& r) {
     at = r.from, end = r.to, s = r.first, strided = r.strided, begun = false;
@@ -253,8 +255,9 @@ struct Pieces {
   }
   __device__ __forceinline__ void next_sequence(const AttentionParams& P) {
     if (++at.b >= base + 32) load(P);
-    s.q0 = __shfl_sync(0xFFFFFFFFu, mine.q0, at.b - base), s.nq = __shfl_sync(0xFFFFFFFFu, mine.nq, at.b - base);
-    s.k0 = __shfl_sync(0xFFFFFFFFu, mine.k0, at.b - base), s.nk = __shfl_sync(0xFFFFFFFFu, mine.nk, at.b - base);
+    const int l = at.b - base;
+    s = sequence_of(P, make_int4(__shfl_sync(0xFFFFFFFFu, mine.x, l), __shfl_sync(0xFFFFFFFFu, mine.y, l),
+                                 __shfl_sync(0xFFFFFFFFu, mine.z, l), __shfl_sync(0xFFFFFFFFu, mine.w, l)));
   }
   __device__ __forceinline__ bool next(const AttentionParams& P, Piece& p) {
     int t;
@@ -339,7 +342,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(piece_empty + kHanded);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   Range* share = reinterpret_cast<Range*>(smem + kOffTail + 320);
-  int64_t* scratch = reinterpret_cast<int64_t*>(smem + kOffTail + 512);
+  longlong2* scratch = reinterpret_cast<longlong2*>(smem + kOffTail + 384);
   Piece* handed = reinterpret_cast<Piece*>(smem + kOffTail + 640);   // [handed]
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
@@ -792,12 +795,12 @@ int moe_fp4_latent_attention(const moe_fp4_latent_attention_args* args, void* wo
                              void* cuda_stream) {
   if (!args) return MOE_FP4_ERR_INVALID_ARG;
   const moe_fp4_latent_attention_args a = *args;
-  if (a.B < 0 || a.H < 1 || a.H > MOE_FP4_LATENT_MAX_HEADS || a.Tq < 0 || a.Tk < 0 || !(a.scale > 0.f) || a.scale > 3e38f ||
+  if (a.B < 0 || a.H < 1 || a.H > MOE_FP4_LATENT_MAX_HEADS || a.Tq < 0 || a.Tk < 0 || !(a.scale > 0.f) || !finite_scale(a.scale) ||
       a.causal < 0 || a.causal > 1)
     return MOE_FP4_ERR_INVALID_ARG;
   // items and TMA coordinates are counted in 32 bits
   const int64_t tiles = a.Tq / (2 * kQ) + std::min<int64_t>(a.B, a.Tq);
-  if (a.Tq > INT32_MAX - 4 * kQ || a.Tk > INT32_MAX - 2 * kK || tiles * a.H >= (1LL << 30)) return MOE_FP4_ERR_UNSUPPORTED;
+  if (a.B > kMaxSequences || a.Tq > INT32_MAX - 4 * kQ || a.Tk > INT32_MAX - 2 * kK || tiles * a.H >= (1LL << 30)) return MOE_FP4_ERR_UNSUPPORTED;
   if (a.B == 0 || a.Tq == 0) return MOE_FP4_OK;
   const auto rows = [](const void* p, int64_t stride, int64_t head_stride, int64_t width) {
     return p && ((uintptr_t)p & 15) == 0 && stride >= width && head_stride >= width && stride % 8 == 0 && head_stride % 8 == 0 &&

@@ -492,9 +492,9 @@ int moe_fp4_fp8_linear(const moe_fp4_mm_dims* dims, const void* x, int x_type, i
  *   out      bf16 [B, H, 512], contiguous, 16-byte aligned
  * A length below 0 or above width * page is taken as the nearest of the two, a page
  * outside the cache reads as zeros; both set error bit 1 (moe_fp4_ops_check).
- * pages * page and width * page below 2^31. */
+ * pages * page and width * page below 2^31; scale finite. */
 typedef struct moe_fp4_latent_decode_args {
-  int32_t B, H, page, pages, width;  /* B >= 0; H 1 .. 1024 */
+  int32_t B, H, page, pages, width;  /* B 0 .. 2^24; H 1 .. 1024 */
   float scale;
   int64_t q_stride, q_head_stride, table_stride;
   const void *q, *cache;
@@ -526,7 +526,7 @@ int moe_fp4_latent_decode(const moe_fp4_latent_decode_args* args, void* workspac
  *   out       bf16 [Tq, H, 128], contiguous
  * All bases 16-byte aligned, strides multiples of 8 elements; scale positive. */
 typedef struct moe_fp4_latent_attention_args {
-  int32_t B, H, causal;              /* B >= 0; H 1 .. 1024 */
+  int32_t B, H, causal;              /* B 0 .. 2^24; H 1 .. 1024 */
   float scale;
   int64_t Tq, Tk;
   int64_t q_stride, q_head_stride, kv_stride, kv_head_stride, rope_stride;

@@ -187,3 +187,28 @@ def test_a_wait_that_runs_out_stores_nothing_wrong(q_lens, k_lens, H):
     planted(lambda: moe.latent_attention(*t, SCALE, out=out))
     right_or_untouched(out, want, torch.full_like(want, 7.0))
     assert torch.equal(moe.latent_attention(*t, SCALE), want)
+
+
+def test_places_beyond_32_bits():
+    """keys whose elements lie beyond 2^32"""
+    H, n = 128, 300
+    t = make([n], [n], H, seed=7)
+    want = moe.latent_attention(*t, SCALE)
+    rows = 2 ** 32 // (H * 256) + 500
+    kv = torch.empty(rows, H, 256, dtype=BF, device=DEV)
+    rope = torch.empty(rows, 64, dtype=BF, device=DEV)
+    kv[rows - n:], rope[rows - n:] = t[1], t[2]
+    assert torch.equal(moe.latent_attention(t[0], kv, rope, t[3], offsets([n], rows - n), SCALE), want)
+    moe.ops_check()
+
+
+def test_two_streams_at_once():
+    a, b = make([700, 70], [9000, 70], 3, seed=1), make([300] * 9, [500] * 9, 24, seed=2)
+    wa, wb = moe.latent_attention(*a, SCALE), moe.latent_attention(*b, SCALE)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        ga, gb = moe.latent_attention(*a, SCALE, stream=one), moe.latent_attention(*b, SCALE, stream=two)
+        torch.cuda.synchronize()
+        assert torch.equal(ga, wa) and torch.equal(gb, wb)
+    moe.ops_check()

@@ -151,3 +151,29 @@ def test_a_wait_that_runs_out_stores_nothing_wrong(lens, H, page):
     planted(lambda: moe.latent_decode(q, cache, table, lengths, SCALE, out=out, workspace=ws))
     right_or_untouched(out, want, torch.full_like(want, 7.0))
     assert torch.equal(moe.latent_decode(q, cache, table, lengths, SCALE, workspace=ws), want)
+
+
+def test_places_beyond_32_bits():
+    """pages whose elements and bytes lie beyond 2^32"""
+    page, lens, H = 64, [300, 129], 16
+    q, small, table, lengths = make(lens, H, page)
+    cache = torch.empty(2 ** 32 // (576 * page) + 200, page, 576, dtype=torch.bfloat16, device=DEV)
+    at = cache.shape[0] - small.shape[0]
+    cache[at:] = small
+    used = table >= 0
+    far = torch.where(used, table + at, table).to(torch.int32)
+    want = moe.latent_decode(q, small, table, lengths, SCALE)
+    assert torch.equal(moe.latent_decode(q, cache, far, lengths, SCALE), want)
+    moe.ops_check()
+
+
+def test_two_streams_at_once():
+    a, b = make([5000, 70], 64, 64, seed=1), make([900] * 20, 24, 16, seed=2)
+    wa, wb = moe.latent_decode(*a, SCALE), moe.latent_decode(*b, SCALE)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        ga, gb = moe.latent_decode(*a, SCALE, stream=one), moe.latent_decode(*b, SCALE, stream=two)
+        torch.cuda.synchronize()
+        assert torch.equal(ga, wa) and torch.equal(gb, wb)
+    moe.ops_check()

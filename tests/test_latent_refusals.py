@@ -40,12 +40,12 @@ def test_decode(lib):
     need = moe.latent_decode_workspace_bytes(16)
     assert need > 0 and moe.latent_decode_workspace_bytes(0) == 0 and moe.latent_decode_workspace_bytes(1025) == 0
     for bad in (dict(B=-1), dict(H=0), dict(H=1025), dict(page=0), dict(page=8), dict(page=40), dict(page=-64), dict(pages=0),
-                dict(width=0), dict(scale=float("nan")), dict(table_stride=3), dict(q=None), dict(cache=None), dict(table=None),
+                dict(width=0), dict(scale=float("nan")), dict(scale=float("-inf")), dict(scale=3e38), dict(table_stride=3), dict(q=None), dict(cache=None), dict(table=None),
                 dict(lengths=None), dict(out=None), dict(q=FAKE + 8), dict(cache=FAKE + 2), dict(table=FAKE + 2),
                 dict(lengths=FAKE + 2), dict(out=FAKE + 8), dict(q_stride=575), dict(q_stride=16 * 576 + 4),
                 dict(q_head_stride=570), dict(q_head_stride=580), dict(q_stride=1 << 39), dict(work=None), dict(work=FAKE + 16)):
         assert call(**bad) == -1, bad
-    for big in (dict(pages=1 << 25), dict(width=1 << 25, table_stride=1 << 25), dict(B=1 << 30)):
+    for big in (dict(pages=1 << 25), dict(width=1 << 25, table_stride=1 << 25), dict(B=1 << 30), dict(B=(1 << 24) + 1)):
         assert call(**big) == -2, big
     assert call(size=need - 1) == -3
     assert call(B=0, q=None, cache=None, work=None) == 0
@@ -65,13 +65,13 @@ def test_attention(lib):
     assert call(work=None) == -1 and call(work=FAKE + 16) == -1
     assert call(size=moe.latent_attention_workspace_bytes() - 1) == -3
     for bad in (dict(B=-1), dict(H=0), dict(H=1025), dict(causal=2), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
-                dict(scale=float("inf")), dict(Tq=-1), dict(Tk=-1), dict(q=None), dict(kv=None), dict(k_rope=None),
+                dict(scale=float("inf")), dict(scale=3e38), dict(Tq=-1), dict(Tk=-1), dict(q=None), dict(kv=None), dict(k_rope=None),
                 dict(q_offsets=None), dict(k_offsets=None), dict(out=None), dict(q=FAKE + 8), dict(kv=FAKE + 8),
                 dict(k_rope=FAKE + 8), dict(out=FAKE + 8), dict(q_offsets=FAKE + 2), dict(k_offsets=FAKE + 2), dict(q_stride=188),
                 dict(q_stride=196), dict(q_head_stride=184), dict(kv_stride=248), dict(kv_head_stride=260), dict(rope_stride=56),
                 dict(rope_stride=66), dict(q_stride=1 << 39)):
         assert call(**bad) == -1, bad
-    for big in (dict(Tq=2**31), dict(Tk=2**31), dict(Tq=2**31 - 1000, H=1024), dict(B=2**31 - 1, Tq=2**30)):
+    for big in (dict(Tq=2**31), dict(Tk=2**31), dict(Tq=2**31 - 1000, H=1024), dict(B=2**31 - 1, Tq=2**30), dict(B=2**24 + 1)):
         assert call(**big) == -2, big
     assert call(Tq=0, q=None, kv=None, out=None) == 0 and call(B=0, q=None) == 0
 
