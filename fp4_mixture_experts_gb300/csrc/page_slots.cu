@@ -9,7 +9,8 @@
 // the tokens, finding a token's request by bisection.  A page's first new token
 // enters it in the table; entries that this call enters are read by nobody in it.
 //
-// Latency bounds it: 32 requests of a token each take 3 us.
+// Latency bounds it: 32 requests of a token each take 3.2 us, 256 of 131072 tokens
+// together 6.5, 8192 requests 36.
 #include <algorithm>
 
 #include "moe_fp4_internal.cuh"
