@@ -137,9 +137,10 @@ struct Place {
 struct Range {
   Place from, to;
   Sequence first;
-  int strided;
+  int strided, snake;
 };
-constexpr int kManyItems = 6;  // items a CTA
+constexpr int kManyItems = 6;   // items a CTA
+constexpr int kLongSequence = 8;  // items a sequence's head, in the mean
 
 // Inclusive sums over the block's threads; *total: over all of them.  scratch: two
 // words for each warp.
@@ -173,7 +174,10 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 // With kManyItems items for each CTA they stay whole and are dealt out in turn, a
 // sequence's last queries first, its heads side by side: what runs at the same time
 // then reads the same keys (8192 tokens, 64 heads, 13.5 items a CTA: 1129 us, 1285 with
-// even ranges of whole heads; 4608 tokens, 7.6 items: 393 and 449).
+// even ranges of whole heads; 4608 tokens, 7.6 items: 393 and 449).  Under a causal
+// mask a long sequence's items cost less one after the other, so that every second
+// round is dealt out backwards (4608 tokens 343 -> 321 us, 8192 974 -> 936, 16384 with 16 heads
+// 1025 -> 924; 32 sequences of 2 items 126 -> 131, so these are not).
 __device__ void find_range(const AttentionParams& P, int range, longlong2* scratch, Range* out) {
   const bool once = P.B <= kThreads;  // each sequence has its thread
   Sequence s{};
@@ -191,7 +195,10 @@ __device__ void find_range(const AttentionParams& P, int range, longlong2* scrat
   }
   upto = block_scan(sum, scratch, &total);
   const bool strided = total.x >= (long long)kManyItems * gridDim.x;
-  if (threadIdx.x == 0) out->strided = strided;
+  if (threadIdx.x == 0) {
+    out->strided = strided;
+    out->snake = P.causal && total.x >= (long long)kLongSequence * P.B * P.H;
+  }
   if (strided) {
     if (threadIdx.x == 0) {
       out->from = Place{0, 0, 0, 0};
@@ -244,8 +251,9 @@ constexpr int kHanded = 3;  // pieces on their way
 // The pieces of a CTA's share, item by item; one warp walks them and holds 32
 // sequences, one a lane.
 struct Pieces {
-  Place at, end;      // at.t counts a sequence's items of all heads where they are dealt out in turn
+  Place at, end;      // at.t counts a sequence's items of all heads where they are dealt out in turn (begun: to an even one next)
   bool begun, strided;
+  int step[2];        // to the next item of those dealt out in turn, from an even and from an odd one
   int base;
   int4 mine;          // this lane's sequence's offsets (as loaded: nothing waits for them here)
   Sequence s;         // the current one
@@ -255,7 +263,10 @@ struct Pieces {
   }
   __device__ __forceinline__ void start(const AttentionParams& P, const Range& r) {
     at = r.from, end = r.to, s = r.first, strided = r.strided, begun = false;
-    if (strided) at.t = (int)blockIdx.x - (int)gridDim.x;
+    const int n = gridDim.x, mine = blockIdx.x;
+    step[0] = r.snake ? 2 * (n - 1 - mine) + 1 : n;
+    step[1] = r.snake ? 2 * mine + 1 : n;
+    if (strided) at.t = mine - step[1], begun = true;
     load(P);  // (needed from the second sequence on)
   }
   __device__ __forceinline__ void next_sequence(const AttentionParams& P) {
@@ -268,7 +279,8 @@ struct Pieces {
     int t;
     bool last = false;
     if (strided) {
-      at.t += gridDim.x;
+      at.t += begun ? step[1] : step[0];
+      begun = !begun;
       int count;
       while (at.b < P.B && at.t >= (count = items_of(s) * P.H)) {
         at.t -= count;
