@@ -712,60 +712,78 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
 }
 
 // The pieces of items that several ranges share, joined in the ranges' order: a
-// CTA an item and eight elements of its queries' results, a query a thread.
-constexpr int kJoinChunks = kValue / 8;
+// CTA an item and eight elements of its queries' results, a query a thread, the
+// loads of kJoinAhead pieces at a time on their way (500 queries behind 20000 tokens, one
+// head, 40 pieces an item: 34 us, 52 with one at a time).
+constexpr int kJoinChunks = kValue / 8, kJoinAhead = 4;
 __global__ void __launch_bounds__(kRows) latent_attention_join_kernel(AttentionParams P) {
   griddep_begin();
-  __shared__ int flags[kMaxRanges];
-  __shared__ uint32_t found[kMaxRanges / 32];
-  const int r0 = threadIdx.x;  // (kRows threads, a range each)
-  const int4 info = r0 < P.ranges ? P.info[r0] : make_int4(0, 0, 0, 0);
-  flags[r0] = info.x;
-  // an item's first piece: it begins the item and leaves it unfinished
-  const bool first = (info.x & kUnfinished) && !((info.x & kContinues) && (info.x & kOnePiece));
-  const uint32_t mask = __ballot_sync(0xFFFFFFFFu, first);
-  if ((r0 & 31) == 0) found[r0 >> 5] = mask;
+  constexpr int kWords = kMaxRanges / 32;
+  __shared__ uint32_t first[kWords], has[kWords], ends[kWords];  // bits of the ranges
+  __shared__ int busy[kMaxRanges];    // the ranges that have pieces
+  __shared__ int4 chains[kMaxRanges]; // of each cut item: its first range, that one's slot and place in busy, its pieces
+  const int mine = threadIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;  // (kRows threads, a range each)
+  const int4 info = mine < P.ranges ? P.info[mine] : make_int4(0, 0, 0, 0);
+  const bool busy_range = info.x & kHasPieces, one = info.x & kOnePiece;
+  // an item's first piece begins it and leaves it unfinished; the first pieces of the ranges behind follow, up to the
+  // first that ends it
+  const bool begins = (info.x & kUnfinished) && !((info.x & kContinues) && one);
+  const uint32_t f = __ballot_sync(0xFFFFFFFFu, begins), h = __ballot_sync(0xFFFFFFFFu, busy_range);
+  const uint32_t e = __ballot_sync(0xFFFFFFFFu, busy_range && !((info.x & kUnfinished) && one));
+  if (lane == 0) first[warp] = f, has[warp] = h, ends[warp] = e;
   __syncthreads();
-  int count = 0;
+  const uint32_t below = (1u << lane) - 1;
+  int count = 0, at = __popc(f & below), place = __popc(h & below), pieces = 1;
+  bool open = true;  // the item's end has not been met
 #pragma unroll
-  for (int k = 0; k < kMaxRanges / 32; ++k) count += __popc(found[k]);
-  const int row = threadIdx.x, warp = threadIdx.x >> 5;
-  for (int item = blockIdx.x; item < count * kJoinChunks; item += gridDim.x) {
-    int skip = item / kJoinChunks, r = 0;
-    const int c = item % kJoinChunks;
-    for (int k = 0; k < kMaxRanges / 32; ++k) {
-      const int here = __popc(found[k]);
-      if (skip < here) {
-        r = 32 * k + __fns(found[k], 0, skip + 1);
-        break;
-      }
-      skip -= here;
+  for (int k = 0; k < kWords; ++k) {
+    if (k < warp) at += __popc(first[k]), place += __popc(has[k]);
+    count += __popc(first[k]);
+    if (k >= warp && open) {
+      const uint32_t behind = k == warp ? ~(below << 1 | 1u) : 0xFFFFFFFFu, end = ends[k] & behind;
+      open = end == 0;
+      pieces += __popc(has[k] & behind & (open ? 0xFFFFFFFFu : end ^ (end - 1)));
     }
-    const int4 what = P.info[r];
+  }
+  if (busy_range) busy[place] = mine;
+  if (begins) chains[at] = make_int4(mine, 2 * mine + (one ? 0 : 1), place, pieces);
+  __syncthreads();
+  const int row = threadIdx.x;
+  for (int item = blockIdx.x; item < count * kJoinChunks; item += gridDim.x) {
+    const int c = item % kJoinChunks;
+    const int4 chain = chains[item / kJoinChunks];
+    const int pieces = chain.w;
+    const int4 what = P.info[chain.x];
     float o[8] = {}, l = 0.f, top = -INFINITY;
     bool complete = true;
-    auto add = [&](int64_t slot) {
-      complete &= P.done[slot * 8 + warp] != 0;
-      const float2 ml = P.ml[slot * kRows + row];
-      const float4* const s = P.sums + (slot * (kValue / 4) + 2 * c) * kRows + row;
-      const float4 a = s[0], b = s[kRows];
-      const float to = fmaxf(top, ml.x), off = to == -INFINITY ? 0.f : to;
-      const float f = exp2f(ml.x - off), was = exp2f(top - off);
-      // (a piece without a step for the query's tile holds no sums)
-      const bool has = ml.x > -INFINITY || ml.y != 0.f;
-      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    for (int k0 = 0; k0 < pieces; k0 += kJoinAhead) {
+      float2 ml[kJoinAhead];
+      float4 v[kJoinAhead][2];
+      int done[kJoinAhead];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = o[j] * was + (has ? f * v[j] : 0.f);
-      l = l * was + f * ml.y;
-      top = to;
-    };
-    add(2 * r + ((flags[r] & kOnePiece) ? 0 : 1));
-    while (true) {  // the first pieces of the ranges behind, up to the one that ends the item
-      do ++r;
-      while (r < P.ranges && !(flags[r] & kHasPieces));
-      if (r >= P.ranges) break;
-      add(2 * r);
-      if (!((flags[r] & kUnfinished) && (flags[r] & kOnePiece))) break;
+      for (int k = 0; k < kJoinAhead; ++k) {
+        if (k0 + k < pieces) {
+          const int64_t slot = k0 + k == 0 ? chain.y : 2 * busy[chain.z + k0 + k];
+          done[k] = P.done[slot * 8 + warp];
+          ml[k] = P.ml[slot * kRows + row];
+          const float4* const s = P.sums + (slot * (kValue / 4) + 2 * c) * kRows + row;
+          v[k][0] = s[0], v[k][1] = s[kRows];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kJoinAhead; ++k) {
+        if (k0 + k >= pieces) break;
+        complete &= done[k] != 0;
+        const float to = fmaxf(top, ml[k].x), off = to == -INFINITY ? 0.f : to;
+        const float f = exp2f(ml[k].x - off), was = exp2f(top - off);
+        // (a piece without a step for the query's tile holds no sums)
+        const bool sums = ml[k].x > -INFINITY || ml[k].y != 0.f;
+        const float e[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = o[j] * was + (sums ? f * e[j] : 0.f);
+        l = l * was + f * ml[k].y;
+        top = to;
+      }
     }
     if (!complete || row >= what.z) continue;  // a wait ran out; behind the item's last query
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
@@ -775,6 +793,7 @@ __global__ void __launch_bounds__(kRows) latent_attention_join_kernel(AttentionP
     *reinterpret_cast<uint4*>(P.out + ((int64_t)(what.y + row) * P.H + what.w) * kValue + 8 * c) = make_uint4(v[0], v[1], v[2], v[3]);
   }
 }
+static_assert(kMaxRanges == kRows, "a thread looks at a range");
 
 // The kernel's limits on the current device, once; an error if it was compiled to
 // fewer registers than its split needs (the softmax's warps would wait for ever).
