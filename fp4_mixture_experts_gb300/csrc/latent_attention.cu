@@ -68,6 +68,12 @@ constexpr int kCut = 4;                       // where: at multiples of this
 constexpr int kMaxRanges = 256;
 constexpr int kRows = 2 * kQ;                 // queries of an item
 
+// Sequences of few queries and keys, which have a kernel of their own.
+constexpr int kFewQueries = 8, kFewKeys = 32, kFewItems = 12;  // items an SM
+__host__ __device__ inline bool few(int64_t nq, int64_t nk) {
+  return nq <= kFewQueries && nk <= kFewKeys;
+}
+
 struct AttentionParams {
   const int32_t* q_offsets;
   const int32_t* k_offsets;
@@ -79,6 +85,7 @@ struct AttentionParams {
   float4* sums;        // [slot][32][queries] of 4 elements
   int B, H, Tq, Tk;
   int ranges, causal;
+  int others;          // sequences of few queries and keys are the other kernel's
   float scale_log2;
   int fault;
   uint64_t wait_ns;
@@ -97,6 +104,7 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionParams& P, int4 o
   Sequence s;
   s.q0 = min(max(o.x, 0), P.Tq), s.nq = max(0, min(o.y, P.Tq) - s.q0);
   s.k0 = min(max(o.z, 0), P.Tk), s.nk = max(0, min(o.w, P.Tk) - s.k0);
+  if (P.others && few(s.nq, s.nk)) s.nq = 0;
   return s;
 }
 __device__ __forceinline__ Sequence sequence_at(const AttentionParams& P, int b) { return sequence_of(P, offsets_at(P, b)); }
@@ -711,6 +719,107 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
   }
 }
 
+// ---- sequences of few queries and keys ----
+// A tile of 128 queries and 128 keys of a head takes the kernel above ~3.5 us on an SM,
+// however few of them there are.  Here a warp takes a head of a sequence, four
+// queries at a time, all its keys at once: for S a lane has a key and reads its row,
+// the queries come from shared memory (fp32, the same word for all lanes); for P V a
+// lane has four elements of the values and P comes by shuffles.  (64 sequences, 128
+// heads, of 1 x 1, 4 x 16, 8 x 32 queries and keys: 24, 36, 112 us; with tensor cores 180 to
+// 195; 33 of 1 or 2 tokens 20 and 103; one token, 16 heads, 4.5 and 9.4.  With 16 queries
+// the sequences of a mixed batch take 74 us instead of 62, with more keys the rows'
+// loads, 16 bytes a lane, take longer than the MMAs.)  For fewer than kFewItems heads of
+// sequences an SM a launch more does not pay (10 sequences, 128 heads: 35 us, 46 with both),
+// unless it is the only one.
+struct FewParams {
+  AttentionParams a;
+  const uint16_t *q, *kv, *rope;
+  int64_t q_stride, q_head_stride, kv_stride, kv_head_stride, rope_stride;
+};
+constexpr int kFewWarps = 4, kFewGroup = 4;
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+}
+
+__global__ void __launch_bounds__(32 * kFewWarps) latent_attention_few_kernel(const FewParams P) {
+  griddep_begin();
+  constexpr int kD = kNope + kRope;
+  __shared__ __align__(16) float queries[kFewWarps][kFewGroup][kD];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quads = (P.a.H + kFewWarps - 1) / kFewWarps;
+  const int b = blockIdx.x / quads, h = (blockIdx.x - b * quads) * kFewWarps + warp;
+  AttentionParams all = P.a;
+  all.others = 0;
+  const Sequence s = sequence_at(all, b);
+  if (h >= P.a.H || !few(s.nq, s.nk)) return;  // (no barrier follows)
+  float(&q)[kFewGroup][kD] = queries[warp];
+  const int key = min(lane, max(s.nk - 1, 0));
+  const uint16_t* const k_row = P.kv + (s.k0 + (int64_t)key) * P.kv_stride + h * P.kv_head_stride;
+  const uint16_t* const r_row = P.rope + (s.k0 + (int64_t)key) * P.rope_stride;
+  const uint16_t* const values = P.kv + (int64_t)s.k0 * P.kv_stride + h * P.kv_head_stride + kNope + lane * 4;
+  for (int g0 = 0; g0 < s.nq; g0 += kFewGroup) {
+    const int n = min(kFewGroup, s.nq - g0);
+    __syncwarp();
+    for (int i = lane; i < kFewGroup * (kD / 8); i += 32) {
+      const int r = i / (kD / 8), c = i - r * (kD / 8);
+      float f[8] = {};
+      if (r < n) unpack8(*reinterpret_cast<const uint4*>(P.q + (s.q0 + (int64_t)g0 + r) * P.q_stride + h * P.q_head_stride + c * 8), f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[r][c * 8 + j] = f[j] * P.a.scale_log2;
+    }
+    __syncwarp();
+    float p[kFewGroup] = {}, l[kFewGroup], o[kFewGroup][4] = {};
+    if (lane < s.nk) {
+#pragma unroll 8
+      for (int c = 0; c < kD / 8; ++c) {
+        float f[8];
+        unpack8(c < kNope / 8 ? *reinterpret_cast<const uint4*>(k_row + c * 8)
+                              : *reinterpret_cast<const uint4*>(r_row + (c - kNope / 8) * 8), f);
+#pragma unroll
+        for (int i = 0; i < kFewGroup; ++i) {
+          const float4 a = *reinterpret_cast<const float4*>(&q[i][c * 8]), e = *reinterpret_cast<const float4*>(&q[i][c * 8 + 4]);
+          p[i] = fmaf(a.x, f[0], fmaf(a.y, f[1], fmaf(a.z, f[2], fmaf(a.w, f[3], p[i]))));
+          p[i] = fmaf(e.x, f[4], fmaf(e.y, f[5], fmaf(e.z, f[6], fmaf(e.w, f[7], p[i]))));
+        }
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kFewGroup; ++i) {
+      const float v = lane < s.nk && (!P.a.causal || lane <= g0 + i + s.nk - s.nq) ? p[i] : -INFINITY;
+      float top = v;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+      p[i] = exp2f(v - (top == -INFINITY ? 0.f : top));
+      l[i] = p[i];
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], d);
+    }
+#pragma unroll 4
+    for (int j = 0; j < s.nk; ++j) {
+      const uint2 w = *reinterpret_cast<const uint2*>(values + j * P.kv_stride);
+      const float v[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                          __uint_as_float(w.y & 0xFFFF0000u)};
+#pragma unroll
+      for (int i = 0; i < kFewGroup; ++i) {
+        const float pj = __shfl_sync(0xFFFFFFFFu, p[i], j);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) o[i][d] = fmaf(pj, v[d], o[i][d]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kFewGroup; ++i) {
+      const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;  // a query that sees nothing: zeros
+      if (i < n)
+        *reinterpret_cast<uint2*>(P.a.out + ((s.q0 + (int64_t)g0 + i) * P.a.H + h) * kValue + lane * 4) =
+            make_uint2(pack_bf16(o[i][0] * inv, o[i][1] * inv), pack_bf16(o[i][2] * inv, o[i][3] * inv));
+    }
+  }
+}
+
 // The pieces of items that several ranges share, joined in the ranges' order: a
 // CTA an item and eight elements of its queries' results, a query a thread, the
 // loads of kJoinAhead pieces at a time on their way (500 queries behind 20000 tokens, one
@@ -836,7 +945,7 @@ int moe_fp4_latent_attention(const moe_fp4_latent_attention_args* args, void* wo
     return MOE_FP4_ERR_INVALID_ARG;
   // items and TMA coordinates are counted in 32 bits
   const int64_t tiles = a.Tq / (2 * kQ) + std::min<int64_t>(a.B, a.Tq);
-  if (a.B > kMaxSequences || a.Tq > INT32_MAX - 4 * kQ || a.Tk > INT32_MAX - 2 * kK || tiles * a.H >= (1LL << 30)) return MOE_FP4_ERR_UNSUPPORTED;
+  if (a.B > kMaxSequences || a.Tq > INT32_MAX - 4 * kQ || a.Tk > INT32_MAX - 2 * kK || tiles * a.H >= (1LL << 30) || (int64_t)a.B * a.H >= (1LL << 31)) return MOE_FP4_ERR_UNSUPPORTED;
   if (a.B == 0 || a.Tq == 0) return MOE_FP4_OK;
   const auto rows = [](const void* p, int64_t stride, int64_t head_stride, int64_t width) {
     return p && ((uintptr_t)p & 15) == 0 && stride >= width && head_stride >= width && stride % 8 == 0 && head_stride % 8 == 0 &&
@@ -867,6 +976,18 @@ int moe_fp4_latent_attention(const moe_fp4_latent_attention_args* args, void* wo
   } else {
     map_kv = map_rope = map_q;  // nothing is loaded through them
   }
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  // Sequences of few queries and keys, where there may be many of them, or no others.  (The fault tests' long waits are
+  // the other kernel's.)
+  const bool only = few(a.Tq, a.Tk);
+  P.others = (only || (a.Tq <= (int64_t)kFewQueries * a.B && (int64_t)a.B * a.H >= (int64_t)kFewItems * num_sms())) && !P.fault;
+  if (P.others) {
+    const FewParams F{P, static_cast<const uint16_t*>(a.q), static_cast<const uint16_t*>(a.kv), static_cast<const uint16_t*>(a.k_rope),
+                      a.q_stride, a.q_head_stride, a.kv_stride, a.kv_head_stride, a.rope_stride};
+    if (launch_early(latent_attention_few_kernel, dim3((unsigned)(a.B * ((a.H + kFewWarps - 1) / kFewWarps))), dim3(32 * kFewWarps), 0, st, F) != cudaSuccess)
+      return MOE_FP4_ERR_CUDA;
+    if (only) return MOE_FP4_OK;
+  }
   if (ready() != cudaSuccess) return MOE_FP4_ERR_CUDA;
   // ranges for all SMs if items may be cut, else for the items that there may be
   const bool cut = a.Tk > kMinSplit * kK;
@@ -879,7 +1000,6 @@ int moe_fp4_latent_attention(const moe_fp4_latent_attention_args* args, void* wo
   ws += align256(slots * 8 * sizeof(int32_t));
   P.ml = reinterpret_cast<float2*>(ws);
   P.sums = reinterpret_cast<float4*>(ws + slots * kRows * sizeof(float2));
-  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   if (launch_early(latent_attention_kernel, dim3(P.ranges), dim3(kThreads), kSmem, st, map_q, map_kv, map_rope, P) != cudaSuccess)
     return MOE_FP4_ERR_CUDA;
   if (!cut) return MOE_FP4_OK;

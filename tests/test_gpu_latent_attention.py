@@ -78,6 +78,30 @@ def test_ragged(q_lens, k_lens, H, causal):
     moe.ops_check()
 
 
+# sequences of few queries and keys, at the limits of their own kernel and beyond, alone and beside long ones
+FEW = [(8, 32), (4, 32), (1, 32), (3, 0), (5, 2), (1, 1), (0, 7), (7, 18), (8, 1), (2, 31), (5, 25), (4, 4)]
+MORE = [(8, 33), (9, 32), (1, 33), (2, 600), (16, 16)]
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("pairs,H", [(FEW, 160), (FEW * 3 + MORE, 50), (FEW * 100 + [(1000, 1500)], 2), ([(1, 1)] * 300, 130), ([(4, 30)], 1), (FEW + MORE, 3)])
+def test_few_queries_and_keys(pairs, H, causal):
+    q_lens, k_lens = [p[0] for p in pairs], [p[1] for p in pairs]
+    t = make(q_lens, k_lens, H, seed=H, before=1, after=2)
+    out = moe.latent_attention(*t, SCALE, causal=causal)
+    check_all(out, *t, causal, heads=sorted({0, H // 2, H - 1}))
+    assert torch.equal(out[1:1 + sum(q_lens)], moe.latent_attention(*t, SCALE, causal=causal)[1:1 + sum(q_lens)])
+    if causal:                                                    # a key that a query does not see
+        for b in (i for i, (nq, nk) in enumerate(pairs) if nq > 1 and nk > 1):
+            last_q, last_k = int(t[3][b + 1]) - 1, int(t[4][b + 1]) - 1
+            if (nq := pairs[b][0]) <= pairs[b][1]:
+                t[1][last_k, :, :128], t[2][last_k] = float("nan"), float("inf")
+                again = moe.latent_attention(*t, SCALE)
+                assert torch.equal(again[last_q - nq + 1:last_q], out[last_q - nq + 1:last_q])
+                break
+    moe.ops_check()
+
+
 def test_a_sequence_is_the_same_beside_any_neighbours():
     """infinities and NaN in the sequences around it, in the same tiles, do not reach it"""
     q_lens, k_lens = [70, 90, 60], [70, 150, 60]
