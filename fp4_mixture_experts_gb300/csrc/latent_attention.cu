@@ -65,6 +65,7 @@ constexpr float kGrow = 8.f;                  // log2 of what P may grow to
 
 constexpr int kMinSplit = 8;                  // steps of an item that may be cut
 constexpr int kCut = 4;                       // where: at multiples of this
+constexpr int kCostTwo = 6, kCostOne = 5;     // see step_cost
 constexpr int kMaxRanges = 256;
 constexpr int kRows = 2 * kQ;                 // queries of an item
 
@@ -117,25 +118,32 @@ __device__ __forceinline__ int steps_of(const AttentionParams& P, const Sequence
   return (int)((keys + kK - 1) / kK);
 }
 
-// An item costs its steps and one more for its beginning and end.  Cost of the
-// items before t of a sequence's head, t <= items_of(s): under a causal mask item u
-// < items - 1 has max(0, 2 (u + 1) + ceil((nk - nq) / 128)) steps.
+// An item costs its steps and one more for its beginning and end; a step of one tile
+// of queries, 1.6 us, is to one of two tiles, 2.0 us, as kCostOne to kCostTwo.
+__device__ __forceinline__ int step_cost(const Sequence& s, int t) { return s.nq - t * kRows > kQ ? kCostTwo : kCostOne; }
+// Cost of the items before t of a sequence's head, t <= items_of(s): under a causal
+// mask item u < items - 1 has max(0, 2 (u + 1) + ceil((nk - nq) / 128)) steps.
 __device__ __forceinline__ int64_t cost_before(const AttentionParams& P, const Sequence& s, int t) {
   if (t == 0) return 0;
-  const int items = items_of(s);
-  if (!P.causal) return (int64_t)t * (steps_of(P, s, 0) + 1);
-  const int64_t off = (int64_t)s.nk - s.nq, a = off >= 0 ? (off + kK - 1) / kK : -(-off / kK);
-  const int64_t u1 = min(t, items - 1);             // u + 1 = 1 .. u1, from u0 on above 0
-  const int64_t u0 = a >= 0 ? 1 : -a / 2 + 1;
-  int64_t cost = t;
-  if (u0 <= u1) cost += u1 * (u1 + 1) - (u0 - 1) * u0 + a * (u1 - u0 + 1);
-  if (t == items) cost += steps_of(P, s, items - 1);
+  const int items = items_of(s), whole = min(t, items - 1);
+  int64_t cost = whole;
+  if (!P.causal) {
+    cost += (int64_t)whole * steps_of(P, s, 0);
+  } else {
+    const int64_t off = (int64_t)s.nk - s.nq, a = off >= 0 ? (off + kK - 1) / kK : -(-off / kK);
+    const int64_t u1 = whole;                         // u + 1 = 1 .. u1, from u0 on above 0
+    const int64_t u0 = a >= 0 ? 1 : -a / 2 + 1;
+    if (u0 <= u1) cost += u1 * (u1 + 1) - (u0 - 1) * u0 + a * (u1 - u0 + 1);
+  }
+  cost *= kCostTwo;
+  if (t == items) cost += (int64_t)(steps_of(P, s, items - 1) + 1) * step_cost(s, items - 1);
   return cost;
 }
 
 // A place in the work of all items, in the order of sequences, heads and items: an
-// item and a step in it.  Only items of more than kMinSplit steps are cut, at
-// multiples of kCut (the places of several ranges may then be the same one).
+// item and a step in it, or behind its last one.  Only items of more than kMinSplit
+// steps are cut, at multiples of kCut; a place is the nearest one there is (those
+// of several ranges may then be the same).
 struct Place {
   int b, h, t, x;
 };
@@ -234,9 +242,16 @@ __device__ void find_range(const AttentionParams& P, int range, longlong2* scrat
           else
             hi = mid;
         }
-        const int n = steps_of(P, s, lo);
-        const int x = (int)min(z - cost_before(P, s, lo), (int64_t)n - 1);
-        (i == 0 ? out->from : out->to) = Place{b0 + (int)threadIdx.x, (int)h, lo, n > kMinSplit ? x - x % kCut : 0};
+        const int n = steps_of(P, s, lo), c = step_cost(s, lo);
+        const int y2 = (int)(z - cost_before(P, s, lo));
+        int x;
+        if (n > kMinSplit) {
+          x = (y2 / c + kCut / 2) / kCut * kCut;
+          if (x + kCut / 2 > n) x = n;
+        } else {
+          x = 2 * y2 > (n + 1) * c ? n : 0;
+        }
+        (i == 0 ? out->from : out->to) = Place{b0 + (int)threadIdx.x, (int)h, lo, x};
         if (i == 0) out->first = s;
       }
       before += all.y;
@@ -270,7 +285,8 @@ struct Pieces {
     mine = offsets_at(P, base + (threadIdx.x & 31));
   }
   __device__ __forceinline__ void start(const AttentionParams& P, const Range& r) {
-    at = r.from, end = r.to, s = r.first, strided = r.strided, begun = false;
+    at = r.from, end = r.to, s = r.first, strided = r.strided;
+    begun = at.x > 0 && at.x >= steps_of(P, s, at.t);  // behind its end: the next one begins
     const int n = gridDim.x, mine = blockIdx.x;
     step[0] = r.snake ? 2 * (n - 1 - mine) + 1 : n;
     step[1] = r.snake ? 2 * mine + 1 : n;
@@ -330,6 +346,28 @@ struct Pieces {
     return true;
   }
 };
+
+// In each group of four lanes: lane i's element j to lane j's element i.
+__device__ __forceinline__ void transpose4(uint4 (&v)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int d = 1; d <= 2; d <<= 1) {
+    const bool upper = lane & d;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j & d) continue;
+      // the half that belongs to the other lane
+      uint4 &a = v[j], &b = v[j + d];
+      const uint4 give = upper ? a : b;
+      const uint4 got = make_uint4(__shfl_xor_sync(0xFFFFFFFFu, give.x, d), __shfl_xor_sync(0xFFFFFFFFu, give.y, d),
+                                   __shfl_xor_sync(0xFFFFFFFFu, give.z, d), __shfl_xor_sync(0xFFFFFFFFu, give.w, d));
+      if (upper)
+        a = got;
+      else
+        b = got;
+    }
+  }
+}
 
 // Registers of a thread: the loads and MMAs give theirs up to the softmax, which
 // holds a row of S.  The launch brings kThreads x 168 (checked before the first
@@ -666,11 +704,14 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         if (lane == 0) mbar_arrive(&p_full[t]);
       }
       if (!ok) break;
-      const bool whole = w.from == 0 && w.to == w.n, any = w.from < w.upto[t], mine = row < here;
-      uint16_t* const out = P.out + ((int64_t)(w.q0 + t * kQ + row) * P.H + w.h) * kValue;
+      const bool whole = w.from == 0 && w.to == w.n, any = w.from < w.upto[t];
+      // this lane's part of the rows of its group of four
+      const int group_row = row & ~3;
+      uint16_t* const group_out = P.out + ((int64_t)(w.q0 + t * kQ + group_row) * P.H + w.h) * kValue + (lane & 3) * 8;
       if (whole && !any) {
-        if (mine)
-          for (int c = 0; c < kValue; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < 4 && group_row + j < here; ++j)
+          for (int c = 0; c < kValue; c += 32)
+            *reinterpret_cast<uint4*>(group_out + (int64_t)j * P.H * kValue + c) = make_uint4(0, 0, 0, 0);
         continue;
       }
       if (any) {
@@ -685,14 +726,19 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
           tmem_ld32(o_col + c, o);
           tmem_wait_ld();
           if (whole) {
+            uint4 v[4];
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              uint32_t v[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                v[k] = pack_bf16(__uint_as_float(o[j + 2 * k]) * inv, __uint_as_float(o[j + 2 * k + 1]) * inv);
-              if (mine) *reinterpret_cast<uint4*>(out + c + j) = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t* const e = o + 8 * j;
+              const auto two = [&](int k) { return pack_bf16(__uint_as_float(e[k]) * inv, __uint_as_float(e[k + 1]) * inv); };
+              v[j] = make_uint4(two(0), two(2), two(4), two(6));
             }
+            // 64 bytes of a row to the four lanes of its group, which store them side by side (a row a lane would touch 32
+            // lines with each store: 2.6 us an item instead of 1.2)
+            transpose4(v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (group_row + j < here) *reinterpret_cast<uint4*>(group_out + (int64_t)j * P.H * kValue + c) = v[j];
           } else {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
