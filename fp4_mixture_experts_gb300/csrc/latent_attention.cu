@@ -347,25 +347,15 @@ struct Pieces {
   }
 };
 
-// In each group of four lanes: lane i's element j to lane j's element i.
-__device__ __forceinline__ void transpose4(uint4 (&v)[4]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int d = 1; d <= 2; d <<= 1) {
-    const bool upper = lane & d;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j & d) continue;
-      // the half that belongs to the other lane
-      uint4 &a = v[j], &b = v[j + d];
-      const uint4 give = upper ? a : b;
-      const uint4 got = make_uint4(__shfl_xor_sync(0xFFFFFFFFu, give.x, d), __shfl_xor_sync(0xFFFFFFFFu, give.y, d),
-                                   __shfl_xor_sync(0xFFFFFFFFu, give.z, d), __shfl_xor_sync(0xFFFFFFFFu, give.w, d));
-      if (upper)
-        a = got;
-      else
-        b = got;
-    }
+// 32 bytes, in one store where they start on as many.
+__device__ __forceinline__ void store32(void* p, const uint4& a, const uint4& b, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+                 "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = a;
+    static_cast<uint4*>(p)[1] = b;
   }
 }
 
@@ -634,59 +624,62 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     while (ok && next_piece()) {
       const int here = min(w.rows - t * kQ, kQ);  // queries of the tile
       const int seen = P.causal ? min(w.nk, w.lim[t] + row) : w.nk;  // keys that this query sees
+      const bool rows_here = (warp & 3) * 32 < here;  // (else nothing is read of what lies in this warp's lanes)
       float m = -INFINITY, l = 0.f;
       for (int i = w.from; i < w.upto[t]; ++i, ++turn) {
         if (!(ok = wait(&s_full[t], turn & 1))) break;
         tmem_fence_after();
-        uint32_t s[4][32];
+        if (rows_here) {
+          uint32_t s[4][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, s[c]);
-        tmem_wait_ld();
-        // a tile that some query of the warp does not see whole
-        const int left = seen - i * kK;
-        if (__any_sync(0xFFFFFFFFu, left < kK)) {
+          for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, s[c]);
+          tmem_wait_ld();
+          // a tile that some query of the warp does not see whole
+          const int left = seen - i * kK;
+          if (__any_sync(0xFFFFFFFFu, left < kK)) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= left) s[c / 32][c % 32] = __float_as_uint(-INFINITY);
-        }
-        float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            for (int c = 0; c < 128; ++c)
+              if (c >= left) s[c / 32][c % 32] = __float_as_uint(-INFINITY);
+          }
+          float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 128; ++c) top4[c & 3] = fmaxf(top4[c & 3], __uint_as_float(s[c / 32][c % 32]));
-        float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-        top *= P.scale_log2;  // (positive)
-        if (__any_sync(0xFFFFFFFFu, top > m + kGrow)) {
-          const float to = fmaxf(m, top);
-          const float f = to == m ? 1.f : exp2_fast(m - to);  // the first maximum: 0
-          m = to, l *= f;
-          if (i > w.from) {
-            // this warp's lanes of O; the MMAs before this S have ended
+          for (int c = 0; c < 128; ++c) top4[c & 3] = fmaxf(top4[c & 3], __uint_as_float(s[c / 32][c % 32]));
+          float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+          top *= P.scale_log2;  // (positive)
+          if (__any_sync(0xFFFFFFFFu, top > m + kGrow)) {
+            const float to = fmaxf(m, top);
+            const float f = to == m ? 1.f : exp2_fast(m - to);  // the first maximum: 0
+            m = to, l *= f;
+            if (i > w.from) {
+              // this warp's lanes of O; the MMAs before this S have ended
 #pragma unroll 1
-            for (int c = 0; c < kValue; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(o_col + c, o);
-              tmem_wait_ld();
+              for (int c = 0; c < kValue; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(o_col + c, o);
+                tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tc::tmem_st32(o_col + c, o);
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tc::tmem_st32(o_col + c, o);
+              }
             }
           }
-        }
-        const float off = m == -INFINITY ? 0.f : -m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const float off = m == -INFINITY ? 0.f : -m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t p[32];
+          for (int half = 0; half < 2; ++half) {
+            uint32_t p[32];
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const int at = 64 * half + c;
-            const float a = exp2_fast(fmaf(__uint_as_float(s[at / 32][at % 32]), P.scale_log2, off));
-            const float b = exp2_fast(fmaf(__uint_as_float(s[at / 32][at % 32 + 1]), P.scale_log2, off));
-            sum[c & 2] += a, sum[(c & 2) + 1] += b;
-            p[c / 2] = pack_bf16(a, b);
+            for (int c = 0; c < 64; c += 2) {
+              const int at = 64 * half + c;
+              const float a = exp2_fast(fmaf(__uint_as_float(s[at / 32][at % 32]), P.scale_log2, off));
+              const float b = exp2_fast(fmaf(__uint_as_float(s[at / 32][at % 32 + 1]), P.scale_log2, off));
+              sum[c & 2] += a, sum[(c & 2) + 1] += b;
+              p[c / 2] = pack_bf16(a, b);
+            }
+            tc::tmem_st32(s_col + 32 * half, p);
           }
-          tc::tmem_st32(s_col + 32 * half, p);
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         const int keys = w.nk - i * kK;
         if (keys < kK && keys % 16 != 0) {
           // Rows behind the sequence's end that the last MMA step takes in are zeros: whatever is there must not meet a
@@ -704,14 +697,12 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         if (lane == 0) mbar_arrive(&p_full[t]);
       }
       if (!ok) break;
-      const bool whole = w.from == 0 && w.to == w.n, any = w.from < w.upto[t];
-      // this lane's part of the rows of its group of four
-      const int group_row = row & ~3;
-      uint16_t* const group_out = P.out + ((int64_t)(w.q0 + t * kQ + group_row) * P.H + w.h) * kValue + (lane & 3) * 8;
+      const bool whole = w.from == 0 && w.to == w.n, any = w.from < w.upto[t], mine = row < here;
+      uint16_t* const out = P.out + ((int64_t)(w.q0 + t * kQ + row) * P.H + w.h) * kValue;
+      const bool wide = (reinterpret_cast<uintptr_t>(P.out) & 31) == 0;
       if (whole && !any) {
-        for (int j = 0; j < 4 && group_row + j < here; ++j)
-          for (int c = 0; c < kValue; c += 32)
-            *reinterpret_cast<uint4*>(group_out + (int64_t)j * P.H * kValue + c) = make_uint4(0, 0, 0, 0);
+        if (mine)
+          for (int c = 0; c < kValue; c += 8) *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
         continue;
       }
       if (any) {
@@ -721,7 +712,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // a query that sees nothing: zeros
         float4* const sums = P.sums + (int64_t)w.slot * (kValue / 4) * kRows + t * kQ + row;
 #pragma unroll 1
-        for (int c = 0; c < kValue; c += 32) {
+        for (int c = rows_here ? 0 : kValue; c < kValue; c += 32) {
           uint32_t o[32];
           tmem_ld32(o_col + c, o);
           tmem_wait_ld();
@@ -733,12 +724,9 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
               const auto two = [&](int k) { return pack_bf16(__uint_as_float(e[k]) * inv, __uint_as_float(e[k + 1]) * inv); };
               v[j] = make_uint4(two(0), two(2), two(4), two(6));
             }
-            // 64 bytes of a row to the four lanes of its group, which store them side by side (a row a lane would touch 32
-            // lines with each store: 2.6 us an item instead of 1.2)
-            transpose4(v);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (group_row + j < here) *reinterpret_cast<uint4*>(group_out + (int64_t)j * P.H * kValue + c) = v[j];
+            // A store touches a line for each of its lanes, so that 32 bytes a lane take half the time of 16 (2.6 and 1.5 us
+            // an item; 64 bytes of a row on four lanes, by shuffles, 1.5 to 1.6).
+            if (mine) store32(out + c, v[0], v[1], wide), store32(out + c + 16, v[2], v[3], wide);
           } else {
 #pragma unroll
             for (int j = 0; j < 32; j += 4)

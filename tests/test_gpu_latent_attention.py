@@ -236,3 +236,16 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         assert torch.equal(ga, wa) and torch.equal(gb, wb)
     moe.ops_check()
+
+
+@pytest.mark.parametrize("q_lens,k_lens,H", [([300, 1, 0, 33], [300, 700, 5, 20], 5), ([200], [5000], 2), ([3, 1, 8], [3, 30, 8], 7)])
+def test_results_that_start_on_16_bytes_only(q_lens, k_lens, H):
+    """the same bits as where they start on 32, and nothing beside them"""
+    t = make(q_lens, k_lens, H, seed=9)
+    expect = moe.latent_attention(*t, SCALE)
+    flat = torch.full((expect.numel() + 16,), 7.0, dtype=BF, device=DEV)
+    out = flat[8:-8].view(expect.shape)
+    assert out.data_ptr() % 32 == 16
+    moe.latent_attention(*t, SCALE, out=out)
+    assert torch.equal(out, expect) and (flat[:8] == 7).all() and (flat[-8:] == 7).all()
+    moe.ops_check()
