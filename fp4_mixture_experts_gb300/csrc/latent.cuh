@@ -37,7 +37,16 @@ struct Waits {
   // a bounded wait of the whole (converged) warp
   __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
     if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-    const bool ok = mbar_wait(bar, parity, abort_flag, err, kErrWaitTimeout, limit_ns);
+    // (mbar_wait in fewer instructions: the kernels wait in many places, and are near what the instruction cache holds)
+    const uint64_t since = global_timer_ns();
+    bool ok;
+    do
+      ok = mbar_try_wait_sleep(bar, parity);
+    while (!ok && !*abort_flag && global_timer_ns() - since <= limit_ns);
+    if (!ok) {
+      *abort_flag = 1;
+      atomicOr(err, kErrWaitTimeout);
+    }
     return __all_sync(0xFFFFFFFFu, ok);
   }
   __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) const {

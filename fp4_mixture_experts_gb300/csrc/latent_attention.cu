@@ -113,9 +113,8 @@ __device__ __forceinline__ int items_of(const Sequence& s) { return s.nq / kRows
 
 // Steps (tiles of keys) of item t of a sequence's head: what its last query sees.
 __device__ __forceinline__ int steps_of(const AttentionParams& P, const Sequence& s, int t) {
-  const int64_t last = min((int64_t)s.nq, (int64_t)(t + 1) * kRows);
-  const int64_t keys = P.causal ? max(last + s.nk - s.nq, (int64_t)0) : s.nk;
-  return (int)((keys + kK - 1) / kK);
+  const int behind = P.causal ? max(s.nq - (t + 1) * kRows, 0) : 0;  // queries, each of which sees one key more
+  return (max(s.nk - behind, 0) + kK - 1) / kK;
 }
 
 // An item costs its steps and one more for its beginning and end; a step of one tile

@@ -249,3 +249,26 @@ def test_results_that_start_on_16_bytes_only(q_lens, k_lens, H):
     moe.latent_attention(*t, SCALE, out=out)
     assert torch.equal(out, expect) and (flat[:8] == 7).all() and (flat[-8:] == 7).all()
     moe.ops_check()
+
+
+# a tile of queries or less: steps of keys, of either half, whole and cut, between others of two tiles
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("q_lens,k_lens,H", [([128], [129], 1), ([1], [257], 3), ([100, 300, 20], [400, 300, 1100], 2),
+                                             ([64], [9000], 5), ([37, 129, 128, 256, 1, 90], [700, 640, 385, 900, 384, 1921], 40),
+                                             ([130, 120, 5], [100, 60, 3], 3), ([128] * 9, [128 * i + 7 for i in range(9)], 16)])
+def test_one_tile_of_queries(q_lens, k_lens, H, causal):
+    t = make(q_lens, k_lens, H, seed=21)
+    out = torch.full((sum(q_lens), H, 128), 7.0, dtype=BF, device=DEV)
+    moe.latent_attention(*t, SCALE, causal=causal, out=out)
+    check_all(out, *t, causal)
+    assert torch.equal(out, moe.latent_attention(*t, SCALE, causal=causal))
+    moe.ops_check()
+
+
+def test_one_tile_of_queries_scores_far_apart():
+    """the halves' maxima differ by more than any sum can bridge, in either order"""
+    for far in (40, 300, 700):
+        t = make([50], [1000], 2, seed=far)
+        t[1][far:far + 20, :, :128] *= 30
+        check_all(moe.latent_attention(*t, SCALE), *t, True)
+    moe.ops_check()
