@@ -86,6 +86,7 @@ struct AttentionParams {
   float4* sums;        // [slot][32][queries] of 4 elements
   int B, H, Tq, Tk;
   int ranges, causal;
+  int dealt;           // no item is cut, and each CTA has one at most
   int others;          // sequences of few queries and keys are the other kernel's
   float scale_log2;
   int fault;
@@ -194,6 +195,11 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 // round is dealt out backwards (4608 tokens 343 -> 321 us, 8192 974 -> 936, 16384 with 16 heads
 // 1025 -> 924; 32 sequences of 2 items 126 -> 131, so these are not).
 __device__ void find_range(const AttentionParams& P, int range, longlong2* scratch, Range* out) {
+  if (P.dealt) {
+    if (threadIdx.x == 0) *out = Range{Place{0, 0, 0, 0}, Place{0, 0, 0, 0}, sequence_at(P, 0), 1, 0};
+    __syncthreads();
+    return;
+  }
   const bool once = P.B <= kThreads;  // each sequence has its thread
   Sequence s{};
   longlong2 sum = make_longlong2(0, 0), total, upto;  // items, and their cost
@@ -863,7 +869,8 @@ __global__ void __launch_bounds__(kRows) latent_attention_join_kernel(AttentionP
   constexpr int kWords = kMaxRanges / 32;
   __shared__ uint32_t first[kWords], has[kWords], ends[kWords];  // bits of the ranges
   __shared__ int busy[kMaxRanges];    // the ranges that have pieces
-  __shared__ int4 chains[kMaxRanges]; // of each cut item: its first range, that one's slot and place in busy, its pieces
+  __shared__ int4 chains[kMaxRanges]; // of each cut item: its head, its first range's slot and place in busy, its pieces
+  __shared__ int2 queries[kMaxRanges];  // the first one, how many
   const int mine = threadIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;  // (kRows threads, a range each)
   const int4 info = mine < P.ranges ? P.info[mine] : make_int4(0, 0, 0, 0);
   const bool busy_range = info.x & kHasPieces, one = info.x & kOnePiece;
@@ -888,14 +895,14 @@ __global__ void __launch_bounds__(kRows) latent_attention_join_kernel(AttentionP
     }
   }
   if (busy_range) busy[place] = mine;
-  if (begins) chains[at] = make_int4(mine, 2 * mine + (one ? 0 : 1), place, pieces);
+  if (begins) chains[at] = make_int4(info.w, 2 * mine + (one ? 0 : 1), place, pieces), queries[at] = make_int2(info.y, info.z);
   __syncthreads();
   const int row = threadIdx.x;
   for (int item = blockIdx.x; item < count * kJoinChunks; item += gridDim.x) {
     const int c = item % kJoinChunks;
     const int4 chain = chains[item / kJoinChunks];
     const int pieces = chain.w;
-    const int4 what = P.info[chain.x];
+    const int2 what = queries[item / kJoinChunks];
     float o[8] = {}, l = 0.f, top = -INFINITY;
     bool complete = true;
     for (int k0 = 0; k0 < pieces; k0 += kJoinAhead) {
@@ -927,12 +934,12 @@ __global__ void __launch_bounds__(kRows) latent_attention_join_kernel(AttentionP
         top = to;
       }
     }
-    if (!complete || row >= what.z) continue;  // a wait ran out; behind the item's last query
+    if (!complete || row >= what.y) continue;  // a wait ran out; behind the item's last query
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
     uint32_t v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
-    *reinterpret_cast<uint4*>(P.out + ((int64_t)(what.y + row) * P.H + what.w) * kValue + 8 * c) = make_uint4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<uint4*>(P.out + ((int64_t)(what.x + row) * P.H + chain.x) * kValue + 8 * c) = make_uint4(v[0], v[1], v[2], v[3]);
   }
 }
 static_assert(kMaxRanges == kRows, "a thread looks at a range");
@@ -1025,6 +1032,7 @@ int moe_fp4_latent_attention(const moe_fp4_latent_attention_args* args, void* wo
   // ranges for all SMs if items may be cut, else for the items that there may be
   const bool cut = a.Tk > kMinSplit * kK;
   P.ranges = cut ? most_ranges() : (int)std::min<int64_t>(most_ranges(), tiles * a.H);
+  P.dealt = !cut && tiles * a.H <= P.ranges;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const size_t slots = 2 * (size_t)most_ranges();
   P.info = reinterpret_cast<int4*>(ws);
