@@ -185,6 +185,17 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return (uint64_t)a >> 32 == 0 && (uint64_t)b >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
+// The nearest place to `cost` behind an item's beginning.
+__device__ __forceinline__ Place place_in(const AttentionParams& P, const Sequence& s, int b, int h, int t, int cost) {
+  const int n = steps_of(P, s, t), c = step_cost(s, t);
+  int x = 2 * cost > (n + 1) * c ? n : 0;
+  if (n > kMinSplit) {
+    x = (cost / c + kCut / 2) / kCut * kCut;
+    if (x + kCut / 2 > n) x = n;
+  }
+  return Place{b, h, t, x};
+}
+
 // This CTA's range, to *out in shared memory; whole block.
 //
 // With kManyItems items for each CTA they stay whole and are dealt out in turn, a
@@ -195,11 +206,6 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 // round is dealt out backwards (4608 tokens 343 -> 321 us, 8192 974 -> 936, 16384 with 16 heads
 // 1025 -> 924; 32 sequences of 2 items 126 -> 131, so these are not).
 __device__ void find_range(const AttentionParams& P, int range, longlong2* scratch, Range* out) {
-  if (P.dealt) {
-    if (threadIdx.x == 0) *out = Range{Place{0, 0, 0, 0}, Place{0, 0, 0, 0}, sequence_at(P, 0), 1, 0};
-    __syncthreads();
-    return;
-  }
   const bool once = P.B <= kThreads;  // each sequence has its thread
   Sequence s{};
   longlong2 sum = make_longlong2(0, 0), total, upto;  // items, and their cost
@@ -247,16 +253,7 @@ __device__ void find_range(const AttentionParams& P, int range, longlong2* scrat
           else
             hi = mid;
         }
-        const int n = steps_of(P, s, lo), c = step_cost(s, lo);
-        const int y2 = (int)(z - cost_before(P, s, lo));
-        int x;
-        if (n > kMinSplit) {
-          x = (y2 / c + kCut / 2) / kCut * kCut;
-          if (x + kCut / 2 > n) x = n;
-        } else {
-          x = 2 * y2 > (n + 1) * c ? n : 0;
-        }
-        (i == 0 ? out->from : out->to) = Place{b0 + (int)threadIdx.x, (int)h, lo, x};
+        (i == 0 ? out->from : out->to) = place_in(P, s, b0 + (int)threadIdx.x, (int)h, lo, (int)(z - cost_before(P, s, lo)));
         if (i == 0) out->first = s;
       }
       before += all.y;
@@ -264,6 +261,56 @@ __device__ void find_range(const AttentionParams& P, int range, longlong2* scrat
     }
   }
   __syncthreads();
+}
+
+// The same by one warp, for up to 32 sequences, a lane each: without the block's
+// barriers, and with the search for an item in one step.
+__device__ __forceinline__ Range find_range_by_warp(const AttentionParams& P, int range) {
+  const int lane = threadIdx.x & 31;
+  Range out;
+  const Sequence mine = sequence_at(P, lane);
+  out.first = Sequence{__shfl_sync(0xFFFFFFFFu, mine.q0, 0), __shfl_sync(0xFFFFFFFFu, mine.nq, 0),
+                       __shfl_sync(0xFFFFFFFFu, mine.k0, 0), __shfl_sync(0xFFFFFFFFu, mine.nk, 0)};
+  out.from = out.to = Place{0, 0, 0, 0};
+  out.strided = 1, out.snake = 0;
+  if (P.dealt) return out;
+  const int64_t each = cost_before(P, mine, items_of(mine));
+  longlong2 upto = make_longlong2((long long)items_of(mine) * P.H, each * P.H);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long x = __shfl_up_sync(0xFFFFFFFFu, upto.x, d), y = __shfl_up_sync(0xFFFFFFFFu, upto.y, d);
+    if (lane >= d) upto.x += x, upto.y += y;
+  }
+  const int64_t items = __shfl_sync(0xFFFFFFFFu, upto.x, 31), total = __shfl_sync(0xFFFFFFFFu, upto.y, 31);
+  out.strided = items >= (int64_t)kManyItems * gridDim.x;
+  out.snake = P.causal && items >= (int64_t)kLongSequence * P.B * P.H;
+  if (out.strided) return out;
+  out.from = out.to = Place{P.B, 0, 0, 0};
+  const int64_t even = quotient(total, P.ranges), rest = total - even * P.ranges;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    const int64_t at = even * (range + i) + min((int64_t)(range + i), rest);
+    const uint32_t where = __ballot_sync(0xFFFFFFFFu, upto.y - each * P.H <= at && at < upto.y);
+    if (where == 0) continue;  // (behind all)
+    const int b = __ffs(where) - 1;
+    const Sequence s{__shfl_sync(0xFFFFFFFFu, mine.q0, b), __shfl_sync(0xFFFFFFFFu, mine.nq, b),
+                     __shfl_sync(0xFFFFFFFFu, mine.k0, b), __shfl_sync(0xFFFFFFFFu, mine.nk, b)};
+    const int64_t head = __shfl_sync(0xFFFFFFFFu, each, b), y = at - (__shfl_sync(0xFFFFFFFFu, upto.y, b) - head * P.H);
+    const int h = (int)quotient(y, head);
+    const int64_t z = y - h * head;
+    int64_t before = 0;
+    int lo = 0, n = items_of(s);  // the last item that begins at or before z is one of these
+    do {
+      const int step = (n + 31) / 32;
+      const int64_t c = lane * step < n ? cost_before(P, s, lo + lane * step) : z + 1;
+      const int k = 31 - __clz(__ballot_sync(0xFFFFFFFFu, c <= z));
+      before = __shfl_sync(0xFFFFFFFFu, c, k);
+      lo += k * step, n = min(step, n - k * step);
+    } while (n > 1);
+    (i == 0 ? out.from : out.to) = place_in(P, s, b, h, lo, (int)(z - before));
+    if (i == 0) out.first = s;
+  }
+  return out;
 }
 
 // A piece of an item, as the warps hand it on in shared memory.
@@ -424,7 +471,11 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
   const int slot0 = 2 * blockIdx.x;
   if (threadIdx.x < 16) P.done[slot0 * 8 + threadIdx.x] = 0;
   tmem_fence_before();
-  find_range(P, blockIdx.x, scratch, share);
+  const bool by_warp = P.B <= 32;  // (dealt is only so)
+  if (by_warp)
+    __syncthreads();
+  else
+    find_range(P, blockIdx.x, scratch, share);
   tmem_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
   const Waits wait{abort_flag, P.err, P.wait_ns};
@@ -589,7 +640,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     } else if (warp == 2) {
       // ---------------- the share's pieces ----------------
       Pieces all;
-      all.start(P, *share);
+      all.start(P, by_warp ? find_range_by_warp(P, blockIdx.x) : *share);
       int count = 0, steps = 0, flags = 0;
       int4 unfinished = make_int4(0, 0, 0, 0);
       while (true) {
@@ -1032,7 +1083,7 @@ int moe_fp4_latent_attention(const moe_fp4_latent_attention_args* args, void* wo
   // ranges for all SMs if items may be cut, else for the items that there may be
   const bool cut = a.Tk > kMinSplit * kK;
   P.ranges = cut ? most_ranges() : (int)std::min<int64_t>(most_ranges(), tiles * a.H);
-  P.dealt = !cut && tiles * a.H <= P.ranges;
+  P.dealt = !cut && a.B <= 32 && tiles * a.H <= P.ranges;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const size_t slots = 2 * (size_t)most_ranges();
   P.info = reinterpret_cast<int4*>(ws);
