@@ -12,10 +12,11 @@
 // tensor cores do one's P V and next Q K^T, the other's softmax runs.  An MMA of 128 x
 // 128 x 16 takes 105 cycles with A in shared memory (Q) and 73 with A in tensor memory
 // (P), so that 128 x 128 scores are 1,260 + 584 cycles of MMAs and, at 16 exponentials
-// a cycle, 1,024 of exponentials: the MMAs bound it (8192 tokens, 64 heads, causal: 979 us,
-// 1.40 PFLOP/s, about 2,050 cycles; without any softmax 880).  S lies in tensor memory, a query a lane, so that maximum and sum
-// need no other thread; P overwrites it as bf16 and is the MMA's A operand from
-// there; V is the B operand as it lies (MN-major).
+// a cycle, 1,024 of exponentials: the MMAs bound it (8192 tokens, 64 heads, causal:
+// 920 us, 1.49 PFLOP/s, about 1,930 cycles; without any softmax 880).  S lies in
+// tensor memory, a query a lane, so that maximum and sum need no other thread; P
+// overwrites it as bf16 and is the MMA's A operand from there; V is the B operand as
+// it lies (MN-major).
 //
 // The running maximum moves only when a score exceeds it by more than 2^8: then a
 // warp multiplies its lanes of O, in tensor memory, before it gives P to the MMAs;
@@ -25,18 +26,18 @@
 // which 3 of keys and 2 of values go for each step, given back in that order.  (Two
 // stages of keys and one of values take the same 128 KB, but a step's values are
 // then on their way only when the last one's are used: 8192 tokens, 64 heads 1130 us,
-// 1080 without any softmax.)  Warps: 0 loads, 1
-// issues the MMAs, 2 finds the pieces of work and hands them to the others, 4..7 and
-// 8..11 are the tiles' softmax and results.
+// 1080 without any softmax.)  Warps: 0 loads, 1 issues the MMAs, 2 finds the pieces of
+// work and hands them to the others, 4..7 and 8..11 are the tiles' softmax and
+// results.  The code is about as long as an SM's instruction cache is large: what
+// makes it longer costs 1 to 2 us an item.
 //
 // Items are dealt out to one CTA an SM; where there are few, by their cost: all
 // items' steps are numbered through, in the order of sequences, heads and queries,
 // and cut into even ranges, wherever that is in an item of some length; its pieces
 // leave their sums (fp32), maxima and row sums in the workspace, which a second
 // kernel joins in the ranges' order (64 queries behind 30000 tokens, 16 heads: 403 us on
-// 16 SMs, 69 so).  The same lengths
-// give the same bits.  Waits are bounded; results are stored only by warps none of
-// whose waits ran out.
+// 16 SMs, 62 so).  The same lengths give the same bits.  Waits are bounded; results
+// are stored only by warps none of whose waits ran out.
 #include <algorithm>
 
 #include "latent.cuh"
@@ -204,7 +205,7 @@ __device__ __forceinline__ Place place_in(const AttentionParams& P, const Sequen
 // even ranges of whole heads; 4608 tokens, 7.6 items: 393 and 449).  Under a causal
 // mask a long sequence's items cost less one after the other, so that every second
 // round is dealt out backwards (4608 tokens 343 -> 321 us, 8192 974 -> 936, 16384 with 16 heads
-// 1025 -> 924; 32 sequences of 2 items 126 -> 131, so these are not).
+// 1025 -> 924; 32 sequences of 2 items 126 -> 131, so these are not; before the results' wider stores).
 __device__ void find_range(const AttentionParams& P, int range, longlong2* scratch, Range* out) {
   const bool once = P.B <= kThreads;  // each sequence has its thread
   Sequence s{};
@@ -551,7 +552,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
       constexpr uint32_t id_pv = idesc_bf16(kQ, kValue, false, true), id_pv_half = idesc_bf16(kQ, kValue / 2, false, true);
       int items = 0, g = 0, use[2] = {0, 0}, turn[2] = {0, 0};  // items, steps, turns of O's and of P's barriers
       auto keys16 = [&](int i) { return min(kK, (w.nk - i * kK + 15) & ~15); };  // of a tile, to whole MMA steps
-      // S of tile t with the keys of step gk of the ring, the item's i
+      // S of tile t with the keys of step gk of the ring
       auto qk = [&](int t, int gk, uint32_t id_qk) {
         if (elect_one()) {
           const uint32_t q_lo = desc_lo(base + t * kQSlabs * kSlab, 16);
@@ -810,7 +811,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
 }
 
 // ---- sequences of few queries and keys ----
-// A tile of 128 queries and 128 keys of a head takes the kernel above ~3.5 us on an SM,
+// A tile of 128 queries and 128 keys of a head takes the kernel above ~3 us on an SM,
 // however few of them there are.  Here a warp takes a head of a sequence, four
 // queries at a time, all its keys at once: for S a lane has a key and reads its row,
 // the queries come from shared memory (fp32, the same word for all lanes); for P V a
