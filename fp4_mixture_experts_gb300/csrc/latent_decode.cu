@@ -28,7 +28,7 @@
 // What it takes: an MMA of 16 elements of K 61 cycles for QK (M = N = 64) and 75 for PV
 // (M = 128, N = 64), 3,396 a tile, 1.8 us, where HBM brings an SM's tile in 1.7: 4
 // sequences of 131072 tokens, 64 heads, 124 us, 4.9 TB/s; with 128 heads every tile is read
-// by two CTAs, 209 us.  One sequence of 4608 tokens 16 us: the first tile's scores are
+// by two CTAs, 209 us.  One sequence of 4608 tokens 14.6 us: the first tile's scores are
 // there after 5, its sums after 7.
 //
 // Warps: 0 and 1 load (tokens; 0 the queries too), 2 issues the MMAs, 3 writes the
@@ -618,8 +618,9 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 // The pieces of cut sequences, joined: an item is four heads and a quarter of the
 // latent vector of a sequence, an element and four heads a thread, as the pieces
 // lie, every fourth piece a part of the CTA.  A part's lanes find the factors of its
-// pieces (to its own maximum), 32 at a time; the parts meet in shared memory.
-template <int kJoinParts>
+// pieces (to its own maximum), 32 at a time, the first kAhead pieces' sums on their way
+// meanwhile; the parts meet in shared memory.
+template <int kJoinParts, int kAhead>
 __global__ void __launch_bounds__(128 * kJoinParts) latent_join_kernel(DecodeParams P) {
   griddep_begin();
   __shared__ int4 list[kMaxRanges];  // sequence, first and last range, first slot's number
@@ -677,6 +678,14 @@ __global__ void __launch_bounds__(128 * kJoinParts) latent_join_kernel(DecodePar
     const float4* const sums = reinterpret_cast<const float4*>(P.sums) + (quad & 7) * 32 + lane;
     for (int r0 = first + part; r0 <= last; r0 += 32 * kJoinParts) {
       const int r = r0 + lane * kJoinParts, n = min(32, (last - r0) / kJoinParts + 1);
+      const auto sums_at = [&](int k) {
+        return sums[((slot_of(r0 + k * kJoinParts) * 4 + j0) * halves + h0 / 32) * 4 * 8 * 32 + q * 8 * 32];
+      };
+      // the first ones are on their way while the factors are found
+      float4 ahead[kAhead > 0 ? kAhead : 1];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (k < n) ahead[k] = sums_at(k);
       float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, s[4] = {0.f, 0.f, 0.f, 0.f}, f[4];
       if (r <= last) {
         complete &= P.done[slot_of(r)] != 0;
@@ -696,14 +705,17 @@ __global__ void __launch_bounds__(128 * kJoinParts) latent_join_kernel(DecodePar
         l[h] = l[h] * was + f[h] * s[h];
         top[h] = to;
       }
-#pragma unroll 8
-      for (int k = 0; k < n; ++k) {
-        const float4 v = sums[((slot_of(r0 + k * kJoinParts) * 4 + j0) * halves + h0 / 32) * 4 * 8 * 32 + q * 8 * 32];
+      const auto add = [&](int k, const float4& v) {
         o[0] += __shfl_sync(0xFFFFFFFFu, f[0], k) * v.x;
         o[1] += __shfl_sync(0xFFFFFFFFu, f[1], k) * v.y;
         o[2] += __shfl_sync(0xFFFFFFFFu, f[2], k) * v.z;
         o[3] += __shfl_sync(0xFFFFFFFFu, f[3], k) * v.w;
-      }
+      };
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (k < n) add(k, ahead[k]);
+#pragma unroll 8
+      for (int k = kAhead; k < n; ++k) add(k, sums_at(k));
     }
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
@@ -820,8 +832,12 @@ int moe_fp4_latent_decode(const moe_fp4_latent_decode_args* args, void* workspac
   // Four parts share a sequence's pieces where there are many: the ranges are 8 and more a sequence.  (One of 512 tiles
   // in 128 pieces, 16 heads: 27 us, 52 with one part; 32 of 72 tiles, 64 heads: 68 and 56.)
   const bool many = s.ranges >= 8 * a.B;
+  // Loads ahead take registers for two CTAs an SM: where one does (a sequence of 4608 tokens, 64 heads: 16.2 us, 14.6 so;
+  // four of 131072: 124 and 126).
+  const bool ahead = many && items <= num_sms();
+  auto* const join = ahead ? latent_join_kernel<4, 8> : many ? latent_join_kernel<4, 0> : latent_join_kernel<1, 1>;
   const unsigned grid = (unsigned)std::min<int64_t>(items, (many ? 4 : 16) * num_sms());
-  return launch_early(many ? latent_join_kernel<4> : latent_join_kernel<1>, dim3(grid), dim3(many ? 512 : 128), 0, st, P) == cudaSuccess
+  return launch_early(join, dim3(grid), dim3(many ? 512 : 128), 0, st, P) == cudaSuccess
              ? MOE_FP4_OK
              : MOE_FP4_ERR_CUDA;
 }
