@@ -829,13 +829,12 @@ int moe_fp4_latent_decode(const moe_fp4_latent_decode_args* args, void* workspac
   // at most a sequence is cut for each range but the first
   const int64_t items = (int64_t)std::min(a.B, s.ranges - 1) * s.groups * s.heads;  // a quarter of four heads each
   if (items == 0) return MOE_FP4_OK;
-  // Four parts share a sequence's pieces where there are many: the ranges are 8 and more a sequence.  (One of 512 tiles
-  // in 128 pieces, 16 heads: 27 us, 52 with one part; 32 of 72 tiles, 64 heads: 68 and 56.)
-  const bool many = s.ranges >= 8 * a.B;
-  // Loads ahead take registers for two CTAs an SM: where one does (a sequence of 4608 tokens, 64 heads: 16.2 us, 14.6 so;
-  // four of 131072: 124 and 126).
-  const bool ahead = many && items <= num_sms();
-  auto* const join = ahead ? latent_join_kernel<4, 8> : many ? latent_join_kernel<4, 0> : latent_join_kernel<1, 1>;
+  // Four parts share a sequence's pieces where these are many for the items: the ranges are 20 and more a sequence, or
+  // 8 where the items leave a CTA an SM, which then has the registers for loads ahead.  (64 heads, with one part and with
+  // four: 6 sequences of 16000 tokens 47.1 and 46.1 us, 8 of 8000 31.0 and 34.7, 16 of 4000 31.9 and 38.6; 16 heads, 8 of
+  // 1000 19.5 and 14.4.  Loads ahead: a sequence of 4608 tokens, 64 heads, 16.2 and 14.6; four of 131072 124 and 126.)
+  const bool few = items <= num_sms(), many = s.ranges >= (few ? 8 : 20) * (int64_t)a.B;
+  auto* const join = !many ? latent_join_kernel<1, 1> : few ? latent_join_kernel<4, 8> : latent_join_kernel<4, 0>;
   const unsigned grid = (unsigned)std::min<int64_t>(items, (many ? 4 : 16) * num_sms());
   return launch_early(join, dim3(grid), dim3(many ? 512 : 128), 0, st, P) == cudaSuccess
              ? MOE_FP4_OK
