@@ -321,6 +321,20 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           ++piece;
         }
         row = next;
+        // The next tile comes to L2 while no stage is free for it.
+        if (i >= kStages - 1 && i + 1 < w.nt) {
+          if (copies == 1) {
+            const int r = __shfl_sync(0xFFFFFFFFu, row, 0);
+            if (warp == 0 && r != none && elect_one()) tma_prefetch_3d(&map_c, 0, r, 0);
+          } else {
+            for (int c = 0; c < copies; ++c) {
+              const int r = __shfl_sync(0xFFFFFFFFu, row, c);
+              if (r != none && elect_one())
+                for (int sl = warp; sl < kSlabs; sl += 2) tma_prefetch_3d(&map_c, 0, r, sl);
+            }
+          }
+          __syncwarp();
+        }
       }
     }
     // every issued copy has landed before shared memory is given back
