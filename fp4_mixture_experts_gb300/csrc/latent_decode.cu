@@ -27,9 +27,11 @@
 //
 // What it takes: an MMA of 16 elements of K 61 cycles for QK (M = N = 64) and 75 for PV
 // (M = 128, N = 64), 3,396 a tile, 1.8 us, where HBM brings an SM's tile in 1.7: 4
-// sequences of 131072 tokens, 64 heads, 124 us, 4.9 TB/s; with 128 heads every tile is read
-// by two CTAs, 209 us.  One sequence of 4608 tokens 14.6 us: the first tile's scores are
-// there after 5, its sums after 7.
+// sequences of 131072 tokens, 64 heads, 114 us, 5.3 TB/s; with 128 heads every tile is read
+// by two CTAs, 188 us.  There is room for two tiles, each held from its first byte to its
+// last MMA; the one behind them is fetched to L2 meanwhile (without: 124 and 206 us; two
+// ahead are no better).  One sequence of 4608 tokens 14.6 us: the first tile's scores
+// are there after 5, its sums after 7.
 //
 // Warps: 0 and 1 load (tokens; 0 the queries too), 2 issues the MMAs, 3 writes the
 // results of sequences without tokens, 4..7 are the softmax, the rescaling and the
