@@ -177,3 +177,36 @@ def test_two_streams_at_once():
         torch.cuda.synchronize()
         assert torch.equal(ga, wa) and torch.equal(gb, wb)
     moe.ops_check()
+
+
+# pieces of a sequence joined by one part or four, in one round of 32 and in several, with few and with many heads
+@pytest.mark.parametrize("lens,H,page", [([9000] + [64] * 7, 64, 64), ([9000, 64, 64, 64], 64, 64), ([32768], 16, 64), ([5000] * 6, 16, 32),
+                                         ([4000] * 16, 64, 64), ([8000] + [500] * 7, 128, 64), ([700] * 12, 33, 16)])
+def test_pieces_joined(lens, H, page):
+    q, cache, table, lengths = make(lens, H, page, seed=len(lens))
+    out = moe.latent_decode(q, cache, table, lengths, SCALE)
+    check_all(out, q, cache, table, lens)
+    assert torch.equal(out, moe.latent_decode(q, cache, table, lengths, SCALE))
+    moe.ops_check()
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_pages_outside_among_many_tiles(page):
+    """as zeros, wherever they are in a range of tiles; the other sequences are as without them"""
+    lens = [3000] * 60
+    q, cache, table, lengths = make(lens, 16, page, seed=5)
+    whole = moe.latent_decode(q, cache, table, lengths, SCALE)
+    moe.ops_check()
+    last = (3000 - 1) // page
+    for i, bad in zip((0, 7, last // 2, last - 1, last), (-1, cache.shape[0], 2 ** 31 - 1, -2 ** 31, cache.shape[0] + 5)):
+        table[3, i] = bad
+    out = moe.latent_decode(q, cache, table, lengths, SCALE)
+    with pytest.raises(moe.MoeFp4Error):
+        moe.ops_check()
+    t = torch.arange(3000, device=DEV)
+    pages = table[3, t // page].long()
+    c = torch.where(((pages >= 0) & (pages < cache.shape[0]))[:, None], cache[pages.clamp(0, cache.shape[0] - 1), t % page], 0)
+    check(out[3], *attend(q[3], c, c[:, :512], SCALE), "pages outside read as zeros")
+    others = [b for b in range(60) if b != 3]
+    assert torch.equal(out[others], whole[others])
+    moe.ops_check()
