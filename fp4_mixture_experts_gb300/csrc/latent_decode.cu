@@ -33,7 +33,7 @@
 // ahead are no better).  One sequence of 4608 tokens 14.6 us: the first tile's scores
 // are there after 5, its sums after 7.
 //
-// Warps: 0 and 1 load (tokens; 0 the queries too), 2 issues the MMAs, 3 writes the
+// Warps: 0 and, for tiles of many copies, 1 load (tokens; 0 the queries too), 2 issues the MMAs, 3 writes the
 // results of sequences without tokens, 4..7 are the softmax, the rescaling and the
 // results.  Waits are bounded; a piece whose wait ran
 // out stores nothing, and a sequence with such a piece is not joined.
@@ -228,9 +228,12 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
   float* factor = reinterpret_cast<float*>(smem + kOffTail + 256);   // [heads]
   int64_t* scratch = reinterpret_cast<int64_t*>(smem + kOffTail + 512);
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+  // Load warps: the second one where a tile is many copies.  Each that waits for a stage announces its next copies: one
+  // that did not could be overtaken by two phases of the stage, and would wait for ever.
+  const int loaders = P.box == kTile ? 1 : 2;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&kv_full[s], P.box == kTile ? 1 : 2), mbar_init(&kv_empty[s], 1);
+    for (int s = 0; s < kStages; ++s) mbar_init(&kv_full[s], loaders), mbar_init(&kv_empty[s], 1);
     for (int s = 0; s < 2; ++s) mbar_init(&s_full[s], 1), mbar_init(&s_free[s], 4);
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -266,7 +269,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     const int copies = kTile / P.box;  // of a slab
     int g = 0, piece = 0;
     bool ok = true;
-    while (ok && w.next(P)) {
+    while (ok && warp < loaders && w.next(P)) {
       // the tokens' first row in the cache, for copy `lane` of a tile; a tile ahead.  A page outside the cache reads
       // as zeros.
       const int none = P.pages * P.page;
@@ -291,7 +294,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
           const int here = min(copies, (w.len - (w.t0 + i) * kTile + P.box - 1) / P.box);
           const int r0 = __shfl_sync(0xFFFFFFFFu, row, 0);
           if (copies == 1) {
-            if (warp == 0 && elect_one()) {
+            if (elect_one()) {
               mbar_expect_tx(&kv_full[s], kStage);
               tma_load_3d(st, &map_c, 0, r0, 0, &kv_full[s]);
             }
@@ -327,7 +330,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         if (i >= kStages - 1 && i + 1 < w.nt) {
           if (copies == 1) {
             const int r = __shfl_sync(0xFFFFFFFFu, row, 0);
-            if (warp == 0 && r != none && elect_one()) tma_prefetch_3d(&map_c, 0, r, 0);
+            if (r != none && elect_one()) tma_prefetch_3d(&map_c, 0, r, 0);
           } else {
             for (int c = 0; c < copies; ++c) {
               const int r = __shfl_sync(0xFFFFFFFFu, row, c);
@@ -341,7 +344,7 @@ latent_decode_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     }
     // every issued copy has landed before shared memory is given back
     __syncwarp();
-    if (warp == 0 || copies > 1) {
+    if (warp < loaders) {
       for (int q = max(0, g - kStages); q < g; ++q) wait.drain(&kv_full[q % kStages], (q / kStages) & 1);
       if (piece > 0) wait.drain(q_full, (piece - 1) & 1);
     }
