@@ -74,10 +74,11 @@ __global__ void __launch_bounds__(kThreads) fp8_quantize_kernel(const Fp8QuantPa
   }
 }
 
+// (every row is read once, and a product reads the codes next)
 template <bool F32>
 cudaError_t launch_quant(const Fp8QuantParams& P, int align, cudaStream_t st) {
   const int64_t threads = (P.rows * P.segments) << P.lanes_log;
-  auto* k = align == 32   ? fp8_quantize_kernel<F32, 32>
+  auto* k = align == 32   ? fp8_quantize_kernel<F32, kLeaving>
             : align == 16 ? fp8_quantize_kernel<F32, 16>
                           : fp8_quantize_kernel<F32, 0>;
   return launch_spread(k, (unsigned)((threads + kThreads - 1) / kThreads), kThreads, st, P);

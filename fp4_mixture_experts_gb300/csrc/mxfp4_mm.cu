@@ -534,7 +534,7 @@ int moe_fp4_mxfp4_linear(const moe_fp4_mm_dims* dims, const void* x, int x_type,
   const cudaError_t e =
       once != 0 && workspace_bytes >= base + once
           ? launch_mxfp4_quantize_once(R, reinterpret_cast<int32_t*>(codes + base), codes, scales, st)
-          : launch_mxfp4_quantize(R, codes, scales, true, st);
+          : launch_mxfp4_quantize(R, codes, scales, true, true, st);
   if (e != cudaSuccess) return MOE_FP4_ERR_CUDA;
   return launch_mm<Fp4>(d, codes, scales, offsets, w, w_scales, y, true, st) == cudaSuccess ? MOE_FP4_OK : MOE_FP4_ERR_CUDA;
 }

@@ -29,7 +29,9 @@ struct MxRows {
 };
 
 int check_mx_rows(const MxRows& R);  // a moe_fp4_status
-cudaError_t launch_mxfp4_quantize(const MxRows& R, uint8_t* codes, uint8_t* scales, bool tiled, cudaStream_t st);
+// for_product: a product reads the codes next (tiled ones)
+cudaError_t launch_mxfp4_quantize(const MxRows& R, uint8_t* codes, uint8_t* scales, bool tiled, bool for_product,
+                                  cudaStream_t st);
 // The same result (tiled) for rows that are used several times: every row of x
 // is quantised once, with up to once_cap of its uses, twice the mean; the others
 // one by one.  lists: once_lists integers.
@@ -117,20 +119,33 @@ __device__ __forceinline__ uint32_t e2m1x8(const float* v) {
 // 16 consecutive elements as they are: 16 words of fp32, or 8 words of bf16
 // pairs.  They start on ALIGN bytes: 32 or 16, or 0 (on an element).  With loads
 // of 32 bytes a warp's requests for fp32 touch a line half as often (6667 x 2528,
-// fp32: 10.0 us, 11.9 with loads of 16 bytes).  They leave the caches first, so that
-// the codes are still in L2 when the product reads them (8192 x 4096 bf16 rows and
-// their MXFP4 product with 8192 columns 101 -> 96 us, 8192 x 8192 rows in FP8 198 ->
-// 195, SwiGLU of 4608 x 4096 59.4 -> 57.9).
+// fp32: 10.0 us, 11.9 with loads of 16 bytes).
+//
+// kLeaving is an ALIGN of 32 bytes whose elements leave the caches first: for rows that
+// are read once and whose codes a product reads next, which are then still in L2 (bf16
+// rows and their product of 4096 columns: FP8 4608 x 4096 59.6 -> 57.3 us, 2048 x 7168 49.8
+// -> 48.1, no slower for fewer; MXFP4 from 32 MB of rows on, 4608 x 7168 60 -> 57, 2600 x
+// 7168 38.5 -> 38.2, but 2048 x 7168 27.5 -> 27.9).  What is read again must not: rows
+// quantised by themselves in a loop (4608 x 4096 6.8 -> 8.2 us), gathered ones, which are
+// read once for each use (2048 rows, 8 uses 25 -> 29), and the few rows that all CTAs of
+// their kernel read (16 x 16384 by 2048 25 -> 27).
+constexpr int kLeaving = 33;
 template <bool F32, int ALIGN>
 __device__ __forceinline__ void load16_raw(const void* x, int64_t at, uint32_t (&w)[16]) {
-  if (ALIGN == 32) {
+#define MOE_LOAD32(form)                                                                                        \
+  asm volatile("ld.global" form ".v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"                               \
+               : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]), "=r"(w[i + 5]),    \
+                 "=r"(w[i + 6]), "=r"(w[i + 7])                                                                 \
+               : "l"(p + 4 * i))
+  if (ALIGN == 32 || ALIGN == kLeaving) {
     const char* p = static_cast<const char*>(x) + at * (F32 ? 4 : 2);
 #pragma unroll
     for (int i = 0; i < (F32 ? 16 : 8); i += 8)
-      asm volatile("ld.global.L1::no_allocate.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]), "=r"(w[i + 5]),
-                     "=r"(w[i + 6]), "=r"(w[i + 7])
-                   : "l"(p + 4 * i));
+      if (ALIGN == kLeaving)
+        MOE_LOAD32(".L1::no_allocate.L2::evict_first");
+      else
+        MOE_LOAD32("");
+#undef MOE_LOAD32
   } else if (ALIGN == 16) {
     const uint4* p = F32 ? reinterpret_cast<const uint4*>(static_cast<const float*>(x) + at)
                          : reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);

@@ -384,16 +384,21 @@ cudaError_t launch_quant(const QuantParams& P, bool tiled, cudaStream_t st) {
 
 template <bool F32>
 cudaError_t launch_quant(const QuantParams& P, int align, bool tiled, cudaStream_t st) {
-  return align == 32   ? launch_quant<F32, 32>(P, tiled, st)
+  return align == kLeaving ? launch_quant<F32, kLeaving, true>(P, st)
+         : align == 32 ? launch_quant<F32, 32>(P, tiled, st)
          : align == 16 ? launch_quant<F32, 16>(P, tiled, st)
                        : launch_quant<F32, 0>(P, tiled, st);
 }
 
 }  // namespace
 
-cudaError_t launch_mxfp4_quantize(const MxRows& R, uint8_t* codes, uint8_t* scales, bool tiled, cudaStream_t st) {
+cudaError_t launch_mxfp4_quantize(const MxRows& R, uint8_t* codes, uint8_t* scales, bool tiled, bool for_product,
+                                  cudaStream_t st) {
   const QuantParams P{R.x, R.x_rows, R.x_stride, R.row_index, R.offsets, codes, scales, R.rows, R.K, R.div, R.groups};
-  return R.f32 ? launch_quant<true>(P, R.align(), tiled, st) : launch_quant<false>(P, R.align(), tiled, st);
+  // rows that leave the caches first: many that are read once (kLeaving says from how many on it pays)
+  const bool leaving = for_product && tiled && !R.row_index && R.rows * R.K * (R.f32 ? 4 : 2) >= (32LL << 20);
+  const int align = leaving && R.align() == 32 ? kLeaving : R.align();
+  return R.f32 ? launch_quant<true>(P, align, tiled, st) : launch_quant<false>(P, align, tiled, st);
 }
 
 cudaError_t launch_mxfp4_quantize_once(const MxRows& R, int32_t* lists, uint8_t* codes, uint8_t* scales,
@@ -457,7 +462,7 @@ int moe_fp4_mxfp4_quantize(const void* x, int x_type, int64_t x_rows, int64_t x_
   if (!codes || !scales || ((uintptr_t)codes & 15) || (tiled && ((uintptr_t)scales & 15)))
     return MOE_FP4_ERR_INVALID_ARG;
   if (group_offsets && !tiled) return MOE_FP4_ERR_INVALID_ARG;
-  return launch_mxfp4_quantize(R, codes, scales, tiled != 0, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
+  return launch_mxfp4_quantize(R, codes, scales, tiled != 0, false, static_cast<cudaStream_t>(cuda_stream)) == cudaSuccess
              ? MOE_FP4_OK
              : MOE_FP4_ERR_CUDA;
 }
