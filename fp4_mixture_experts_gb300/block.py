@@ -175,6 +175,19 @@ def rotary(x, positions, base: float = 10000.0):
     return torch.stack([a * cos - b * sin, a * sin + b * cos], -1).flatten(-2).to(x.dtype)
 
 
+def write_rows(cache, slots, rows):
+    """The tokens' latent vectors, bf16 [T, 576], to their places in cache (slots int64 [T]); a token without a place (slot -1,
+    or one beyond the cache) writes nothing.
+
+    PyTorch's copies by index end the process's CUDA context on such an index.  So the difference to the bits that a place
+    holds is added to them, as integers: for a token without a place 0, anywhere, which changes nothing, whatever is there
+    and whoever writes it meanwhile."""
+    import torch
+    words = cache.view(-1, LATENT + ROPE).view(torch.int64)
+    at = slots.clamp(0, words.shape[0] - 1)
+    words.index_add_(0, at, (rows.view(torch.int64) - words.index_select(0, at)) * (at == slots)[:, None])
+
+
 def cached_rows(cache, block_table, pages: PageSlots, tokens: int):
     """The latent vectors of all tokens of a batch's sequences, side by side in the requests' order: [tokens, 576];
     tokens: their number (pages.k_offsets' last)."""
@@ -189,11 +202,11 @@ def cached_rows(cache, block_table, pages: PageSlots, tokens: int):
 def attention_forward(residual, normed, weights: AttentionWeights, cache, block_table, pages: PageSlots, prompt: bool,
                       cached_tokens: int | None = None, eps: float = 1e-6, workspace=None):
     """One attention block on residual [T, d] (bf16 or fp32) and its norm normed (bf16 [T, d]); returns (residual',
-    normed').  pages is page_slots' result for these T tokens (none of them without a slot), whose latent vectors are
-    written to cache (bf16 [pages, page, 576]).  prompt: any number of new tokens a sequence, the expanded form;
+    normed').  pages is page_slots' result for these T tokens, whose latent vectors are written to cache (bf16 [pages,
+    page, 576]; those of tokens without a slot are not).  prompt: any number of new tokens a sequence, the expanded form;
     cached_tokens, for sequences with tokens in the cache already, is the number of all their tokens (pages.k_offsets'
-    last; None: all tokens are new).  Otherwise one new token a sequence, the absorbed form; workspace is
-    latent_decode's."""
+    last; None: all tokens are new).  Otherwise one new token a sequence, the absorbed form (requests that only fill the
+    batch up are the last ones, of no tokens); workspace is latent_decode's."""
     import torch
     W, T, H = weights, normed.shape[0], weights.heads
     scale = (NOPE + ROPE) ** -0.5
@@ -201,7 +214,7 @@ def attention_forward(residual, normed, weights: AttentionWeights, cache, block_
     r = down.shape[1] - LATENT - ROPE
     c = rms_norm(down[:, r:r + LATENT], W.kv_norm, eps=eps)
     new = torch.cat([c, rotary(down[:, r + LATENT:], pages.positions, W.rope_base)], 1)
-    cache.view(-1, LATENT + ROPE).index_copy_(0, pages.slots, new)
+    write_rows(cache, pages.slots, new)
     q = fp8_linear(rms_norm(down[:, :r], W.q_norm, eps=eps), W.w_q, W.w_q_tiled).view(T, H, NOPE + ROPE)
     turned = rotary(q[..., NOPE:], pages.positions, W.rope_base)
     if prompt:

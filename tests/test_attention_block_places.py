@@ -1,0 +1,128 @@
+"""The attention block's own indexing, without a GPU: its operators are replaced by
+plain ones, so that an index out of range is an exception here and not a fault there.
+Tokens without a place (slot -1, or beyond the cache) are what page_slots gives padded
+batches and batches that the free pages do not hold."""
+import pytest
+import torch
+
+from fp4_mixture_experts_gb300 import block
+from fp4_mixture_experts_gb300._ops import PageSlots
+
+BF = torch.bfloat16
+D, R, H, PAGE, PAGES = 32, 16, 3, 4, 6
+
+
+def plain(monkeypatch):
+    """the operators in their plain form; what attention got, by name"""
+    got = {}
+
+    def fp8_linear(x, w, w_scale, offsets=None, **kw):
+        if offsets is None:
+            return (x.float() @ w.float().t()).to(BF)
+        o = offsets.tolist()
+        return torch.cat([x[o[e]:o[e + 1]].float() @ w[e].float().t() for e in range(len(w))]).to(BF)
+
+    def rms_norm(x, weight=None, eps=1e-6):
+        return (x.float() * torch.rsqrt(x.float().square().mean(-1, keepdim=True) + eps)).to(BF)
+
+    def latent_decode(q, cache, block_table, lengths, scale, workspace=None):
+        got["decode"] = (q, cache, block_table, lengths)
+        return torch.zeros(q.shape[0], q.shape[1], 512, dtype=BF)
+
+    def latent_attention(q, kv, k_rope, q_offsets, k_offsets, scale):
+        got["attention"] = (q, kv, k_rope, q_offsets, k_offsets)
+        return torch.zeros(*q.shape[:2], 128, dtype=BF)
+
+    for f in (fp8_linear, rms_norm, latent_decode, latent_attention):
+        monkeypatch.setattr(block, f.__name__, f)
+    monkeypatch.setattr(block, "block_residual", lambda residual, y, **kw: (residual + y, y))
+    return got
+
+
+def weights():
+    g = torch.Generator().manual_seed(1)
+    m = lambda *shape: (0.1 * torch.randn(*shape, generator=g)).to(BF)  # noqa: E731
+    kw = {n + "_scale": None for n in ("w_down", "w_q", "w_kv", "w_k", "w_v", "w_o")}
+    return block.AttentionWeights(w_down=m(R + 576, D), q_norm=None, kv_norm=None, w_q=m(192 * H, R), w_kv=m(256 * H, 512), w_k=m(H, 512, 128),
+                                  w_v=m(H, 128, 512), w_o=m(D, 128 * H), next_norm=None, **kw)
+
+
+def i32(a):
+    return torch.tensor(a, dtype=torch.int32)
+
+
+def slots(lens, new, table, T, out=None):
+    """what page_slots gives, and `out` in place of some slots: {token: slot}"""
+    s, positions, q, k = [], [], [0], [0]
+    for b, (n, t) in enumerate(zip(lens, new)):
+        for i in range(n, n + t):
+            s.append(int(table[b, i // PAGE]) * PAGE + i % PAGE)
+            positions.append(i)
+        q.append(q[-1] + t)
+        k.append(k[-1] + n + t)
+    s, positions = s + [-1] * (T - len(s)), positions + [0] * (T - len(positions))
+    for i, v in (out or {}).items():
+        s[i] = v
+    return PageSlots(torch.tensor(s, dtype=torch.int64), i32(positions), i32([n + t for n, t in zip(lens, new)]), i32(q), i32(k), i32(0))
+
+
+def run(W, cache, table, p, T, prompt, **kw):
+    residual = torch.randn(T, D, generator=torch.Generator().manual_seed(T)).to(BF)
+    return block.attention_forward(residual, residual, W, cache, table, p, prompt, **kw)
+
+
+def bits(x):
+    return x.view(torch.int16)
+
+
+TABLE = i32([[3, 1], [0, 5], [4, 2]])
+
+
+@pytest.mark.parametrize("prompt", [False, True])
+@pytest.mark.parametrize("out", [{1: -1}, {0: -1}, {2: -1}, {0: -1, 2: -1}, {0: -1, 1: -1, 2: -1}, {1: PAGES * PAGE}, {0: 2 ** 40, 2: -1},
+                                 {0: 2 ** 40, 1: 2 ** 33, 2: -7}, {}])
+def test_tokens_without_a_place_are_not_written(prompt, out, monkeypatch):
+    plain(monkeypatch)
+    W, lens, new = weights(), [0, 4, 6], [1, 1, 1]
+    want = torch.full((PAGES, PAGE, 576), float("nan"), dtype=BF)
+    want[0, 0] = -0.0
+    cache = want.clone()
+    all_placed = want.clone()
+    full = slots(lens, new, TABLE, 3)
+    run(W, all_placed, TABLE, full, 3, prompt)
+    for i in set(range(3)) - set(out):
+        s = int(full.slots[i])
+        want.view(-1, 576)[s] = all_placed.view(-1, 576)[s]
+    run(W, cache, TABLE, slots(lens, new, TABLE, 3, out), 3, prompt)
+    assert torch.equal(bits(cache), bits(want))
+    assert not torch.isnan(want.view(-1, 576)[full.slots[[i for i in range(3) if i not in out]]]).any()
+
+
+def test_a_token_at_the_first_place_beside_ones_without(monkeypatch):
+    plain(monkeypatch)
+    W, cache = weights(), torch.full((PAGES, PAGE, 576), 7.0, dtype=BF)
+    other = cache.clone()
+    table = i32([[0], [3]])
+    run(W, other, table, slots([0, 0], [2, 1], table, 3), 3, True)
+    run(W, cache, table, slots([0, 0], [2, 1], table, 3, {1: -1, 2: -1}), 3, True)
+    assert torch.equal(cache.view(-1, 576)[0], other.view(-1, 576)[0]) and (cache.view(-1, 576)[1:] == 7).all()
+
+
+def test_a_padded_step(monkeypatch):
+    """requests without a token behind the others: their rows are there, nothing of theirs is written"""
+    got = plain(monkeypatch)
+    W, cache = weights(), torch.full((PAGES, PAGE, 576), 7.0, dtype=BF)
+    table = i32([[3, 1], [0, 5], [9, 9], [-1, -1]])
+    p = slots([5, 2, 0, 0], [1, 1, 0, 0], table, 4)
+    out, _ = run(W, cache, table, p, 4, False)
+    assert out.shape == (4, D)
+    changed = (cache.view(-1, 576) != 7).any(1).nonzero().flatten().tolist()
+    assert changed == sorted(p.slots[:2].tolist())
+    assert got["decode"][3].tolist() == [6, 3, 0, 0]
+
+
+def test_no_tokens_at_all(monkeypatch):
+    plain(monkeypatch)
+    W, cache = weights(), torch.full((PAGES, PAGE, 576), 7.0, dtype=BF)
+    out, _ = run(W, cache, TABLE, slots([3, 4, 6], [0, 0, 0], TABLE, 0), 0, True)
+    assert out.shape == (0, D) and (cache == 7).all()
