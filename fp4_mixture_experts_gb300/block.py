@@ -165,10 +165,20 @@ class AttentionWeights:
 def rotary(x, positions, base: float = 10000.0):
     """bf16 x [T, 64] or [T, H, 64] turned by the tokens' positions (int32 [T]): elements 2 i and 2 i + 1 are a pair, turned
     by position base^(-i / 32).  Angles in 64 bits: at position 10^6 those in 32 are 1/16 apart."""
+    return turned(x, *turns(positions, base))
+
+
+def turns(positions, base: float):
+    """cosines and sines of the positions' angles, fp32 [T, 32] each"""
     import torch
-    i = torch.arange(ROPE // 2, dtype=torch.float64, device=x.device)
+    i = torch.arange(ROPE // 2, dtype=torch.float64, device=positions.device)
     angle = positions.double()[:, None] * base ** (-i / (ROPE // 2))
-    cos, sin = angle.cos().float(), angle.sin().float()
+    return angle.cos().float(), angle.sin().float()
+
+
+def turned(x, cos, sin):
+    """rotary's x turned by these"""
+    import torch
     if x.dim() == 3:
         cos, sin = cos[:, None], sin[:, None]
     a, b = x[..., 0::2].float(), x[..., 1::2].float()
@@ -213,19 +223,20 @@ def attention_forward(residual, normed, weights: AttentionWeights, cache, block_
     down = fp8_linear(normed, W.w_down, W.w_down_tiled)
     r = down.shape[1] - LATENT - ROPE
     c = rms_norm(down[:, r:r + LATENT], W.kv_norm, eps=eps)
-    new = torch.cat([c, rotary(down[:, r + LATENT:], pages.positions, W.rope_base)], 1)
+    angles = turns(pages.positions, W.rope_base)
+    new = torch.cat([c, turned(down[:, r + LATENT:], *angles)], 1)
     write_rows(cache, pages.slots, new)
     q = fp8_linear(rms_norm(down[:, :r], W.q_norm, eps=eps), W.w_q, W.w_q_tiled).view(T, H, NOPE + ROPE)
-    turned = rotary(q[..., NOPE:], pages.positions, W.rope_base)
+    q_rope = turned(q[..., NOPE:], *angles)
     if prompt:
         rows = new if cached_tokens is None else cached_rows(cache, block_table, pages, cached_tokens)
         kv = fp8_linear(rows[:, :LATENT], W.w_kv, W.w_kv_tiled).view(-1, H, NOPE + VALUE)
-        q = torch.cat([q[..., :NOPE], turned], 2)
+        q = torch.cat([q[..., :NOPE], q_rope], 2)
         o = latent_attention(q, kv, rows[:, LATENT:], pages.q_offsets, pages.k_offsets, scale)
     else:
         by_head = torch.arange(H + 1, dtype=torch.int32, device=q.device) * T
         ql = fp8_linear(q[..., :NOPE].transpose(0, 1).reshape(H * T, NOPE), W.w_k, W.w_k_tiled, offsets=by_head)
-        q = torch.cat([ql.view(H, T, LATENT), turned.transpose(0, 1)], 2).transpose(0, 1)
+        q = torch.cat([ql.view(H, T, LATENT), q_rope.transpose(0, 1)], 2).transpose(0, 1)
         ol = latent_decode(q, cache, block_table, pages.lengths, scale, workspace=workspace)
         o = fp8_linear(ol.transpose(0, 1).reshape(H * T, LATENT), W.w_v, W.w_v_tiled, offsets=by_head)
         o = o.view(H, T, VALUE).transpose(0, 1)
