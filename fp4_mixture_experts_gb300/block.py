@@ -200,13 +200,15 @@ def write_rows(cache, slots, rows):
 
 def cached_rows(cache, block_table, pages: PageSlots, tokens: int):
     """The latent vectors of all tokens of a batch's sequences, side by side in the requests' order: [tokens, 576];
-    tokens: their number (pages.k_offsets' last)."""
+    tokens: their number (pages.k_offsets' last) or more, whose rows then hold anything.  Pages outside the cache read as
+    zeros, as in latent_decode (PyTorch's own reads there would end the process's CUDA context)."""
     import torch
     i = torch.arange(tokens, dtype=torch.int32, device=cache.device)
-    b = torch.searchsorted(pages.k_offsets[1:], i, right=True)
+    b = torch.searchsorted(pages.k_offsets[1:], i, right=True).clamp_(max=block_table.shape[0] - 1)
     at = (i - pages.k_offsets[b]).long()
-    size = cache.shape[1]
-    return cache[block_table[b, at // size].long(), at % size]
+    page = block_table[b, (at // cache.shape[1]).clamp_(max=block_table.shape[1] - 1)].long()
+    inside = page.clamp(0, cache.shape[0] - 1)
+    return cache[inside, at % cache.shape[1]].masked_fill_((inside != page)[:, None], 0)
 
 
 def attention_forward(residual, normed, weights: AttentionWeights, cache, block_table, pages: PageSlots, prompt: bool,
@@ -215,7 +217,7 @@ def attention_forward(residual, normed, weights: AttentionWeights, cache, block_
     normed').  pages is page_slots' result for these T tokens, whose latent vectors are written to cache (bf16 [pages,
     page, 576]; those of tokens without a slot are not).  prompt: any number of new tokens a sequence, the expanded form;
     cached_tokens, for sequences with tokens in the cache already, is the number of all their tokens (pages.k_offsets'
-    last; None: all tokens are new).  Otherwise one new token a sequence, the absorbed form (requests that only fill the
+    last) or more; None: all tokens are new.  Otherwise one new token a sequence, the absorbed form (requests that only fill the
     batch up are the last ones, of no tokens); workspace is latent_decode's."""
     import torch
     W, T, H = weights, normed.shape[0], weights.heads

@@ -126,3 +126,41 @@ def test_no_tokens_at_all(monkeypatch):
     W, cache = weights(), torch.full((PAGES, PAGE, 576), 7.0, dtype=BF)
     out, _ = run(W, cache, TABLE, slots([3, 4, 6], [0, 0, 0], TABLE, 0), 0, True)
     assert out.shape == (0, D) and (cache == 7).all()
+
+
+def rows_of(cache, table, lens):
+    """the sequences' vectors side by side; pages outside the cache are zeros"""
+    out = []
+    for b, n in enumerate(lens):
+        for i in range(n):
+            page = int(table[b, i // PAGE])
+            out.append(cache[page, i % PAGE] if 0 <= page < len(cache) else torch.zeros(576, dtype=BF))
+    return torch.stack(out)
+
+
+@pytest.mark.parametrize("more", [0, 1, 5, 40])
+@pytest.mark.parametrize("lens,new", [([3, 0, 5], [2, 4, 1]), ([0, 0, 0], [1, 1, 1]), ([3, 4, 6], [0, 2, 2]), ([0, 7, 0], [0, 1, 0])])
+def test_rows_of_cached_tokens_behind_the_last_one(lens, new, more, monkeypatch):
+    """room for more tokens than the batch has, as for a captured prompt"""
+    got = plain(monkeypatch)
+    W, T = weights(), sum(new)
+    cache = torch.randn(PAGES, PAGE, 576, generator=torch.Generator().manual_seed(2)).to(BF)
+    after = [n + t for n, t in zip(lens, new)]
+    run(W, cache, TABLE, slots(lens, new, TABLE, T), T, True, cached_tokens=sum(after) + more)
+    q, kv, k_rope, qo, ko = got["attention"]
+    assert kv.shape[0] == k_rope.shape[0] == sum(after) + more
+    assert torch.equal(k_rope[:sum(after)], rows_of(cache, TABLE, after)[:, 512:])
+    assert ko.tolist()[-1] == sum(after)
+
+
+@pytest.mark.parametrize("bad", [-1, -PAGES, PAGES, 2 ** 31 - 1, -2 ** 31])
+def test_cached_pages_outside_the_cache_read_as_zeros(bad, monkeypatch):
+    got = plain(monkeypatch)
+    W, lens, new = weights(), [5, 3, 8], [1, 1, 0]
+    cache = torch.randn(PAGES, PAGE, 576, generator=torch.Generator().manual_seed(2)).to(BF)
+    table = TABLE.clone()
+    p = slots(lens, new, table, 2)
+    table[1, 0] = bad
+    run(W, cache, table, p, 2, True, cached_tokens=18)
+    assert torch.equal(got["attention"][2], rows_of(cache, table, [6, 4, 8])[:, 512:])
+    assert not got["attention"][2][6:10].any() and not got["attention"][1][6:10].any()

@@ -100,3 +100,38 @@ def test_too_few_free_pages(prompt):
         assert torch.equal(bits(a[:3]), bits(b[:3]))
     changed = (bits(few) != bits(cache)).view(-1, 576).any(1).nonzero().flatten().tolist()
     assert changed == sorted(p.slots.tolist()[:3])
+
+
+@pytest.mark.parametrize("room", [0, 1, 200])
+def test_more_of_prompts_with_room_for_further_tokens(room):
+    """cached tokens and new ones behind them, rows for more than there are: the same bits"""
+    W, lens, new = attention_weights(), [20, 3, 16, 9], [7, 0, 30, 1]
+    cache, table, free = filled(W, lens)
+    T, n = sum(new), sum(lens) + sum(new)
+    x = inputs(T)
+    normed = moe.rms_norm(x, W.next_norm)
+    p = moe.page_slots(i32(lens), i32(new), table, free, PAGE, T)
+    one, two = cache.clone(), cache.clone()
+    want = block.attention_forward(x, normed, W, one, table, p, True, cached_tokens=n)
+    rows = block.cached_rows(one, table, p, n + room)
+    b = torch.repeat_interleave(torch.arange(4, device=DEV), p.lengths)
+    at = torch.cat([torch.arange(k, device=DEV) for k in p.lengths.tolist()])
+    assert torch.equal(rows[:n], one[table[b, at // PAGE].long(), at % PAGE])
+    got = block.attention_forward(x, normed, W, two, table, p, True, cached_tokens=n + room)
+    moe.ops_check()
+    assert torch.equal(bits(one), bits(two))
+    for a, c in zip(got, want):
+        assert torch.equal(bits(a), bits(c))
+
+
+@pytest.mark.parametrize("bad", [-1, 40, 2 ** 31 - 1])
+def test_cached_pages_outside_the_cache(bad):
+    W, lens, new = attention_weights(), [20, 3, 16, 9], [7, 2, 3, 1]
+    cache, table, free = filled(W, lens)
+    p = moe.page_slots(i32(lens), i32(new), table, free, PAGE, sum(new))
+    moe.ops_check()
+    n = int(p.k_offsets[-1])
+    want = block.cached_rows(cache, table, p, n)
+    table[2, 0] = bad                                       # the third sequence's first 16 tokens
+    want[27 + 5:27 + 5 + 16] = 0
+    assert torch.equal(bits(block.cached_rows(cache, table, p, n)), bits(want))
