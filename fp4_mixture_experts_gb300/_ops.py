@@ -192,7 +192,8 @@ def latent_attention(q, kv, k_rope, q_offsets, k_offsets, scale, causal: bool = 
     projection writes them), k_rope bf16 [Tk, 64]; heads and rows start on 16 bytes.  Sequence b has queries
     [q_offsets[b], q_offsets[b+1]) and keys [k_offsets[b], k_offsets[b+1]) (int32 [B + 1]); causal: its last query sees
     all keys, each one before it one less.  A query that sees no key gets zeros, queries of no sequence are left as
-    they were.  Values are to be finite; scale is positive."""
+    they were.  Offsets that decrease or lie behind the rows (but for 2^31 - 1, their end) are reported by ops_check.
+    Values are to be finite; scale is positive."""
     return _native.latent_attention(q, kv, k_rope, q_offsets, k_offsets, scale, causal, out, workspace, _handle(stream))
 
 

@@ -27,9 +27,9 @@
 // stages of keys and one of values take the same 128 KB, but a step's values are
 // then on their way only when the last one's are used: 8192 tokens, 64 heads 1130 us,
 // 1080 without any softmax.)  Warps: 0 loads, 1 issues the MMAs, 2 finds the pieces of
-// work and hands them to the others, 4..7 and 8..11 are the tiles' softmax and
-// results.  The code is about as long as an SM's instruction cache is large: what
-// makes it longer costs 1 to 2 us an item.
+// work and hands them to the others, 3 looks for offsets that are no sequences' (in one
+// CTA), 4..7 and 8..11 are the tiles' softmax and results.  The code is about as long as
+// an SM's instruction cache is large: what makes it longer costs 1 to 2 us an item.
 //
 // Items are dealt out to one CTA an SM; where there are few, by their cost: all
 // items' steps are numbered through, in the order of sequences, heads and queries,
@@ -109,6 +109,11 @@ __device__ __forceinline__ Sequence sequence_of(const AttentionParams& P, int4 o
   s.k0 = min(max(o.z, 0), P.Tk), s.nk = max(0, min(o.w, P.Tk) - s.k0);
   if (P.others && few(s.nq, s.nk)) s.nq = 0;
   return s;
+}
+// offsets below the ones before them, or behind the rows (INT32_MAX: the rows' end)
+__device__ __forceinline__ bool misplaced(const AttentionParams& P, int4 o) {
+  const auto behind = [](int v, int rows) { return v > rows && v != INT32_MAX; };
+  return o.y < o.x || o.w < o.z || behind(o.x, P.Tq) || behind(o.y, P.Tq) || behind(o.z, P.Tk) || behind(o.w, P.Tk);
 }
 __device__ __forceinline__ Sequence sequence_at(const AttentionParams& P, int b) { return sequence_of(P, offsets_at(P, b)); }
 __device__ __forceinline__ int items_of(const Sequence& s) { return s.nq / kRows + (s.nq % kRows != 0); }
@@ -670,6 +675,11 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         if (!more) break;
       }
       if (lane == 0) P.info[blockIdx.x] = make_int4(flags, unfinished.y, unfinished.z, unfinished.w);
+    } else if (blockIdx.x == 0) {
+      // ---------------- offsets that are no sequences' ----------------
+      bool bad = false;
+      for (int b = lane; b < P.B; b += 32) bad |= misplaced(P, offsets_at(P, b));
+      if (bad) atomicOr(P.err, kErrBadExpertId);
     }
   } else {
     set_registers_more<kRegsMany>();
@@ -826,6 +836,7 @@ struct FewParams {
   AttentionParams a;
   const uint16_t *q, *kv, *rope;
   int64_t q_stride, q_head_stride, kv_stride, kv_head_stride, rope_stride;
+  int only;  // no other kernel looks at the offsets
 };
 constexpr int kFewWarps = 4, kFewGroup = 4;
 
@@ -844,7 +855,9 @@ __global__ void __launch_bounds__(32 * kFewWarps) latent_attention_few_kernel(co
   const int b = blockIdx.x / quads, h = (blockIdx.x - b * quads) * kFewWarps + warp;
   AttentionParams all = P.a;
   all.others = 0;
-  const Sequence s = sequence_at(all, b);
+  const int4 o4 = offsets_at(all, b);
+  const Sequence s = sequence_of(all, o4);
+  if (P.only && h == 0 && lane == 0 && misplaced(all, o4)) atomicOr(&g_attention_err[0], kErrBadExpertId);
   if (h >= P.a.H || !few(s.nq, s.nk)) return;  // (no barrier follows)
   float(&q)[kFewGroup][kD] = queries[warp];
   const int key = min(lane, max(s.nk - 1, 0));
@@ -1075,7 +1088,7 @@ int moe_fp4_latent_attention(const moe_fp4_latent_attention_args* args, void* wo
   P.others = (only || (a.Tq <= (int64_t)kFewQueries * a.B && (int64_t)a.B * a.H >= (int64_t)kFewItems * num_sms())) && !P.fault;
   if (P.others) {
     const FewParams F{P, static_cast<const uint16_t*>(a.q), static_cast<const uint16_t*>(a.kv), static_cast<const uint16_t*>(a.k_rope),
-                      a.q_stride, a.q_head_stride, a.kv_stride, a.kv_head_stride, a.rope_stride};
+                      a.q_stride, a.q_head_stride, a.kv_stride, a.kv_head_stride, a.rope_stride, only};
     if (launch_early(latent_attention_few_kernel, dim3((unsigned)(a.B * ((a.H + kFewWarps - 1) / kFewWarps))), dim3(32 * kFewWarps), 0, st, F) != cudaSuccess)
       return MOE_FP4_ERR_CUDA;
     if (only) return MOE_FP4_OK;

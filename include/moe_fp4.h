@@ -521,8 +521,9 @@ int moe_fp4_latent_decode(const moe_fp4_latent_decode_args* args, void* workspac
  *   q         bf16 [Tq, H, 192], element strides q_stride, q_head_stride
  *   kv        bf16 [Tk, H, 256]: kn and v of a head side by side
  *   k_rope    bf16 [Tk, 64], the heads' shared rotary key kr
- *   q_offsets, k_offsets  int32 [B + 1] on the device, not decreasing (taken into
- *             [0, Tq] and [0, Tk])
+ *   q_offsets, k_offsets  int32 [B + 1] on the device, not decreasing, up to Tq and
+ *             Tk: negative ones are taken as 0, INT32_MAX as the rows' end; decreasing
+ *             ones and others behind the rows, taken as their end, set error bit 1
  *   out       bf16 [Tq, H, 128], contiguous
  * All bases 16-byte aligned, strides multiples of 8 elements; scale positive. */
 typedef struct moe_fp4_latent_attention_args {
