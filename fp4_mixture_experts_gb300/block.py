@@ -217,8 +217,9 @@ def attention_forward(residual, normed, weights: AttentionWeights, cache, block_
     normed').  pages is page_slots' result for these T tokens, whose latent vectors are written to cache (bf16 [pages,
     page, 576]; those of tokens without a slot are not).  prompt: any number of new tokens a sequence, the expanded form;
     cached_tokens, for sequences with tokens in the cache already, is the number of all their tokens (pages.k_offsets'
-    last) or more; None: all tokens are new.  Otherwise one new token a sequence, the absorbed form (requests that only fill the
-    batch up are the last ones, of no tokens); workspace is latent_decode's."""
+    last) or more; None: all tokens are new (if they are not, or cached_tokens is too small, ops_check reports it).  Otherwise
+    one new token a sequence, the absorbed form (requests that only fill the batch up are the last ones, of no tokens);
+    workspace is latent_decode's."""
     import torch
     W, T, H = weights, normed.shape[0], weights.heads
     scale = (NOPE + ROPE) ** -0.5
@@ -231,10 +232,14 @@ def attention_forward(residual, normed, weights: AttentionWeights, cache, block_
     q = fp8_linear(rms_norm(down[:, :r], W.q_norm, eps=eps), W.w_q, W.w_q_tiled).view(T, H, NOPE + ROPE)
     q_rope = turned(q[..., NOPE:], *angles)
     if prompt:
-        rows = new if cached_tokens is None else cached_rows(cache, block_table, pages, cached_tokens)
+        rows, k_offsets = new, pages.k_offsets
+        if cached_tokens is None:  # where some are not new, offsets that latent_attention reports
+            k_offsets = torch.where(k_offsets == pages.q_offsets, k_offsets, 2 ** 31 - 2)
+        else:
+            rows = cached_rows(cache, block_table, pages, cached_tokens)
         kv = fp8_linear(rows[:, :LATENT], W.w_kv, W.w_kv_tiled).view(-1, H, NOPE + VALUE)
         q = torch.cat([q[..., :NOPE], q_rope], 2)
-        o = latent_attention(q, kv, rows[:, LATENT:], pages.q_offsets, pages.k_offsets, scale)
+        o = latent_attention(q, kv, rows[:, LATENT:], pages.q_offsets, k_offsets, scale)
     else:
         by_head = torch.arange(H + 1, dtype=torch.int32, device=q.device) * T
         ql = fp8_linear(q[..., :NOPE].transpose(0, 1).reshape(H * T, NOPE), W.w_k, W.w_k_tiled, offsets=by_head)

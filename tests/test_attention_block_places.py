@@ -164,3 +164,20 @@ def test_cached_pages_outside_the_cache_read_as_zeros(bad, monkeypatch):
     run(W, cache, table, p, 2, True, cached_tokens=18)
     assert torch.equal(got["attention"][2], rows_of(cache, table, [6, 4, 8])[:, 512:])
     assert not got["attention"][2][6:10].any() and not got["attention"][1][6:10].any()
+
+
+@pytest.mark.parametrize("T", [4, 30])
+@pytest.mark.parametrize("lens,new", [([0, 0, 0], [1, 2, 1]), ([0, 4, 0], [1, 2, 1]), ([0, 0, 3], [2, 2, 0]), ([1, 0, 0], [0, 3, 1])])
+def test_keys_of_the_new_tokens_alone_are_for_batches_without_cached_ones(T, lens, new, monkeypatch):
+    """else the offsets lie behind the rows, which latent_attention reports"""
+    got = plain(monkeypatch)
+    W, cache = weights(), torch.zeros(PAGES, PAGE, 576, dtype=BF)
+    p = slots(lens, new, TABLE, T)
+    run(W, cache, TABLE, p, T, True)
+    q, kv, k_rope, qo, ko = got["attention"]
+    assert kv.shape[0] == T and torch.equal(qo, p.q_offsets)
+    if any(lens):
+        assert ((ko > T) & (ko < 2 ** 31 - 1)).any()
+    else:
+        assert torch.equal(ko, p.k_offsets)
+    assert ko.dtype == torch.int32 and (ko[1:] >= ko[:-1]).all()

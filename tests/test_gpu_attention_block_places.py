@@ -135,3 +135,21 @@ def test_cached_pages_outside_the_cache(bad):
     table[2, 0] = bad                                       # the third sequence's first 16 tokens
     want[27 + 5:27 + 5 + 16] = 0
     assert torch.equal(bits(block.cached_rows(cache, table, p, n)), bits(want))
+
+
+def test_cached_tokens_that_are_left_out_are_reported():
+    W, lens, new = attention_weights(), [20, 0, 16, 9], [7, 2, 3, 1]
+    cache, table, free = filled(W, lens)
+    for pad in (0, 100):
+        T = sum(new) + pad
+        x, n = inputs(T), sum(lens) + sum(new)
+        normed = moe.rms_norm(x, W.next_norm)
+        t = table.clone()
+        p = moe.page_slots(i32(lens), i32(new), t, free, PAGE, T)
+        moe.ops_check()
+        for kw in ({}, dict(cached_tokens=n - 1)):
+            block.attention_forward(x, normed, W, cache.clone(), t, p, True, **kw)
+            with pytest.raises(moe.MoeFp4Error):
+                moe.ops_check()
+        block.attention_forward(x, normed, W, cache.clone(), t, p, True, cached_tokens=n)
+        moe.ops_check()
