@@ -218,10 +218,12 @@ def attention_forward(residual, normed, weights: AttentionWeights, cache, block_
     page, 576]; those of tokens without a slot are not).  prompt: any number of new tokens a sequence, the expanded form;
     cached_tokens, for sequences with tokens in the cache already, is the number of all their tokens (pages.k_offsets'
     last) or more; None: all tokens are new (if they are not, or cached_tokens is too small, ops_check reports it).  Otherwise
-    one new token a sequence, the absorbed form (requests that only fill the batch up are the last ones, of no tokens);
-    workspace is latent_decode's."""
+    one new token a sequence, the absorbed form, for T requests (those without a new token, which fill the batch up, behind
+    the others: ops_check reports it if they are not); workspace is latent_decode's."""
     import torch
     W, T, H = weights, normed.shape[0], weights.heads
+    if not prompt and pages.lengths.shape[0] != T:
+        raise ValueError("the absorbed form takes a row for each request")
     scale = (NOPE + ROPE) ** -0.5
     down = fp8_linear(normed, W.w_down, W.w_down_tiled)
     r = down.shape[1] - LATENT - ROPE
@@ -244,7 +246,10 @@ def attention_forward(residual, normed, weights: AttentionWeights, cache, block_
         by_head = torch.arange(H + 1, dtype=torch.int32, device=q.device) * T
         ql = fp8_linear(q[..., :NOPE].transpose(0, 1).reshape(H * T, NOPE), W.w_k, W.w_k_tiled, offsets=by_head)
         q = torch.cat([ql.view(H, T, LATENT), q_rope.transpose(0, 1)], 2).transpose(0, 1)
-        ol = latent_decode(q, cache, block_table, pages.lengths, scale, workspace=workspace)
+        # token b is request b's; where it is not (one without a token is ahead), a length that latent_decode reports
+        own = torch.arange(1, T + 1, dtype=torch.int32, device=q.device).minimum(pages.q_offsets[-1:])
+        lengths = torch.where(pages.q_offsets[1:] == own, pages.lengths, -1)
+        ol = latent_decode(q, cache, block_table, lengths, scale, workspace=workspace)
         o = fp8_linear(ol.transpose(0, 1).reshape(H * T, LATENT), W.w_v, W.w_v_tiled, offsets=by_head)
         o = o.view(H, T, VALUE).transpose(0, 1)
     y = fp8_linear(o.reshape(T, H * VALUE), W.w_o, W.w_o_tiled)

@@ -181,3 +181,29 @@ def test_keys_of_the_new_tokens_alone_are_for_batches_without_cached_ones(T, len
     else:
         assert torch.equal(ko, p.k_offsets)
     assert ko.dtype == torch.int32 and (ko[1:] >= ko[:-1]).all()
+
+
+@pytest.mark.parametrize("lens,new,right", [([5, 2, 0], [1, 1, 1], True), ([5, 2, 0], [1, 1, 0], True), ([5, 2, 6], [1, 0, 0], True),
+                                            ([0, 0, 0], [0, 0, 0], True), ([5, 2, 6], [1, 0, 1], False), ([5, 0, 0], [0, 1, 1], False),
+                                            ([5, 2, 6], [2, 1, 0], False), ([5, 2, 6], [0, 0, 1], False)])
+def test_a_decoded_token_belongs_to_its_row_s_sequence(lens, new, right, monkeypatch):
+    """a request without a token ahead of one with one, or two tokens of one: lengths that latent_decode reports"""
+    got = plain(monkeypatch)
+    W, cache = weights(), torch.zeros(PAGES, PAGE, 576, dtype=BF)
+    p = slots(lens, new, TABLE, 3)
+    run(W, cache, TABLE, p, 3, False)
+    lengths = got["decode"][3]
+    assert lengths.dtype == torch.int32
+    if right:
+        assert torch.equal(lengths, p.lengths)
+    else:
+        assert (lengths < 0).any()
+
+
+@pytest.mark.parametrize("T", [1, 2, 4])
+def test_a_decoded_row_for_each_request(T, monkeypatch):
+    plain(monkeypatch)
+    cache = torch.zeros(PAGES, PAGE, 576, dtype=BF)
+    with pytest.raises(ValueError):
+        run(weights(), cache, TABLE, slots([5, 2, 6], [1, 0, 0], TABLE, T), T, False)
+    assert not cache.any()

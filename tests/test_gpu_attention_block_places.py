@@ -153,3 +153,20 @@ def test_cached_tokens_that_are_left_out_are_reported():
                 moe.ops_check()
         block.attention_forward(x, normed, W, cache.clone(), t, p, True, cached_tokens=n)
         moe.ops_check()
+
+
+def test_a_request_without_a_token_ahead_of_others_is_reported():
+    W, lens = attention_weights(), [20, 3, 16]
+    cache, table, free = filled(W, lens)
+    x = inputs(3)
+    normed = moe.rms_norm(x, W.next_norm)
+    for new, right in (([1, 1, 1], True), ([1, 1, 0], True), ([1, 0, 1], False), ([0, 1, 1], False), ([0, 0, 0], True)):
+        t = table.clone()
+        p = moe.page_slots(i32(lens), i32(new), t, free, PAGE, 3)
+        moe.ops_check()
+        block.attention_forward(x, normed, W, cache.clone(), t, p, False)
+        if right:
+            moe.ops_check()
+        else:
+            with pytest.raises(moe.MoeFp4Error):
+                moe.ops_check()
