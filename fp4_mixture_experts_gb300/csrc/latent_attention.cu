@@ -39,6 +39,7 @@
 // 16 SMs, 62 so).  The same lengths give the same bits.  Waits are bounded; results
 // are stored only by warps none of whose waits ran out.
 #include <algorithm>
+#include <cfloat>
 
 #include "latent.cuh"
 
@@ -776,7 +777,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         if (!(ok = wait(&o_full[t], use & 1))) break;
         ++use;
         tmem_fence_after();
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // a query that sees nothing: zeros
+        const float inv = seen > 0 ? 1.f / l : 0.f;  // a query that sees nothing: zeros
         float4* const sums = P.sums + (int64_t)w.slot * (kValue / 4) * kRows + t * kQ + row;
 #pragma unroll 1
         for (int c = rows_here ? 0 : kValue; c < kValue; c += 32) {
@@ -806,7 +807,8 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         if (lane == 0) mbar_arrive(&o_free[t]);
       }
       if (!whole) {
-        P.ml[(int64_t)w.slot * kRows + t * kQ + row] = make_float2(m, l);
+        // (a maximum above -infinity also where all scores are that: the query has seen something)
+        P.ml[(int64_t)w.slot * kRows + t * kQ + row] = make_float2(seen > w.from * kK ? fmaxf(m, -FLT_MAX) : m, l);
         if (lane == 0) P.done[w.slot * 8 + warp - 4] = 1;
       }
     }
@@ -916,7 +918,8 @@ __global__ void __launch_bounds__(32 * kFewWarps) latent_attention_few_kernel(co
     }
 #pragma unroll
     for (int i = 0; i < kFewGroup; ++i) {
-      const float inv = l[i] > 0.f || l[i] != l[i] ? 1.f / l[i] : 0.f;  // a query that sees nothing: zeros
+      const int seen = P.a.causal ? min(s.nk, g0 + i + 1 + s.nk - s.nq) : s.nk;
+      const float inv = seen > 0 ? 1.f / l[i] : 0.f;  // a query that sees nothing: zeros
       if (i < n)
         *reinterpret_cast<uint2*>(P.a.out + ((s.q0 + (int64_t)g0 + i) * P.a.H + h) * kValue + lane * 4) =
             make_uint2(pack_bf16(o[i][0] * inv, o[i][1] * inv), pack_bf16(o[i][2] * inv, o[i][3] * inv));
@@ -1000,7 +1003,7 @@ __global__ void __launch_bounds__(kRows) latent_attention_join_kernel(AttentionP
       }
     }
     if (!complete || row >= what.y) continue;  // a wait ran out; behind the item's last query
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    const float inv = top > -INFINITY ? 1.f / l : 0.f;
     uint32_t v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);

@@ -477,7 +477,8 @@ int moe_fp4_fp8_linear(const moe_fp4_mm_dims* dims, const void* x, int x_type, i
 /* Absorbed form, one new token a sequence, over a paged cache of the latent
  * vectors: with c_j the 576 elements of token j of a sequence,
  *   s_j = scale q . c_j,   out = sum_j softmax(s)_j c_j[0 .. 511]
- * for j < lengths[b]; a sequence of no tokens gets zeros.  fp32 scores,
+ * for j < lengths[b]; a sequence of no tokens gets zeros, a head whose scores are all
+ * -infinity NaN.  fp32 scores,
  * statistics and sums; P is rounded to bf16 for its product, the result once to
  * bf16.  What the cache holds behind a sequence's end is not used, whatever it
  * is; its values up to there are to be finite (an infinity or a NaN reaches every
@@ -514,8 +515,8 @@ int moe_fp4_latent_decode(const moe_fp4_latent_decode_args* args, void* workspac
  * its cached tokens and of the new ones), nq and nk of them; for query i
  *   s_j = scale (q_i[0 .. 127] . kn_j + q_i[128 .. 191] . kr_j)
  *   out_i = sum_j softmax(s)_j v_j        over j < nk; causal: j <= i + nk - nq
- * for every head; a query that sees no key gets zeros, queries of no sequence are
- * left as they were.  fp32 scores, statistics and sums; P is rounded to bf16 for
+ * for every head; a query that sees no key gets zeros (one whose scores are all
+ * -infinity NaN, as the formula does), queries of no sequence are left as they were.  fp32 scores, statistics and sums; P is rounded to bf16 for
  * its product, the result once to bf16.  Values (v) are to be finite; what a
  * sequence's neighbours hold does not reach it.  The same call gives the same bits.
  *   q         bf16 [Tq, H, 192], element strides q_stride, q_head_stride
