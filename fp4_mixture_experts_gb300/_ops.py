@@ -201,9 +201,9 @@ class PageSlots(NamedTuple):
     """What page_slots returns (GPU tensors)."""
     slots: object      # int64 [tokens]: page * page_size + place in it
     positions: object  # int32 [tokens]
-    lengths: object    # int32 [B], with the new tokens
+    lengths: object    # int32 [B], with the new tokens that have a place
     q_offsets: object  # int32 [B + 1], of the new tokens
-    k_offsets: object  # int32 [B + 1], of all tokens
+    k_offsets: object  # int32 [B + 1], of all tokens of lengths
     taken: object      # int32 []: pages taken from the front of free_pages
 
 
@@ -214,7 +214,7 @@ def page_slots(lengths, new_tokens, block_table, free_pages, page_size: int, tok
     and entered in block_table (int32 [B, width], in place).  tokens: the size of slots and positions, at least the
     number of new tokens; behind the last one slots are -1.  out: an earlier result of the same sizes, to be
     overwritten.  Requests that their rows do not hold, too few free pages or too many tokens are reported by
-    ops_check, their tokens' slots are -1."""
+    ops_check; the tokens without a place have slot -1 and are not in lengths and k_offsets."""
     f = _native.page_slots
     return PageSlots(*f(lengths, new_tokens, block_table, free_pages, page_size, tokens, *(out or (None,) * 6),
                         _handle(stream)))
