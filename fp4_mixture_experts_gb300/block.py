@@ -234,11 +234,11 @@ def attention_forward(residual, normed, weights: AttentionWeights, cache, block_
     q = fp8_linear(rms_norm(down[:, :r], W.q_norm, eps=eps), W.w_q, W.w_q_tiled).view(T, H, NOPE + ROPE)
     q_rope = turned(q[..., NOPE:], *angles)
     if prompt:
-        rows, k_offsets = new, pages.k_offsets
-        if cached_tokens is None:  # where some are not new, offsets that latent_attention reports
-            k_offsets = torch.where(k_offsets == pages.q_offsets, k_offsets, 2 ** 31 - 2)
+        if cached_tokens is None:  # the new tokens' rows; an offset that latent_attention reports where a request has others
+            rows, k_offsets = new, pages.q_offsets.clone()
+            k_offsets[1:].masked_fill_(pages.lengths > k_offsets[1:] - k_offsets[:-1], 2 ** 31 - 2)
         else:
-            rows = cached_rows(cache, block_table, pages, cached_tokens)
+            rows, k_offsets = cached_rows(cache, block_table, pages, cached_tokens), pages.k_offsets
         kv = fp8_linear(rows[:, :LATENT], W.w_kv, W.w_kv_tiled).view(-1, H, NOPE + VALUE)
         q = torch.cat([q[..., :NOPE], q_rope], 2)
         o = latent_attention(q, kv, rows[:, LATENT:], pages.q_offsets, k_offsets, scale)

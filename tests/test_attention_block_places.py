@@ -180,7 +180,18 @@ def test_keys_of_the_new_tokens_alone_are_for_batches_without_cached_ones(T, len
         assert ((ko > T) & (ko < 2 ** 31 - 1)).any()
     else:
         assert torch.equal(ko, p.k_offsets)
-    assert ko.dtype == torch.int32 and (ko[1:] >= ko[:-1]).all()
+    assert ko.dtype == torch.int32
+
+
+def test_keys_of_new_tokens_that_have_no_place(monkeypatch):
+    """a prompt whose second request's last tokens found no page: its lengths and the key offsets do not count them, the
+    rows of keys are the new tokens' all the same"""
+    got = plain(monkeypatch)
+    W, cache = weights(), torch.zeros(PAGES, PAGE, 576, dtype=BF)
+    p = slots([0, 0, 0], [3, 6, 2], TABLE, 11, {7: -1, 8: -1})
+    p = p._replace(lengths=i32([3, 4, 2]), k_offsets=i32([0, 3, 7, 9]))
+    run(W, cache, TABLE, p, 11, True)
+    assert got["attention"][4].tolist() == [0, 3, 9, 11] and got["attention"][1].shape[0] == 11
 
 
 @pytest.mark.parametrize("lens,new,right", [([5, 2, 0], [1, 1, 1], True), ([5, 2, 0], [1, 1, 0], True), ([5, 2, 6], [1, 0, 0], True),

@@ -170,3 +170,23 @@ def test_a_request_without_a_token_ahead_of_others_is_reported():
         else:
             with pytest.raises(moe.MoeFp4Error):
                 moe.ops_check()
+
+
+def test_a_prompt_that_the_free_pages_do_not_hold():
+    """the second of three: the others' results are as without it missing any"""
+    W, new = attention_weights(), [20, 40, 9]
+    T, x = sum(new), inputs(sum(new))
+    normed = moe.rms_norm(x, W.next_norm)
+    cache = torch.full((12, PAGE, 576), float("nan"), dtype=torch.bfloat16, device=DEV)
+    free, results = i32(list(range(12))), []
+    for n in (12, 4):                                       # the second request's third page, and the third one's, are missing
+        table = torch.full((3, 4), 5, dtype=torch.int32, device=DEV)
+        p = moe.page_slots(i32([0] * 3), i32(new), table, free[:n], PAGE, T)
+        results.append(block.attention_forward(x, normed, W, cache.clone(), table, p, True))
+        if n < 12:
+            assert p.lengths.tolist() == [20, 32, 0] and int(p.taken) == 4
+            with pytest.raises(moe.MoeFp4Error):
+                moe.ops_check()
+    moe.ops_check()
+    for a, b in zip(*results):                              # (keys and queries are the new tokens', with a place or without)
+        assert torch.equal(bits(a), bits(b))
