@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads) page_slots_kernel(const PageParams Q
       if (sum.x > P.tokens || sum.y > P.free_count || keys > INT32_MAX) bad = kErrBadExpertId;
     }
   }
-  if (first_cta && bad) atomicOr(&g_pages_err[0], bad);
+  if (!first_cta) bad = 0;  // (one CTA reports the requests)
   __syncthreads();
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < P.tokens; i += (int64_t)gridDim.x * kThreads) {
     int64_t slot = -1, position = 0;
@@ -153,7 +153,10 @@ __global__ void __launch_bounds__(kThreads) page_slots_kernel(const PageParams Q
             if (in_page == 0) *entry = page;
           }
         }
-        if (page >= 0) slot = (int64_t)page * P.page + in_page;
+        if (page >= 0)
+          slot = (int64_t)page * P.page + in_page;
+        else
+          bad = kErrBadExpertId;  // no page for it, or the row or the free list names none
       } else {
         position = 0;
       }
@@ -161,6 +164,7 @@ __global__ void __launch_bounds__(kThreads) page_slots_kernel(const PageParams Q
     P.slots[i] = slot;
     P.positions[i] = (int32_t)position;
   }
+  if (bad) atomicOr(&g_pages_err[0], bad);
 }
 
 }  // namespace

@@ -556,12 +556,13 @@ int moe_fp4_latent_attention(const moe_fp4_latent_attention_args* args, void* wo
  *   taken      int32: pages taken, the first ones of free_pages, each entered
  * A batch of fewer than `tokens` new tokens (a padded one) gets slot -1 and position
  * 0 behind its last.  Negative lengths (taken as 0), a request that its row of the
- * table does not hold, more new tokens than `tokens` and too few free pages set error
- * bit 1 (moe_fp4_ops_check).  Tokens without a place get slot -1 and are not counted in
- * out_lengths and k_offsets: a later call may place them, and nobody reads what a row of
- * the table held behind its request.  (Beside its queries, all of the new tokens, such a
- * request then has fewer keys.)  The outputs overlap no input; table is written in
- * place. */
+ * table does not hold, more new tokens than `tokens`, too few free pages, and a negative
+ * page in free_pages or in the table, where a new token lies in it, set error
+ * bit 1 (moe_fp4_ops_check).  Tokens without a place get slot -1 and, but for those in a
+ * negative page, are not counted in out_lengths and k_offsets: a later call may place
+ * them, and nobody reads what a row of the table held behind its request.  (Beside its
+ * queries, all of the new tokens, such a request then has fewer keys.)  The outputs
+ * overlap no input; table is written in place. */
 typedef struct moe_fp4_page_slots_args {
   int32_t B, page, width;            /* B 0 .. 8192, width * page below 2^31 */
   int64_t tokens, free_count, table_stride;

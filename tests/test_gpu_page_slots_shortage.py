@@ -120,3 +120,28 @@ def test_pages_are_taken_for_tokens_with_a_place_only():
     t, p, lost = check_call([0, 0], [20, 40], np.full((2, 4), -1, dtype=np.int32), [7, 8, 9, 10, 11], 16, 30)
     assert lost == 30 and int(p.taken) == 3 and p.lengths.tolist() == [20, 10]
     assert t.tolist() == [[7, 8, -1, -1], [9, -1, -1, -1]]
+
+
+@pytest.mark.parametrize("bad", [-1, -7, -2 ** 31])
+def test_an_owned_page_that_the_table_does_not_name_is_reported(bad):
+    for row, lens in ((0, [10, 20, 5]), (1, [16, 30, 0]), (2, [1, 1, 3])):
+        table = np.array([[3, 1, 9], [4, 0, 5], [7, 8, 2]], dtype=np.int32)
+        at = lens[row] // 16
+        table[row, at] = bad
+        p = moe.page_slots(i32(lens), i32([1, 1, 1]), i32(table), i32([20, 21, 22]), 16, 3)
+        if lens[row] % 16:                                  # else that page is a new one
+            assert p.slots[row] == -1
+            with pytest.raises(moe.MoeFp4Error):
+                moe.ops_check()
+        else:
+            assert p.slots[row] >= 0
+        moe.ops_check()
+        assert (p.slots >= 0).sum() == (2 if lens[row] % 16 else 3)
+
+
+def test_a_negative_free_page_is_reported():
+    p = moe.page_slots(i32([0, 3]), i32([20, 1]), i32([[-1, -1], [4, -1]]), i32([6, -2]), 16, 21)
+    with pytest.raises(moe.MoeFp4Error):
+        moe.ops_check()
+    assert p.slots.tolist() == [6 * 16 + i for i in range(16)] + [-1] * 4 + [4 * 16 + 3]
+    moe.ops_check()
