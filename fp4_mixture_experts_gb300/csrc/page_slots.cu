@@ -167,6 +167,22 @@ __global__ void __launch_bounds__(kThreads) page_slots_kernel(const PageParams Q
   if (bad) atomicOr(&g_pages_err[0], bad);
 }
 
+struct Bytes {
+  uintptr_t at, size;
+};
+Bytes bytes_at(const void* p, int64_t size) { return {(uintptr_t)p, (uintptr_t)size}; }
+bool overlap(const Bytes& x, const Bytes& y) {
+  return x.size > 0 && y.size > 0 && x.at < y.at + y.size && y.at < x.at + x.size;
+}
+// whether some of x is in a row of the table (not only between rows)
+bool in_table(const moe_fp4_page_slots_args& a, const Bytes& x) {
+  const uintptr_t base = (uintptr_t)a.table, row = 4 * (uintptr_t)a.width, stride = 4 * (uintptr_t)a.table_stride;
+  if (a.B == 0 || !overlap(x, {base, (uintptr_t)(a.B - 1) * stride + row})) return false;
+  if (x.at <= base) return true;  // it reaches the first row
+  const uintptr_t in_row = (x.at - base) % stride;
+  return in_row < row || in_row + x.size > stride;
+}
+
 }  // namespace
 
 cudaError_t page_slots_error(int32_t** word) { return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_pages_err); }
@@ -189,14 +205,20 @@ extern "C" int moe_fp4_page_slots(const moe_fp4_page_slots_args* args, void* cud
       ((uintptr_t)a.free_pages & 3) || ((uintptr_t)a.positions & 3) || ((uintptr_t)a.out_lengths & 3) ||
       ((uintptr_t)a.q_offsets & 3) || ((uintptr_t)a.k_offsets & 3) || ((uintptr_t)a.taken & 3))
     return MOE_FP4_ERR_INVALID_ARG;
-  // other CTAs read the lengths while one writes these
-  const uintptr_t bytes = (uintptr_t)a.B * 4;
-  const auto apart = [bytes](const void* in, const void* out) {
-    return (uintptr_t)in + bytes <= (uintptr_t)out || (uintptr_t)out + bytes + 4 <= (uintptr_t)in;
-  };
-  for (const void* in : {(const void*)a.lengths, (const void*)a.new_tokens})
-    if (a.B > 0 && (!apart(in, a.out_lengths) || !apart(in, a.q_offsets) || !apart(in, a.k_offsets)))
-      return MOE_FP4_ERR_INVALID_ARG;
+  // what a CTA writes, others read or write meanwhile, if it is the same memory
+  const Bytes in[] = {bytes_at(a.lengths, 4 * (int64_t)a.B), bytes_at(a.new_tokens, 4 * (int64_t)a.B), bytes_at(a.free_pages, 4 * a.free_count)};
+  const Bytes out[] = {bytes_at(a.slots, 8 * a.tokens),         bytes_at(a.positions, 4 * a.tokens),
+                       bytes_at(a.out_lengths, 4 * (int64_t)a.B), bytes_at(a.q_offsets, 4 * ((int64_t)a.B + 1)),
+                       bytes_at(a.k_offsets, 4 * ((int64_t)a.B + 1)), bytes_at(a.taken, 4)};
+  for (const Bytes& i : in)
+    if (in_table(a, i)) return MOE_FP4_ERR_INVALID_ARG;
+  for (const Bytes& o : out) {
+    if (in_table(a, o)) return MOE_FP4_ERR_INVALID_ARG;
+    for (const Bytes& i : in)  // (out_lengths, beside the requests' numbers, as of B + 1)
+      if (overlap(&o == &out[2] && &i != &in[2] ? Bytes{o.at, o.size + 4} : o, i)) return MOE_FP4_ERR_INVALID_ARG;
+    for (const Bytes* p = out; p != &o; ++p)
+      if (overlap(o, *p)) return MOE_FP4_ERR_INVALID_ARG;
+  }
   PageParams P{a};
   const int smem = (a.B + 1) * (int)sizeof(longlong2);
   if (smem > 48 * 1024 - 256 &&
