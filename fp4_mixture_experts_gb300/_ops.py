@@ -199,7 +199,7 @@ def latent_attention(q, kv, k_rope, q_offsets, k_offsets, scale, causal: bool = 
 
 class PageSlots(NamedTuple):
     """What page_slots returns (GPU tensors)."""
-    slots: object      # int64 [tokens]: page * page_size + place in it
+    slots: object      # int64 [tokens]: page * page_size + place in it; -1: none (block.write_rows leaves such tokens out)
     positions: object  # int32 [tokens]
     lengths: object    # int32 [B], with the new tokens that have a place
     q_offsets: object  # int32 [B + 1], of the new tokens

@@ -28,7 +28,7 @@ the paged cache and attends, every projection an FP8 product:
     residual' = residual + W_o o;  normed' = norm(residual')     (block_residual)
 
 (the rotary turn, the concatenations and the cache's scatter and gather in
-PyTorch's own operations).
+PyTorch's own operations; indices that point nowhere are kept from those).
 
 prepare() lays the scales out once, when the weights are loaded.  Everything
 runs on the current stream.

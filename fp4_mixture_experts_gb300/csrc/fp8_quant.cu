@@ -6,7 +6,10 @@
 // 2^-e (ties to even).  Eight lanes share a block, 16 elements each: loads of 32 or
 // 16 bytes, three shuffles for amax, one 16-byte store of codes.  The products'
 // scale tiles hold a byte for 32 elements: the same one four times, one word.
-// HBM bounds it: 8192 x 8192 bf16 31 us, 201 MB, 6.5 TB/s.
+// Its instructions and HBM bound it side by side: 8192 x 8192 bf16 27 us in one launch
+// with cold caches, 134 MB read at 5.0 TB/s (69% of DRAM's peak) and 0.72 instructions a
+// cycle of a scheduler; 8192 x 4096 16 us, 55% and 0.68.  The codes stay in L2 for the
+// product (12 of 67 MB are written meanwhile).
 #include <algorithm>
 
 #include "moe_fp4_internal.cuh"

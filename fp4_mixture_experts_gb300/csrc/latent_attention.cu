@@ -13,7 +13,8 @@
 // 128 x 16 takes 105 cycles with A in shared memory (Q) and 73 with A in tensor memory
 // (P), so that 128 x 128 scores are 1,260 + 584 cycles of MMAs and, at 16 exponentials
 // a cycle, 1,024 of exponentials: the MMAs bound it (8192 tokens, 64 heads, causal:
-// 920 us, 1.49 PFLOP/s, about 1,930 cycles; without any softmax 880).  S lies in
+// 920 us in short runs, 1.49 PFLOP/s, about 1,930 cycles, without any softmax 880; 990 to
+// 1030 in a long loop of calls, under the power cap).  S lies in
 // tensor memory, a query a lane, so that maximum and sum need no other thread; P
 // overwrites it as bf16 and is the MMA's A operand from there; V is the B operand as
 // it lies (MN-major).

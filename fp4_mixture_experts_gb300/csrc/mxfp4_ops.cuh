@@ -123,12 +123,13 @@ __device__ __forceinline__ uint32_t e2m1x8(const float* v) {
 //
 // kLeaving is an ALIGN of 32 bytes whose elements leave the caches first: for rows that
 // are read once and whose codes a product reads next, which are then still in L2 (bf16
-// rows and their product of 4096 columns: FP8 4608 x 4096 59.6 -> 57.3 us, 2048 x 7168 49.8
-// -> 48.1, no slower for fewer; MXFP4 from 32 MB of rows on, 4608 x 7168 60 -> 57, 2600 x
-// 7168 38.5 -> 38.2, but 2048 x 7168 27.5 -> 27.9).  What is read again must not: rows
-// quantised by themselves in a loop (4608 x 4096 6.8 -> 8.2 us), gathered ones, which are
-// read once for each use (2048 rows, 8 uses 25 -> 29), and the few rows that all CTAs of
-// their kernel read (16 x 16384 by 2048 25 -> 27).
+// rows and their product of 4096 columns, in a graph of calls: FP8 4608 x 4096 59.6 -> 57.3
+// us, 2048 x 7168 49.8 -> 48.1, no slower for fewer; MXFP4 from 32 MB of rows on, 4608 x
+// 7168 60 -> 57, 2600 x 7168 38.5 -> 38.2, but 2048 x 7168 27.5 -> 27.9).  What is read
+// again must not: rows quantised by themselves in a loop (4608 x 4096 6.8 -> 8.2 us),
+// gathered ones, which are read once for each use (2048 rows, 8 uses, cold caches 25 ->
+// 29), and the few rows that all CTAs of their kernel read (16 x 16384 by 2048, cold
+// caches 25 -> 27).
 constexpr int kLeaving = 33;
 template <bool F32, int ALIGN>
 __device__ __forceinline__ void load16_raw(const void* x, int64_t at, uint32_t (&w)[16]) {

@@ -482,7 +482,8 @@ int moe_fp4_fp8_linear(const moe_fp4_mm_dims* dims, const void* x, int x_type, i
  * statistics and sums; P is rounded to bf16 for its product, the result once to
  * bf16.  What the cache holds behind a sequence's end is not used, whatever it
  * is; its values up to there are to be finite (an infinity or a NaN reaches every
- * head of the sequence).  The same call gives the same bits.
+ * head of the sequence).  The same call gives the same bits; a sequence's last bits
+ * depend on the lengths beside it.
  *   q        bf16 [B, H, 576] (latent part, rotary part), element strides
  *            q_stride and q_head_stride: multiples of 8, base 16-byte aligned
  *   cache    bf16 [pages, page, 576], contiguous, 16-byte aligned; page a multiple
@@ -517,8 +518,10 @@ int moe_fp4_latent_decode(const moe_fp4_latent_decode_args* args, void* workspac
  *   out_i = sum_j softmax(s)_j v_j        over j < nk; causal: j <= i + nk - nq
  * for every head; a query that sees no key gets zeros (one whose scores are all
  * -infinity NaN, as the formula does), queries of no sequence are left as they were.  fp32 scores, statistics and sums; P is rounded to bf16 for
- * its product, the result once to bf16.  Values (v) are to be finite; what a
- * sequence's neighbours hold does not reach it.  The same call gives the same bits.
+ * its product (not for sequences of at most 8 queries and 32 keys in batches of many
+ * such, which have a kernel of their own), the result once to bf16.  Values (v) are to be
+ * finite; what a sequence's neighbours hold does not reach it.  The same call gives the
+ * same bits; a sequence's last bits depend on the sizes of the batch beside it.
  *   q         bf16 [Tq, H, 192], element strides q_stride, q_head_stride
  *   kv        bf16 [Tk, H, 256]: kn and v of a head side by side
  *   k_rope    bf16 [Tk, 64], the heads' shared rotary key kr
