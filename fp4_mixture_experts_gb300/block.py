@@ -193,9 +193,15 @@ def write_rows(cache, slots, rows):
     holds is added to them, as integers: for a token without a place 0, anywhere, which changes nothing, whatever is there
     and whoever writes it meanwhile."""
     import torch
+    if cache.dtype != torch.bfloat16 or cache.dim() != 3 or cache.shape[2] != LATENT + ROPE or not cache.is_contiguous():
+        raise ValueError("cache must be contiguous bf16 [pages, page, 576]")
+    if rows.dtype != cache.dtype or rows.shape != (slots.numel(), LATENT + ROPE):
+        raise ValueError("rows must be bf16 [T, 576] with a slot each")
+    if cache.numel() == 0:
+        return
     words = cache.view(-1, LATENT + ROPE).view(torch.int64)
     at = slots.clamp(0, words.shape[0] - 1)
-    words.index_add_(0, at, (rows.view(torch.int64) - words.index_select(0, at)) * (at == slots)[:, None])
+    words.index_add_(0, at, (rows.contiguous().view(torch.int64) - words.index_select(0, at)) * (at == slots)[:, None])
 
 
 def cached_rows(cache, block_table, pages: PageSlots, tokens: int):

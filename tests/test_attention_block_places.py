@@ -218,3 +218,34 @@ def test_a_decoded_row_for_each_request(T, monkeypatch):
     with pytest.raises(ValueError):
         run(weights(), cache, TABLE, slots([5, 2, 6], [1, 0, 0], TABLE, T), T, False)
     assert not cache.any()
+
+
+def test_rows_to_a_cache_of_no_pages():
+    cache = torch.zeros(0, PAGE, 576, dtype=BF)
+    block.write_rows(cache, torch.tensor([0, -1, 7]), torch.ones(3, 576, dtype=BF))
+    block.write_rows(cache, torch.zeros(0, dtype=torch.int64), torch.ones(0, 576, dtype=BF))
+
+
+@pytest.mark.parametrize("rows", [torch.ones(3, 576, dtype=torch.float16), torch.ones(3, 576), torch.ones(2, 576, dtype=BF),
+                                  torch.ones(3, 512, dtype=BF), torch.ones(576, dtype=BF), torch.ones(1, 576, dtype=BF)])
+def test_rows_of_another_type_or_number_are_refused(rows):
+    cache = torch.zeros(PAGES, PAGE, 576, dtype=BF)
+    with pytest.raises(ValueError):
+        block.write_rows(cache, torch.tensor([0, -1, 7]), rows)
+    assert not cache.any()
+
+
+@pytest.mark.parametrize("cache", [torch.zeros(PAGES, PAGE, 576, dtype=torch.float16), torch.zeros(PAGES, PAGE, 512, dtype=BF),
+                                   torch.zeros(PAGES, PAGE, 640, dtype=BF)[:, :, :576]])
+def test_another_cache_is_refused(cache):
+    with pytest.raises(ValueError):
+        block.write_rows(cache, torch.tensor([0, -1, 7]), torch.ones(3, 576, dtype=BF))
+
+
+def test_rows_of_any_strides():
+    wide = torch.randn(5, 601, generator=torch.Generator().manual_seed(1)).to(BF)
+    cache = torch.zeros(PAGES, PAGE, 576, dtype=BF)
+    block.write_rows(cache, torch.tensor([3, -1, 0, 23, 8]), wide[:, 3:579])
+    want = torch.zeros(PAGES * PAGE, 576, dtype=BF)
+    want[[3, 0, 23, 8]] = wide[[0, 2, 3, 4], 3:579]
+    assert torch.equal(cache.view(-1, 576), want)
