@@ -186,8 +186,8 @@ def turned(x, cos, sin):
 
 
 def write_rows(cache, slots, rows):
-    """The tokens' latent vectors, bf16 [T, 576], to their places in cache (slots int64 [T]); a token without a place (slot -1,
-    or one beyond the cache) writes nothing.
+    """The tokens' latent vectors, bf16 [T, 576], to their places in cache (slots int64 [T], no two the same place); a token
+    without a place (slot -1, or one beyond the cache) writes nothing.
 
     PyTorch's copies by index end the process's CUDA context on such an index.  So the difference to the bits that a place
     holds is added to them, as integers: for a token without a place 0, anywhere, which changes nothing, whatever is there
